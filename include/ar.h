@@ -413,6 +413,126 @@ int ar_reduce_fp8(const uint8_t* const* codes, const uint8_t* const* scales, int
                   int n_out, size_t n, void* stream);
 
 /*
+ * Operators on either side of the all-reduce.  In a tensor-parallel
+ * transformer block a row-parallel projection makes each rank's buffer, the
+ * all-reduce sums them, the residual is added, the sum is normed, and the
+ * norm's result (in 8 bits) feeds the next column-parallel projection.
+ *
+ * fp8 matrices.  A matrix [rows x cols] travels as E4M3 codes (as in
+ * ar_quantize_fp8) with a scale for each block of AR_BLOCK = 128 columns and
+ * block_rows = 1 or 128 rows; element (i, j) stands for
+ * value(codes[i*ld + j]) * scale(i / block_rows, j / 128).
+ *   codes      device pointer, 16-byte aligned
+ *   ld         bytes from row to row: at least cols, a multiple of 16.  Bytes
+ *              of a row after its cols-th are never read as values and never
+ *              written.
+ *   scales     device pointer, naturally aligned; the scale of block (i, j)
+ *              is element i*scale_rs + j*scale_cs.  Of an output no two
+ *              blocks may share an element.
+ *   scale_fmt  AR_SCALE_F32: binary32.  AR_SCALE_E8M0: one byte b, the scale
+ *              is 2^(b - 127), 255 is NaN (the scale bytes of
+ *              ar_quantize_fp8, and of the OCP Microscaling formats).
+ * Quantising picks, with amax the largest finite magnitude of the block,
+ *   F32   s = max(amax / 448, 2^-126), and the codes of x * (1 / s);
+ *   E8M0  s = 2^k, k the smallest integer in [-127, 127] with
+ *         amax <= 448 * 2^k (-127 for a block of zeros), and the codes of
+ *         x * 2^-k (exact),
+ * each the nearest code (ties to even), 0x7F for a NaN or infinite element.
+ * A matrix without rows or columns may have NULL pointers.
+ */
+#define AR_BLOCK 128
+#define AR_SCALE_F32 0
+#define AR_SCALE_E8M0 1
+#define AR_FMT_BF16 0
+#define AR_FMT_F32 1
+#define AR_NORM_MAX_COLS 65536
+
+typedef struct ar_fp8_matrix {
+  uint8_t* codes;
+  size_t ld;
+  void* scales;
+  size_t scale_rs, scale_cs;
+  int scale_fmt;
+  int block_rows;
+} ar_fp8_matrix;
+
+/*
+ * Reduce, residual and root-mean-square norm in one pass:
+ *   h = ((x_0 + x_1) + ... + x_{P-1}) (+ residual)     binary32
+ *   res_out = rn(h)
+ *   y = h * (1 / sqrt(mean over the row of h^2 + eps)) * weight   binary32
+ * The norm reads the unrounded h; y is written as bf16 (`y`) and / or
+ * quantised from its binary32 value (`q`, block_rows 1).
+ *   ins       host array of P device pointers, each [rows x cols] bf16
+ *   residual  [rows x cols] bf16, or NULL
+ *   weight    cols gains, weight_fmt AR_FMT_BF16 or AR_FMT_F32, or NULL: ones
+ *   res_out, y  [rows x cols] bf16, either may be NULL; each may be exactly
+ *             an input or the residual (in place)
+ *   q         the fp8 result, or NULL.  One of res_out, y and q is needed.
+ *   eps       >= 0.  A row of zeros with eps 0 gives NaN.
+ * cols at most AR_NORM_MAX_COLS (AR_ERR_UNSUPPORTED).  Any cols >= 1: rows
+ * that start on no vector boundary are read and written in place.
+ */
+int ar_reduce_norm(const void* const* ins, int P, const void* residual, const void* weight, int weight_fmt,
+                   size_t rows, size_t cols, float eps, void* res_out, void* y, const ar_fp8_matrix* q,
+                   void* stream);
+
+/*
+ * Gradient of the norm.  dy is the gradient of y, dres of res_out; with
+ * r = 1 / sqrt(mean h^2 + eps), x = h r and g = dy * weight:
+ *   dx[i]      = rn(dres + r * (g - x * mean over the row of (g x)))
+ *   dweight[j] = sum over rows of dy x                          binary32
+ * dx is the gradient of h, hence of every contribution and of the residual.
+ *   dy, h     [rows x cols] bf16; h is what ar_reduce_norm wrote to res_out
+ *   dres      [rows x cols] bf16, or NULL
+ *   dx        [rows x cols] bf16, may be exactly dy, h or dres; or NULL
+ *   dweight   cols binary32 values, overwritten; or NULL
+ *   workspace ar_norm_bwd_workspace(rows, cols) bytes, 16-byte aligned, for
+ *             dweight (NULL without it); no particular contents
+ * The sums' order is fixed by rows and cols: results repeat bit for bit.
+ */
+size_t ar_norm_bwd_workspace(size_t rows, size_t cols);
+int ar_norm_bwd(const void* dy, const void* h, const void* weight, int weight_fmt, const void* dres, size_t rows,
+                size_t cols, float eps, void* dx, float* dweight, void* workspace, size_t workspace_bytes,
+                void* stream);
+
+/*
+ * Quantise a bf16 matrix x [rows x cols], row r at x + r * ldx (elements),
+ * into q.  transpose == 0: q is [rows x cols]; otherwise q is x transposed,
+ * [cols x rows], blocks taken along its own rows.  q->block_rows is 1 or 128.
+ * x is 2-byte aligned at least; reads nothing between rows.
+ */
+int ar_quantize_block(const void* x, size_t ldx, size_t rows, size_t cols, const ar_fp8_matrix* q, int transpose,
+                      void* stream);
+
+/*
+ * fp8 matrix products of one shape, one for each of G problems (the shards
+ * of G ranks), in one call:
+ *   C_g[m,n] = sum over blocks j of 128 along K of
+ *              sa(m,j) * sb(n,j) * sum over k in block j of a[m,k] * b[n,k]
+ * products and sums in binary32 (matrix cores), the result rounded once to
+ * bf16 or kept.  Row-major a [M x K] with block_rows 1 (activations), b
+ * [N x K] with block_rows 128 (weights) or 1.
+ *   a, b      host arrays of G matrices; ld, strides, scale_fmt and
+ *             block_rows are the same for all of a, and for all of b, and
+ *             scale_fmt is the same for both
+ *   c         host array of G device pointers, [M x N], out_fmt AR_FMT_BF16 or
+ *             AR_FMT_F32, row m at c + m * ldc (elements), ldc >= N
+ *   G         1..AR_MAX_RANKS
+ *   workspace device memory, 16-byte aligned, zero before its first use; a
+ *             call leaves its counters zero again.  With at least
+ *             ar_gemm_fp8_workspace(M, N, K, G) bytes, products with few
+ *             rows and columns are split along K over the device; with less, or
+ *             NULL, they are not.  Calls that overlap in time must not share
+ *             it.
+ * K == 0 writes zeros.  M, N, K below 2^31, N below 2^22 (AR_ERR_UNSUPPORTED).
+ * With a given shape and workspace results repeat bit for bit.
+ */
+size_t ar_gemm_fp8_workspace(size_t M, size_t N, size_t K, int G);
+int ar_gemm_fp8(const ar_fp8_matrix* a, const ar_fp8_matrix* b, void* const* c, int G, size_t M, size_t N, size_t K,
+                size_t ldc, int out_fmt, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Initialise an error record for ar_unpack_fused / ar_rd_schedule on
  * `stream`: d_err[0] = 0, d_err[1] = UINT64_MAX.  Uses a one-thread kernel,
  * not a memset, so it may be recorded in a HIP graph.

@@ -38,6 +38,9 @@ __all__ = [
     "AR_KERNEL_2STAGE_INPLACE_SMALL",
     "AR_SMALL_ELEMS",
     "FP8_BLOCK",
+    "ar_reduce_norm", "ar_norm_bwd", "ar_quantize_block", "ar_gemm_fp8", "norm_bwd_workspace", "gemm_fp8_workspace",
+    "fp8_codes_empty", "fp8_scales_empty",
+    "AR_BLOCK", "AR_SCALE_F32", "AR_SCALE_E8M0", "AR_FMT_BF16", "AR_FMT_F32", "AR_NORM_MAX_COLS",
 ]
 
 AR_OK = 0
@@ -78,6 +81,12 @@ AR_KERNEL_UBATCH_BOUNDED = 20
 AR_KERNEL_2STAGE_INPLACE_SMALL = 21
 AR_SMALL_ELEMS = 2097152
 FP8_BLOCK = 32                  # elements per power-of-two scale
+AR_BLOCK = 128                  # columns per scale of an fp8 matrix
+AR_SCALE_F32 = 0
+AR_SCALE_E8M0 = 1
+AR_FMT_BF16 = 0
+AR_FMT_F32 = 1
+AR_NORM_MAX_COLS = 65536
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_HERE, "libarcore.so")
@@ -86,6 +95,12 @@ _lib = None
 _vp = ctypes.c_void_p
 _sz = ctypes.c_size_t
 _u32 = ctypes.c_uint32
+
+
+class _Fp8Matrix(ctypes.Structure):
+    """ar_fp8_matrix"""
+    _fields_ = [("codes", _vp), ("ld", _sz), ("scales", _vp), ("scale_rs", _sz), ("scale_cs", _sz),
+                ("scale_fmt", ctypes.c_int), ("block_rows", ctypes.c_int)]
 
 
 class ARError(RuntimeError):
@@ -140,6 +155,21 @@ def lib():
         L.ar_reduce_fp8.restype = ctypes.c_int
         L.ar_reduce_fp8.argtypes = [ctypes.POINTER(_vp), ctypes.POINTER(_vp), ctypes.c_int,
                                     ctypes.POINTER(_vp), ctypes.c_int, _sz, _vp]
+        mp, f32 = ctypes.POINTER(_Fp8Matrix), ctypes.c_float
+        L.ar_reduce_norm.restype = ctypes.c_int
+        L.ar_reduce_norm.argtypes = [ctypes.POINTER(_vp), ctypes.c_int, _vp, _vp, ctypes.c_int, _sz, _sz, f32, _vp,
+                                     _vp, mp, _vp]
+        L.ar_norm_bwd_workspace.restype = _sz
+        L.ar_norm_bwd_workspace.argtypes = [_sz, _sz]
+        L.ar_norm_bwd.restype = ctypes.c_int
+        L.ar_norm_bwd.argtypes = [_vp, _vp, _vp, ctypes.c_int, _vp, _sz, _sz, f32, _vp, _vp, _vp, _sz, _vp]
+        L.ar_quantize_block.restype = ctypes.c_int
+        L.ar_quantize_block.argtypes = [_vp, _sz, _sz, _sz, mp, ctypes.c_int, _vp]
+        L.ar_gemm_fp8_workspace.restype = _sz
+        L.ar_gemm_fp8_workspace.argtypes = [_sz, _sz, _sz, ctypes.c_int]
+        L.ar_gemm_fp8.restype = ctypes.c_int
+        L.ar_gemm_fp8.argtypes = [mp, mp, ctypes.POINTER(_vp), ctypes.c_int, _sz, _sz, _sz, _sz, ctypes.c_int, _vp,
+                                  _sz, _vp]
         L.ar_set_launch_shape.restype = ctypes.c_int
         L.ar_set_launch_shape.argtypes = [ctypes.c_int] * 6
         ip = ctypes.POINTER(ctypes.c_int)
@@ -223,7 +253,7 @@ def prepare(func, *args, **kwargs) -> Prepared:
     step's all-reduce): a wrapper call spends about 0.45 us per tensor in
     checks and pointer lookups, a prepared call none.  ``func`` is one of the
     device calls of this module."""
-    if func not in _PREPARABLE:
+    if func not in _PREPARABLE and func not in _PREPARABLE_BLOCK:
         raise ValueError(f"prepare() takes a device call of this module, not {func!r}")
     slot = []
     _tls.capture = slot
@@ -441,6 +471,179 @@ def ar_reduce_fp8(codes: Sequence, scales: Sequence, outs: Sequence, n: int | No
           _stream(stream))
 
 
+# ------------------------------------------- norm, block quantiser, fp8 product
+
+def _mat(t, elem_sizes, name: str, shape=None):
+    """(pointer, row stride in elements) of a 2-D device tensor whose rows
+    are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} must have shape {'(rows, cols)' if shape is None else tuple(shape)}, "
+                         f"not {tuple(t.shape)}")
+    if t.element_size() not in elem_sizes:
+        raise ValueError(f"{name} must have {' or '.join(map(str, elem_sizes))}-byte elements")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), (t.stride(0) if rows > 1 else cols)
+
+
+def _rows_of(t, name: str, shape):
+    """Pointer of a contiguous bf16 matrix of that shape."""
+    ptr = _dev_ptr(t, 2, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    return ptr
+
+
+def _fp8_matrix(codes, scales, shape, block_rows: int, name: str) -> _Fp8Matrix:
+    rows, cols = shape
+    ptr, ld = _mat(codes, (1,), f"{name} codes", shape)
+    if rows <= 1:
+        ld = -(-cols // 16) * 16
+    want = (-(-rows // block_rows), -(-cols // AR_BLOCK))
+    if not scales.is_cuda:
+        raise ValueError(f"{name} scales must be a device tensor")
+    if tuple(scales.shape) != want:
+        raise ValueError(f"{name} scales must have shape {want}, not {tuple(scales.shape)}")
+    if scales.element_size() == 4 and scales.is_floating_point():
+        fmt = AR_SCALE_F32
+    elif scales.element_size() == 1:
+        fmt = AR_SCALE_E8M0
+    else:
+        raise ValueError(f"{name} scales must be binary32 or power-of-two bytes")
+    # the stride of an axis of one block says nothing
+    rs = scales.stride(0) if want[0] > 1 else 0
+    cs = scales.stride(1) if want[1] > 1 else 0
+    return _Fp8Matrix(ptr, ld, scales.data_ptr(), rs, cs, fmt, block_rows)
+
+
+def _gain(weight, cols: int):
+    if weight is None:
+        return None, AR_FMT_BF16
+    if weight.numel() != cols:
+        raise ValueError(f"weight holds {weight.numel()} elements, {cols} needed")
+    es = weight.element_size()
+    if es not in (2, 4):
+        raise ValueError("weight must be bf16 or binary32")
+    return _dev_ptr(weight, es, "weight"), AR_FMT_F32 if es == 4 else AR_FMT_BF16
+
+
+def fp8_codes_empty(rows: int, cols: int, device, dtype=None):
+    """An uninitialised [rows, cols] code matrix whose rows start on 16-byte
+    boundaries (uint8, or `dtype`, e.g. torch.float8_e4m3fn)."""
+    import torch
+    ld = -(-int(cols) // 16) * 16
+    return torch.empty(int(rows), ld, dtype=dtype or torch.uint8, device=device)[:, :int(cols)]
+
+
+def fp8_scales_empty(rows: int, cols: int, device, block_rows: int = 1, e8m0: bool = False):
+    """Uninitialised scales of a [rows, cols] matrix, shape [ceil(rows /
+    block_rows), ceil(cols / 128)], binary32 or (e8m0) bytes; stored block
+    column by block column, so that ar_gemm_fp8 reads consecutive rows'
+    scales from consecutive addresses."""
+    import torch
+    return torch.empty(-(-int(cols) // AR_BLOCK), -(-int(rows) // block_rows), device=device,
+                       dtype=torch.uint8 if e8m0 else torch.float32).t()
+
+
+def ar_reduce_norm(ins: Sequence, weight=None, residual=None, res_out=None, y=None, codes=None, scales=None,
+                   eps: float = 1e-6, stream=None) -> None:
+    """h = sum of ins[p] (+ residual), res_out = bf16(h), y = h / rms(h) *
+    weight as bf16 (`y`) and / or E4M3 with a scale for each 128 columns
+    (`codes`, `scales`).  All of ins, residual, res_out and y are contiguous
+    [rows, cols] matrices; codes may have padded rows (a stride that is a
+    multiple of 16), scales any strides."""
+    if ins[0].dim() != 2:
+        raise ValueError("ins must be [rows, cols] matrices")
+    rows, cols = shape = tuple(ins[0].shape)
+    ip = [_rows_of(t, f"ins[{i}]", shape) for i, t in enumerate(ins)]
+    rp = None if residual is None else _rows_of(residual, "residual", shape)
+    op = None if res_out is None else _rows_of(res_out, "res_out", shape)
+    yp = None if y is None else _rows_of(y, "y", shape)
+    wp, wf = _gain(weight, cols)
+    if (codes is None) != (scales is None):
+        raise ValueError("codes and scales come together")
+    q = None if codes is None else ctypes.pointer(_fp8_matrix(codes, scales, shape, 1, "output"))
+    _call("ar_reduce_norm", _ptr_array(ip), len(ip), rp, wp, wf, rows, cols, ctypes.c_float(eps), op, yp, q,
+          _stream(stream))
+
+
+def norm_bwd_workspace(rows: int, cols: int) -> int:
+    """Bytes of workspace that ar_norm_bwd needs for dweight."""
+    return int(lib().ar_norm_bwd_workspace(int(rows), int(cols)))
+
+
+def ar_norm_bwd(dy, h, weight=None, dx=None, dres=None, dweight=None, workspace=None, eps: float = 1e-6,
+                stream=None) -> None:
+    """Gradient of ar_reduce_norm's norm: dx (of h: of every contribution and
+    of the residual; dres is the gradient that reached res_out) and dweight
+    (binary32).  dweight needs norm_bwd_workspace(rows, cols) bytes."""
+    if h.dim() != 2:
+        raise ValueError("h must be a [rows, cols] matrix")
+    rows, cols = shape = tuple(h.shape)
+    yp, hp = _rows_of(dy, "dy", shape), _rows_of(h, "h", shape)
+    rp = None if dres is None else _rows_of(dres, "dres", shape)
+    xp = None if dx is None else _rows_of(dx, "dx", shape)
+    wp, wf = _gain(weight, cols)
+    dp = None
+    if dweight is not None:
+        if dweight.numel() != cols:
+            raise ValueError(f"dweight holds {dweight.numel()} elements, {cols} needed")
+        dp = _dev_ptr(dweight, 4, "dweight")
+    sp, sb = _workspace(workspace)
+    _call("ar_norm_bwd", yp, hp, wp, wf, rp, rows, cols, ctypes.c_float(eps), xp, dp, sp, sb, _stream(stream))
+
+
+def _workspace(t):
+    if t is None or t.numel() == 0:
+        return None, 0
+    return _dev_ptr(t, t.element_size(), "workspace"), t.numel() * t.element_size()
+
+
+def ar_quantize_block(x, codes, scales, block_rows: int = 1, transpose: bool = False, stream=None) -> None:
+    """Quantise a bf16 matrix (rows contiguous, any row stride) to E4M3 codes
+    with a scale for each block of block_rows (1 or 128) x 128; transpose:
+    codes and scales are those of x transposed."""
+    xp, ldx = _mat(x, (2,), "x")
+    rows, cols = x.shape
+    q = _fp8_matrix(codes, scales, (cols, rows) if transpose else (rows, cols), int(block_rows), "output")
+    _call("ar_quantize_block", xp, ldx, rows, cols, ctypes.pointer(q), int(bool(transpose)), _stream(stream))
+
+
+def gemm_fp8_workspace(M: int, N: int, K: int, G: int = 1) -> int:
+    """Bytes of workspace with which ar_gemm_fp8 may split a product along K
+    (zero-initialised once by the caller; 0: none is used)."""
+    return int(lib().ar_gemm_fp8_workspace(int(M), int(N), int(K), int(G)))
+
+
+def ar_gemm_fp8(a_codes: Sequence, a_scales: Sequence, b_codes: Sequence, b_scales: Sequence, outs: Sequence,
+                b_block_rows: int = 128, workspace=None, stream=None) -> None:
+    """outs[g] = a[g] b[g]^T for len(outs) fp8 problems of one shape: a [M, K]
+    with a scale for each 1 x 128 block, b [N, K] with one for each
+    b_block_rows x 128, outs [M, N] bf16 or binary32 by their element size."""
+    G = len(outs)
+    if not (G == len(a_codes) == len(a_scales) == len(b_codes) == len(b_scales)) or G == 0:
+        raise ValueError("need one matrix and one scale matrix of a and of b, and one output, per problem")
+    if a_codes[0].dim() != 2 or b_codes[0].dim() != 2:
+        raise ValueError("a and b must be matrices")
+    (M, K), N = tuple(a_codes[0].shape), int(b_codes[0].shape[0])
+    am = (_Fp8Matrix * G)(*[_fp8_matrix(c, s, (M, K), 1, f"a[{i}]") for i, (c, s) in enumerate(zip(a_codes, a_scales))])
+    bm = (_Fp8Matrix * G)(*[_fp8_matrix(c, s, (N, K), int(b_block_rows), f"b[{i}]")
+                            for i, (c, s) in enumerate(zip(b_codes, b_scales))])
+    es = outs[0].element_size()
+    cp = []
+    for i, t in enumerate(outs):
+        ptr, ld = _mat(t, (2, 4), f"outs[{i}]", (M, N))
+        if t.element_size() != es or ld != _mat(outs[0], (2, 4), "outs[0]")[1]:
+            raise ValueError("outs must share one element size and one row stride")
+        cp.append(ptr)
+    sp, sb = _workspace(workspace)
+    _call("ar_gemm_fp8", am, bm, _ptr_array(cp), G, M, N, K, ld, AR_FMT_F32 if es == 4 else AR_FMT_BF16, sp, sb,
+          _stream(stream))
+
+
 def ar_err_init(d_err, stream=None) -> None:
     (ep,) = _bufs([d_err], 8, "d_err", 2)
     _call("ar_err_init", ep, _stream(stream))
@@ -465,3 +668,4 @@ def ar_get_launch_shape(kind: int) -> tuple:
 _PREPARABLE = frozenset([ar_reduce_oneshot, ar_reduce_2stage, ar_reduce_2stage_static, ar_pack_fused,
                          ar_unpack_fused, ar_unpack_fused_wait, ar_rd_schedule, ar_reduce_ubatch,
                          ar_reduce_ubatch_flags, ar_quantize_fp8, ar_reduce_fp8, ar_err_init])
+_PREPARABLE_BLOCK = frozenset([ar_reduce_norm, ar_norm_bwd, ar_quantize_block, ar_gemm_fp8])

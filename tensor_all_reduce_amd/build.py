@@ -15,7 +15,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libarcore.so")
 BENCH_LIB = os.path.join(HERE, "libarbench.so")
-SOURCES = ["ar_api.hip", "ar_reduce.hip", "ar_fused.hip", "ar_fp8.hip"]
+SOURCES = ["ar_api.hip", "ar_reduce.hip", "ar_fused.hip", "ar_fp8.hip", "ar_norm.hip", "ar_block8.hip",
+           "ar_gemm8.hip"]
 BENCH_SOURCES = ["ar_bench.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -266,6 +266,51 @@ int check_err(const uint64_t* d_err) {
   return AR_OK;
 }
 
+// ---- norm, block quantiser, fp8 matrix product ----------------------------
+
+bool mul3_overflows(size_t a, size_t b, size_t c) { return mul_overflows(a, b) || mul_overflows(a * b, c); }
+
+// First byte after a strided matrix's last element, or false if it overflows.
+bool extent(size_t rows, size_t rs, size_t cols, size_t cs, size_t elem, size_t* bytes) {
+  if (mul_overflows(rows - 1, rs) || mul_overflows(cols - 1, cs)) return false;
+  const size_t x = (rows - 1) * rs, y = (cols - 1) * cs;
+  if (x + y < x || x + y + 1 == 0 || mul_overflows(x + y + 1, elem)) return false;
+  *bytes = (x + y + 1) * elem;
+  return true;
+}
+
+// Checks an fp8 matrix [rows x cols] (rows, cols >= 1) and gives the spans of
+// its codes and scales.
+int check_matrix(const ar_fp8_matrix& q, size_t rows, size_t cols, bool output, Span* codes, Span* scales) {
+  if (!q.codes || !q.scales) return AR_ERR_INVALID;
+  if (q.scale_fmt != AR_SCALE_F32 && q.scale_fmt != AR_SCALE_E8M0) return AR_ERR_INVALID;
+  if (q.block_rows != 1 && q.block_rows != AR_BLOCK) return AR_ERR_INVALID;
+  if (q.ld < cols) return AR_ERR_INVALID;
+  const size_t es = q.scale_fmt == AR_SCALE_F32 ? 4 : 1;
+  if (!aligned16(q.codes) || (q.ld & 15u) || (reinterpret_cast<uintptr_t>(q.scales) & (es - 1))) return AR_ERR_ALIGN;
+  const size_t sr = (rows - 1) / q.block_rows + 1, sc = (cols - 1) / AR_BLOCK + 1;
+  size_t cb, sb;
+  if (!extent(rows, q.ld, cols, 1, 1, &cb) || !extent(sr, q.scale_rs, sc, q.scale_cs, es, &sb)) return AR_ERR_INVALID;
+  if (output) {
+    // distinct blocks, distinct elements: one stride steps over all of the other
+    const bool by_row = (sr == 1 || q.scale_rs > (sc - 1) * q.scale_cs) && (sc == 1 || q.scale_cs >= 1);
+    const bool by_col = (sc == 1 || q.scale_cs > (sr - 1) * q.scale_rs) && (sr == 1 || q.scale_rs >= 1);
+    if (!by_row && !by_col) return AR_ERR_ALIAS;
+  }
+  *codes = span_of(q.codes, cb);
+  *scales = span_of(q.scales, sb);
+  return AR_OK;
+}
+
+bool eps_ok(float eps) { return eps >= 0.0f && eps <= 3.402823466e38f; }
+
+int check_gain(const void* weight, int fmt, size_t cols, Span* s) {
+  if (fmt != AR_FMT_BF16 && fmt != AR_FMT_F32) return AR_ERR_INVALID;
+  if (!aligned16(weight)) return AR_ERR_ALIGN;
+  *s = span_of(weight, cols * (fmt == AR_FMT_F32 ? 4 : 2));
+  return AR_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -618,6 +663,199 @@ int ar_get_launch_shape(int kind, int* block, int* vec, int* nt_loads, int* stor
   *stores = s.stores;
   *wg_per_cu = s.wg_per_cu;
   return AR_OK;
+}
+
+int ar_reduce_norm(const void* const* ins, int P, const void* residual, const void* weight, int weight_fmt,
+                   size_t rows, size_t cols, float eps, void* res_out, void* y, const ar_fp8_matrix* q,
+                   void* stream) {
+  if (mul_overflows(rows, cols)) return AR_ERR_INVALID;
+  const size_t n = rows * cols;
+  if (ins && P >= 1 && P <= AR_MAX_RANKS && n == 0) return AR_OK;
+  ar::InPtrs in{};
+  Span si[AR_MAX_RANKS + 2];  // contributions, residual, gains
+  int rc = check_ranks(ins, P, n, &in, si), ni = P;
+  if (rc) return rc;
+  if ((!res_out && !y && !q) || !eps_ok(eps)) return AR_ERR_INVALID;
+  if (cols > AR_NORM_MAX_COLS) return AR_ERR_UNSUPPORTED;
+  if (!aligned16(residual) || !aligned16(res_out) || !aligned16(y)) return AR_ERR_ALIGN;
+  if (residual) si[ni++] = span_of(residual, n * 2);
+  Span so[2], sw;
+  int no = 0;
+  if (res_out) so[no++] = span_of(res_out, n * 2);
+  if (y) so[no++] = span_of(y, n * 2);
+  if ((rc = check_outputs(si, ni, so, no))) return rc;
+  if ((rc = check_gain(weight, weight_fmt, weight ? cols : 0, &sw))) return rc;
+  if (weight) {
+    if ((rc = check_disjoint(sw, so, no))) return rc;
+    si[ni++] = sw;
+  }
+  ar::NormArgs a{};
+  if (q) {
+    Span sc, ss;
+    if (q->block_rows != 1) return AR_ERR_INVALID;
+    if ((rc = check_matrix(*q, rows, cols, true, &sc, &ss))) return rc;
+    if ((rc = check_disjoint(sc, si, ni)) || (rc = check_disjoint(ss, si, ni)) || (rc = check_disjoint(sc, so, no)) ||
+        (rc = check_disjoint(ss, so, no)) || overlap(sc, ss))
+      return AR_ERR_ALIAS;
+    a.codes = q->codes;
+    a.scales = q->scales;
+    a.codes_ld = q->ld;
+    a.scale_rs = q->scale_rs;
+    a.scale_cs = q->scale_cs;
+    a.scale_e8m0 = q->scale_fmt == AR_SCALE_E8M0;
+  }
+  a.residual = static_cast<const uint16_t*>(residual);
+  a.weight = weight;
+  a.weight_f32 = weight_fmt == AR_FMT_F32;
+  a.res_out = static_cast<uint16_t*>(res_out);
+  a.y = static_cast<uint16_t*>(y);
+  a.rows = rows;
+  a.cols = (unsigned)cols;
+  a.eps = eps;
+  ar::Launch L;
+  if ((rc = resolve(&L, stream))) return rc;
+  return hip_status(ar::launch_reduce_norm(L, in, P, a));
+}
+
+size_t ar_norm_bwd_workspace(size_t rows, size_t cols) {
+  return (size_t)ar::norm_bwd_grid(rows) * (cols > AR_NORM_MAX_COLS ? 0 : cols) * sizeof(float);
+}
+
+int ar_norm_bwd(const void* dy, const void* h, const void* weight, int weight_fmt, const void* dres, size_t rows,
+                size_t cols, float eps, void* dx, float* dweight, void* workspace, size_t workspace_bytes,
+                void* stream) {
+  if (cols == 0 || (rows == 0 && !dweight)) return AR_OK;
+  if ((rows && (!dy || !h || (!dx && !dweight))) || !eps_ok(eps)) return AR_ERR_INVALID;
+  if (mul3_overflows(rows, cols, 2)) return AR_ERR_INVALID;
+  if (cols > AR_NORM_MAX_COLS) return AR_ERR_UNSUPPORTED;
+  if (!aligned16(dy) || !aligned16(h) || !aligned16(dres) || !aligned16(dx) || !aligned16(dweight) ||
+      !aligned16(workspace))
+    return AR_ERR_ALIGN;
+  const size_t n = rows * cols, need = ar_norm_bwd_workspace(rows, cols);
+  if (dweight && need && (!workspace || workspace_bytes < need)) return AR_ERR_INVALID;
+  int rc;
+  Span si[4] = {span_of(dy, n * 2), span_of(h, n * 2)}, sx, sw;
+  int ni = 2;
+  if (dres) si[ni++] = span_of(dres, n * 2);
+  if (dx) {
+    sx = span_of(dx, n * 2);
+    if ((rc = check_outputs(si, ni, &sx, 1))) return rc;
+  }
+  if ((rc = check_gain(weight, weight_fmt, weight ? cols : 0, &sw))) return rc;
+  if (weight) {
+    if (dx && overlap(sw, sx)) return AR_ERR_ALIAS;
+    si[ni++] = sw;
+  }
+  if (dweight) {
+    const Span sd = span_of(dweight, cols * 4), sp = span_of(workspace, need);
+    if (overlap(sd, sp) || check_disjoint(sd, si, ni) || check_disjoint(sp, si, ni) ||
+        (dx && (overlap(sd, sx) || overlap(sp, sx))))
+      return AR_ERR_ALIAS;
+  }
+  ar::Launch L;
+  if ((rc = resolve(&L, stream))) return rc;
+  ar::NormBwdArgs a{};
+  a.dy = static_cast<const uint16_t*>(dy);
+  a.h = static_cast<const uint16_t*>(h);
+  a.dres = static_cast<const uint16_t*>(dres);
+  a.weight = weight;
+  a.weight_f32 = weight_fmt == AR_FMT_F32;
+  a.dx = static_cast<uint16_t*>(dx);
+  a.partial = dweight ? static_cast<float*>(workspace) : nullptr;
+  a.rows = rows;
+  a.cols = (unsigned)cols;
+  a.eps = eps;
+  return hip_status(ar::launch_norm_bwd(L, a, dweight));
+}
+
+int ar_quantize_block(const void* x, size_t ldx, size_t rows, size_t cols, const ar_fp8_matrix* q, int transpose,
+                      void* stream) {
+  if (rows == 0 || cols == 0) return AR_OK;
+  if (!x || !q || ldx < cols) return AR_ERR_INVALID;
+  if (reinterpret_cast<uintptr_t>(x) & 1u) return AR_ERR_ALIGN;
+  size_t xb;
+  if (!extent(rows, ldx, cols, 1, 2, &xb)) return AR_ERR_INVALID;
+  Span sc, ss;
+  int rc = check_matrix(*q, transpose ? cols : rows, transpose ? rows : cols, true, &sc, &ss);
+  if (rc) return rc;
+  const Span sx = span_of(x, xb);
+  if (overlap(sx, sc) || overlap(sx, ss) || overlap(sc, ss)) return AR_ERR_ALIAS;
+  if (!ar::quant_block_fits(rows, cols)) return AR_ERR_UNSUPPORTED;
+  ar::Launch L;
+  if ((rc = resolve(&L, stream))) return rc;
+  ar::QuantArgs a{};
+  a.x = static_cast<const uint16_t*>(x);
+  a.codes = q->codes;
+  a.scales = q->scales;
+  a.ldx = ldx;
+  a.codes_ld = q->ld;
+  a.scale_rs = q->scale_rs;
+  a.scale_cs = q->scale_cs;
+  a.rows = rows;
+  a.cols = cols;
+  return hip_status(ar::launch_quant_block(L, a, q->block_rows, transpose != 0, q->scale_fmt == AR_SCALE_E8M0));
+}
+
+size_t ar_gemm_fp8_workspace(size_t M, size_t N, size_t K, int G) {
+  if (M == 0 || N == 0 || K == 0 || G < 1 || G > AR_MAX_RANKS || (M | N | K) >> 31) return 0;
+  return ar::gemm_fp8_workspace(M, N, K, G);
+}
+
+int ar_gemm_fp8(const ar_fp8_matrix* a, const ar_fp8_matrix* b, void* const* c, int G, size_t M, size_t N, size_t K,
+                size_t ldc, int out_fmt, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!a || !b || !c || G < 1 || G > AR_MAX_RANKS) return AR_ERR_INVALID;
+  if ((out_fmt != AR_FMT_BF16 && out_fmt != AR_FMT_F32) || ldc < N) return AR_ERR_INVALID;
+  if ((M | N | K) >> 31 || N >> 22) return AR_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return AR_OK;
+  const size_t es = out_fmt == AR_FMT_F32 ? 4 : 2;
+  size_t cb;
+  if (!extent(M, ldc, N, 1, es, &cb)) return AR_ERR_INVALID;
+  if (!aligned16(workspace)) return AR_ERR_ALIGN;
+  ar::GemmArgs g{};
+  Span si[4 * AR_MAX_RANKS], so[AR_MAX_RANKS + 1];
+  int rc, ni = 0, no = 0;
+  for (int i = 0; i < G; ++i) {
+    if (!c[i]) return AR_ERR_INVALID;
+    if (!aligned16(c[i])) return AR_ERR_ALIGN;
+    if (a[i].scale_fmt != b[0].scale_fmt || b[i].scale_fmt != b[0].scale_fmt || a[i].block_rows != 1 ||
+        b[i].block_rows != b[0].block_rows || a[i].ld != a[0].ld || b[i].ld != b[0].ld ||
+        a[i].scale_rs != a[0].scale_rs || a[i].scale_cs != a[0].scale_cs || b[i].scale_rs != b[0].scale_rs ||
+        b[i].scale_cs != b[0].scale_cs)
+      return AR_ERR_INVALID;
+    if (K > 0) {
+      if ((rc = check_matrix(a[i], M, K, false, &si[ni], &si[ni + 1])) ||
+          (rc = check_matrix(b[i], N, K, false, &si[ni + 2], &si[ni + 3])))
+        return rc;
+      ni += 4;
+    }
+    so[no++] = span_of(c[i], cb);
+    g.a[i] = a[i].codes;
+    g.b[i] = b[i].codes;
+    g.sa[i] = a[i].scales;
+    g.sb[i] = b[i].scales;
+    g.c[i] = c[i];
+  }
+  size_t need = ar_gemm_fp8_workspace(M, N, K, G);
+  if (!workspace || workspace_bytes < need) need = 0;
+  if (need) so[no++] = span_of(workspace, need);
+  for (int o = 0; o < no; ++o) {
+    if ((rc = check_disjoint(so[o], si, ni))) return rc;
+    if ((rc = check_disjoint(so[o], so + o + 1, no - o - 1))) return rc;
+  }
+  g.lda = a[0].ld;
+  g.ldb = b[0].ld;
+  g.ldc = ldc;
+  g.sa_rs = a[0].scale_rs;
+  g.sa_cs = a[0].scale_cs;
+  g.sb_rs = b[0].scale_rs;
+  g.sb_cs = b[0].scale_cs;
+  g.M = (unsigned)M;
+  g.N = (unsigned)N;
+  g.K = (unsigned)K;
+  ar::Launch L;
+  if ((rc = resolve(&L, stream))) return rc;
+  return hip_status(ar::launch_gemm_fp8(L, g, G, b[0].scale_fmt == AR_SCALE_E8M0, b[0].block_rows == 1,
+                                        out_fmt == AR_FMT_F32, need ? workspace : nullptr));
 }
 
 int ar_err_init(uint64_t* d_err, void* stream) {

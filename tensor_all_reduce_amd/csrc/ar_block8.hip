@@ -1,0 +1,168 @@
+// bf16 matrices to E4M3 codes with a scale for each 1 x 128 or 128 x 128
+// block, as they stand or transposed: the operands of the fp8 matrix product.
+//
+// One 256-lane workgroup takes a 128 x 128 tile of x, which holds whole
+// blocks of every form, so each element is read once and its scale is known
+// before it is written.
+#include "ar_device.hpp"
+#include "ar_e4m3.hpp"
+#include "ar_internal.hpp"
+
+namespace ar {
+namespace {
+
+typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(2)));
+
+constexpr int kTile = AR_BLOCK;
+constexpr int kTurnLd = kTile + 16;  // bytes from row to row of the transposed tile in LDS
+
+template <bool E8M0>
+__device__ __forceinline__ void put_scale(const QuantArgs& a, size_t r, size_t c, uint32_t kept) {
+  const size_t k = r * a.scale_rs + c * a.scale_cs;
+  if constexpr (E8M0) static_cast<uint8_t*>(a.scales)[k] = (uint8_t)kept;
+  else static_cast<uint32_t*>(a.scales)[k] = kept;
+}
+
+// Lane t holds columns 8 (t % 16) .. + 7 of rows 8 (t / 16) .. + 7.
+template <bool SQUARE, bool TURN, bool E8M0>
+__global__ __launch_bounds__(256) void k_quant_block(QuantArgs a, unsigned tiles_c) {
+  __shared__ uint32_t top[4][kTile];
+  __shared__ __align__(16) uint8_t turned[TURN ? kTile * kTurnLd : 16];
+  const size_t tr = blockIdx.x / tiles_c, tc = blockIdx.x % tiles_c;
+  const int lc = (threadIdx.x % 16) * 8, lr = (threadIdx.x / 16) * 8, wave = threadIdx.x / kWave;
+  const size_t r0 = tr * kTile + lr, c0 = tc * kTile + lc;
+  float f[8][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (r0 + i < a.rows && c0 < a.cols) {
+      const uint16_t* p = a.x + (r0 + i) * a.ldx + c0;
+      if (c0 + 8 <= a.cols) {
+        v = *reinterpret_cast<const u32x4u*>(p);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t e = c0 + j < a.cols ? (uint32_t)p[j] : 0u;
+          v[j >> 1] |= (j & 1) ? (e << 16) : e;
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      f[i][2 * k] = lo_f32(v[k]);
+      f[i][2 * k + 1] = hi_f32(v[k]);
+    }
+  }
+
+  // inv[i]: of row i (straight) or of column i (transposed)
+  float inv[8];
+  if constexpr (SQUARE) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = max(m, finite_mag(f[i][j]));
+    m = row16_max(m);
+    if (threadIdx.x % 16 == 0) top[0][threadIdx.x / 16] = m;
+    __syncthreads();
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = max(m, top[0][i]);
+    const BlockScale s = block_scale<E8M0>(m);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) inv[i] = s.inv;
+    if (threadIdx.x == 0) put_scale<E8M0>(a, TURN ? tc : tr, TURN ? tr : tc, s.kept);
+  } else if constexpr (!TURN) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = max(m, finite_mag(f[i][j]));
+      const BlockScale s = block_scale<E8M0>(row16_max(m));
+      inv[i] = s.inv;
+      if (threadIdx.x % 16 == 0 && r0 + i < a.rows) put_scale<E8M0>(a, r0 + i, tc, s.kept);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = max(m, finite_mag(f[i][j]));
+      m = max(m, (uint32_t)__shfl_xor((int)m, 16));
+      m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+      if (lane_id() < 16) top[wave][lc + j] = m;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t m = max(max(top[0][lc + j], top[1][lc + j]), max(top[2][lc + j], top[3][lc + j]));
+      const BlockScale s = block_scale<E8M0>(m);
+      inv[j] = s.inv;
+      if (threadIdx.x < 16 && c0 + j < a.cols) put_scale<E8M0>(a, c0 + j, tr, s.kept);
+    }
+  }
+
+  if constexpr (!TURN) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (r0 + i >= a.rows || c0 >= a.cols) continue;
+      const uint32_t lo = codes4_scaled(f[i], inv[i]), hi = codes4_scaled(f[i] + 4, inv[i]);
+      uint8_t* c = a.codes + (r0 + i) * a.codes_ld + c0;
+      if (c0 + 8 <= a.cols) {
+        *reinterpret_cast<uint64_t*>(c) = (uint64_t)lo | ((uint64_t)hi << 32);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c0 + j < a.cols) c[j] = (uint8_t)((j < 4 ? lo : hi) >> (8 * (j & 3)));
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float col[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) col[i] = f[i][j];
+      const uint32_t lo = codes4_scaled(col, inv[j]), hi = codes4_scaled(col + 4, inv[j]);
+      *reinterpret_cast<uint64_t*>(&turned[(lc + j) * kTurnLd + lr]) = (uint64_t)lo | ((uint64_t)hi << 32);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int q = k * 256 + threadIdx.x, c = q / 8, r = (q % 8) * 16;  // 16 codes of output row c
+      const size_t gc = tc * kTile + c, gr = tr * kTile + r;
+      if (gc >= a.cols || gr >= a.rows) continue;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(&turned[c * kTurnLd + r]);
+      uint8_t* p = a.codes + gc * a.codes_ld + gr;
+      if (gr + 16 <= a.rows) {
+        *reinterpret_cast<u32x4*>(p) = v;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (gr + j < a.rows) p[j] = (uint8_t)(v[j >> 2] >> (8 * (j & 3)));
+      }
+    }
+  }
+}
+
+template <bool SQUARE, bool TURN>
+hipError_t quant_st(const Launch& L, const QuantArgs& a, bool e8m0) {
+  const size_t tc = cdiv(a.cols, kTile), tr = cdiv(a.rows, kTile);
+  const dim3 grid((unsigned)(tr * tc));
+  if (e8m0) return launch_k(k_quant_block<SQUARE, TURN, true>, grid, dim3(256), 0, L.stream, a, (unsigned)tc);
+  return launch_k(k_quant_block<SQUARE, TURN, false>, grid, dim3(256), 0, L.stream, a, (unsigned)tc);
+}
+
+}  // namespace
+
+// 256 lanes a tile: HIP takes fewer than 2^32 lanes along one axis.
+bool quant_block_fits(size_t rows, size_t cols) {
+  const size_t tc = (cols - 1) / kTile + 1, tr = (rows - 1) / kTile + 1;
+  return tc <= 0xFFFFFFu && tr <= 0xFFFFFFu / tc;
+}
+
+hipError_t launch_quant_block(const Launch& L, const QuantArgs& a, int block_rows, bool turn, bool e8m0) {
+  if (block_rows == AR_BLOCK) return turn ? quant_st<true, true>(L, a, e8m0) : quant_st<true, false>(L, a, e8m0);
+  return turn ? quant_st<false, true>(L, a, e8m0) : quant_st<false, false>(L, a, e8m0);
+}
+
+}  // namespace ar

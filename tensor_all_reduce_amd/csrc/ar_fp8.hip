@@ -18,33 +18,13 @@
 // ldexp by the scale (exact), rank-order binary32 sums, the integer
 // nearest-even rounding to bf16 shared with the other reduce kernels.
 #include "ar_device.hpp"
+#include "ar_e4m3.hpp"
 #include "ar_internal.hpp"
 
 namespace ar {
 namespace {
 
 constexpr int kFp8Block = 32;
-
-// Largest of the 4 values held by one quad of lanes (lanes 4q..4q+3).
-// DPP quad permutations [1,0,3,2] and [2,3,0,1]; every lane must be active.
-__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));
-  return v;
-}
-
-// Scale exponent k from the binary32 bits A of the block's largest finite
-// magnitude: the smallest k in [-127, 127] with A <= 448 * 2^k.  For a
-// normal A = (1 + F/2^23) * 2^(E-127) and 448 = 1.75 * 2^8, that is E - 135,
-// plus one when the significand exceeds 1.75 (F > 0x600000).  Zero and
-// binary32 subnormals (below 2^-126, far below 448 * 2^-127) give -127;
-// the largest finite bf16 gives 120, so no upper clamp is reached.
-__device__ __forceinline__ int fp8_scale_exp(uint32_t A) {
-  const int E = (int)(A >> 23);
-  if (E == 0) return -127;
-  const int k = E - 135 + ((A & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-  return k < -127 ? -127 : k;
-}
 
 // Binary32 bits of bf16 element j (0..7) of a 16-byte group.
 __device__ __forceinline__ uint32_t elem_bits(const uint32_t (&w)[4], int j) {

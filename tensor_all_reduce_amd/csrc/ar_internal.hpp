@@ -136,6 +136,57 @@ hipError_t launch_quant_fp8(const Launch& L, const InPtrs& xs, const ByteOut& co
 hipError_t launch_reduce_fp8(const Launch& L, const ByteIn& codes, const ByteIn& scales,
                              const OutPtrs& out, int P, int nout, size_t n);
 
+// Operands of the norm, its gradient, the block quantiser and the fp8 matrix
+// product, checked by the API layer.
+struct NormArgs {
+  const uint16_t* residual;  // nullptr: none
+  const void* weight;        // nullptr: ones
+  uint16_t *res_out, *y;     // nullptr: not written
+  uint8_t* codes;            // nullptr: not written
+  void* scales;
+  size_t rows, codes_ld, scale_rs, scale_cs;
+  unsigned cols;
+  int weight_f32, scale_e8m0;
+  float eps;
+};
+hipError_t launch_reduce_norm(const Launch& L, const InPtrs& in, int P, const NormArgs& a);
+
+struct NormBwdArgs {
+  const uint16_t *dy, *h, *dres;  // dres nullptr: none
+  const void* weight;             // nullptr: ones
+  uint16_t* dx;                   // nullptr: not written
+  float* partial;                 // [norm_bwd_grid(rows)][cols] sums; nullptr: no dweight
+  size_t rows;
+  unsigned cols;
+  int weight_f32;
+  float eps;
+};
+unsigned norm_bwd_grid(size_t rows);
+hipError_t launch_norm_bwd(const Launch& L, const NormBwdArgs& a, float* dweight);
+
+struct QuantArgs {
+  const uint16_t* x;
+  uint8_t* codes;
+  void* scales;
+  size_t ldx, codes_ld, scale_rs, scale_cs;
+  size_t rows, cols;  // of x
+};
+bool quant_block_fits(size_t rows, size_t cols);  // whether its grid fits a launch
+hipError_t launch_quant_block(const Launch& L, const QuantArgs& a, int block_rows, bool turn, bool e8m0);
+
+struct GemmArgs {
+  const uint8_t* a[AR_MAX_RANKS];
+  const uint8_t* b[AR_MAX_RANKS];
+  const void* sa[AR_MAX_RANKS];
+  const void* sb[AR_MAX_RANKS];
+  void* c[AR_MAX_RANKS];
+  size_t lda, ldb, ldc, sa_rs, sa_cs, sb_rs, sb_cs;
+  unsigned M, N, K;
+};
+size_t gemm_fp8_workspace(size_t M, size_t N, size_t K, int G);
+hipError_t launch_gemm_fp8(const Launch& L, const GemmArgs& g, int G, bool e8m0, bool b_rows, bool out_f32,
+                           void* workspace);  // gemm_fp8_workspace bytes, or nullptr
+
 hipError_t launch_pack(const Launch& L, const void* x, uint64_t* w, size_t n, uint32_t seq);
 hipError_t launch_unpack(const Launch& L, const uint64_t* w, void* x, size_t n, uint32_t seq,
                          uint64_t* d_err);
