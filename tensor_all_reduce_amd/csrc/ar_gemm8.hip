@@ -5,6 +5,8 @@
 #include "ar_device.hpp"
 #include "ar_internal.hpp"
 
+#include <utility>
+
 namespace ar {
 namespace {
 
@@ -13,15 +15,23 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kBK = AR_BLOCK;  // one scale block: 128 codes = 8 chunks of 16 bytes
 
-// 16 codes k .. k+15 of a row; codes at K and after read as zero, so that
-// neither operand's padding (which may hold NaN codes) reaches a product.
-__device__ __forceinline__ u32x4 load_chunk(const uint8_t* row, unsigned k, unsigned K) {
-  if (k + 16 <= K) return *reinterpret_cast<const u32x4*>(row + k);
-  u32x4 v = {0u, 0u, 0u, 0u};
+// Keeps codes k .. k+15 of a row that lie before K, zeros after: neither
+// operand's padding (which may hold NaN codes) reaches a product.
+__device__ __forceinline__ u32x4 mask_chunk(u32x4 v, unsigned k, unsigned K) {
 #pragma unroll
-  for (unsigned j = 0; j < 16; ++j)
-    if (k + j < K) v[j >> 2] |= (uint32_t)row[k + j] << (8 * (j & 3));
+  for (unsigned w = 0; w < 4; ++w) {
+    const unsigned at = k + 4 * w, n = K > at ? K - at : 0;
+    v[w] &= n >= 4 ? ~0u : (1u << (8 * n)) - 1u;
+  }
   return v;
+}
+
+// Start of the 16 codes read for codes k .. k+15: k itself, or, past the
+// row's end, its last 16 (masked away by the caller).
+__device__ __forceinline__ unsigned chunk_at(unsigned k, unsigned K) { return min(k, (K - 1) & ~15u); }
+
+__device__ __forceinline__ u32x4 load_chunk(const uint8_t* row, unsigned k, unsigned K) {
+  return mask_chunk(*reinterpret_cast<const u32x4*>(row + chunk_at(k, K)), k, K);
 }
 
 // Chunk c of row r sits at position c ^ (r % 8): the 16 rows that a wave
@@ -30,6 +40,306 @@ __device__ __forceinline__ int lds_at(int r, int c) { return r * 8 + (c ^ (r & 7
 
 __device__ __forceinline__ float e8m0_f32(uint8_t b) {
   return b == 255 ? __uint_as_float(0x7FC00000u) : __builtin_ldexpf(1.0f, (int)b - 127);
+}
+
+// Four consecutive results of a row from element `at` (column n).
+template <bool OUT32>
+__device__ __forceinline__ void store4(void* c, size_t at, unsigned n, unsigned N, bool aligned, f32x4 v) {
+  if (n + 4 <= N && aligned) {
+    if constexpr (OUT32) {
+      *reinterpret_cast<f32x4*>(static_cast<float*>(c) + at) = v;
+    } else {
+      typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+      *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(c) + at) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    }
+    return;
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    if (n + r < N) {
+      if constexpr (OUT32) static_cast<float*>(c)[at + r] = v[r];
+      else static_cast<uint16_t*>(c)[at + r] = to_bf16(v[r]);
+    }
+}
+
+typedef __bf16 b16x8 __attribute__((ext_vector_type(8)));
+
+// 32 codes of one row: what a lane gives to one 16 x 16 x 128 product.
+union Frag {
+  u32x4 h[2];
+  i32x8 v;
+  uint32_t w[8];
+};
+
+// The same 32 codes as bf16 (exact), for four 16 x 16 x 32 products.
+struct Wide {
+  b16x8 p[4];
+};
+__device__ __forceinline__ Wide widen(const Frag& f) {
+  typedef __bf16 b16x2 __attribute__((ext_vector_type(2)));
+  Wide r;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const b16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(f.w[i], 1.0f, false);
+    const b16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(f.w[i], 1.0f, true);
+    b16x8& d = r.p[i / 2];
+    const int o = 4 * (i & 1);
+    d[o] = lo[0];
+    d[o + 1] = lo[1];
+    d[o + 2] = hi[0];
+    d[o + 3] = hi[1];
+  }
+  return r;
+}
+
+// f(0) ... f(N - 1), each index a compile-time constant.
+template <typename F, int... I>
+__device__ __forceinline__ void each_of(F& f, std::integer_sequence<int, I...>) {
+  (f(SPc<I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(F&& f) {
+  each_of(f, std::make_integer_sequence<int, N>{});
+}
+
+// Copies 16 bytes a lane from base + off to LDS, the lanes of a wave side by
+// side from byte address `lds`: no register holds them on the way.  The
+// caller waits for it (vmcnt) before a barrier.
+__device__ __forceinline__ void copy_to_lds(const uint8_t* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :: "s"(lds), "v"(off), "s"(base) : "memory");
+}
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+
+// BM x 256 tile of C in 512 lanes, K >= 1.  8 waves, 2 along M by 4 along N,
+// each with JT x 4 products of 16 x 16 x 128 a block.
+//
+// A wave holds the four b fragments of its block and a ring of R fragments of
+// a; each register is refilled as soon as its product is issued, from the
+// same block or from the next one, which by then is in the other LDS buffer.
+// One barrier a block, after which the copies of block k + 2 start into the
+// buffer of block k.
+template <int BM, bool E8M0, bool BROWS, bool OUT32>
+__global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, unsigned tiles_n) {
+  constexpr int BN = 256, IT = 4, JT = BM / 32, R = OUT32 ? 2 : 4, BJ = JT - R;
+  constexpr bool HW = E8M0 && !OUT32;        // scales applied by the matrix cores
+  constexpr uint32_t kBuf = (BM + BN) * kBK;
+  __shared__ __align__(16) char lab[2][kBuf];  // rows of a, then of b
+  // scales of a block, the four rows r, r + 16, r + 32, r + 48 of each 64
+  // side by side: bytes (HW) or binary32 words
+  __shared__ __align__(16) uint32_t ls[3][HW ? 128 : 512];
+  const int z = blockIdx.z, t = threadIdx.x, lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane(t / kWave);
+  const int lr = lane & 15, lq = lane >> 4;
+  const int wm = (wave & 1) * (BM / 2), wn = (wave >> 1) * 64;
+
+  // tile of this workgroup: XCD x (workgroups reach the 8 XCDs in turn) takes
+  // a contiguous run of tiles, ordered in columns of 8 tiles along M, so that
+  // the tiles an XCD works on at once share rows of a and of b in its L2
+  unsigned id = blockIdx.x;
+  const unsigned tiles = tiles_m * tiles_n;
+  if (id < (tiles & ~7u)) id = (id & 7u) * (tiles >> 3) + (id >> 3);
+  const unsigned per = 8 * tiles_n, band = id / per, in = id % per;
+  const unsigned bm = min(8u, tiles_m - band * 8);
+  const unsigned m0 = (band * 8 + in % bm) * BM, n0 = (in / bm) * BN;
+
+  const uint8_t* A = g.a[z] + (size_t)m0 * g.lda;
+  const uint8_t* B = g.b[z] + (size_t)n0 * g.ldb;
+  // a wave copies 8 rows at a time; chunk c of a row goes to position c ^ (row % 8)
+  const unsigned crow = wave * 8 + (lane >> 3), ccol = ((lane & 7) ^ (lane >> 3)) * 16;
+  uint32_t oa[BM / 64], ob[BN / 64];
+#pragma unroll
+  for (int i = 0; i < BM / 64; ++i) oa[i] = (min(m0 + i * 64 + crow, g.M - 1) - m0) * (uint32_t)g.lda;
+#pragma unroll
+  for (int i = 0; i < BN / 64; ++i) ob[i] = (min(n0 + i * 64 + crow, g.N - 1) - n0) * (uint32_t)g.ldb;
+  // this lane's scale: of row t of a, or of row t - BM of b
+  const bool is_a = wave * kWave < BM;       // the same in a wave
+  const unsigned sn = min(n0 + t - BM, g.N - 1);
+  const size_t srow = is_a ? (size_t)min(m0 + t, g.M - 1) * g.sa_rs : (size_t)(BROWS ? sn : sn / AR_BLOCK) * g.sb_rs;
+  const void* sbase = is_a ? g.sa[z] : g.sb[z];
+  const size_t scol = is_a ? g.sa_cs : g.sb_cs;
+  const int sput = ((t >> 6) * 16 + (t & 15)) * 4 + ((t >> 4) & 3);
+  const unsigned nk = (g.K + kBK - 1) / kBK;
+  const unsigned whole = g.K / kBK;          // K blocks without a tail
+
+  auto load_scale = [&](unsigned k) -> uint32_t {
+    const size_t i = srow + k * scol;
+    if constexpr (E8M0) {
+      const uint8_t b = static_cast<const uint8_t*>(sbase)[i];
+      if constexpr (HW) return b;
+      else return __float_as_uint(e8m0_f32(b));
+    } else {
+      return static_cast<const uint32_t*>(sbase)[i];
+    }
+  };
+  auto put_scale = [&](int r, uint32_t v) {
+    if constexpr (HW) reinterpret_cast<uint8_t*>(ls[r])[sput] = (uint8_t)v;
+    else ls[r][sput] = v;
+  };
+  auto copy = [&](unsigned k, unsigned buf) {
+    const unsigned at = chunk_at(k * kBK + ccol, g.K);
+    const uint32_t to = lds_address(lab[buf]) + wave * 8 * kBK;
+#pragma unroll
+    for (int i = 0; i < BM / 64; ++i) copy_to_lds(A, oa[i] + at, to + i * 64 * kBK);
+#pragma unroll
+    for (int i = 0; i < BN / 64; ++i) copy_to_lds(B, ob[i] + at, to + (BM + i * 64) * kBK);
+  };
+  // codes 16 lq .. + 15 and 64 + 16 lq .. + 15 of row lr of a fragment: both
+  // operands take K in this order
+  const uint32_t r0 = lds_at(lr, lq) * 16, r1 = lds_at(lr, lq + 4) * 16;
+  auto read_a = [&](unsigned buf, int j, Frag& f) {
+    const char* p = lab[buf] + wm * kBK;
+    f.h[0] = *reinterpret_cast<const u32x4*>(p + r0 + j * 16 * kBK);
+    f.h[1] = *reinterpret_cast<const u32x4*>(p + r1 + j * 16 * kBK);
+  };
+  auto read_b = [&](unsigned buf, int i, Frag& f) {
+    const char* p = lab[buf] + (BM + wn) * kBK;
+    f.h[0] = *reinterpret_cast<const u32x4*>(p + r0 + i * 16 * kBK);
+    f.h[1] = *reinterpret_cast<const u32x4*>(p + r1 + i * 16 * kBK);
+  };
+  auto mask = [&](unsigned k, Frag& f) {
+    f.h[0] = mask_chunk(f.h[0], k * kBK + lq * 16, g.K);
+    f.h[1] = mask_chunk(f.h[1], k * kBK + lq * 16 + 64, g.K);
+  };
+
+  f32x4 acc[IT][JT];
+#pragma unroll
+  for (int i = 0; i < IT; ++i)
+#pragma unroll
+    for (int j = 0; j < JT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  Frag fa[R], fb[IT];
+  // binary32 scales: a block's product waits D products for its turn to be
+  // scaled and added, while the matrix cores run on
+  constexpr int D = OUT32 ? IT : 3, NP = 2 * IT;
+  f32x4 p[HW ? 1 : NP];
+  f32x4 sa[HW ? 1 : JT / 4];                 // scales of a: rows of this lane
+  f32x4 sb[!HW && BROWS ? IT : 1];           // of b: this lane's four rows of each fragment, or one
+  uint32_t sah[JT / 4], sbh;                 // the same as bytes (HW)
+  uint32_t sc;
+  int cur = 0, nxt = 1, aft = 2;             // scale buffers of blocks k, k + 1, k + 2
+
+  auto read_sa = [&](int buf, int h) {
+    if constexpr (HW) sah[h] = ls[buf][wm / 4 + h * 16 + lr];
+    else sa[h] = *reinterpret_cast<const f32x4*>(&ls[buf][wm + h * 64 + lr * 4]);
+  };
+  auto read_sb = [&](int buf) {
+    if constexpr (HW) {
+      sbh = ls[buf][(BM + wn) / 4 + lr];
+    } else if constexpr (BROWS) {
+#pragma unroll
+      for (int i = 0; i < IT; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sb[i][r] = __uint_as_float(ls[buf][BM + wn + (lq * 4 + r) * 4 + i]);
+    } else {
+      sb[0][0] = __uint_as_float(ls[buf][BM + wn]);
+    }
+  };
+  // scales and adds product n (row j = n / 4 of fragments of a)
+  auto add = [&](auto nn) {
+    constexpr int n = decltype(nn)::value, i = n % IT, j = n / IT;
+    const float s = sa[j / 4][j % 4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      acc[i][j][r] = __builtin_fmaf(p[n % NP][r], s * sb[BROWS ? i : 0][BROWS ? r : 0], acc[i][j][r]);
+  };
+
+  auto step = [&](unsigned k, unsigned buf, auto tail) {
+    if constexpr (decltype(tail)::value) {
+#pragma unroll
+      for (int i = 0; i < IT; ++i) mask(k, fb[i]);
+    }
+    Wide wb[OUT32 ? IT : 1];
+    if constexpr (OUT32) {
+#pragma unroll
+      for (int i = 0; i < IT; ++i) wb[i] = widen(fb[i]);
+    }
+    auto column = [&](auto jj) {
+      constexpr int j = decltype(jj)::value;
+      Frag& a = fa[j % R];
+      if constexpr (decltype(tail)::value) mask(k, a);
+      Wide wa;
+      if constexpr (OUT32) {
+        wa = widen(a);
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+#pragma unroll
+          for (int i = 0; i < IT; ++i)
+            p[(j * IT + i) % NP] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                wb[i].p[h], wa.p[h], h ? p[(j * IT + i) % NP] : f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+      }
+      auto cell = [&](auto ii) {
+        constexpr int i = decltype(ii)::value, n = j * IT + i;
+        if constexpr (HW)
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[i].v, a.v, acc[i][j], 0, 0, i, (int)sbh, j % 4,
+                                                                    (int)sah[j / 4]);
+        else if constexpr (!OUT32)
+          p[n % NP] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[i].v, a.v, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0,
+                                                                     0, 0);
+        if constexpr (j == JT - 1) read_b(buf ^ 1, i, fb[i]);
+        if constexpr (!HW && n >= D) add(SPc<n - D>{});
+      };
+      each<IT>(cell);
+      if constexpr (j == BJ) {
+        // every wave's copies of block k + 1 are in LDS, and none still
+        // reads block k, whose buffer block k + 2 takes (past the end the
+        // last block is copied again, and not used)
+        put_scale(nxt, sc);
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        const unsigned k2 = min(k + 2, nk - 1);
+        copy(k2, buf);
+        sc = load_scale(k2);
+      }
+      read_a(j < BJ ? buf : buf ^ 1, (j + R) % JT, fa[j % R]);
+      if constexpr (HW && j == JT - 1) {
+        read_sb(nxt);
+#pragma unroll
+        for (int h = 0; h < JT / 4; ++h) read_sa(nxt, h);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    each<JT>(column);
+    if constexpr (!HW) {
+      each<D>([&](auto n) { add(SPc<JT * IT - D + decltype(n)::value>{}); });
+      read_sb(nxt);
+#pragma unroll
+      for (int h = 0; h < JT / 4; ++h) read_sa(nxt, h);
+    }
+    const int r = cur;
+    cur = nxt;
+    nxt = aft;
+    aft = r;
+  };
+
+  copy(0, 0);
+  copy(min(1u, nk - 1), 1);
+  put_scale(0, load_scale(0));
+  sc = load_scale(min(1u, nk - 1));
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  read_sb(0);
+#pragma unroll
+  for (int h = 0; h < JT / 4; ++h) read_sa(0, h);
+#pragma unroll
+  for (int i = 0; i < IT; ++i) read_b(0, i, fb[i]);
+#pragma unroll
+  for (int j = 0; j < R; ++j) read_a(0, j, fa[j]);
+  for (unsigned k = 0; k < whole; ++k) step(k, k & 1, std::false_type{});
+  if (whole < nk) step(whole, whole & 1, std::true_type{});
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no copy outlives the workgroup's LDS
+
+#pragma unroll
+  for (int j = 0; j < JT; ++j) {
+    const unsigned m = m0 + wm + j * 16 + lr;
+    if (m >= g.M) continue;
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const unsigned n = n0 + wn + i * 16 + lq * 4;
+      store4<OUT32>(g.c[z], m * g.ldc + n, n, g.N, (g.ldc & 3) == 0, acc[i][j]);
+    }
+  }
 }
 
 // 128 x 128 tile of C in a 256-lane workgroup, 64 x 64 a wave as 4 x 4
@@ -129,6 +439,14 @@ __global__ __launch_bounds__(256) void k_gemm_tile(GemmArgs g) {
 
 template <bool E8M0, bool BROWS>
 hipError_t gemm_o(const Launch& L, const GemmArgs& g, int G, bool out_f32) {
+  if (g.lda < (1u << 23) && g.ldb < (1u << 23) && g.M > 64 && g.K > 0) {
+    const unsigned bm = (out_f32 || (BROWS && !E8M0)) ? 128 : 256;
+    const unsigned tm = (unsigned)cdiv(g.M, bm), tn = (unsigned)cdiv(g.N, 256);
+    const dim3 grid(tm * tn, 1, (unsigned)G);
+    if (out_f32) return launch_k(k_gemm_big<128, E8M0, BROWS, true>, grid, dim3(512), 0, L.stream, g, tm, tn);
+    constexpr int BM = BROWS && !E8M0 ? 128 : 256;
+    return launch_k(k_gemm_big<BM, E8M0, BROWS, false>, grid, dim3(512), 0, L.stream, g, tm, tn);
+  }
   const dim3 grid((unsigned)cdiv(g.M, 128), (unsigned)cdiv(g.N, 128), (unsigned)G);
   if (out_f32) return launch_k(k_gemm_tile<E8M0, BROWS, true>, grid, dim3(256), 0, L.stream, g);
   return launch_k(k_gemm_tile<E8M0, BROWS, false>, grid, dim3(256), 0, L.stream, g);
