@@ -124,7 +124,7 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 // buffer of block k.
 template <int BM, bool E8M0, bool BROWS, bool OUT32>
 __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, unsigned tiles_n) {
-  constexpr int BN = 256, IT = 4, JT = BM / 32, R = OUT32 ? 2 : 4, BJ = JT - R;
+  constexpr int BN = 256, IT = 4, JT = BM / 32, R = 4;
   constexpr bool HW = E8M0 && !OUT32;        // scales applied by the matrix cores
   constexpr uint32_t kBuf = (BM + BN) * kBK;
   __shared__ __align__(16) char lab[2][kBuf];  // rows of a, then of b
@@ -216,98 +216,133 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
   // scaled and added, while the matrix cores run on
   constexpr int D = OUT32 ? IT : 3, NP = 2 * IT;
   f32x4 p[HW ? 1 : NP];
-  f32x4 sa[HW ? 1 : JT / 4];                 // scales of a: rows of this lane
-  f32x4 sb[!HW && BROWS ? IT : 1];           // of b: this lane's four rows of each fragment, or one
-  uint32_t sah[JT / 4], sbh;                 // the same as bytes (HW)
+  using ScaleA = std::conditional_t<HW, uint32_t, f32x4>;  // of a: four rows of this lane
+  struct ScaleB {
+    uint32_t bytes;                          // HW: the row of each fragment
+    f32x4 row[!HW && BROWS ? IT : 1];        // else this lane's four rows of each fragment, or [0][0] for all
+  };
+  ScaleA sa[JT / 4];
+  ScaleB sb;
   uint32_t sc;
   int cur = 0, nxt = 1, aft = 2;             // scale buffers of blocks k, k + 1, k + 2
 
-  auto read_sa = [&](int buf, int h) {
-    if constexpr (HW) sah[h] = ls[buf][wm / 4 + h * 16 + lr];
-    else sa[h] = *reinterpret_cast<const f32x4*>(&ls[buf][wm + h * 64 + lr * 4]);
+  auto read_sa = [&](int buf, int h, ScaleA& v) {
+    if constexpr (HW) v = ls[buf][wm / 4 + h * 16 + lr];
+    else v = *reinterpret_cast<const f32x4*>(&ls[buf][wm + h * 64 + lr * 4]);
   };
-  auto read_sb = [&](int buf) {
+  auto read_sb = [&](int buf, ScaleB& v) {
     if constexpr (HW) {
-      sbh = ls[buf][(BM + wn) / 4 + lr];
+      v.bytes = ls[buf][(BM + wn) / 4 + lr];
     } else if constexpr (BROWS) {
 #pragma unroll
-      for (int i = 0; i < IT; ++i)
+      for (int r = 0; r < 4; ++r) {
+        const f32x4 q = *reinterpret_cast<const f32x4*>(&ls[buf][BM + wn + (lq * 4 + r) * 4]);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) sb[i][r] = __uint_as_float(ls[buf][BM + wn + (lq * 4 + r) * 4 + i]);
+        for (int i = 0; i < IT; ++i) v.row[i][r] = q[i];
+      }
     } else {
-      sb[0][0] = __uint_as_float(ls[buf][BM + wn]);
+      v.row[0][0] = __uint_as_float(ls[buf][BM + wn]);
     }
   };
-  // scales and adds product n (row j = n / 4 of fragments of a)
+
+  // Order of a block's products: column by column of a's fragments but for
+  // the last four columns, which go row by row.  So the first part frees
+  // fragments of a one by one, for the block's last four, and the second
+  // fragments of b, for the next block.
+  constexpr int F = (JT - 4) * IT;           // products of the first part
+  constexpr int BAR = F + 3;                 // the barrier comes after this product
   auto add = [&](auto nn) {
-    constexpr int n = decltype(nn)::value, i = n % IT, j = n / IT;
-    const float s = sa[j / 4][j % 4];
+    constexpr int n = decltype(nn)::value, i = n < F ? n % IT : (n - F) / 4, j = n < F ? n / IT : JT - 4 + (n - F) % 4;
+    if constexpr (!HW) {
+      const float s = sa[j / 4][j % 4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      acc[i][j][r] = __builtin_fmaf(p[n % NP][r], s * sb[BROWS ? i : 0][BROWS ? r : 0], acc[i][j][r]);
+      for (int r = 0; r < 4; ++r)
+        acc[i][j][r] = __builtin_fmaf(p[n % NP][r], s * sb.row[BROWS ? i : 0][BROWS ? r : 0], acc[i][j][r]);
+    }
+  };
+
+  auto piece = [&](auto qq, unsigned at, unsigned buf) {
+    constexpr int q = decltype(qq)::value;
+    const uint32_t to = lds_address(lab[buf]) + (wave + q * 8) * 8 * kBK;
+    if constexpr (q < BM / 64) copy_to_lds(A, oa[q] + at, to);
+    else copy_to_lds(B, ob[q - BM / 64] + at, to);
   };
 
   auto step = [&](unsigned k, unsigned buf, auto tail) {
-    if constexpr (decltype(tail)::value) {
+    constexpr bool TAIL = decltype(tail)::value;
+    if constexpr (TAIL) {
 #pragma unroll
       for (int i = 0; i < IT; ++i) mask(k, fb[i]);
     }
-    Wide wb[OUT32 ? IT : 1];
-    if constexpr (OUT32) {
-#pragma unroll
-      for (int i = 0; i < IT; ++i) wb[i] = widen(fb[i]);
-    }
-    auto column = [&](auto jj) {
-      constexpr int j = decltype(jj)::value;
+    const unsigned k2 = min(k + 2, nk - 1);
+    const unsigned at = chunk_at(k2 * kBK + ccol, g.K), at1 = chunk_at(min(k + 1, nk - 1) * kBK + ccol, g.K);
+    ScaleA nsa;
+    ScaleB nsb;
+    if constexpr (JT == 8) read_sa(cur, 1, sa[JT / 4 - 1]);
+    Wide wa[OUT32 ? 4 : 1];
+    auto cell = [&](auto nn) {
+      constexpr int n = decltype(nn)::value, i = n < F ? n % IT : (n - F) / 4, j = n < F ? n / IT : JT - 4 + (n - F) % 4;
       Frag& a = fa[j % R];
-      if constexpr (decltype(tail)::value) mask(k, a);
-      Wide wa;
-      if constexpr (OUT32) {
-        wa = widen(a);
+      if constexpr (TAIL && i == 0) mask(k, a);
+      if constexpr (HW) {
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[i].v, a.v, acc[i][j], 0, 0, i, (int)sb.bytes, j % 4,
+                                                                  (int)sa[j / 4]);
+      } else if constexpr (!OUT32) {
+        p[n % NP] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[i].v, a.v, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+      } else {
+        // JT is 4: a row of four products, each the sum of four of 32 codes
+        if constexpr (n < 4) wa[n] = widen(a);
+        if constexpr (n % 4 == 3) {
+          const Wide wb = widen(fb[i]);
 #pragma unroll
-        for (int h = 0; h < 4; ++h)
+          for (int h = 0; h < 4; ++h)
 #pragma unroll
-          for (int i = 0; i < IT; ++i)
-            p[(j * IT + i) % NP] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                wb[i].p[h], wa.p[h], h ? p[(j * IT + i) % NP] : f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+            for (int c = 0; c < 4; ++c)
+              p[(n - 3 + c) % NP] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  wb.p[h], wa[c].p[h], h ? p[(n - 3 + c) % NP] : f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+        }
       }
-      auto cell = [&](auto ii) {
-        constexpr int i = decltype(ii)::value, n = j * IT + i;
-        if constexpr (HW)
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[i].v, a.v, acc[i][j], 0, 0, i, (int)sbh, j % 4,
-                                                                    (int)sah[j / 4]);
-        else if constexpr (!OUT32)
-          p[n % NP] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[i].v, a.v, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0,
-                                                                     0, 0);
-        if constexpr (j == JT - 1) read_b(buf ^ 1, i, fb[i]);
-        if constexpr (!HW && n >= D) add(SPc<n - D>{});
-      };
-      each<IT>(cell);
-      if constexpr (j == BJ) {
+      if constexpr (!HW && !OUT32 && n >= D) add(SPc<n - D>{});
+      if constexpr (OUT32 && n >= 7 && n % 4 == 3) {
+        each<4>([&](auto c) { add(SPc<n - 7 + decltype(c)::value>{}); });
+      }
+      if constexpr (n == BAR) {
         // every wave's copies of block k + 1 are in LDS, and none still
         // reads block k, whose buffer block k + 2 takes (past the end the
         // last block is copied again, and not used)
-        put_scale(nxt, sc);
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        const unsigned k2 = min(k + 2, nk - 1);
-        copy(k2, buf);
-        sc = load_scale(k2);
       }
-      read_a(j < BJ ? buf : buf ^ 1, (j + R) % JT, fa[j % R]);
-      if constexpr (HW && j == JT - 1) {
-        read_sb(nxt);
-#pragma unroll
-        for (int h = 0; h < JT / 4; ++h) read_sa(nxt, h);
+      if constexpr (n == BAR + 1) {
+        // scales go through a register: those of block k + 2 came during the
+        // last block (nothing is in flight here, so nothing is waited for)
+        put_scale(aft, sc);
+        sc = load_scale(min(k + 3, nk - 1));
+      }
+      if constexpr (n == BAR + 3) {
+        read_sb(nxt, nsb);
+        read_sa(nxt, 0, nsa);
+      }
+      // a wave's copies, spread over the products so that they never queue
+      // up before one: the first of block k + 2, then, before the barrier,
+      // the rest of block k + 1
+      constexpr int after = n - BAR - 1, EARLY = (JT * IT - BAR) / 2;
+      if constexpr (after >= 1 && after % 2 == 1 && after / 2 < EARLY) {
+        piece(SPc<after / 2>{}, at, buf);
+      } else if constexpr (n < BAR && n % 3 == 0 && EARLY + n / 3 < (BM + BN) / 64) {
+        piece(SPc<EARLY + n / 3>{}, at1, buf ^ 1);
+      }
+      if constexpr (n < F) {
+        if constexpr (i == IT - 1) read_a(buf, j + 4, fa[j % R]);
+      } else {
+        if constexpr (j == JT - 1) read_b(buf ^ 1, i, fb[i]);
+        if constexpr (i == IT - 1) read_a(buf ^ 1, j - (JT - 4), fa[j % R]);
       }
       __builtin_amdgcn_sched_barrier(0);
     };
-    each<JT>(column);
-    if constexpr (!HW) {
-      each<D>([&](auto n) { add(SPc<JT * IT - D + decltype(n)::value>{}); });
-      read_sb(nxt);
-#pragma unroll
-      for (int h = 0; h < JT / 4; ++h) read_sa(nxt, h);
-    }
+    each<JT * IT>(cell);
+    if constexpr (!HW) each<D>([&](auto n) { add(SPc<JT * IT - D + decltype(n)::value>{}); });
+    sb = nsb;
+    sa[0] = nsa;
     const int r = cur;
     cur = nxt;
     nxt = aft;
@@ -317,11 +352,11 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
   copy(0, 0);
   copy(min(1u, nk - 1), 1);
   put_scale(0, load_scale(0));
-  sc = load_scale(min(1u, nk - 1));
+  put_scale(1, load_scale(min(1u, nk - 1)));
+  sc = load_scale(min(2u, nk - 1));
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  read_sb(0);
-#pragma unroll
-  for (int h = 0; h < JT / 4; ++h) read_sa(0, h);
+  read_sb(0, sb);
+  read_sa(0, 0, sa[0]);
 #pragma unroll
   for (int i = 0; i < IT; ++i) read_b(0, i, fb[i]);
 #pragma unroll
