@@ -5,6 +5,7 @@
 #include "ar_device.hpp"
 #include "ar_internal.hpp"
 
+#include <algorithm>
 #include <utility>
 
 namespace ar {
@@ -102,90 +103,106 @@ __device__ __forceinline__ void each(F&& f) {
   each_of(f, std::make_integer_sequence<int, N>{});
 }
 
-// Copies 16 bytes a lane from base + off to LDS, the lanes of a wave side by
-// side from byte address `lds`: no register holds them on the way.  The
-// caller waits for it (vmcnt) before a barrier.
-__device__ __forceinline__ void copy_to_lds(const uint8_t* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-               :: "s"(lds), "v"(off), "s"(base) : "memory");
+// Copies 16 bytes a lane from byte `voff` + `soff` of a buffer to LDS, the
+// lanes of a wave side by side from byte address `lds`: no register holds
+// them on the way.  A lane beyond the buffer's end reads nothing.  The caller
+// waits for it (vmcnt) before a barrier.
+typedef uint32_t Resource __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ void copy_to_lds(Resource r, uint32_t voff, uint32_t soff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :: "s"(lds), "v"(voff), "s"(r), "s"(soff) : "memory");
+}
+
+// `rows` rows of a code matrix from `p` on, as a bounded buffer.  (Word 3:
+// the 32-bit data format; untyped access takes any.)
+__device__ __forceinline__ Resource rows_buffer(const uint8_t* p, unsigned rows, unsigned most, size_t ld, unsigned K) {
+  const uint64_t a = reinterpret_cast<uint64_t>(p);
+  const uint32_t bytes = (min(rows, most) - 1) * (uint32_t)ld + ((K + 15) & ~15u);
+  return Resource{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
+                  (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32)),
+                  (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00020000u};
 }
 
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
 
-// BM x 256 tile of C in 512 lanes, K >= 1.  8 waves, 2 along M by 4 along N,
+// BM x 256 tiles of C in 512 lanes, K >= 1.  8 waves, 2 along M by 4 along N,
 // each with JT x 4 products of 16 x 16 x 128 a block.
 //
-// A wave holds the four b fragments of its block and a ring of R fragments of
-// a; each register is refilled as soon as its product is issued, from the
-// same block or from the next one, which by then is in the other LDS buffer.
-// One barrier a block, after which the copies of block k + 2 start into the
-// buffer of block k.
+// A wave holds the four b fragments of its block and a ring of four fragments
+// of a; each register is refilled as soon as its last product is issued, from
+// the same block or from the next one, which by then is in the other LDS
+// buffer.  One barrier a block, after which the copies of block k + 2 start
+// into the buffer of block k.  A workgroup takes tile after tile, and the
+// blocks of the next follow those of one without a gap.
 template <int BM, bool E8M0, bool BROWS, bool OUT32>
 __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, unsigned tiles_n) {
   constexpr int BN = 256, IT = 4, JT = BM / 32, R = 4;
   constexpr bool HW = E8M0 && !OUT32;        // scales applied by the matrix cores
   constexpr uint32_t kBuf = (BM + BN) * kBK;
+  constexpr int kOut = OUT32 ? 4 : 2;        // bytes of a result
   __shared__ __align__(16) char lab[2][kBuf];  // rows of a, then of b
   // scales of a block, the four rows r, r + 16, r + 32, r + 48 of each 64
   // side by side: bytes (HW) or binary32 words
   __shared__ __align__(16) uint32_t ls[3][HW ? 128 : 512];
+  __shared__ __align__(16) char lout[8][16 * 64 * kOut];  // 16 rows of a wave's results
   const int z = blockIdx.z, t = threadIdx.x, lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(t / kWave);
   const int lr = lane & 15, lq = lane >> 4;
   const int wm = (wave & 1) * (BM / 2), wn = (wave >> 1) * 64;
-
-  // tile of this workgroup: XCD x (workgroups reach the 8 XCDs in turn) takes
-  // a contiguous run of tiles, ordered in columns of 8 tiles along M, so that
-  // the tiles an XCD works on at once share rows of a and of b in its L2
-  unsigned id = blockIdx.x;
-  const unsigned tiles = tiles_m * tiles_n;
-  if (id < (tiles & ~7u)) id = (id & 7u) * (tiles >> 3) + (id >> 3);
-  const unsigned per = 8 * tiles_n, band = id / per, in = id % per;
-  const unsigned bm = min(8u, tiles_m - band * 8);
-  const unsigned m0 = (band * 8 + in % bm) * BM, n0 = (in / bm) * BN;
-
-  const uint8_t* A = g.a[z] + (size_t)m0 * g.lda;
-  const uint8_t* B = g.b[z] + (size_t)n0 * g.ldb;
-  // a wave copies 8 rows at a time; chunk c of a row goes to position c ^ (row % 8)
-  const unsigned crow = wave * 8 + (lane >> 3), ccol = ((lane & 7) ^ (lane >> 3)) * 16;
-  uint32_t oa[BM / 64], ob[BN / 64];
-#pragma unroll
-  for (int i = 0; i < BM / 64; ++i) oa[i] = (min(m0 + i * 64 + crow, g.M - 1) - m0) * (uint32_t)g.lda;
-#pragma unroll
-  for (int i = 0; i < BN / 64; ++i) ob[i] = (min(n0 + i * 64 + crow, g.N - 1) - n0) * (uint32_t)g.ldb;
-  // this lane's scale: of row t of a, or of row t - BM of b
-  const bool is_a = wave * kWave < BM;       // the same in a wave
-  const unsigned sn = min(n0 + t - BM, g.N - 1);
-  const size_t srow = is_a ? (size_t)min(m0 + t, g.M - 1) * g.sa_rs : (size_t)(BROWS ? sn : sn / AR_BLOCK) * g.sb_rs;
-  const void* sbase = is_a ? g.sa[z] : g.sb[z];
-  const size_t scol = is_a ? g.sa_cs : g.sb_cs;
-  const int sput = ((t >> 6) * 16 + (t & 15)) * 4 + ((t >> 4) & 3);
   const unsigned nk = (g.K + kBK - 1) / kBK;
   const unsigned whole = g.K / kBK;          // K blocks without a tail
+  const unsigned tiles = tiles_m * tiles_n;
 
-  auto load_scale = [&](unsigned k) -> uint32_t {
-    const size_t i = srow + k * scol;
+  // XCD x (workgroups reach the 8 XCDs in turn) takes a contiguous run of
+  // tiles, ordered in columns of 8 tiles along M, so that the tiles an XCD
+  // works on at once share rows of a and of b in its L2
+  struct Tile {
+    unsigned m0, n0;
+  };
+  auto tile_at = [&](unsigned id) {
+    if (id < (tiles & ~7u)) id = (id & 7u) * (tiles >> 3) + (id >> 3);
+    const unsigned per = 8 * tiles_n, band = id / per, in = id % per;
+    const unsigned bm = min(8u, tiles_m - band * 8);
+    return Tile{(unsigned)__builtin_amdgcn_readfirstlane((int)((band * 8 + in % bm) * BM)),
+                (unsigned)__builtin_amdgcn_readfirstlane((int)(in / bm * BN))};
+  };
+  auto a_rows = [&](Tile q) { return rows_buffer(g.a[z] + (size_t)q.m0 * g.lda, g.M - q.m0, BM, g.lda, g.K); };
+  auto b_rows = [&](Tile q) { return rows_buffer(g.b[z] + (size_t)q.n0 * g.ldb, g.N - q.n0, BN, g.ldb, g.K); };
+
+  // a wave copies 8 rows at a time; chunk c of a row goes to position c ^ (row % 8)
+  const unsigned crow = wave * 8 + (lane >> 3), ccol = ((lane & 7) ^ (lane >> 3)) * 16;
+  const uint32_t va = crow * (uint32_t)g.lda + ccol, vb = crow * (uint32_t)g.ldb + ccol;
+  auto piece = [&](auto qq, Resource ra, Resource rb, uint32_t at, unsigned buf) {
+    constexpr int q = decltype(qq)::value;
+    const uint32_t to = lds_address(lab[buf]) + (wave + q * 8) * 8 * kBK;
+    if constexpr (q < BM / 64) copy_to_lds(ra, va, q * 64 * (uint32_t)g.lda + at, to);
+    else copy_to_lds(rb, vb, (q - BM / 64) * 64 * (uint32_t)g.ldb + at, to);
+  };
+  constexpr int kPieces = (BM + BN) / 64;
+
+  // this lane's scale: of row t of a, or of row t - BM of b
+  const bool is_a = wave * kWave < BM;       // the same in a wave
+  const char* sbase = static_cast<const char*>(is_a ? g.sa[z] : g.sb[z]);
+  const uint32_t srs = (uint32_t)(is_a ? g.sa_rs : g.sb_rs), scs = (uint32_t)(is_a ? g.sa_cs : g.sb_cs);
+  const unsigned slast = (is_a ? g.M : g.N) - 1, slane = is_a ? t : t - BM;
+  const int sput = ((t >> 6) * 16 + (t & 15)) * 4 + ((t >> 4) & 3);
+  auto load_scale = [&](Tile q, unsigned k) -> uint32_t {
+    unsigned row = min((is_a ? q.m0 : q.n0) + slane, slast);
+    if (!BROWS && !is_a) row /= AR_BLOCK;
+    const size_t i = (uint64_t)row * srs + (uint64_t)k * scs;
     if constexpr (E8M0) {
-      const uint8_t b = static_cast<const uint8_t*>(sbase)[i];
+      const uint8_t b = reinterpret_cast<const uint8_t*>(sbase)[i];
       if constexpr (HW) return b;
       else return __float_as_uint(e8m0_f32(b));
     } else {
-      return static_cast<const uint32_t*>(sbase)[i];
+      return reinterpret_cast<const uint32_t*>(sbase)[i];
     }
   };
   auto put_scale = [&](int r, uint32_t v) {
     if constexpr (HW) reinterpret_cast<uint8_t*>(ls[r])[sput] = (uint8_t)v;
     else ls[r][sput] = v;
-  };
-  auto copy = [&](unsigned k, unsigned buf) {
-    const unsigned at = chunk_at(k * kBK + ccol, g.K);
-    const uint32_t to = lds_address(lab[buf]) + wave * 8 * kBK;
-#pragma unroll
-    for (int i = 0; i < BM / 64; ++i) copy_to_lds(A, oa[i] + at, to + i * 64 * kBK);
-#pragma unroll
-    for (int i = 0; i < BN / 64; ++i) copy_to_lds(B, ob[i] + at, to + (BM + i * 64) * kBK);
   };
   // codes 16 lq .. + 15 and 64 + 16 lq .. + 15 of row lr of a fragment: both
   // operands take K in this order
@@ -206,11 +223,6 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
   };
 
   f32x4 acc[IT][JT];
-#pragma unroll
-  for (int i = 0; i < IT; ++i)
-#pragma unroll
-    for (int j = 0; j < JT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
   Frag fa[R], fb[IT];
   // binary32 scales: a block's product waits D products for its turn to be
   // scaled and added, while the matrix cores run on
@@ -261,21 +273,22 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
     }
   };
 
-  auto piece = [&](auto qq, unsigned at, unsigned buf) {
-    constexpr int q = decltype(qq)::value;
-    const uint32_t to = lds_address(lab[buf]) + (wave + q * 8) * 8 * kBK;
-    if constexpr (q < BM / 64) copy_to_lds(A, oa[q] + at, to);
-    else copy_to_lds(B, ob[q - BM / 64] + at, to);
-  };
+  unsigned buf = 0;                          // LDS buffer of block k
+  Tile now, then;                            // this tile and the next
+  Resource now_a, now_b, then_a, then_b;
+  // block k + d: of this tile, or from the next one's start
+  auto ahead = [&](unsigned k, unsigned d) { return k + d < nk ? k + d : k + d - nk; };
 
-  auto step = [&](unsigned k, unsigned buf, auto tail) {
+  auto step = [&](unsigned k, auto tail) {
     constexpr bool TAIL = decltype(tail)::value;
     if constexpr (TAIL) {
 #pragma unroll
       for (int i = 0; i < IT; ++i) mask(k, fb[i]);
     }
-    const unsigned k2 = min(k + 2, nk - 1);
-    const unsigned at = chunk_at(k2 * kBK + ccol, g.K), at1 = chunk_at(min(k + 1, nk - 1) * kBK + ccol, g.K);
+    const bool over1 = k + 1 >= nk, over2 = k + 2 >= nk, over3 = k + 3 >= nk;
+    const Resource ra1 = over1 ? then_a : now_a, rb1 = over1 ? then_b : now_b;
+    const Resource ra2 = over2 ? then_a : now_a, rb2 = over2 ? then_b : now_b;
+    const uint32_t at1 = ahead(k, 1) * kBK, at2 = ahead(k, 2) * kBK;
     ScaleA nsa;
     ScaleB nsb;
     if constexpr (JT == 8) read_sa(cur, 1, sa[JT / 4 - 1]);
@@ -308,15 +321,14 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
       }
       if constexpr (n == BAR) {
         // every wave's copies of block k + 1 are in LDS, and none still
-        // reads block k, whose buffer block k + 2 takes (past the end the
-        // last block is copied again, and not used)
+        // reads block k, whose buffer block k + 2 takes
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
       }
       if constexpr (n == BAR + 1) {
         // scales go through a register: those of block k + 2 came during the
         // last block (nothing is in flight here, so nothing is waited for)
         put_scale(aft, sc);
-        sc = load_scale(min(k + 3, nk - 1));
+        sc = load_scale(over3 ? then : now, ahead(k, 3));
       }
       if constexpr (n == BAR + 3) {
         read_sb(nxt, nsb);
@@ -326,10 +338,10 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
       // up before one: the first of block k + 2, then, before the barrier,
       // the rest of block k + 1
       constexpr int after = n - BAR - 1, EARLY = (JT * IT - BAR) / 2;
-      if constexpr (after >= 1 && after % 2 == 1 && after / 2 < EARLY) {
-        piece(SPc<after / 2>{}, at, buf);
-      } else if constexpr (n < BAR && n % 3 == 0 && EARLY + n / 3 < (BM + BN) / 64) {
-        piece(SPc<EARLY + n / 3>{}, at1, buf ^ 1);
+      if constexpr (after >= 1 && after % 2 == 1 && after / 2 < EARLY && after / 2 < kPieces) {
+        piece(SPc<after / 2>{}, ra2, rb2, at2, buf);
+      } else if constexpr (n < BAR && n % 3 == 0 && EARLY + n / 3 < kPieces) {
+        piece(SPc<EARLY + n / 3>{}, ra1, rb1, at1, buf ^ 1);
       }
       if constexpr (n < F) {
         if constexpr (i == IT - 1) read_a(buf, j + 4, fa[j % R]);
@@ -347,13 +359,73 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
     cur = nxt;
     nxt = aft;
     aft = r;
+    buf ^= 1;
   };
 
-  copy(0, 0);
-  copy(min(1u, nk - 1), 1);
-  put_scale(0, load_scale(0));
-  put_scale(1, load_scale(min(1u, nk - 1)));
-  sc = load_scale(min(2u, nk - 1));
+  // Results go out 16 rows of a wave at a time through its own LDS, so that
+  // neighbouring lanes store neighbouring bytes of a row.
+  auto store = [&](Tile q) {
+    char* const out = lout[wave];
+    constexpr int kRow = 64 * kOut, kLanes = kRow / 16;  // bytes of a row, lanes that store it
+    const unsigned n = q.n0 + wn + (lane % kLanes) * (16 / kOut);
+    const bool vec = (g.ldc * kOut) % 16 == 0 && n + 16 / kOut <= g.N;
+#pragma unroll
+    for (int j = 0; j < JT; ++j) {
+#pragma unroll
+      for (int i = 0; i < IT; ++i) {
+        const f32x4 v = acc[i][j];
+        if constexpr (OUT32) {
+          *reinterpret_cast<f32x4*>(out + lr * kRow + ((i * 4 + lq) ^ (lr & 7)) * 16) = v;
+        } else {
+          typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+          *reinterpret_cast<u32x2*>(out + lr * kRow + ((i * 2 + (lq >> 1)) ^ (lr & 7)) * 16 + (lq & 1) * 8) =
+              u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int h = 0; h < 16 * kLanes / kWave; ++h) {
+        const int row = h * (kWave / kLanes) + lane / kLanes;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(out + row * kRow + ((lane % kLanes) ^ (row & 7)) * 16);
+        const unsigned m = q.m0 + wm + j * 16 + row;
+        if (m >= g.M) continue;
+        char* to = static_cast<char*>(g.c[z]) + (m * g.ldc + n) * kOut;
+        if (vec) {
+          st4<true>(reinterpret_cast<u32x4*>(to), v);   // streamed: the L2 keeps a and b
+        } else {
+#pragma unroll
+          for (unsigned e = 0; e < 16 / kOut; ++e)
+            if (n + e < g.N) {
+              if constexpr (OUT32) reinterpret_cast<uint32_t*>(to)[e] = v[e];
+              else reinterpret_cast<uint16_t*>(to)[e] = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
+            }
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+  };
+
+  unsigned id = blockIdx.x;
+  now = tile_at(id);
+  now_a = a_rows(now);
+  now_b = b_rows(now);
+  // the next tile (without one, this tile again: its blocks are copied and not used)
+  auto look_ahead = [&] {
+    if (id + gridDim.x < tiles) then = tile_at(id + gridDim.x);
+    else then = now;
+    then_a = a_rows(then);
+    then_b = b_rows(then);
+  };
+  look_ahead();
+  {
+    const bool one = nk == 1;
+    const Resource ra1 = one ? then_a : now_a, rb1 = one ? then_b : now_b;
+    each<kPieces>([&](auto q) { piece(q, now_a, now_b, 0, 0); });
+    each<kPieces>([&](auto q) { piece(q, ra1, rb1, ahead(0, 1) * kBK, 1); });
+    put_scale(0, load_scale(now, 0));
+    put_scale(1, load_scale(one ? then : now, ahead(0, 1)));
+    sc = load_scale(nk <= 2 ? then : now, ahead(0, 2));
+  }
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   read_sb(0, sb);
   read_sa(0, 0, sa[0]);
@@ -361,20 +433,22 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
   for (int i = 0; i < IT; ++i) read_b(0, i, fb[i]);
 #pragma unroll
   for (int j = 0; j < R; ++j) read_a(0, j, fa[j]);
-  for (unsigned k = 0; k < whole; ++k) step(k, k & 1, std::false_type{});
-  if (whole < nk) step(whole, whole & 1, std::true_type{});
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no copy outlives the workgroup's LDS
-
+  for (;;) {
 #pragma unroll
-  for (int j = 0; j < JT; ++j) {
-    const unsigned m = m0 + wm + j * 16 + lr;
-    if (m >= g.M) continue;
+    for (int i = 0; i < IT; ++i)
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      const unsigned n = n0 + wn + i * 16 + lq * 4;
-      store4<OUT32>(g.c[z], m * g.ldc + n, n, g.N, (g.ldc & 3) == 0, acc[i][j]);
-    }
+      for (int j = 0; j < JT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (unsigned k = 0; k < whole; ++k) step(k, std::false_type{});
+    if (whole < nk) step(whole, std::true_type{});
+    store(now);
+    id += gridDim.x;
+    if (id >= tiles) break;
+    now = then;
+    now_a = then_a;
+    now_b = then_b;
+    look_ahead();
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no copy outlives the workgroup's LDS
 }
 
 // 128 x 128 tile of C in a 256-lane workgroup, 64 x 64 a wave as 4 x 4
@@ -474,10 +548,11 @@ __global__ __launch_bounds__(256) void k_gemm_tile(GemmArgs g) {
 
 template <bool E8M0, bool BROWS>
 hipError_t gemm_o(const Launch& L, const GemmArgs& g, int G, bool out_f32) {
-  if (g.lda < (1u << 23) && g.ldb < (1u << 23) && g.M > 64 && g.K > 0) {
+  const size_t wide = (g.lda | g.ldb) >> 23 | (g.sa_rs | g.sa_cs | g.sb_rs | g.sb_cs) >> 32;
+  if (!wide && g.M > 64 && g.K > 256) {
     const unsigned bm = (out_f32 || (BROWS && !E8M0)) ? 128 : 256;
     const unsigned tm = (unsigned)cdiv(g.M, bm), tn = (unsigned)cdiv(g.N, 256);
-    const dim3 grid(tm * tn, 1, (unsigned)G);
+    const dim3 grid(std::min(tm * tn, (unsigned)L.cus), 1, (unsigned)G);
     if (out_f32) return launch_k(k_gemm_big<128, E8M0, BROWS, true>, grid, dim3(512), 0, L.stream, g, tm, tn);
     constexpr int BM = BROWS && !E8M0 ? 128 : 256;
     return launch_k(k_gemm_big<BM, E8M0, BROWS, false>, grid, dim3(512), 0, L.stream, g, tm, tn);

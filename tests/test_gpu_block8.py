@@ -236,3 +236,24 @@ def test_product_repeats_and_replays():
         step(o2, w2, s2)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(outs + o2, want + want))
+
+
+@pytest.mark.parametrize("e8m0", FMT)
+@pytest.mark.parametrize("K,brows", [(300, 128), (513, 1), (1152, 128)])
+def test_product_of_many_tiles_is_exact(K, brows, e8m0):
+    """More tiles than the device has compute units, ragged along M and N:
+    every workgroup takes several, and the blocks of one follow another's."""
+    M, N = 4130, 4360
+    g = np.random.default_rng([17, K, brows])
+    note(f"product M={M} N={N} K={K} brows={brows} e8m0={e8m0}")
+
+    def scales(rows, br):
+        k = g.integers(-1, 2, size=(-(-rows // br), -(-K // 128)))
+        return (k + 127).astype(np.uint8) if e8m0 else (2.0 ** k).astype(np.float32)
+
+    A, B = (int_codes(g, M, K), scales(M, 1)), (int_codes(g, N, K), scales(N, brows))
+    want = (ref.dequantise(*A, 1).astype(np.float32) @ ref.dequantise(*B, brows).astype(np.float32).T)   # exact in binary32
+    got, = run([A], [B], brows, M, N, K, True, 5, True)
+    assert np.array_equal(got, want), f"{int((got != want).sum())} differ"
+    got, = run([A], [B], brows, M, N, K, False, 8, True)
+    assert np.array_equal(got, ref.as_bf16(want)), "bf16"
