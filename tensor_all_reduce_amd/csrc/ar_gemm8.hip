@@ -451,6 +451,161 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no copy outlives the workgroup's LDS
 }
 
+// Joins the parts of a result that workgroups have summed over slices of K.
+// A part holds each lane's accumulators, `Q` vectors, as the lanes have them.
+// The last workgroup to arrive adds all parts in slice order, so the result
+// does not depend on who was last.  Parts are written through the L2 of the
+// writer's XCD; the counter is zero again afterwards.  Returns whether this
+// workgroup has the result (in v).  `lds_word`: a word of LDS that is free.
+template <int Q>
+__device__ __forceinline__ bool join_parts(f32x4 (&v)[Q], uint32_t* counter, char* parts, int slice, int slices,
+                                           uint32_t* lds_word) {
+  const unsigned lanes = blockDim.x, bytes = Q * lanes * 16;
+  char* mine = parts + (size_t)slice * bytes;
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    union { f32x4 f; u32x4 u; } x;
+    x.f = v[q];
+    st16<2>(mine, bytes, (q * lanes + threadIdx.x) * 16, x.u);
+  }
+  __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+  __syncthreads();
+  if (threadIdx.x == 0) *lds_word = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  if (*lds_word != (uint32_t)slices - 1) return false;
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+  if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+  for (int q = 0; q < Q; ++q) v[q] = *reinterpret_cast<const f32x4*>(parts + (q * lanes + threadIdx.x) * 16);
+  for (int s = 1; s < slices; ++s)
+#pragma unroll
+    for (int q = 0; q < Q; ++q) v[q] += *reinterpret_cast<const f32x4*>(parts + (size_t)s * bytes + (q * lanes + threadIdx.x) * 16);
+  return true;
+}
+
+// Few rows of a: 16 MT x 64 of C in four waves of 16 columns, K >= 1.  The
+// codes of b are read once and there is little to compute on them, so the
+// kernel is a copy engine: a ring of ST blocks in LDS, all but one of them on
+// their way, two workgroups a CU.  blockIdx: columns, rows, problem and slice
+// of K (`per` blocks each).
+constexpr int kFewCols = 64, kFewBlocks = 32;  // columns; blocks whose scales are held at a time
+template <int MT, bool E8M0, bool BROWS, bool OUT32>
+__global__ __launch_bounds__(256) void k_gemm_few(GemmArgs g, int slices, unsigned per, uint32_t* counters, char* parts) {
+  constexpr int BM = 16 * MT, ST = MT == 2 ? 5 : 4;
+  constexpr bool HW = E8M0 && !OUT32;
+  constexpr int kCopies = 2 + MT / 2;        // of a wave and block
+  __shared__ __align__(16) char ring[ST][(BM + kFewCols) * kBK];  // rows of a, then of b
+  __shared__ uint32_t lsa[kFewBlocks][BM], lsb[kFewBlocks][BROWS ? kFewCols : 1];
+  const int z = blockIdx.z / slices, slice = blockIdx.z % slices, t = threadIdx.x, lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane(t / kWave);
+  const int lr = lane & 15, lq = lane >> 4;
+  const unsigned n0 = blockIdx.x * kFewCols, m0 = blockIdx.y * BM;
+  const unsigned nk = (g.K + kBK - 1) / kBK, kb0 = slice * per, kb1 = min(kb0 + per, nk);
+  const Resource ra = rows_buffer(g.a[z] + (size_t)m0 * g.lda, g.M - m0, BM, g.lda, g.K);
+  const Resource rb = rows_buffer(g.b[z] + (size_t)n0 * g.ldb, g.N - n0, kFewCols, g.ldb, g.K);
+  const unsigned crow = lane >> 3, ccol = ((lane & 7) ^ (lane >> 3)) * 16;
+  const uint32_t va = crow * (uint32_t)g.lda + ccol, vb = crow * (uint32_t)g.ldb + ccol;
+  auto copy = [&](unsigned kb, unsigned buf) {
+    Resource a = ra, b = rb;
+    if (kb >= kb1) a[2] = b[2] = 0;          // past the slice: nothing is read
+    const uint32_t to = lds_address(ring[buf]), at = kb * kBK;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const unsigned r = wave * 16 + i * 8;
+      copy_to_lds(b, vb, r * (uint32_t)g.ldb + at, to + (BM + r) * kBK);
+    }
+#pragma unroll
+    for (int i = 0; i < MT / 2; ++i) {
+      const unsigned r = (wave * (MT / 2) + i) * 8;
+      copy_to_lds(a, va, r * (uint32_t)g.lda + at, to + r * kBK);
+    }
+  };
+  auto scale_at = [&](const void* p, size_t i) -> uint32_t {
+    if constexpr (HW) return static_cast<const uint8_t*>(p)[i];
+    else if constexpr (E8M0) return __float_as_uint(e8m0_f32(static_cast<const uint8_t*>(p)[i]));
+    else return static_cast<const uint32_t*>(p)[i];
+  };
+
+  f32x4 acc[MT];
+#pragma unroll
+  for (int j = 0; j < MT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const uint32_t r0 = lds_at(lr, lq) * 16, r1 = lds_at(lr, lq + 4) * 16;
+  for (unsigned base = kb0; base < kb1; base += kFewBlocks) {
+    const unsigned n = min((unsigned)kFewBlocks, kb1 - base);
+    // no wave still uses the last round's blocks and scales
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+    for (unsigned c = 0; c < ST - 1; ++c) copy(c < n ? base + c : kb1, c);
+    for (unsigned i = t; i < n * BM; i += 256)
+      lsa[i / BM][i % BM] = scale_at(g.sa[z], (size_t)min(m0 + i % BM, g.M - 1) * g.sa_rs + (size_t)(base + i / BM) * g.sa_cs);
+    constexpr int BS = BROWS ? kFewCols : 1;
+    for (unsigned i = t; i < n * BS; i += 256) {
+      const unsigned row = min(n0 + i % BS, g.N - 1);
+      lsb[i / BS][i % BS] = scale_at(g.sb[z], (size_t)(BROWS ? row : row / AR_BLOCK) * g.sb_rs + (size_t)(base + i / BS) * g.sb_cs);
+    }
+    unsigned buf = 0;
+    for (unsigned c = 0; c < n; ++c) {
+      // this wave's copies of the block have landed (those of the ST - 2
+      // blocks after it may be on their way), then every wave's
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((ST - 2) * kCopies) : "memory");
+      const unsigned free = buf == 0 ? ST - 1 : buf - 1;   // the block before: no wave reads it any more
+      copy(c + ST - 1 < n ? base + c + ST - 1 : kb1, free);
+      const unsigned kb = base + c;
+      const bool tail = (kb + 1) * kBK > g.K;
+      auto read = [&](int row, Frag& f) {
+        f.h[0] = *reinterpret_cast<const u32x4*>(ring[buf] + row * kBK + r0);
+        f.h[1] = *reinterpret_cast<const u32x4*>(ring[buf] + row * kBK + r1);
+        if (tail) {
+          f.h[0] = mask_chunk(f.h[0], kb * kBK + lq * 16, g.K);
+          f.h[1] = mask_chunk(f.h[1], kb * kBK + lq * 16 + 64, g.K);
+        }
+      };
+      Frag fa[MT], fb;
+      read(BM + wave * 16, fb);
+#pragma unroll
+      for (int j = 0; j < MT; ++j) read(j * 16, fa[j]);
+      if constexpr (HW) {
+        const uint32_t sb = lsb[c][BROWS ? wave * 16 + lr : 0];
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+          acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb.v, fa[j].v, acc[j], 0, 0, 0, (int)sb, 0,
+                                                                 (int)lsa[c][j * 16 + lr]);
+      } else {
+        float sb[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sb[r] = __uint_as_float(lsb[c][BROWS ? wave * 16 + lq * 4 + r : 0]);
+        Wide wb;
+        if constexpr (OUT32) wb = widen(fb);
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+          f32x4 p = {0.f, 0.f, 0.f, 0.f};
+          if constexpr (OUT32) {
+            const Wide wa = widen(fa[j]);
+#pragma unroll
+            for (int h = 0; h < 4; ++h) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb.p[h], wa.p[h], p, 0, 0, 0);
+          } else {
+            p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb.v, fa[j].v, p, 0, 0, 0, 0, 0, 0);
+          }
+          const float sa = __uint_as_float(lsa[c][j * 16 + lr]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[j][r] = __builtin_fmaf(p[r], sa * sb[r], acc[j][r]);
+        }
+      }
+      buf = buf + 1 == ST ? 0 : buf + 1;
+    }
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no copy outlives the workgroup's LDS
+  if (slices > 1) {
+    const size_t tile = ((size_t)z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
+    if (!join_parts(acc, counters + tile, parts + tile * slices * (MT * 256 * 16), slice, slices, &lsb[0][0])) return;
+  }
+#pragma unroll
+  for (int j = 0; j < MT; ++j) {
+    const unsigned m = m0 + j * 16 + lr, n = n0 + wave * 16 + lq * 4;
+    if (m < g.M) store4<OUT32>(g.c[z], m * g.ldc + n, n, g.N, (g.ldc & 3) == 0, acc[j]);
+  }
+}
+
 // 128 x 128 tile of C in a 256-lane workgroup, 64 x 64 a wave as 4 x 4
 // products of 16 x 16 x 128.  b is the first operand, so a lane ends with
 // four consecutive n of one m.
@@ -546,10 +701,57 @@ __global__ __launch_bounds__(256) void k_gemm_tile(GemmArgs g) {
     }
 }
 
+// How a product is cut: the tile, and the slices of K that different
+// workgroups take.  Planned for the 256 CUs of the device, so that a
+// workspace's size does not depend on where it is asked for.
+constexpr unsigned kPlanCus = 256;
+struct Plan {
+  int mt;           // few rows: fragments of 16 rows of a; 0: large tiles
+  unsigned slices, per;
+  size_t tiles;     // of all problems
+};
+
+unsigned blocks_of(unsigned K) { return (K + kBK - 1) / kBK; }
+
+// Up to 64 rows of a: 64 columns a workgroup, two workgroups a CU; slices of
+// at least 4 blocks until the device is full.
+Plan plan_few(unsigned M, unsigned N, unsigned K, int G) {
+  Plan p{};
+  p.mt = M <= 32 ? 2 : 4;
+  p.tiles = cdiv(M, 16 * p.mt) * cdiv(N, kFewCols) * G;
+  const unsigned nk = blocks_of(K);
+  const size_t want = cdiv(2 * kPlanCus, p.tiles);
+  p.slices = (unsigned)std::max<size_t>(1, std::min<size_t>(want, nk / 4));
+  p.per = (unsigned)cdiv(nk, p.slices);
+  p.slices = (unsigned)cdiv(nk, p.per);
+  return p;
+}
+
+size_t counter_bytes(const Plan& p) { return cdiv(p.tiles * 4, 256) * 256; }
+size_t few_bytes(const Plan& p) {
+  return p.slices > 1 ? counter_bytes(p) + p.tiles * p.slices * (p.mt * 256 * 16) : 0;
+}
+
+template <bool E8M0, bool BROWS, bool OUT32>
+hipError_t gemm_few(const Launch& L, const GemmArgs& g, int G, void* ws) {
+  Plan p = plan_few(g.M, g.N, g.K, G);
+  if (!ws) {
+    p.slices = 1;
+    p.per = blocks_of(g.K);
+  }
+  uint32_t* counters = static_cast<uint32_t*>(ws);
+  char* parts = static_cast<char*>(ws) + counter_bytes(p);
+  const dim3 grid((unsigned)cdiv(g.N, kFewCols), (unsigned)cdiv(g.M, 16 * p.mt), (unsigned)G * p.slices);
+  auto k = p.mt == 2 ? k_gemm_few<2, E8M0, BROWS, OUT32> : k_gemm_few<4, E8M0, BROWS, OUT32>;
+  return launch_k(k, grid, dim3(256), 0, L.stream, g, (int)p.slices, p.per, counters, parts);
+}
+
 template <bool E8M0, bool BROWS>
-hipError_t gemm_o(const Launch& L, const GemmArgs& g, int G, bool out_f32) {
+hipError_t gemm_o(const Launch& L, const GemmArgs& g, int G, bool out_f32, void* ws) {
   const size_t wide = (g.lda | g.ldb) >> 23 | (g.sa_rs | g.sa_cs | g.sb_rs | g.sb_cs) >> 32;
-  if (!wide && g.M > 64 && g.K > 256) {
+  if (!wide && g.M <= 64 && g.K > 0)
+    return out_f32 ? gemm_few<E8M0, BROWS, true>(L, g, G, ws) : gemm_few<E8M0, BROWS, false>(L, g, G, ws);
+  if (!wide && g.K > 256) {
     const unsigned bm = (out_f32 || (BROWS && !E8M0)) ? 128 : 256;
     const unsigned tm = (unsigned)cdiv(g.M, bm), tn = (unsigned)cdiv(g.N, 256);
     const dim3 grid(std::min(tm * tn, (unsigned)L.cus), 1, (unsigned)G);
@@ -564,11 +766,14 @@ hipError_t gemm_o(const Launch& L, const GemmArgs& g, int G, bool out_f32) {
 
 }  // namespace
 
-size_t gemm_fp8_workspace(size_t, size_t, size_t, int) { return 0; }
+size_t gemm_fp8_workspace(size_t M, size_t N, size_t K, int G) {
+  return M <= 64 ? few_bytes(plan_few((unsigned)M, (unsigned)N, (unsigned)K, G)) : 0;
+}
 
-hipError_t launch_gemm_fp8(const Launch& L, const GemmArgs& g, int G, bool e8m0, bool b_rows, bool out_f32, void*) {
-  if (e8m0) return b_rows ? gemm_o<true, true>(L, g, G, out_f32) : gemm_o<true, false>(L, g, G, out_f32);
-  return b_rows ? gemm_o<false, true>(L, g, G, out_f32) : gemm_o<false, false>(L, g, G, out_f32);
+hipError_t launch_gemm_fp8(const Launch& L, const GemmArgs& g, int G, bool e8m0, bool b_rows, bool out_f32,
+                           void* ws) {
+  if (e8m0) return b_rows ? gemm_o<true, true>(L, g, G, out_f32, ws) : gemm_o<true, false>(L, g, G, out_f32, ws);
+  return b_rows ? gemm_o<false, true>(L, g, G, out_f32, ws) : gemm_o<false, false>(L, g, G, out_f32, ws);
 }
 
 }  // namespace ar
