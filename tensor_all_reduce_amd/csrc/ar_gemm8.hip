@@ -72,17 +72,18 @@ union Frag {
   uint32_t w[8];
 };
 
-// The same 32 codes as bf16 (exact), for four 16 x 16 x 32 products.
+// The same 32 codes as bf16 (exact), for four 16 x 16 x 32 products; times
+// `scale`, a power of two.
 struct Wide {
   b16x8 p[4];
 };
-__device__ __forceinline__ Wide widen(const Frag& f) {
+__device__ __forceinline__ Wide widen(const Frag& f, float scale = 1.0f) {
   typedef __bf16 b16x2 __attribute__((ext_vector_type(2)));
   Wide r;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const b16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(f.w[i], 1.0f, false);
-    const b16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(f.w[i], 1.0f, true);
+    const b16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(f.w[i], scale, false);
+    const b16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(f.w[i], scale, true);
     b16x8& d = r.p[i / 2];
     const int o = 4 * (i & 1);
     d[o] = lo[0];
@@ -127,6 +128,59 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
 
+// Joins the parts of a result that workgroups have summed over slices of K.
+// A part holds each lane's accumulators, `Q` vectors, as the lanes have them.
+// The last workgroup to arrive adds all parts in slice order, so the result
+// does not depend on who was last.  Parts are written through the L2 of the
+// writer's XCD; the counter is zero again afterwards.  Returns whether this
+// workgroup has the result (in v).  `lds_word`: a word of LDS that is free.
+template <int Q>
+__device__ __forceinline__ bool join_parts(f32x4 (&v)[Q], uint32_t* counter, char* parts, int slice, int slices,
+                                           uint32_t* lds_word) {
+  const unsigned lanes = blockDim.x, bytes = Q * lanes * 16;
+  char* mine = parts + (size_t)slice * bytes;
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    union { f32x4 f; u32x4 u; } x;
+    x.f = v[q];
+    st16<2>(mine, bytes, (q * lanes + threadIdx.x) * 16, x.u);
+  }
+  __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+  __syncthreads();
+  if (threadIdx.x == 0) *lds_word = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  if (*lds_word != (uint32_t)slices - 1) return false;
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+  if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  // 16 vectors at a time are on their way at once: read one after the other,
+  // each would cost a trip to memory
+  constexpr int QB = Q < 4 ? Q : 4, SB = 16 / QB;
+#pragma unroll
+  for (int q0 = 0; q0 < Q; q0 += QB) {
+    f32x4 sum[QB];
+#pragma unroll
+    for (int q = 0; q < QB; ++q) sum[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < slices; s += SB) {
+      f32x4 x[SB][QB];
+#pragma unroll
+      for (int b = 0; b < SB; ++b)
+#pragma unroll
+        for (int q = 0; q < QB; ++q) {
+          x[b][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+          if (s + b < slices)
+            x[b][q] = *reinterpret_cast<const f32x4*>(parts + (size_t)(s + b) * bytes + ((q0 + q) * lanes + threadIdx.x) * 16);
+        }
+#pragma unroll
+      for (int b = 0; b < SB; ++b)
+#pragma unroll
+        for (int q = 0; q < QB; ++q) sum[q] += x[b][q];
+    }
+#pragma unroll
+    for (int q = 0; q < QB; ++q) v[q0 + q] = sum[q];
+  }
+  return true;
+}
+
 // BM x 256 tiles of C in 512 lanes, K >= 1.  8 waves, 2 along M by 4 along N,
 // each with JT x 4 products of 16 x 16 x 128 a block.
 //
@@ -135,11 +189,14 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 // the same block or from the next one, which by then is in the other LDS
 // buffer.  One barrier a block, after which the copies of block k + 2 start
 // into the buffer of block k.  A workgroup takes tile after tile, and the
-// blocks of the next follow those of one without a gap.
-template <int BM, bool E8M0, bool BROWS, bool OUT32>
-__global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, unsigned tiles_n) {
+// blocks of the next follow those of one without a gap.  SPLIT: it has one
+// tile and a slice of K, `per` blocks of it, and the parts are joined.
+template <int BM, bool E8M0, bool BROWS, bool OUT32, bool SPLIT>
+__global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, unsigned tiles_n, int slices, unsigned per,
+                                                  uint32_t* counters, char* parts) {
   constexpr int BN = 256, IT = 4, JT = BM / 32, R = 4;
   constexpr bool HW = E8M0 && !OUT32;        // scales applied by the matrix cores
+  constexpr bool FOLD = E8M0 && OUT32;       // or as codes become bf16
   constexpr uint32_t kBuf = (BM + BN) * kBK;
   constexpr int kOut = OUT32 ? 4 : 2;        // bytes of a result
   __shared__ __align__(16) char lab[2][kBuf];  // rows of a, then of b
@@ -147,12 +204,15 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
   // side by side: bytes (HW) or binary32 words
   __shared__ __align__(16) uint32_t ls[3][HW ? 128 : 512];
   __shared__ __align__(16) char lout[8][16 * 64 * kOut];  // 16 rows of a wave's results
-  const int z = blockIdx.z, t = threadIdx.x, lane = lane_id();
+  const int z = SPLIT ? blockIdx.z / slices : blockIdx.z, slice = SPLIT ? blockIdx.z % slices : 0;
+  const int t = threadIdx.x, lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(t / kWave);
   const int lr = lane & 15, lq = lane >> 4;
   const int wm = (wave & 1) * (BM / 2), wn = (wave >> 1) * 64;
-  const unsigned nk = (g.K + kBK - 1) / kBK;
-  const unsigned whole = g.K / kBK;          // K blocks without a tail
+  const unsigned kb0 = SPLIT ? slice * per : 0;  // first block
+  const unsigned K = SPLIT ? min(g.K - kb0 * kBK, per * kBK) : g.K;
+  const unsigned nk = (K + kBK - 1) / kBK;
+  const unsigned whole = K / kBK;            // K blocks without a tail
   const unsigned tiles = tiles_m * tiles_n;
 
   // XCD x (workgroups reach the 8 XCDs in turn) takes a contiguous run of
@@ -168,8 +228,8 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
     return Tile{(unsigned)__builtin_amdgcn_readfirstlane((int)((band * 8 + in % bm) * BM)),
                 (unsigned)__builtin_amdgcn_readfirstlane((int)(in / bm * BN))};
   };
-  auto a_rows = [&](Tile q) { return rows_buffer(g.a[z] + (size_t)q.m0 * g.lda, g.M - q.m0, BM, g.lda, g.K); };
-  auto b_rows = [&](Tile q) { return rows_buffer(g.b[z] + (size_t)q.n0 * g.ldb, g.N - q.n0, BN, g.ldb, g.K); };
+  auto a_rows = [&](Tile q) { return rows_buffer(g.a[z] + (size_t)q.m0 * g.lda + kb0 * kBK, g.M - q.m0, BM, g.lda, K); };
+  auto b_rows = [&](Tile q) { return rows_buffer(g.b[z] + (size_t)q.n0 * g.ldb + kb0 * kBK, g.N - q.n0, BN, g.ldb, K); };
 
   // a wave copies 8 rows at a time; chunk c of a row goes to position c ^ (row % 8)
   const unsigned crow = wave * 8 + (lane >> 3), ccol = ((lane & 7) ^ (lane >> 3)) * 16;
@@ -191,7 +251,7 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
   auto load_scale = [&](Tile q, unsigned k) -> uint32_t {
     unsigned row = min((is_a ? q.m0 : q.n0) + slane, slast);
     if (!BROWS && !is_a) row /= AR_BLOCK;
-    const size_t i = (uint64_t)row * srs + (uint64_t)k * scs;
+    const size_t i = (uint64_t)row * srs + (uint64_t)(kb0 + min(k, nk - 1)) * scs;
     if constexpr (E8M0) {
       const uint8_t b = reinterpret_cast<const uint8_t*>(sbase)[i];
       if constexpr (HW) return b;
@@ -218,8 +278,8 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
     f.h[1] = *reinterpret_cast<const u32x4*>(p + r1 + i * 16 * kBK);
   };
   auto mask = [&](unsigned k, Frag& f) {
-    f.h[0] = mask_chunk(f.h[0], k * kBK + lq * 16, g.K);
-    f.h[1] = mask_chunk(f.h[1], k * kBK + lq * 16 + 64, g.K);
+    f.h[0] = mask_chunk(f.h[0], k * kBK + lq * 16, K);
+    f.h[1] = mask_chunk(f.h[1], k * kBK + lq * 16 + 64, K);
   };
 
   f32x4 acc[IT][JT];
@@ -227,11 +287,11 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
   // binary32 scales: a block's product waits D products for its turn to be
   // scaled and added, while the matrix cores run on
   constexpr int D = OUT32 ? IT : 3, NP = 2 * IT;
-  f32x4 p[HW ? 1 : NP];
+  f32x4 p[HW || FOLD ? 1 : NP];
   using ScaleA = std::conditional_t<HW, uint32_t, f32x4>;  // of a: four rows of this lane
   struct ScaleB {
-    uint32_t bytes;                          // HW: the row of each fragment
-    f32x4 row[!HW && BROWS ? IT : 1];        // else this lane's four rows of each fragment, or [0][0] for all
+    uint32_t bytes;                          // HW: of row lr of each fragment
+    f32x4 row[!HW && !FOLD && BROWS ? IT : 1];  // FOLD: the same; else of this lane's four rows of each, or [0][0] of all
   };
   ScaleA sa[JT / 4];
   ScaleB sb;
@@ -245,6 +305,8 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
   auto read_sb = [&](int buf, ScaleB& v) {
     if constexpr (HW) {
       v.bytes = ls[buf][(BM + wn) / 4 + lr];
+    } else if constexpr (FOLD) {
+      v.row[0] = *reinterpret_cast<const f32x4*>(&ls[buf][BM + wn + lr * 4]);
     } else if constexpr (BROWS) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
@@ -265,7 +327,7 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
   constexpr int BAR = F + 3;                 // the barrier comes after this product
   auto add = [&](auto nn) {
     constexpr int n = decltype(nn)::value, i = n < F ? n % IT : (n - F) / 4, j = n < F ? n / IT : JT - 4 + (n - F) % 4;
-    if constexpr (!HW) {
+    if constexpr (!HW && !FOLD) {
       const float s = sa[j / 4][j % 4];
 #pragma unroll
       for (int r = 0; r < 4; ++r)
@@ -304,8 +366,15 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
         p[n % NP] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[i].v, a.v, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
       } else {
         // JT is 4: a row of four products, each the sum of four of 32 codes
-        if constexpr (n < 4) wa[n] = widen(a);
-        if constexpr (n % 4 == 3) {
+        if constexpr (n < 4) wa[n] = widen(a, FOLD ? sa[0][n] : 1.0f);
+        if constexpr (FOLD && n % 4 == 3) {
+          const Wide wb = widen(fb[i], sb.row[0][i]);
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[i][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb.p[h], wa[c].p[h], acc[i][c], 0, 0, 0);
+        }
+        if constexpr (!FOLD && n % 4 == 3) {
           const Wide wb = widen(fb[i]);
 #pragma unroll
           for (int h = 0; h < 4; ++h)
@@ -316,7 +385,7 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
         }
       }
       if constexpr (!HW && !OUT32 && n >= D) add(SPc<n - D>{});
-      if constexpr (OUT32 && n >= 7 && n % 4 == 3) {
+      if constexpr (OUT32 && !FOLD && n >= 7 && n % 4 == 3) {
         each<4>([&](auto c) { add(SPc<n - 7 + decltype(c)::value>{}); });
       }
       if constexpr (n == BAR) {
@@ -411,7 +480,7 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
   now_b = b_rows(now);
   // the next tile (without one, this tile again: its blocks are copied and not used)
   auto look_ahead = [&] {
-    if (id + gridDim.x < tiles) then = tile_at(id + gridDim.x);
+    if (!SPLIT && id + gridDim.x < tiles) then = tile_at(id + gridDim.x);
     else then = now;
     then_a = a_rows(then);
     then_b = b_rows(then);
@@ -440,6 +509,15 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
       for (int j = 0; j < JT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     for (unsigned k = 0; k < whole; ++k) step(k, std::false_type{});
     if (whole < nk) step(whole, std::true_type{});
+    if constexpr (SPLIT) {
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");   // LDS is free
+      const size_t tile = (size_t)z * tiles + id;
+      if (!join_parts(reinterpret_cast<f32x4(&)[IT * JT]>(acc), counters + tile, parts + tile * slices * (BM * BN * 4), slice,
+                      slices, &ls[0][0]))
+        return;
+      store(now);
+      return;
+    }
     store(now);
     id += gridDim.x;
     if (id >= tiles) break;
@@ -451,47 +529,16 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no copy outlives the workgroup's LDS
 }
 
-// Joins the parts of a result that workgroups have summed over slices of K.
-// A part holds each lane's accumulators, `Q` vectors, as the lanes have them.
-// The last workgroup to arrive adds all parts in slice order, so the result
-// does not depend on who was last.  Parts are written through the L2 of the
-// writer's XCD; the counter is zero again afterwards.  Returns whether this
-// workgroup has the result (in v).  `lds_word`: a word of LDS that is free.
-template <int Q>
-__device__ __forceinline__ bool join_parts(f32x4 (&v)[Q], uint32_t* counter, char* parts, int slice, int slices,
-                                           uint32_t* lds_word) {
-  const unsigned lanes = blockDim.x, bytes = Q * lanes * 16;
-  char* mine = parts + (size_t)slice * bytes;
-#pragma unroll
-  for (int q = 0; q < Q; ++q) {
-    union { f32x4 f; u32x4 u; } x;
-    x.f = v[q];
-    st16<2>(mine, bytes, (q * lanes + threadIdx.x) * 16, x.u);
-  }
-  __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
-  __syncthreads();
-  if (threadIdx.x == 0) *lds_word = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  __syncthreads();
-  if (*lds_word != (uint32_t)slices - 1) return false;
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-  if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-#pragma unroll
-  for (int q = 0; q < Q; ++q) v[q] = *reinterpret_cast<const f32x4*>(parts + (q * lanes + threadIdx.x) * 16);
-  for (int s = 1; s < slices; ++s)
-#pragma unroll
-    for (int q = 0; q < Q; ++q) v[q] += *reinterpret_cast<const f32x4*>(parts + (size_t)s * bytes + (q * lanes + threadIdx.x) * 16);
-  return true;
-}
-
 // Few rows of a: 16 MT x 64 of C in four waves of 16 columns, K >= 1.  The
 // codes of b are read once and there is little to compute on them, so the
 // kernel is a copy engine: a ring of ST blocks in LDS, all but one of them on
-// their way, two workgroups a CU.  blockIdx: columns, rows, problem and slice
+// their way, and three or four workgroups a CU (8 x 8192 x 1024 with one row:
+// 13.4 us with a ring of 3 and four workgroups, 17.3 with 5 and two).  blockIdx: columns, rows, problem and slice
 // of K (`per` blocks each).
-constexpr int kFewCols = 64, kFewBlocks = 32;  // columns; blocks whose scales are held at a time
+constexpr int kFewCols = 64, kFewBlocks = 16;  // columns; blocks whose scales are held at a time
 template <int MT, bool E8M0, bool BROWS, bool OUT32>
 __global__ __launch_bounds__(256) void k_gemm_few(GemmArgs g, int slices, unsigned per, uint32_t* counters, char* parts) {
-  constexpr int BM = 16 * MT, ST = MT == 2 ? 5 : 4;
+  constexpr int BM = 16 * MT, ST = 3;
   constexpr bool HW = E8M0 && !OUT32;
   constexpr int kCopies = 2 + MT / 2;        // of a wave and block
   __shared__ __align__(16) char ring[ST][(BM + kFewCols) * kBK];  // rows of a, then of b
@@ -713,15 +760,17 @@ struct Plan {
 
 unsigned blocks_of(unsigned K) { return (K + kBK - 1) / kBK; }
 
-// Up to 64 rows of a: 64 columns a workgroup, two workgroups a CU; slices of
-// at least 4 blocks until the device is full.
+// Up to 64 rows of a: 64 columns a workgroup; slices of at least 8 blocks
+// until there are two workgroups a CU.  A join costs about 4 us (parts out to
+// memory, a counter, parts back), so more slices lose what they gain: 48 x
+// 4096 x 8192 takes 16.8 us in 8 slices, 19.2 in 4, 21.6 in 16.
 Plan plan_few(unsigned M, unsigned N, unsigned K, int G) {
   Plan p{};
   p.mt = M <= 32 ? 2 : 4;
   p.tiles = cdiv(M, 16 * p.mt) * cdiv(N, kFewCols) * G;
   const unsigned nk = blocks_of(K);
   const size_t want = cdiv(2 * kPlanCus, p.tiles);
-  p.slices = (unsigned)std::max<size_t>(1, std::min<size_t>(want, nk / 4));
+  p.slices = (unsigned)std::max<size_t>(1, std::min<size_t>(want, nk / 8));
   p.per = (unsigned)cdiv(nk, p.slices);
   p.slices = (unsigned)cdiv(nk, p.per);
   return p;
@@ -746,19 +795,50 @@ hipError_t gemm_few(const Launch& L, const GemmArgs& g, int G, void* ws) {
   return launch_k(k, grid, dim3(256), 0, L.stream, g, (int)p.slices, p.per, counters, parts);
 }
 
+// More than 64 rows: large tiles, one workgroup a CU.  Where 128 x 256 tiles
+// fill half the CUs at most, they are cut into slices of at least 8 blocks.
+Plan plan_big(unsigned M, unsigned N, unsigned K, int G) {
+  Plan p{};
+  p.tiles = cdiv(M, 128) * cdiv(N, 256) * G;
+  const unsigned nk = blocks_of(K);
+  p.slices = (unsigned)std::max<size_t>(1, std::min<size_t>(kPlanCus / p.tiles, nk / 8));
+  p.per = (unsigned)cdiv(nk, p.slices);
+  p.slices = (unsigned)cdiv(nk, p.per);
+  return p;
+}
+size_t big_bytes(const Plan& p) { return p.slices > 1 ? counter_bytes(p) + p.tiles * p.slices * (128 * 256 * 4) : 0; }
+
+template <int BM, bool E8M0, bool BROWS, bool OUT32, bool SPLIT>
+hipError_t gemm_tiles(const Launch& L, const GemmArgs& g, int G, const Plan& p, void* ws) {
+  uint32_t* counters = static_cast<uint32_t*>(ws);
+  char* parts = static_cast<char*>(ws) + counter_bytes(p);
+  const unsigned tm = (unsigned)cdiv(g.M, BM), tn = (unsigned)cdiv(g.N, 256);
+  const dim3 grid(SPLIT ? tm * tn : std::min(tm * tn, (unsigned)L.cus), 1, (unsigned)G * p.slices);
+  return launch_k(k_gemm_big<BM, E8M0, BROWS, OUT32, SPLIT>, grid, dim3(512), 0, L.stream, g, tm, tn, (int)p.slices, p.per,
+                  counters, parts);
+}
+
+template <bool E8M0, bool BROWS, bool OUT32>
+hipError_t gemm_big(const Launch& L, const GemmArgs& g, int G, void* ws) {
+  Plan p = plan_big(g.M, g.N, g.K, G);
+  if (ws && p.slices > 1) return gemm_tiles<128, E8M0, BROWS, OUT32, true>(L, g, G, p, ws);
+  p.slices = 1;
+  p.per = blocks_of(g.K);
+  // 256 rows a tile unless registers do not hold it (products as bf16, a
+  // binary32 scale for each row of b) or it leaves CUs without one
+  if constexpr (!OUT32 && (E8M0 || !BROWS))
+    if (cdiv(g.M, 256) * cdiv(g.N, 256) * G >= (size_t)L.cus / 2 || g.M % 256 == 0 || g.M % 256 > 128)
+      return gemm_tiles<256, E8M0, BROWS, OUT32, false>(L, g, G, p, ws);
+  return gemm_tiles<128, E8M0, BROWS, OUT32, false>(L, g, G, p, ws);
+}
+
 template <bool E8M0, bool BROWS>
 hipError_t gemm_o(const Launch& L, const GemmArgs& g, int G, bool out_f32, void* ws) {
   const size_t wide = (g.lda | g.ldb) >> 23 | (g.sa_rs | g.sa_cs | g.sb_rs | g.sb_cs) >> 32;
   if (!wide && g.M <= 64 && g.K > 0)
     return out_f32 ? gemm_few<E8M0, BROWS, true>(L, g, G, ws) : gemm_few<E8M0, BROWS, false>(L, g, G, ws);
-  if (!wide && g.K > 256) {
-    const unsigned bm = (out_f32 || (BROWS && !E8M0)) ? 128 : 256;
-    const unsigned tm = (unsigned)cdiv(g.M, bm), tn = (unsigned)cdiv(g.N, 256);
-    const dim3 grid(std::min(tm * tn, (unsigned)L.cus), 1, (unsigned)G);
-    if (out_f32) return launch_k(k_gemm_big<128, E8M0, BROWS, true>, grid, dim3(512), 0, L.stream, g, tm, tn);
-    constexpr int BM = BROWS && !E8M0 ? 128 : 256;
-    return launch_k(k_gemm_big<BM, E8M0, BROWS, false>, grid, dim3(512), 0, L.stream, g, tm, tn);
-  }
+  if (!wide && g.K > 256)
+    return out_f32 ? gemm_big<E8M0, BROWS, true>(L, g, G, ws) : gemm_big<E8M0, BROWS, false>(L, g, G, ws);
   const dim3 grid((unsigned)cdiv(g.M, 128), (unsigned)cdiv(g.N, 128), (unsigned)G);
   if (out_f32) return launch_k(k_gemm_tile<E8M0, BROWS, true>, grid, dim3(256), 0, L.stream, g);
   return launch_k(k_gemm_tile<E8M0, BROWS, false>, grid, dim3(256), 0, L.stream, g);
@@ -767,7 +847,9 @@ hipError_t gemm_o(const Launch& L, const GemmArgs& g, int G, bool out_f32, void*
 }  // namespace
 
 size_t gemm_fp8_workspace(size_t M, size_t N, size_t K, int G) {
-  return M <= 64 ? few_bytes(plan_few((unsigned)M, (unsigned)N, (unsigned)K, G)) : 0;
+  const unsigned m = (unsigned)M, n = (unsigned)N, k = (unsigned)K;
+  if (M <= 64) return few_bytes(plan_few(m, n, k, G));
+  return big_bytes(plan_big(m, n, k, G));
 }
 
 hipError_t launch_gemm_fp8(const Launch& L, const GemmArgs& g, int G, bool e8m0, bool b_rows, bool out_f32,
