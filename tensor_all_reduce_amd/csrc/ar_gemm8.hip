@@ -654,8 +654,9 @@ __global__ __launch_bounds__(256) void k_gemm_few(GemmArgs g, int slices, unsign
 }
 
 // 128 x 128 tile of C in a 256-lane workgroup, 64 x 64 a wave as 4 x 4
-// products of 16 x 16 x 128.  b is the first operand, so a lane ends with
-// four consecutive n of one m.
+// products of 16 x 16 x 128: any strides, any K (the other kernels address a
+// tile's rows in 32 bits).  b is the first operand, so a lane ends with four
+// consecutive n of one m.
 template <bool E8M0, bool BROWS, bool OUT32>
 __global__ __launch_bounds__(256) void k_gemm_tile(GemmArgs g) {
   constexpr int BM = 128, BN = 128;
@@ -760,7 +761,7 @@ struct Plan {
 
 unsigned blocks_of(unsigned K) { return (K + kBK - 1) / kBK; }
 
-// Up to 64 rows of a: 64 columns a workgroup; slices of at least 8 blocks
+// 32 or 64 rows of a and 64 columns a workgroup; slices of at least 8 blocks
 // until there are two workgroups a CU.  A join costs about 4 us (parts out to
 // memory, a counter, parts back), so more slices lose what they gain: 48 x
 // 4096 x 8192 takes 16.8 us in 8 slices, 19.2 in 4, 21.6 in 16.
@@ -769,11 +770,22 @@ Plan plan_few(unsigned M, unsigned N, unsigned K, int G) {
   p.mt = M <= 32 ? 2 : 4;
   p.tiles = cdiv(M, 16 * p.mt) * cdiv(N, kFewCols) * G;
   const unsigned nk = blocks_of(K);
-  const size_t want = cdiv(2 * kPlanCus, p.tiles);
-  p.slices = (unsigned)std::max<size_t>(1, std::min<size_t>(want, nk / 8));
+  p.slices = (unsigned)std::max<size_t>(1, std::min<size_t>(2 * kPlanCus / p.tiles, nk / 8));
   p.per = (unsigned)cdiv(nk, p.slices);
   p.slices = (unsigned)cdiv(nk, p.per);
   return p;
+}
+
+// Which kernel: few rows up to 192 of its 64 x 64 tiles, and beyond while
+// tiles times blocks stay within 8192, where a workgroup's whole sum is
+// shorter than a join of large tiles; and for K up to 256, which the large
+// tiles' pipeline is too long for.  Either side, N x K with M rows: 8192 x
+// 8192, M 64: 23 us (large tiles 35), M 128: 38 (35); 8192 x 1024, M 256: 10
+// (17), M 768: 21 (17); 1024 x 8192, M 768: 29 (30), M 1024: 38 (33).
+bool few_rows(unsigned M, unsigned N, unsigned K, int G) {
+  const size_t tiles = cdiv(M, 64) * cdiv(N, kFewCols) * G;
+  if (cdiv(M, 32) > 65535) return false;     // a launch's second axis
+  return tiles <= 192 || blocks_of(K) <= 2 || tiles * blocks_of(K) <= 8192;
 }
 
 size_t counter_bytes(const Plan& p) { return cdiv(p.tiles * 4, 256) * 256; }
@@ -835,7 +847,7 @@ hipError_t gemm_big(const Launch& L, const GemmArgs& g, int G, void* ws) {
 template <bool E8M0, bool BROWS>
 hipError_t gemm_o(const Launch& L, const GemmArgs& g, int G, bool out_f32, void* ws) {
   const size_t wide = (g.lda | g.ldb) >> 23 | (g.sa_rs | g.sa_cs | g.sb_rs | g.sb_cs) >> 32;
-  if (!wide && g.M <= 64 && g.K > 0)
+  if (!wide && g.K > 0 && few_rows(g.M, g.N, g.K, G))
     return out_f32 ? gemm_few<E8M0, BROWS, true>(L, g, G, ws) : gemm_few<E8M0, BROWS, false>(L, g, G, ws);
   if (!wide && g.K > 256)
     return out_f32 ? gemm_big<E8M0, BROWS, true>(L, g, G, ws) : gemm_big<E8M0, BROWS, false>(L, g, G, ws);
@@ -848,7 +860,7 @@ hipError_t gemm_o(const Launch& L, const GemmArgs& g, int G, bool out_f32, void*
 
 size_t gemm_fp8_workspace(size_t M, size_t N, size_t K, int G) {
   const unsigned m = (unsigned)M, n = (unsigned)N, k = (unsigned)K;
-  if (M <= 64) return few_bytes(plan_few(m, n, k, G));
+  if (few_rows(m, n, k, G)) return few_bytes(plan_few(m, n, k, G));
   return big_bytes(plan_big(m, n, k, G));
 }
 

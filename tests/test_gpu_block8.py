@@ -257,3 +257,65 @@ def test_product_of_many_tiles_is_exact(K, brows, e8m0):
     assert np.array_equal(got, want), f"{int((got != want).sum())} differ"
     got, = run([A], [B], brows, M, N, K, False, 8, True)
     assert np.array_equal(got, ref.as_bf16(want)), "bf16"
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("M,N,K", [(2, 70, 300), (200, 4100, 1280)])
+def test_power_of_two_scales_far_apart(M, N, K, f32):
+    """Scales near both ends of the byte's range whose products are moderate."""
+    g = np.random.default_rng([23, M])
+    A, B = int_codes(g, M, K), int_codes(g, N, K)
+    sa = g.integers(10, 14, size=(M, -(-K // 128))).astype(np.uint8)            # 2^-117 .. 2^-114
+    sb = g.integers(238, 242, size=(-(-N // 128), -(-K // 128))).astype(np.uint8)
+    note(f"product with distant scales M={M} N={N} K={K}")
+    want = ref.dequantise(A, sa, 1) @ ref.dequantise(B, sb, 128).T
+    got, = run([(A, sa)], [(B, sb)], 128, M, N, K, f32, 0, True)
+    assert np.array_equal(got, want.astype(np.float32) if f32 else ref.as_bf16(want))
+
+
+@pytest.mark.parametrize("M,N,K", [(130, 8200, 8192 + 17), (200, 260, 2500), (700, 1030, 4200)])
+def test_product_slices_agree(M, N, K):
+    """With and without a workspace (slices of K or not), whole numbers."""
+    g = np.random.default_rng([29, M])
+    A = (int_codes(g, M, K), (2.0 ** g.integers(-1, 2, size=(M, -(-K // 128)))).astype(np.float32))
+    B = (int_codes(g, N, K), (2.0 ** g.integers(-1, 2, size=(-(-N // 128), -(-K // 128)))).astype(np.float32))
+    want = (ref.dequantise(*A, 1).astype(np.float32) @ ref.dequantise(*B, 128).astype(np.float32).T)
+    note(f"product in slices M={M} N={N} K={K}: workspace {tar.gemm_fp8_workspace(M, N, K)}")
+    for split in (True, False):
+        got, = run([A], [B], 128, M, N, K, True, 0, split)
+        assert np.array_equal(got, want), split
+
+
+@pytest.mark.parametrize("f32,e8m0", [(False, False), (True, True), (True, False), (False, True)])
+def test_product_of_rows_far_apart(f32, e8m0):
+    """Rows 8 MiB and more apart, and scales with strides of their own."""
+    M, N, K, ld = 3, 5, 300, (1 << 23) + 16
+    g = np.random.default_rng(31)
+    A, B = int_codes(g, M, K), int_codes(g, N, K)
+    big = torch.full((M + N, ld), 0x7F, dtype=torch.uint8, device=DEV)
+    a, b = big[:M, :K], big[M:, :K]
+    a.copy_(torch.from_numpy(A).to(DEV))
+    b.copy_(torch.from_numpy(B).to(DEV))
+    k = g.integers(-1, 2, size=(M + N, 3))
+    s = torch.from_numpy((k + 127).astype(np.uint8) if e8m0 else (2.0 ** k).astype(np.float32)).to(DEV)
+    sc = torch.zeros(M + N, 21, dtype=s.dtype, device=DEV)[:, ::7]
+    sc.copy_(s)
+    out = torch.empty(M, N, dtype=torch.float32 if f32 else torch.bfloat16, device=DEV)
+    note("product of rows far apart")
+    tar.ar_gemm_fp8([a], [sc[:M]], [b], [sc[M:]], [out], b_block_rows=1)
+    torch.cuda.synchronize()
+    v = ref.spread(2.0 ** k.astype(np.float64), (M + N, K), 1)
+    want = (ref.E4M3[A] * v[:M]) @ (ref.E4M3[B] * v[M:]).T
+    assert np.array_equal(out.float().cpu().numpy(), want.astype(np.float32) if f32 else ref.as_bf16(want))
+
+
+@pytest.mark.parametrize("M,N,K", [(4200, 1000, 200), (70, 9000, 256)])
+def test_product_of_short_rows(M, N, K):
+    g = np.random.default_rng([37, M])
+    A = (int_codes(g, M, K), np.ones((M, 2), dtype=np.float32))
+    B = (int_codes(g, N, K), np.ones((-(-N // 128), 2), dtype=np.float32))
+    want = ref.dequantise(*A, 1).astype(np.float32) @ ref.dequantise(*B, 128).astype(np.float32).T
+    note(f"product of short rows M={M} N={N} K={K}")
+    for f32 in (True, False):
+        got, = run([A], [B], 128, M, N, K, f32, 1, True)
+        assert np.array_equal(got, want if f32 else ref.as_bf16(want))
