@@ -718,7 +718,7 @@ int ar_reduce_norm(const void* const* ins, int P, const void* residual, const vo
 }
 
 size_t ar_norm_bwd_workspace(size_t rows, size_t cols) {
-  return (size_t)ar::norm_bwd_grid(rows) * (cols > AR_NORM_MAX_COLS ? 0 : cols) * sizeof(float);
+  return cols > AR_NORM_MAX_COLS ? 0 : ar::norm_bwd_sums(rows, cols) * sizeof(float);
 }
 
 int ar_norm_bwd(const void* dy, const void* h, const void* weight, int weight_fmt, const void* dres, size_t rows,

@@ -14,7 +14,6 @@ namespace {
 typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(2)));
 
 constexpr int kTile = AR_BLOCK;
-constexpr int kTurnLd = kTile + 16;  // bytes from row to row of the transposed tile in LDS
 
 template <bool E8M0>
 __device__ __forceinline__ void put_scale(const QuantArgs& a, size_t r, size_t c, uint32_t kept) {
@@ -23,36 +22,34 @@ __device__ __forceinline__ void put_scale(const QuantArgs& a, size_t r, size_t c
   else static_cast<uint32_t*>(a.scales)[k] = kept;
 }
 
-// Lane t holds columns 8 (t % 16) .. + 7 of rows 8 (t / 16) .. + 7.
+// Lane t holds columns 8 (t % 16) .. + 7 of rows 8 (t / 16) .. + 7, as bf16:
+// widened for the maximum and again for the codes, since half the registers
+// let twice the workgroups wait for memory at once.
 template <bool SQUARE, bool TURN, bool E8M0>
 __global__ __launch_bounds__(256) void k_quant_block(QuantArgs a, unsigned tiles_c) {
   __shared__ uint32_t top[4][kTile];
-  __shared__ __align__(16) uint8_t turned[TURN ? kTile * kTurnLd : 16];
+  __shared__ __align__(16) uint8_t turned[TURN ? kTile * kTile : 16];
   const size_t tr = blockIdx.x / tiles_c, tc = blockIdx.x % tiles_c;
   const int lc = (threadIdx.x % 16) * 8, lr = (threadIdx.x / 16) * 8, wave = threadIdx.x / kWave;
   const size_t r0 = tr * kTile + lr, c0 = tc * kTile + lc;
-  float f[8][8];
+  u32x4 v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    u32x4 v = {0u, 0u, 0u, 0u};
+    v[i] = u32x4{0u, 0u, 0u, 0u};
     if (r0 + i < a.rows && c0 < a.cols) {
       const uint16_t* p = a.x + (r0 + i) * a.ldx + c0;
       if (c0 + 8 <= a.cols) {
-        v = *reinterpret_cast<const u32x4u*>(p);
+        v[i] = *reinterpret_cast<const u32x4u*>(p);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const uint32_t e = c0 + j < a.cols ? (uint32_t)p[j] : 0u;
-          v[j >> 1] |= (j & 1) ? (e << 16) : e;
+          v[i][j >> 1] |= (j & 1) ? (e << 16) : e;
         }
       }
     }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      f[i][2 * k] = lo_f32(v[k]);
-      f[i][2 * k + 1] = hi_f32(v[k]);
-    }
   }
+  auto at = [&](int i, int j) { return (j & 1) ? hi_f32(v[i][j >> 1]) : lo_f32(v[i][j >> 1]); };
 
   // inv[i]: of row i (straight) or of column i (transposed)
   float inv[8];
@@ -61,7 +58,7 @@ __global__ __launch_bounds__(256) void k_quant_block(QuantArgs a, unsigned tiles
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) m = max(m, finite_mag(f[i][j]));
+      for (int j = 0; j < 8; ++j) m = max(m, finite_mag(at(i, j)));
     m = row16_max(m);
     if (threadIdx.x % 16 == 0) top[0][threadIdx.x / 16] = m;
     __syncthreads();
@@ -77,7 +74,7 @@ __global__ __launch_bounds__(256) void k_quant_block(QuantArgs a, unsigned tiles
     for (int i = 0; i < 8; ++i) {
       uint32_t m = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) m = max(m, finite_mag(f[i][j]));
+      for (int j = 0; j < 8; ++j) m = max(m, finite_mag(at(i, j)));
       const BlockScale s = block_scale<E8M0>(row16_max(m));
       inv[i] = s.inv;
       if (threadIdx.x % 16 == 0 && r0 + i < a.rows) put_scale<E8M0>(a, r0 + i, tc, s.kept);
@@ -87,7 +84,7 @@ __global__ __launch_bounds__(256) void k_quant_block(QuantArgs a, unsigned tiles
     for (int j = 0; j < 8; ++j) {
       uint32_t m = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, finite_mag(f[i][j]));
+      for (int i = 0; i < 8; ++i) m = max(m, finite_mag(at(i, j)));
       m = max(m, (uint32_t)__shfl_xor((int)m, 16));
       m = max(m, (uint32_t)__shfl_xor((int)m, 32));
       if (lane_id() < 16) top[wave][lc + j] = m;
@@ -101,12 +98,17 @@ __global__ __launch_bounds__(256) void k_quant_block(QuantArgs a, unsigned tiles
       if (threadIdx.x < 16 && c0 + j < a.cols) put_scale<E8M0>(a, c0 + j, tr, s.kept);
     }
   }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(v[i]));
 
   if constexpr (!TURN) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (r0 + i >= a.rows || c0 >= a.cols) continue;
-      const uint32_t lo = codes4_scaled(f[i], inv[i]), hi = codes4_scaled(f[i] + 4, inv[i]);
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = at(i, j);
+      const uint32_t lo = codes4_scaled(f, inv[i]), hi = codes4_scaled(f + 4, inv[i]);
       uint8_t* c = a.codes + (r0 + i) * a.codes_ld + c0;
       if (c0 + 8 <= a.cols) {
         *reinterpret_cast<uint64_t*>(c) = (uint64_t)lo | ((uint64_t)hi << 32);
@@ -117,13 +119,16 @@ __global__ __launch_bounds__(256) void k_quant_block(QuantArgs a, unsigned tiles
       }
     }
   } else {
+    // 16 pieces of 8 codes a row of the turned tile, piece q of row c at
+    // q ^ (c / 8): the 16 lanes that write one piece of 16 rows spread over
+    // the banks
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       float col[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) col[i] = f[i][j];
+      for (int i = 0; i < 8; ++i) col[i] = at(i, j);
       const uint32_t lo = codes4_scaled(col, inv[j]), hi = codes4_scaled(col + 4, inv[j]);
-      *reinterpret_cast<uint64_t*>(&turned[(lc + j) * kTurnLd + lr]) = (uint64_t)lo | ((uint64_t)hi << 32);
+      *reinterpret_cast<uint64_t*>(&turned[(lc + j) * kTile + ((lr ^ lc) & (kTile - 1))]) = (uint64_t)lo | ((uint64_t)hi << 32);
     }
     __syncthreads();
 #pragma unroll
@@ -131,14 +136,17 @@ __global__ __launch_bounds__(256) void k_quant_block(QuantArgs a, unsigned tiles
       const int q = k * 256 + threadIdx.x, c = q / 8, r = (q % 8) * 16;  // 16 codes of output row c
       const size_t gc = tc * kTile + c, gr = tr * kTile + r;
       if (gc >= a.cols || gr >= a.rows) continue;
-      const u32x4 v = *reinterpret_cast<const u32x4*>(&turned[c * kTurnLd + r]);
+      const int turn = c & ~7;
+      union { uint64_t h[2]; u32x4 w; } x;
+      x.h[0] = *reinterpret_cast<const uint64_t*>(&turned[c * kTile + (r ^ turn)]);
+      x.h[1] = *reinterpret_cast<const uint64_t*>(&turned[c * kTile + ((r + 8) ^ turn)]);
       uint8_t* p = a.codes + gc * a.codes_ld + gr;
       if (gr + 16 <= a.rows) {
-        *reinterpret_cast<u32x4*>(p) = v;
+        *reinterpret_cast<u32x4*>(p) = x.w;
       } else {
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-          if (gr + j < a.rows) p[j] = (uint8_t)(v[j >> 2] >> (8 * (j & 3)));
+          if (gr + j < a.rows) p[j] = (uint8_t)(x.w[j >> 2] >> (8 * (j & 3)));
       }
     }
   }

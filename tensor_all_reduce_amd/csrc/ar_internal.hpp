@@ -155,13 +155,13 @@ struct NormBwdArgs {
   const uint16_t *dy, *h, *dres;  // dres nullptr: none
   const void* weight;             // nullptr: ones
   uint16_t* dx;                   // nullptr: not written
-  float* partial;                 // [norm_bwd_grid(rows)][cols] sums; nullptr: no dweight
+  float* partial;                 // norm_bwd_sums(rows, cols) values; nullptr: no dweight
   size_t rows;
   unsigned cols;
   int weight_f32;
   float eps;
 };
-unsigned norm_bwd_grid(size_t rows);
+size_t norm_bwd_sums(size_t rows, size_t cols);
 hipError_t launch_norm_bwd(const Launch& L, const NormBwdArgs& a, float* dweight);
 
 struct QuantArgs {

@@ -12,6 +12,8 @@
 #include "ar_e4m3.hpp"
 #include "ar_internal.hpp"
 
+#include <algorithm>
+
 namespace ar {
 namespace {
 
@@ -76,49 +78,131 @@ __device__ __forceinline__ void load_gain(const void* w, int w_f32, unsigned g, 
   }
 }
 
+// Sum over the wave, the same in every lane: DPP swaps within rows of 16
+// lanes (a trip through LDS for each step takes several times as long), then
+// the four rows.
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m);
-  return v;
-}
-
-// Sum over the workgroup, the same in every lane; `part` holds one value per
-// wave.  The order is fixed by the workgroup's size.
-__device__ __forceinline__ float block_sum(float v, float* part) {
-  v = wave_sum(v);
-  const int waves = blockDim.x / kWave;
-  if (waves == 1) return v;
-  if (lane_id() == 0) part[threadIdx.x / kWave] = v;
-  __syncthreads();
-  float s = part[0];
-  for (int i = 1; i < waves; ++i) s += part[i];
-  return s;
+  auto swapped = [](float x, auto ctrl) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), decltype(ctrl)::value, 0xF, 0xF, false));
+  };
+  v += swapped(v, SPc<0xB1>{});              // lane ^ 1
+  v += swapped(v, SPc<0x4E>{});              // lane ^ 2
+  v += swapped(v, SPc<0x141>{});             // the other quad of 8
+  v += swapped(v, SPc<0x140>{});             // the other half of 16
+  auto row = [&](int lane) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane)); };
+  return (row(0) + row(16)) + (row(32) + row(48));
 }
 
 constexpr int kMaxWaves = 16;
 
+// Sums of one value a wave, of up to 16 waves, kept in `part`: 16 slots, those
+// of waves that the workgroup lacks zero.  put_part, a barrier, sum_parts.
+__device__ __forceinline__ void put_part(float v, float* part) {
+  const unsigned waves = blockDim.x / kWave;
+  if (lane_id() == 0) part[threadIdx.x / kWave] = v;
+  if (threadIdx.x >= waves && threadIdx.x < kMaxWaves) part[threadIdx.x] = 0.0f;
+}
+__device__ __forceinline__ float sum_parts(const float* part) {
+  typedef float f32x4 __attribute__((ext_vector_type(4)));
+  const f32x4* p = reinterpret_cast<const f32x4*>(part);
+  const f32x4 a = (p[0] + p[1]) + (p[2] + p[3]);
+  return (a[0] + a[1]) + (a[2] + a[3]);
+}
+
+// Elements from row to row of the gradient's partial sums.
+__host__ __device__ constexpr size_t sum_stride(size_t cols) { return (cols + 3) & ~(size_t)3; }
+
+// The row kernel's three forms: rows of whole aligned groups, with plain or
+// non-temporal accesses, and ragged rows.
+enum RowForm { kRagged = 0, kWhole, kStream };
+
+// Longest ragged row whose aligned groups 8 x 1024 lanes hold; groups of a
+// longer one start with the row, wherever that is.
+constexpr unsigned kMaxShifted = AR_NORM_MAX_COLS - 14;
+
 // One workgroup per row; lane t holds groups t, t + T, ... (V of them).
-template <int P, int V, bool WHOLE, bool E8M0>
+//
+// kRagged (cols no multiple of 8): rows start anywhere, but all of them at
+// the same place in every [rows x cols] buffer.  Groups are those of the
+// buffer, aligned, so the row's first and last are shared with its
+// neighbours; elements of other rows are read (where the buffer holds the
+// whole group), zeroed and not written.  A group then spans up to two scale
+// blocks, whose maxima meet in LDS.
+template <int P, int V, int FORM>
 __global__ __launch_bounds__(1024) void k_reduce_norm(InPtrs in, NormArgs a) {
-  __shared__ float part[kMaxWaves];
+  __shared__ __align__(16) float part[kMaxWaves];
+  __shared__ uint32_t top[FORM == kRagged ? AR_NORM_MAX_COLS / AR_BLOCK : 1];
+  constexpr bool NT = FORM == kStream;
   const size_t row = (size_t)blockIdx.y * gridDim.x + blockIdx.x;
   if (row >= a.rows) return;
-  const unsigned cols = a.cols, groups = (cols + 7) / 8;
-  const size_t at = row * cols;
-  float h[V][8];
+  const unsigned cols = a.cols;
+  const int off = FORM == kRagged && cols <= kMaxShifted ? (int)((row * cols) & 7) : 0;
+  const unsigned groups = (cols + off + 7) / 8;
+  const size_t at = row * cols - off;        // of group 0
+  auto load = [&](const void* base, unsigned g) -> u32x4 {
+    const uint16_t* p = static_cast<const uint16_t*>(base) + at + 8 * (size_t)g;
+    if constexpr (FORM != kRagged) return ld4<NT>(reinterpret_cast<const u32x4*>(p));
+    if (at + 8 * (size_t)g + 8 <= a.rows * cols) return *reinterpret_cast<const u32x4u*>(p);
+    u32x4 v = {0u, 0u, 0u, 0u};              // the buffer's last group
+#pragma unroll
+    for (unsigned j = 0; j < 8; ++j)
+      if (at + 8 * (size_t)g + j < a.rows * cols) v[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
+    return v;
+  };
+  auto mine = [&](unsigned g, int j) {       // element j of group g belongs to this row
+    const int e = (int)(8 * g) - off + j;
+    return FORM != kRagged || (e >= 0 && e < (int)cols);
+  };
+  auto store = [&](uint16_t* base, unsigned g, u32x4 v) {
+    uint16_t* p = base + at + 8 * (size_t)g;
+    if constexpr (FORM != kRagged) {
+      st4<NT>(reinterpret_cast<u32x4*>(p), v);
+      return;
+    }
+    if (mine(g, 0) && mine(g, 7)) {
+      *reinterpret_cast<u32x4u*>(p) = v;
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (mine(g, j)) p[j] = (uint16_t)(v[j >> 1] >> (16 * (j & 1)));
+  };
+  auto gain = [&](unsigned g, float (&w)[8]) {
+    if (FORM != kRagged) {
+      load_gain<true>(a.weight, a.weight_f32, g, cols, w);
+      return;
+    }
+    const int e = (int)(8 * g) - off;
+    if (a.weight && !a.weight_f32 && mine(g, 0) && mine(g, 7)) {
+      widen(*reinterpret_cast<const u32x4u*>(static_cast<const uint16_t*>(a.weight) + e), w);
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      w[j] = 1.0f;
+      if (a.weight && mine(g, j))
+        w[j] = a.weight_f32 ? static_cast<const float*>(a.weight)[e + j]
+                            : bf16_f32(static_cast<const uint16_t*>(a.weight)[e + j]);
+    }
+  };
+
+  // gains are fetched with the row where registers allow: after the row's sum
+  // they would be one more trip to memory
+  constexpr bool EARLY = V <= 2;
+  float h[V][8], w[V][8];
   float ss = 0.0f;
 #pragma unroll
   for (int u = 0; u < V; ++u) {
     const unsigned g = u * blockDim.x + threadIdx.x;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) h[u][j] = 0.0f;
+    for (int j = 0; j < 8; ++j) h[u][j] = w[u][j] = 0.0f;
     if (g >= groups) continue;
     u32x4 x[P];
 #pragma unroll
-    for (int p = 0; p < P; ++p)
-      x[p] = load_group<false, WHOLE>(static_cast<const uint16_t*>(in.p[p]) + at, g, cols);
+    for (int p = 0; p < P; ++p) x[p] = load(in.p[p], g);
     u32x4 r = {0u, 0u, 0u, 0u};
-    if (a.residual) r = load_group<false, WHOLE>(a.residual + at, g, cols);
+    if (a.residual) r = load(a.residual, g);
+    if (EARLY && (a.y || a.codes)) gain(g, w[u]);
     widen(x[0], h[u]);
 #pragma unroll
     for (int p = 1; p < P; ++p) {
@@ -133,50 +217,82 @@ __global__ __launch_bounds__(1024) void k_reduce_norm(InPtrs in, NormArgs a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) h[u][j] += f[j];
     }
-    if (a.res_out) store_group<false, WHOLE>(a.res_out + at, g, cols, narrow(h[u]));
+    if (a.res_out) store(a.res_out, g, narrow(h[u]));
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(h[u][j], h[u][j], ss);
+    for (int j = 0; j < 8; ++j) {
+      if (!mine(g, j)) h[u][j] = 0.0f;
+      ss = __builtin_fmaf(h[u][j], h[u][j], ss);
+    }
   }
   if (!a.y && !a.codes) return;
+  if (FORM == kRagged && a.codes)
+    for (unsigned i = threadIdx.x; i < (cols + AR_BLOCK - 1) / AR_BLOCK; i += blockDim.x) top[i] = 0;
   // a lane's sum is divided before lanes are added, so that only a mean
   // square beyond binary32 overflows, not the sum of a whole row's squares
-  const float r = 1.0f / sqrtf(block_sum(ss / (float)cols, part) + a.eps);
+  put_part(wave_sum(ss / (float)cols), part);
+  __syncthreads();
+  const float r = 1.0f / sqrtf(sum_parts(part) + a.eps);
+
+  auto keep_scale = [&](size_t block, uint32_t kept) {
+    const size_t k = row * a.scale_rs + block * a.scale_cs;
+    if (a.scale_e8m0) static_cast<uint8_t*>(a.scales)[k] = (uint8_t)kept;
+    else static_cast<uint32_t*>(a.scales)[k] = kept;
+  };
+  auto scale_of = [&](uint32_t m) { return a.scale_e8m0 ? block_scale<true>(m) : block_scale<false>(m); };
 #pragma unroll
   for (int u = 0; u < V; ++u) {
     const unsigned g = u * blockDim.x + threadIdx.x;
-    float y[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = 0.0f;
+    uint32_t m = 0;
     if (g < groups) {
-      float w[8];
-      load_gain<WHOLE>(a.weight, a.weight_f32, g, cols, w);
+      if (!EARLY) gain(g, w[u]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = h[u][j] * r * w[j];
-      if (a.y) store_group<false, WHOLE>(a.y + at, g, cols, narrow(y));
+      for (int j = 0; j < 8; ++j) h[u][j] = h[u][j] * r * w[u][j];   // y from here on
+      if (a.y) store(a.y, g, narrow(h[u]));
     }
-    if (a.codes) {
-      uint32_t m = 0;
+    if (!a.codes) continue;
+    if constexpr (FORM != kRagged) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = max(m, finite_mag(h[u][j]));
+      const BlockScale s = scale_of(row16_max(m));
+      const uint64_t c = codes4_scaled(h[u], s.inv) | (uint64_t)codes4_scaled(h[u] + 4, s.inv) << 32;
+      if (g < groups) {
+        st8<NT>(reinterpret_cast<uint64_t*>(a.codes + row * a.codes_ld) + g, c);
+        if ((threadIdx.x & 15u) == 0) keep_scale(g >> 4, s.kept);
+      }
+    } else if (g < groups) {
+      const int e = (int)(8 * g) - off, split = AR_BLOCK - (e & (AR_BLOCK - 1));   // elements before the next block
+      uint32_t m2 = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (!mine(g, j)) continue;
+        const uint32_t f = finite_mag(h[u][j]);
+        if (e >= 0 && j < split) m = max(m, f);
+        else m2 = max(m2, f);
+      }
+      if (e >= 0) atomicMax(&top[e / AR_BLOCK], m);
+      if (e < 0) atomicMax(&top[0], m2);
+      else if (split < 8 && e + split < (int)cols) atomicMax(&top[e / AR_BLOCK + 1], m2);
+    }
+  }
+  if (FORM != kRagged || !a.codes) return;
+  __syncthreads();
+  for (unsigned i = threadIdx.x; i < (cols + AR_BLOCK - 1) / AR_BLOCK; i += blockDim.x) keep_scale(i, scale_of(top[i]).kept);
+#pragma unroll
+  for (int u = 0; u < V; ++u) {
+    const unsigned g = u * blockDim.x + threadIdx.x;
+    if (g >= groups) continue;
+    const int e = (int)(8 * g) - off, b0 = max(e, 0) / AR_BLOCK, b1 = min(e + 7, (int)cols - 1) / AR_BLOCK;
+    const float i0 = scale_of(top[b0]).inv, i1 = b1 == b0 ? i0 : scale_of(top[b1]).inv;
+    const uint64_t c0 = codes4_scaled(h[u], i0) | (uint64_t)codes4_scaled(h[u] + 4, i0) << 32;
+    const uint64_t c1 = codes4_scaled(h[u], i1) | (uint64_t)codes4_scaled(h[u] + 4, i1) << 32;
+    uint8_t* to = a.codes + row * a.codes_ld + e;
+    if (b0 == b1 && mine(g, 0) && mine(g, 7)) {
+      typedef uint32_t u32x2u __attribute__((ext_vector_type(2), aligned(1)));
+      *reinterpret_cast<u32x2u*>(to) = u32x2u{(uint32_t)c0, (uint32_t)(c0 >> 32)};
+    } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (WHOLE || 8 * g + j < cols) m = max(m, finite_mag(y[j]));
-      m = row16_max(m);
-      const BlockScale s = block_scale<E8M0>(m);
-      const uint32_t lo = codes4_scaled(y, s.inv), hi = codes4_scaled(y + 4, s.inv);
-      if (g < groups) {
-        uint8_t* c = a.codes + row * a.codes_ld + 8 * (size_t)g;
-        if (WHOLE || 8 * g + 8 <= cols) {
-          *reinterpret_cast<uint64_t*>(c) = (uint64_t)lo | ((uint64_t)hi << 32);
-        } else {
-#pragma unroll
-          for (unsigned j = 0; j < 8; ++j)
-            if (8 * g + j < cols) c[j] = (uint8_t)((j < 4 ? lo : hi) >> (8 * (j & 3)));
-        }
-        if ((threadIdx.x & 15u) == 0) {
-          const size_t k = row * a.scale_rs + (g >> 4) * a.scale_cs;
-          if constexpr (E8M0) static_cast<uint8_t*>(a.scales)[k] = (uint8_t)s.kept;
-          else static_cast<uint32_t*>(a.scales)[k] = s.kept;
-        }
-      }
+        if (mine(g, j)) to[j] = (uint8_t)(((e + j) / AR_BLOCK == b0 ? c0 : c1) >> (8 * j));
     }
   }
 }
@@ -185,104 +301,123 @@ __global__ __launch_bounds__(1024) void k_reduce_norm(InPtrs in, NormArgs a) {
 //   dx = dres + r (g - x mean(g x)),   dweight = sum over rows of dy x.
 // Workgroup b takes rows b, b + grid, ...; a lane keeps the sums of dy x of
 // its own columns in registers and writes them once, to row b of `partial`.
-template <int V, bool WHOLE>
-__global__ __launch_bounds__(1024) void k_norm_bwd(NormBwdArgs a) {
-  __shared__ float part[2][2][kMaxWaves];
+// A row costs two sums over the workgroup, so the next row's data are on
+// their way while this one's are summed (V = 8 has no registers for that).
+template <int V, int FORM>
+__global__ __launch_bounds__(V == 8 ? 1024 : 512) void k_norm_bwd(NormBwdArgs a) {
+  __shared__ __align__(16) float part[2][2][kMaxWaves];
   const unsigned cols = a.cols, groups = (cols + 7) / 8;
-  const int waves = blockDim.x / kWave;
-  float dw[V][8];
+  constexpr bool AHEAD = V < 8, WHOLE = FORM != kRagged, NT = FORM == kStream;
+  struct Row {
+    u32x4 h[V], dy[V], dres[V];
+  };
+  auto fetch = [&](size_t row, Row& x) {
+    const size_t at = row * cols;
 #pragma unroll
-  for (int u = 0; u < V; ++u)
+    for (int u = 0; u < V; ++u) {
+      const unsigned g = u * blockDim.x + threadIdx.x;
+      x.h[u] = x.dy[u] = x.dres[u] = u32x4{0u, 0u, 0u, 0u};
+      if (g >= groups) continue;
+      x.h[u] = load_group<NT, WHOLE>(a.h + at, g, cols);
+      x.dy[u] = load_group<NT, WHOLE>(a.dy + at, g, cols);
+      if (a.dres) x.dres[u] = load_group<NT, WHOLE>(a.dres + at, g, cols);
+    }
+  };
+  float dw[V][8], w[V][8];
+  Row now;
+  fetch(blockIdx.x, now);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dw[u][j] = 0.0f;
+  for (int u = 0; u < V; ++u) {
+    const unsigned g = u * blockDim.x + threadIdx.x;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[u][j] = w[u][j] = 0.0f;
+    if (g < groups) load_gain<WHOLE>(a.weight, a.weight_f32, g, cols, w[u]);
+  }
   int flip = 0;
   for (size_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
-    const size_t at = row * cols;
-    float h[V][8], dy[V][8], w[V][8];
+    Row next;
+    if (AHEAD) fetch(row + gridDim.x < a.rows ? row + gridDim.x : row, next);
     float ss = 0.0f, gh = 0.0f;
 #pragma unroll
     for (int u = 0; u < V; ++u) {
-      const unsigned g = u * blockDim.x + threadIdx.x;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) h[u][j] = dy[u][j] = w[u][j] = 0.0f;
-      if (g >= groups) continue;
-      widen(load_group<false, WHOLE>(a.h + at, g, cols), h[u]);
-      widen(load_group<false, WHOLE>(a.dy + at, g, cols), dy[u]);
-      load_gain<WHOLE>(a.weight, a.weight_f32, g, cols, w[u]);
+      float h[8], dy[8];
+      widen(now.h[u], h);
+      widen(now.dy[u], dy);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        ss = __builtin_fmaf(h[u][j], h[u][j], ss);
-        gh = __builtin_fmaf(dy[u][j] * w[u][j], h[u][j], gh);
+        ss = __builtin_fmaf(h[j], h[j], ss);
+        gh = __builtin_fmaf(dy[j] * w[u][j], h[j], gh);
       }
     }
-    ss = wave_sum(ss / (float)cols);
-    gh = wave_sum(gh / (float)cols);
     // two sets of slots in turn: a wave may write the next row's sums while
     // another still reads this row's, and is held at the next barrier before
     // it could write these slots again
-    if (lane_id() == 0) {
-      part[flip][0][threadIdx.x / kWave] = ss;
-      part[flip][1][threadIdx.x / kWave] = gh;
-    }
+    put_part(wave_sum(ss / (float)cols), part[flip][0]);
+    put_part(wave_sum(gh / (float)cols), part[flip][1]);
     __syncthreads();
-    ss = part[flip][0][0];
-    gh = part[flip][1][0];
-    for (int i = 1; i < waves; ++i) {
-      ss += part[flip][0][i];
-      gh += part[flip][1][i];
-    }
-    const float r = 1.0f / sqrtf(ss + a.eps);
-    const float m = r * gh;   // mean(g x)
+    const float r = 1.0f / sqrtf(sum_parts(part[flip][0]) + a.eps);
+    const float m = r * sum_parts(part[flip][1]);   // mean(g x)
 #pragma unroll
     for (int u = 0; u < V; ++u) {
       const unsigned g = u * blockDim.x + threadIdx.x;
-      if (g >= groups) continue;
-      float dx[8];
+      float h[8], dy[8], dx[8];
+      // widened again, not kept in twice the registers over the barrier
+      asm volatile("" : "+v"(now.h[u]), "+v"(now.dy[u]));
+      widen(now.h[u], h);
+      widen(now.dy[u], dy);
+      widen(now.dres[u], dx);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float x = h[u][j] * r;
-        dx[j] = r * (dy[u][j] * w[u][j] - x * m);
-        dw[u][j] = __builtin_fmaf(dy[u][j], x, dw[u][j]);
+        const float x = h[j] * r;
+        const float d = r * (dy[j] * w[u][j] - x * m);
+        dx[j] = a.dres ? d + dx[j] : d;
+        dw[u][j] = __builtin_fmaf(dy[j], x, dw[u][j]);
       }
-      if (a.dres) {
-        float f[8];
-        widen(load_group<false, WHOLE>(a.dres + at, g, cols), f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dx[j] += f[j];
-      }
-      if (a.dx) store_group<false, WHOLE>(a.dx + at, g, cols, narrow(dx));
+      if (a.dx && g < groups) store_group<NT, WHOLE>(a.dx + row * cols, g, cols, narrow(dx));
     }
+    if (AHEAD) now = next;
+    else if (row + gridDim.x < a.rows) fetch(row + gridDim.x, now);
   }
   if (!a.partial) return;
+  float* out = a.partial + (size_t)blockIdx.x * sum_stride(cols);
 #pragma unroll
   for (int u = 0; u < V; ++u) {
     const unsigned g = u * blockDim.x + threadIdx.x;
 #pragma unroll
     for (unsigned j = 0; j < 8; ++j)
-      if (8 * g + j < cols) a.partial[(size_t)blockIdx.x * cols + 8 * g + j] = dw[u][j];
+      if (WHOLE ? g < groups : 8 * g + j < cols) out[8 * g + j] = dw[u][j];
   }
 }
 
-// dweight[c] = sum of `n` rows of partial sums: 64 columns a workgroup, four
-// waves take a quarter of the rows each.
-__global__ __launch_bounds__(256) void k_sum_rows(const float* partial, float* out, unsigned n, unsigned cols) {
-  __shared__ float part[4][kWave];
-  const unsigned c = blockIdx.x * kWave + lane_id(), q = threadIdx.x / kWave;
-  float s = 0.0f;
-  if (c < cols)
-    for (unsigned i = q; i < n; i += 4) s += partial[(size_t)i * cols + c];
-  part[q][lane_id()] = s;
+// dweight[c] = sum of `n` rows of partial sums: a workgroup takes 64 columns,
+// four a lane, and each 16 lanes every 64th row.
+__global__ __launch_bounds__(1024) void k_sum_rows(const float* partial, float* out, unsigned n, unsigned cols) {
+  typedef float f32x4 __attribute__((ext_vector_type(4)));
+  __shared__ __align__(16) float part[64][64 + 4];
+  const unsigned c = (threadIdx.x % 16) * 4, q = threadIdx.x / 16, c0 = blockIdx.x * 64;
+  const size_t ld = sum_stride(cols);
+  f32x4 s = {0.f, 0.f, 0.f, 0.f};
+  if (c0 + c < cols) {
+    const float* p = partial + c0 + c;
+#pragma unroll 8
+    for (unsigned i = q; i < n; i += 64) s += *reinterpret_cast<const f32x4*>(p + i * ld);
+  }
+  *reinterpret_cast<f32x4*>(&part[q][c]) = s;
   __syncthreads();
-  if (q == 0 && c < cols) out[c] = (part[0][lane_id()] + part[1][lane_id()]) + (part[2][lane_id()] + part[3][lane_id()]);
+  if (threadIdx.x >= 64 || c0 + threadIdx.x >= cols) return;
+  float t = 0.0f;
+#pragma unroll 16
+  for (int i = 0; i < 64; ++i) t += part[i][threadIdx.x];
+  out[c0 + threadIdx.x] = t;
 }
 
-// Lanes and groups per lane for a row of `cols` elements.
+// Lanes and groups per lane for a row of at most `groups` groups: one group a
+// lane, or `v` where one gives a lane too few loads to wait for, doubled until
+// 1024 lanes hold the row.
 struct RowShape {
   int block, v;
 };
-RowShape row_shape(size_t cols) {
-  const size_t groups = cdiv(cols, 8);
-  int v = 1;
+RowShape row_shape(size_t groups, int v) {
   while (v < 8 && cdiv(groups, v) > 1024) v *= 2;
   return RowShape{(int)(cdiv(cdiv(groups, v), kWave) * kWave), v};
 }
@@ -293,21 +428,26 @@ dim3 row_grid(size_t rows) {
   return dim3((unsigned)x, (unsigned)cdiv(rows, x));
 }
 
+// Non-temporal accesses where a call moves more than the last-level cache
+// holds (256 MiB): 8 ranks, [16384 x 8192], fp8 result: 464 us, plain 526;
+// [1024 x 8192] 31.6, plain 28.9; [128 x 8192] 7.4, plain 5.9.
+constexpr size_t kStreamBytes = (size_t)256 << 20;
+
 template <int P, int V>
 hipError_t norm_pv(const Launch& L, const InPtrs& in, const NormArgs& a, int block) {
-  const bool whole = a.cols % 8 == 0;
   const dim3 grid = row_grid(a.rows), blk(block);
-  if (a.scale_e8m0) {
-    if (whole) return launch_k(k_reduce_norm<P, V, true, true>, grid, blk, 0, L.stream, in, a);
-    return launch_k(k_reduce_norm<P, V, false, true>, grid, blk, 0, L.stream, in, a);
-  }
-  if (whole) return launch_k(k_reduce_norm<P, V, true, false>, grid, blk, 0, L.stream, in, a);
-  return launch_k(k_reduce_norm<P, V, false, false>, grid, blk, 0, L.stream, in, a);
+  if (a.cols % 8) return launch_k(k_reduce_norm<P, V, kRagged>, grid, blk, 0, L.stream, in, a);
+  const size_t bytes = a.rows * a.cols * (2 * (P + (a.residual ? 1 : 0) + (a.res_out ? 1 : 0) + (a.y ? 1 : 0)) + (a.codes ? 1 : 0));
+  if (bytes > kStreamBytes) return launch_k(k_reduce_norm<P, V, kStream>, grid, blk, 0, L.stream, in, a);
+  return launch_k(k_reduce_norm<P, V, kWhole>, grid, blk, 0, L.stream, in, a);
 }
 
+// Two groups a lane for up to 3 contributions (1 rank, [16384 x 8192]: 168
+// us, with one 208; 3 ranks, [1001 x 5003]: 14.1 and 16.9), one for more (8
+// ranks, [16384 x 8192]: 464 us, with two 483; a single row 5.0 and 5.2).
 template <int P>
 hipError_t norm_p(const Launch& L, const InPtrs& in, const NormArgs& a) {
-  const RowShape s = row_shape(a.cols);
+  const RowShape s = row_shape((a.cols + (a.cols % 8 && a.cols <= kMaxShifted ? 14 : 7)) / 8, P < 4 ? 2 : 1);
   switch (s.v) {
     case 1: return norm_pv<P, 1>(L, in, a, s.block);
     case 2: return norm_pv<P, 2>(L, in, a, s.block);
@@ -318,8 +458,11 @@ hipError_t norm_p(const Launch& L, const InPtrs& in, const NormArgs& a) {
 
 template <int V>
 hipError_t bwd_v(const Launch& L, const NormBwdArgs& a, unsigned grid, int block) {
-  if (a.cols % 8 == 0) return launch_k(k_norm_bwd<V, true>, dim3(grid), dim3(block), 0, L.stream, a);
-  return launch_k(k_norm_bwd<V, false>, dim3(grid), dim3(block), 0, L.stream, a);
+  const dim3 g(grid), blk(block);
+  if (a.cols % 8) return launch_k(k_norm_bwd<V, kRagged>, g, blk, 0, L.stream, a);
+  const size_t bytes = a.rows * a.cols * 2 * (2 + (a.dres ? 1 : 0) + (a.dx ? 1 : 0));
+  if (bytes > kStreamBytes) return launch_k(k_norm_bwd<V, kStream>, g, blk, 0, L.stream, a);
+  return launch_k(k_norm_bwd<V, kWhole>, g, blk, 0, L.stream, a);
 }
 
 }  // namespace
@@ -338,11 +481,34 @@ hipError_t launch_reduce_norm(const Launch& L, const InPtrs& in, int P, const No
   }
 }
 
-unsigned norm_bwd_grid(size_t rows) { return (unsigned)(rows < 512 ? rows : 512); }
+namespace {
+
+// Four groups a lane (two or one for short rows) to have loads on their way;
+// 8 waves a CU, which the registers allow.
+RowShape bwd_shape(size_t cols) {
+  const size_t groups = cdiv(cols, 8);
+  int v = 1;
+  while (v < 4 && cdiv(groups, v) > kWave) v *= 2;
+  if (cdiv(groups, v) > 512) v = 8;
+  return RowShape{(int)(cdiv(cdiv(groups, v), kWave) * kWave), v};
+}
+
+// Four rows a workgroup at least, once there is one for each CU: each costs a
+// row of partial sums, written and read ([1000 x 4096]: 1000 workgroups 20.3
+// us, 256 18.1).  (Counted for 256 CUs, so that the order of the sums, and
+// the workspace, do not depend on the device.)
+size_t bwd_grid(size_t rows, size_t cols) {
+  const size_t most = 256 * std::max(1, 8 * kWave / bwd_shape(cols).block);
+  return std::min({rows, most, std::max<size_t>(256, rows / 4)});
+}
+
+}  // namespace
+
+size_t norm_bwd_sums(size_t rows, size_t cols) { return cols ? bwd_grid(rows, cols) * sum_stride(cols) : 0; }
 
 hipError_t launch_norm_bwd(const Launch& L, const NormBwdArgs& a, float* dweight) {
-  const RowShape s = row_shape(a.cols);
-  const unsigned grid = norm_bwd_grid(a.rows);
+  const RowShape s = bwd_shape(a.cols);
+  const unsigned grid = (unsigned)bwd_grid(a.rows, a.cols);
   hipError_t e = hipSuccess;
   if (grid) {
     switch (s.v) {
@@ -353,7 +519,7 @@ hipError_t launch_norm_bwd(const Launch& L, const NormBwdArgs& a, float* dweight
     }
   }
   if (e != hipSuccess || !dweight) return e;
-  return launch_k(k_sum_rows, dim3((unsigned)cdiv(a.cols, kWave)), dim3(256), 0, L.stream,
+  return launch_k(k_sum_rows, dim3((unsigned)cdiv(a.cols, 64)), dim3(1024), 0, L.stream,
                   static_cast<const float*>(a.partial), dweight, grid, a.cols);
 }
 

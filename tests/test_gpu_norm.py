@@ -220,7 +220,8 @@ def test_gradient_matches_formula(rows, cols, dres):
     # the row's two sums, of magnitudes mean h^2 and mean |g x|, each within 100 u
     size = r * (gg + np.abs(x) * (gg * np.abs(x)).mean(1, keepdims=True)) + (0 if dr is None else np.abs(dr))
     assert np.all(np.abs(vals(dx) - want) <= 220 * U * size + 1.01 * ref.U16 * np.abs(want) + 2.0 ** -133), "dx"
-    # a workgroup adds ceil(rows / 512) rows, then 128 partial sums and 2 more; each term within 110 u
+    # a workgroup adds its rows, then at most 64 partial sums of every 64th workgroup and those of 64 (fewer
+    # than the terms counted here for these sizes); each term within 110 u
     terms = -(-rows // 512) + 130 + 110
     assert np.all(np.abs(dwbuf[:cols].cpu().numpy() - wdw) <= terms * U * np.abs(dy64 * x).sum(0)), "dweight"
     assert untouched(xbuf, rows * cols) and bool((dwbuf[cols:] == 7).all())
