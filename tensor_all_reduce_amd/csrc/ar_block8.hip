@@ -25,7 +25,7 @@ __device__ __forceinline__ void put_scale(const QuantArgs& a, size_t r, size_t c
 // Lane t holds columns 8 (t % 16) .. + 7 of rows 8 (t / 16) .. + 7, as bf16:
 // widened for the maximum and again for the codes, since half the registers
 // let twice the workgroups wait for memory at once.
-template <bool SQUARE, bool TURN, bool E8M0>
+template <bool SQUARE, bool TURN, bool E8M0, bool NT>
 __global__ __launch_bounds__(256) void k_quant_block(QuantArgs a, unsigned tiles_c) {
   __shared__ uint32_t top[4][kTile];
   __shared__ __align__(16) uint8_t turned[TURN ? kTile * kTile : 16];
@@ -39,7 +39,8 @@ __global__ __launch_bounds__(256) void k_quant_block(QuantArgs a, unsigned tiles
     if (r0 + i < a.rows && c0 < a.cols) {
       const uint16_t* p = a.x + (r0 + i) * a.ldx + c0;
       if (c0 + 8 <= a.cols) {
-        v[i] = *reinterpret_cast<const u32x4u*>(p);
+        if constexpr (NT) v[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4u*>(p));
+        else v[i] = *reinterpret_cast<const u32x4u*>(p);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -152,12 +153,24 @@ __global__ __launch_bounds__(256) void k_quant_block(QuantArgs a, unsigned tiles
   }
 }
 
-template <bool SQUARE, bool TURN>
-hipError_t quant_st(const Launch& L, const QuantArgs& a, bool e8m0) {
+// Non-temporal loads of an x that the L2s of the 8 XCDs (32 MiB together)
+// cannot hold: of three [4097 x 8192] in turn, transposed, 23.7 us, plain
+// 26.2; of three [8192 x 8192] 36.0 and 41.7; the same [8192 x 8192] again and
+// again, which the last-level cache keeps, 36.0 and 33.4.  Plain stores: the
+// codes are short lines that meet in the L2 (non-temporal ones 35.9 and 37.2).
+constexpr size_t kColdBytes = (size_t)32 << 20;
+
+template <bool SQUARE, bool TURN, bool E8M0>
+hipError_t quant_f(const Launch& L, const QuantArgs& a) {
   const size_t tc = cdiv(a.cols, kTile), tr = cdiv(a.rows, kTile);
   const dim3 grid((unsigned)(tr * tc));
-  if (e8m0) return launch_k(k_quant_block<SQUARE, TURN, true>, grid, dim3(256), 0, L.stream, a, (unsigned)tc);
-  return launch_k(k_quant_block<SQUARE, TURN, false>, grid, dim3(256), 0, L.stream, a, (unsigned)tc);
+  auto k = a.rows * a.cols * 2 > kColdBytes ? k_quant_block<SQUARE, TURN, E8M0, true> : k_quant_block<SQUARE, TURN, E8M0, false>;
+  return launch_k(k, grid, dim3(256), 0, L.stream, a, (unsigned)tc);
+}
+
+template <bool SQUARE, bool TURN>
+hipError_t quant_st(const Launch& L, const QuantArgs& a, bool e8m0) {
+  return e8m0 ? quant_f<SQUARE, TURN, true>(L, a) : quant_f<SQUARE, TURN, false>(L, a);
 }
 
 }  // namespace
