@@ -43,6 +43,16 @@ __device__ __forceinline__ float e8m0_f32(uint8_t b) {
   return b == 255 ? __uint_as_float(0x7FC00000u) : __builtin_ldexpf(1.0f, (int)b - 127);
 }
 
+// Two results as bf16, nearest even by the conversion instruction; NaN as the
+// canonical 0x7FC0.
+__device__ __forceinline__ uint32_t results_bf16x2(float lo, float hi) {
+  typedef __bf16 b16x2 __attribute__((ext_vector_type(2)));
+  union { b16x2 b; uint32_t u; } r;
+  const float nan = __uint_as_float(0x7FC00000u);
+  r.b = b16x2{(__bf16)(__builtin_isnan(lo) ? nan : lo), (__bf16)(__builtin_isnan(hi) ? nan : hi)};
+  return r.u;
+}
+
 // Four consecutive results of a row from element `at` (column n).
 template <bool OUT32>
 __device__ __forceinline__ void store4(void* c, size_t at, unsigned n, unsigned N, bool aligned, f32x4 v) {
@@ -51,7 +61,7 @@ __device__ __forceinline__ void store4(void* c, size_t at, unsigned n, unsigned 
       *reinterpret_cast<f32x4*>(static_cast<float*>(c) + at) = v;
     } else {
       typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-      *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(c) + at) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+      *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(c) + at) = u32x2{results_bf16x2(v[0], v[1]), results_bf16x2(v[2], v[3])};
     }
     return;
   }
@@ -192,8 +202,8 @@ __device__ __forceinline__ bool join_parts(f32x4 (&v)[Q], uint32_t* counter, cha
 // blocks of the next follow those of one without a gap.  SPLIT: it has one
 // tile and a slice of K, `per` blocks of it, and the parts are joined.
 template <int BM, bool E8M0, bool BROWS, bool OUT32, bool SPLIT>
-__global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, unsigned tiles_n, int slices, unsigned per,
-                                                  uint32_t* counters, char* parts) {
+__global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, unsigned tiles_n, int problems, int slices,
+                                                  unsigned per, uint32_t* counters, char* parts) {
   constexpr int BN = 256, IT = 4, JT = BM / 32, R = 4;
   constexpr bool HW = E8M0 && !OUT32;        // scales applied by the matrix cores
   constexpr bool FOLD = E8M0 && OUT32;       // or as codes become bf16
@@ -204,7 +214,7 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
   // side by side: bytes (HW) or binary32 words
   __shared__ __align__(16) uint32_t ls[3][HW ? 128 : 512];
   __shared__ __align__(16) char lout[8][16 * 64 * kOut];  // 16 rows of a wave's results
-  const int z = SPLIT ? blockIdx.z / slices : blockIdx.z, slice = SPLIT ? blockIdx.z % slices : 0;
+  const int slice = SPLIT ? blockIdx.z % slices : 0;
   const int t = threadIdx.x, lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(t / kWave);
   const int lr = lane & 15, lq = lane >> 4;
@@ -213,23 +223,25 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
   const unsigned K = SPLIT ? min(g.K - kb0 * kBK, per * kBK) : g.K;
   const unsigned nk = (K + kBK - 1) / kBK;
   const unsigned whole = K / kBK;            // K blocks without a tail
-  const unsigned tiles = tiles_m * tiles_n;
+  const unsigned each_tiles = tiles_m * tiles_n, tiles = SPLIT ? each_tiles : each_tiles * (unsigned)problems;
 
   // XCD x (workgroups reach the 8 XCDs in turn) takes a contiguous run of
   // tiles, ordered in columns of 8 tiles along M, so that the tiles an XCD
   // works on at once share rows of a and of b in its L2
   struct Tile {
     unsigned m0, n0;
+    int z;                                   // problem
   };
   auto tile_at = [&](unsigned id) {
     if (id < (tiles & ~7u)) id = (id & 7u) * (tiles >> 3) + (id >> 3);
-    const unsigned per = 8 * tiles_n, band = id / per, in = id % per;
+    const unsigned z = SPLIT ? blockIdx.z / slices : id / each_tiles, one = SPLIT ? id : id % each_tiles;
+    const unsigned per = 8 * tiles_n, band = one / per, in = one % per;
     const unsigned bm = min(8u, tiles_m - band * 8);
     return Tile{(unsigned)__builtin_amdgcn_readfirstlane((int)((band * 8 + in % bm) * BM)),
-                (unsigned)__builtin_amdgcn_readfirstlane((int)(in / bm * BN))};
+                (unsigned)__builtin_amdgcn_readfirstlane((int)(in / bm * BN)), __builtin_amdgcn_readfirstlane((int)z)};
   };
-  auto a_rows = [&](Tile q) { return rows_buffer(g.a[z] + (size_t)q.m0 * g.lda + kb0 * kBK, g.M - q.m0, BM, g.lda, K); };
-  auto b_rows = [&](Tile q) { return rows_buffer(g.b[z] + (size_t)q.n0 * g.ldb + kb0 * kBK, g.N - q.n0, BN, g.ldb, K); };
+  auto a_rows = [&](Tile q) { return rows_buffer(g.a[q.z] + (size_t)q.m0 * g.lda + kb0 * kBK, g.M - q.m0, BM, g.lda, K); };
+  auto b_rows = [&](Tile q) { return rows_buffer(g.b[q.z] + (size_t)q.n0 * g.ldb + kb0 * kBK, g.N - q.n0, BN, g.ldb, K); };
 
   // a wave copies 8 rows at a time; chunk c of a row goes to position c ^ (row % 8)
   const unsigned crow = wave * 8 + (lane >> 3), ccol = ((lane & 7) ^ (lane >> 3)) * 16;
@@ -244,20 +256,20 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
 
   // this lane's scale: of row t of a, or of row t - BM of b
   const bool is_a = wave * kWave < BM;       // the same in a wave
-  const char* sbase = static_cast<const char*>(is_a ? g.sa[z] : g.sb[z]);
   const uint32_t srs = (uint32_t)(is_a ? g.sa_rs : g.sb_rs), scs = (uint32_t)(is_a ? g.sa_cs : g.sb_cs);
   const unsigned slast = (is_a ? g.M : g.N) - 1, slane = is_a ? t : t - BM;
   const int sput = ((t >> 6) * 16 + (t & 15)) * 4 + ((t >> 4) & 3);
   auto load_scale = [&](Tile q, unsigned k) -> uint32_t {
     unsigned row = min((is_a ? q.m0 : q.n0) + slane, slast);
     if (!BROWS && !is_a) row /= AR_BLOCK;
+    const void* sbase = is_a ? g.sa[q.z] : g.sb[q.z];
     const size_t i = (uint64_t)row * srs + (uint64_t)(kb0 + min(k, nk - 1)) * scs;
     if constexpr (E8M0) {
-      const uint8_t b = reinterpret_cast<const uint8_t*>(sbase)[i];
+      const uint8_t b = static_cast<const uint8_t*>(sbase)[i];
       if constexpr (HW) return b;
       else return __float_as_uint(e8m0_f32(b));
     } else {
-      return reinterpret_cast<const uint32_t*>(sbase)[i];
+      return static_cast<const uint32_t*>(sbase)[i];
     }
   };
   auto put_scale = [&](int r, uint32_t v) {
@@ -448,7 +460,7 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
         } else {
           typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
           *reinterpret_cast<u32x2*>(out + lr * kRow + ((i * 2 + (lq >> 1)) ^ (lr & 7)) * 16 + (lq & 1) * 8) =
-              u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+              u32x2{results_bf16x2(v[0], v[1]), results_bf16x2(v[2], v[3])};
         }
       }
       __builtin_amdgcn_wave_barrier();
@@ -458,7 +470,7 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
         const u32x4 v = *reinterpret_cast<const u32x4*>(out + row * kRow + ((lane % kLanes) ^ (row & 7)) * 16);
         const unsigned m = q.m0 + wm + j * 16 + row;
         if (m >= g.M) continue;
-        char* to = static_cast<char*>(g.c[z]) + (m * g.ldc + n) * kOut;
+        char* to = static_cast<char*>(g.c[q.z]) + (m * g.ldc + n) * kOut;
         if (vec) {
           st4<true>(reinterpret_cast<u32x4*>(to), v);   // streamed: the L2 keeps a and b
         } else {
@@ -511,7 +523,7 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
     if (whole < nk) step(whole, std::true_type{});
     if constexpr (SPLIT) {
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");   // LDS is free
-      const size_t tile = (size_t)z * tiles + id;
+      const size_t tile = (size_t)now.z * tiles + id;
       if (!join_parts(reinterpret_cast<f32x4(&)[IT * JT]>(acc), counters + tile, parts + tile * slices * (BM * BN * 4), slice,
                       slices, &ls[0][0]))
         return;
@@ -825,9 +837,9 @@ hipError_t gemm_tiles(const Launch& L, const GemmArgs& g, int G, const Plan& p, 
   uint32_t* counters = static_cast<uint32_t*>(ws);
   char* parts = static_cast<char*>(ws) + counter_bytes(p);
   const unsigned tm = (unsigned)cdiv(g.M, BM), tn = (unsigned)cdiv(g.N, 256);
-  const dim3 grid(SPLIT ? tm * tn : std::min(tm * tn, (unsigned)L.cus), 1, (unsigned)G * p.slices);
-  return launch_k(k_gemm_big<BM, E8M0, BROWS, OUT32, SPLIT>, grid, dim3(512), 0, L.stream, g, tm, tn, (int)p.slices, p.per,
-                  counters, parts);
+  const dim3 grid(SPLIT ? tm * tn : std::min(tm * tn * G, (unsigned)L.cus), 1, SPLIT ? (unsigned)G * p.slices : 1);
+  return launch_k(k_gemm_big<BM, E8M0, BROWS, OUT32, SPLIT>, grid, dim3(512), 0, L.stream, g, tm, tn, G, (int)p.slices,
+                  p.per, counters, parts);
 }
 
 template <bool E8M0, bool BROWS, bool OUT32>
