@@ -138,30 +138,31 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
 
-// Joins the parts of a result that workgroups have summed over slices of K.
-// A part holds each lane's accumulators, `Q` vectors, as the lanes have them.
-// The last workgroup to arrive adds all parts in slice order, so the result
-// does not depend on who was last.  Parts are written through the L2 of the
-// writer's XCD; the counter is zero again afterwards.  Returns whether this
-// workgroup has the result (in v).  `lds_word`: a word of LDS that is free.
+// Joins the parts of a result that waves of different workgroups have summed
+// over slices of K: a wave's part holds its lanes' accumulators, `Q` vectors,
+// as the lanes have them, and parts of one result are joined wave by wave, so
+// that no wave waits for its workgroup and the last ones to arrive, which do
+// the work, are spread over the device.  The last wave adds all parts in slice
+// order, so the result does not depend on which was last.  Parts are written
+// through the L2 of the writer's XCD; the counter is zero again afterwards.
+// Returns whether this wave has the result (in v).
 template <int Q>
-__device__ __forceinline__ bool join_parts(f32x4 (&v)[Q], uint32_t* counter, char* parts, int slice, int slices,
-                                           uint32_t* lds_word) {
-  const unsigned lanes = blockDim.x, bytes = Q * lanes * 16;
+__device__ __forceinline__ bool join_parts(f32x4 (&v)[Q], uint32_t* counter, char* parts, int slice, int slices) {
+  constexpr unsigned bytes = Q * kWave * 16;
   char* mine = parts + (size_t)slice * bytes;
 #pragma unroll
   for (int q = 0; q < Q; ++q) {
     union { f32x4 f; u32x4 u; } x;
     x.f = v[q];
-    st16<2>(mine, bytes, (q * lanes + threadIdx.x) * 16, x.u);
+    st16<2>(mine, bytes, (q * kWave + lane_id()) * 16, x.u);
   }
   __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
-  __syncthreads();
-  if (threadIdx.x == 0) *lds_word = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  __syncthreads();
-  if (*lds_word != (uint32_t)slices - 1) return false;
+  uint32_t before = 0;
+  if (lane_id() == 0) before = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  before = __builtin_amdgcn_readfirstlane((int)before);
+  if (before != (uint32_t)slices - 1) return false;
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-  if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (lane_id() == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   // 16 vectors at a time are on their way at once: read one after the other,
   // each would cost a trip to memory
   constexpr int QB = Q < 4 ? Q : 4, SB = 16 / QB;
@@ -178,7 +179,7 @@ __device__ __forceinline__ bool join_parts(f32x4 (&v)[Q], uint32_t* counter, cha
         for (int q = 0; q < QB; ++q) {
           x[b][q] = f32x4{0.f, 0.f, 0.f, 0.f};
           if (s + b < slices)
-            x[b][q] = *reinterpret_cast<const f32x4*>(parts + (size_t)(s + b) * bytes + ((q0 + q) * lanes + threadIdx.x) * 16);
+            x[b][q] = *reinterpret_cast<const f32x4*>(parts + (size_t)(s + b) * bytes + ((q0 + q) * kWave + lane_id()) * 16);
         }
 #pragma unroll
       for (int b = 0; b < SB; ++b)
@@ -522,12 +523,11 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
     for (unsigned k = 0; k < whole; ++k) step(k, std::false_type{});
     if (whole < nk) step(whole, std::true_type{});
     if constexpr (SPLIT) {
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");   // LDS is free
-      const size_t tile = (size_t)now.z * tiles + id;
-      if (!join_parts(reinterpret_cast<f32x4(&)[IT * JT]>(acc), counters + tile, parts + tile * slices * (BM * BN * 4), slice,
-                      slices, &ls[0][0]))
-        return;
-      store(now);
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no copy outlives the workgroup's LDS
+      const size_t w = ((size_t)now.z * tiles + id) * 8 + wave;
+      if (join_parts(reinterpret_cast<f32x4(&)[IT * JT]>(acc), counters + w, parts + w * slices * (IT * JT * kWave * 16), slice,
+                     slices))
+        store(now);
       return;
     }
     store(now);
@@ -655,8 +655,8 @@ __global__ __launch_bounds__(256) void k_gemm_few(GemmArgs g, int slices, unsign
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no copy outlives the workgroup's LDS
   if (slices > 1) {
-    const size_t tile = ((size_t)z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
-    if (!join_parts(acc, counters + tile, parts + tile * slices * (MT * 256 * 16), slice, slices, &lsb[0][0])) return;
+    const size_t w = (((size_t)z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x) * 4 + wave;
+    if (!join_parts(acc, counters + w, parts + w * slices * (MT * kWave * 16), slice, slices)) return;
   }
 #pragma unroll
   for (int j = 0; j < MT; ++j) {
@@ -800,7 +800,7 @@ bool few_rows(unsigned M, unsigned N, unsigned K, int G) {
   return tiles <= 192 || blocks_of(K) <= 2 || tiles * blocks_of(K) <= 8192;
 }
 
-size_t counter_bytes(const Plan& p) { return cdiv(p.tiles * 4, 256) * 256; }
+size_t counter_bytes(const Plan& p) { return cdiv(p.tiles * 8 * 4, 256) * 256; }  // at most 8 waves a tile
 size_t few_bytes(const Plan& p) {
   return p.slices > 1 ? counter_bytes(p) + p.tiles * p.slices * (p.mt * 256 * 16) : 0;
 }
