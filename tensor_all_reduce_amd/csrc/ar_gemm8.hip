@@ -543,14 +543,16 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
 
 // Few rows of a: 16 MT x 64 of C in four waves of 16 columns, K >= 1.  The
 // codes of b are read once and there is little to compute on them, so the
-// kernel is a copy engine: a ring of ST blocks in LDS, all but one of them on
-// their way, and three or four workgroups a CU (8 x 8192 x 1024 with one row:
-// 13.4 us with a ring of 3 and four workgroups, 17.3 with 5 and two).  blockIdx: columns, rows, problem and slice
+// kernel is a copy engine: a ring of groups of BG blocks in LDS, all but one of
+// them on their way, and two to four workgroups a CU.  A group costs a barrier
+// and a chain of latencies, so two blocks a group are faster (48 x 4096 x
+// 8192: 14.7 us, one 16.2; 1 x 1024 x 1024: 5.3, 7.0) unless there are four
+// workgroups a CU to hide it (1 row, 8 problems of 8192 x 1024: 14.1, 12.5).  blockIdx: columns, rows, problem and slice
 // of K (`per` blocks each).
 constexpr int kFewCols = 64, kFewBlocks = 16;  // columns; blocks whose scales are held at a time
-template <int MT, bool E8M0, bool BROWS, bool OUT32>
+template <int MT, int BG, bool E8M0, bool BROWS, bool OUT32>
 __global__ __launch_bounds__(256) void k_gemm_few(GemmArgs g, int slices, unsigned per, uint32_t* counters, char* parts) {
-  constexpr int BM = 16 * MT, ST = 3;
+  constexpr int BM = 16 * MT, NP = BG == 1 ? 3 : 2, ST = BG * NP;  // groups and blocks in the ring
   constexpr bool HW = E8M0 && !OUT32;
   constexpr int kCopies = 2 + MT / 2;        // of a wave and block
   __shared__ __align__(16) char ring[ST][(BM + kFewCols) * kBK];  // rows of a, then of b
@@ -594,7 +596,7 @@ __global__ __launch_bounds__(256) void k_gemm_few(GemmArgs g, int slices, unsign
     // no wave still uses the last round's blocks and scales
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 #pragma unroll
-    for (unsigned c = 0; c < ST - 1; ++c) copy(c < n ? base + c : kb1, c);
+    for (unsigned c = 0; c < ST - BG; ++c) copy(c < n ? base + c : kb1, c);
     for (unsigned i = t; i < n * BM; i += 256)
       lsa[i / BM][i % BM] = scale_at(g.sa[z], (size_t)min(m0 + i % BM, g.M - 1) * g.sa_rs + (size_t)(base + i / BM) * g.sa_cs);
     constexpr int BS = BROWS ? kFewCols : 1;
@@ -603,54 +605,70 @@ __global__ __launch_bounds__(256) void k_gemm_few(GemmArgs g, int slices, unsign
       lsb[i / BS][i % BS] = scale_at(g.sb[z], (size_t)(BROWS ? row : row / AR_BLOCK) * g.sb_rs + (size_t)(base + i / BS) * g.sb_cs);
     }
     unsigned buf = 0;
-    for (unsigned c = 0; c < n; ++c) {
-      // this wave's copies of the block have landed (those of the ST - 2
-      // blocks after it may be on their way), then every wave's
-      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((ST - 2) * kCopies) : "memory");
-      const unsigned free = buf == 0 ? ST - 1 : buf - 1;   // the block before: no wave reads it any more
-      copy(c + ST - 1 < n ? base + c + ST - 1 : kb1, free);
-      const unsigned kb = base + c;
-      const bool tail = (kb + 1) * kBK > g.K;
-      auto read = [&](int row, Frag& f) {
-        f.h[0] = *reinterpret_cast<const u32x4*>(ring[buf] + row * kBK + r0);
-        f.h[1] = *reinterpret_cast<const u32x4*>(ring[buf] + row * kBK + r1);
-        if (tail) {
-          f.h[0] = mask_chunk(f.h[0], kb * kBK + lq * 16, g.K);
-          f.h[1] = mask_chunk(f.h[1], kb * kBK + lq * 16 + 64, g.K);
-        }
-      };
-      Frag fa[MT], fb;
-      read(BM + wave * 16, fb);
+    for (unsigned c0 = 0; c0 < n; c0 += BG) {
+      // this wave's copies of the group have landed (those of the NP - 2
+      // groups after it may be on their way), then every wave's
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NP - 2) * BG * kCopies) : "memory");
+      const unsigned free = buf == 0 ? ST - BG : buf - BG;   // the group before: no wave reads it any more
 #pragma unroll
-      for (int j = 0; j < MT; ++j) read(j * 16, fa[j]);
-      if constexpr (HW) {
-        const uint32_t sb = lsb[c][BROWS ? wave * 16 + lr : 0];
+      for (unsigned h = 0; h < BG; ++h) {
+        const unsigned c = c0 + ST - BG + h;
+        copy(c < n ? base + c : kb1, free + h);
+      }
+      Frag fa[BG][MT], fb[BG];
 #pragma unroll
-        for (int j = 0; j < MT; ++j)
-          acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb.v, fa[j].v, acc[j], 0, 0, 0, (int)sb, 0,
-                                                                 (int)lsa[c][j * 16 + lr]);
-      } else {
-        float sb[4];
+      for (unsigned h = 0; h < BG; ++h) {
+        const unsigned kb = base + c0 + h;
+        auto read = [&](int row, Frag& f) {
+          f.h[0] = *reinterpret_cast<const u32x4*>(ring[buf + h] + row * kBK + r0);
+          f.h[1] = *reinterpret_cast<const u32x4*>(ring[buf + h] + row * kBK + r1);
+        };
+        read(BM + wave * 16, fb[h]);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) sb[r] = __uint_as_float(lsb[c][BROWS ? wave * 16 + lq * 4 + r : 0]);
-        Wide wb;
-        if constexpr (OUT32) wb = widen(fb);
+        for (int j = 0; j < MT; ++j) read(j * 16, fa[h][j]);
+        if ((kb + 1) * kBK > g.K) {
+          auto mask = [&](Frag& f) {
+            f.h[0] = mask_chunk(f.h[0], kb * kBK + lq * 16, g.K);
+            f.h[1] = mask_chunk(f.h[1], kb * kBK + lq * 16 + 64, g.K);
+          };
+          mask(fb[h]);
 #pragma unroll
-        for (int j = 0; j < MT; ++j) {
-          f32x4 p = {0.f, 0.f, 0.f, 0.f};
-          if constexpr (OUT32) {
-            const Wide wa = widen(fa[j]);
-#pragma unroll
-            for (int h = 0; h < 4; ++h) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb.p[h], wa.p[h], p, 0, 0, 0);
-          } else {
-            p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb.v, fa[j].v, p, 0, 0, 0, 0, 0, 0);
-          }
-          const float sa = __uint_as_float(lsa[c][j * 16 + lr]);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[j][r] = __builtin_fmaf(p[r], sa * sb[r], acc[j][r]);
+          for (int j = 0; j < MT; ++j) mask(fa[h][j]);
         }
       }
-      buf = buf + 1 == ST ? 0 : buf + 1;
+#pragma unroll
+      for (unsigned h = 0; h < BG; ++h) {
+        const unsigned c = c0 + h;
+        if (c >= n) break;
+        if constexpr (HW) {
+          const uint32_t sb = lsb[c][BROWS ? wave * 16 + lr : 0];
+#pragma unroll
+          for (int j = 0; j < MT; ++j)
+            acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[h].v, fa[h][j].v, acc[j], 0, 0, 0, (int)sb, 0,
+                                                                   (int)lsa[c][j * 16 + lr]);
+        } else {
+          float sb[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) sb[r] = __uint_as_float(lsb[c][BROWS ? wave * 16 + lq * 4 + r : 0]);
+          Wide wb;
+          if constexpr (OUT32) wb = widen(fb[h]);
+#pragma unroll
+          for (int j = 0; j < MT; ++j) {
+            f32x4 p = {0.f, 0.f, 0.f, 0.f};
+            if constexpr (OUT32) {
+              const Wide wa = widen(fa[h][j]);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb.p[q], wa.p[q], p, 0, 0, 0);
+            } else {
+              p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[h].v, fa[h][j].v, p, 0, 0, 0, 0, 0, 0);
+            }
+            const float sa = __uint_as_float(lsa[c][j * 16 + lr]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[j][r] = __builtin_fmaf(p[r], sa * sb[r], acc[j][r]);
+          }
+        }
+      }
+      buf = buf + BG == ST ? 0 : buf + BG;
     }
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no copy outlives the workgroup's LDS
@@ -815,7 +833,9 @@ hipError_t gemm_few(const Launch& L, const GemmArgs& g, int G, void* ws) {
   uint32_t* counters = static_cast<uint32_t*>(ws);
   char* parts = static_cast<char*>(ws) + counter_bytes(p);
   const dim3 grid((unsigned)cdiv(g.N, kFewCols), (unsigned)cdiv(g.M, 16 * p.mt), (unsigned)G * p.slices);
-  auto k = p.mt == 2 ? k_gemm_few<2, E8M0, BROWS, OUT32> : k_gemm_few<4, E8M0, BROWS, OUT32>;
+  const bool many = p.tiles * p.slices >= 4 * kPlanCus;
+  auto k = p.mt == 4 ? k_gemm_few<4, 2, E8M0, BROWS, OUT32>
+                     : many ? k_gemm_few<2, 1, E8M0, BROWS, OUT32> : k_gemm_few<2, 2, E8M0, BROWS, OUT32>;
   return launch_k(k, grid, dim3(256), 0, L.stream, g, (int)p.slices, p.per, counters, parts);
 }
 
