@@ -792,9 +792,10 @@ struct Plan {
 unsigned blocks_of(unsigned K) { return (K + kBK - 1) / kBK; }
 
 // 32 or 64 rows of a and 64 columns a workgroup; slices of at least 8 blocks
-// until there are two workgroups a CU.  A join costs about 4 us (parts out to
+// until there are two workgroups a CU.  A join costs 3 to 5 us (parts out to
 // memory, a counter, parts back), so more slices lose what they gain: 48 x
-// 4096 x 8192 takes 16.8 us in 8 slices, 19.2 in 4, 21.6 in 16.
+// 4096 x 8192 took 16.3 us in 8 slices, 21.0 in 16; 1 x 1024 x 8192 10.6 in 8
+// and 11.9 in 16.
 Plan plan_few(unsigned M, unsigned N, unsigned K, int G) {
   Plan p{};
   p.mt = M <= 32 ? 2 : 4;
@@ -806,16 +807,18 @@ Plan plan_few(unsigned M, unsigned N, unsigned K, int G) {
   return p;
 }
 
-// Which kernel: few rows up to 192 of its 64 x 64 tiles, and beyond while
-// tiles times blocks stay within 8192, where a workgroup's whole sum is
-// shorter than a join of large tiles; and for K up to 256, which the large
-// tiles' pipeline is too long for.  Either side, N x K with M rows: 8192 x
-// 8192, M 64: 23 us (large tiles 35), M 128: 38 (35); 8192 x 1024, M 256: 10
-// (17), M 768: 21 (17); 1024 x 8192, M 768: 29 (30), M 1024: 38 (33).
+// Which kernel: few rows up to 192 of its 64 x 64 tiles, and beyond while a
+// workgroup for each is resident at once (1024) and tiles times blocks stay
+// within 16384, where large tiles, cut into slices, lose to their join; and
+// for K up to 256, which the large tiles' pipeline is too long for.  Either
+// side, us, few rows first: N 8192, K 8192: M 64 21 and 32, M 128 30 and 33,
+// M 192 40 and 35; N 8192, K 1024: M 256 8 and 17, M 512 14 and 17, M 768 20
+// and 17; N 1024, K 8192: M 512 18 and 25, M 1024 30 and 30; N 4096, K 4096:
+// M 512 22 and 27, M 768 35 and 32.
 bool few_rows(unsigned M, unsigned N, unsigned K, int G) {
   const size_t tiles = cdiv(M, 64) * cdiv(N, kFewCols) * G;
   if (cdiv(M, 32) > 65535) return false;     // a launch's second axis
-  return tiles <= 192 || blocks_of(K) <= 2 || tiles * blocks_of(K) <= 8192;
+  return tiles <= 192 || blocks_of(K) <= 2 || (tiles <= 1024 && tiles * blocks_of(K) <= 16384);
 }
 
 size_t counter_bytes(const Plan& p) { return cdiv(p.tiles * 8 * 4, 256) * 256; }  // at most 8 waves a tile
