@@ -335,8 +335,8 @@ __global__ __launch_bounds__(V == 8 ? 1024 : 512) void k_norm_bwd(NormBwdArgs a)
   }
   int flip = 0;
   for (size_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
-    Row next;
-    if (AHEAD) fetch(row + gridDim.x < a.rows ? row + gridDim.x : row, next);
+    Row next = now;
+    if (AHEAD && row + gridDim.x < a.rows) fetch(row + gridDim.x, next);
     float ss = 0.0f, gh = 0.0f;
 #pragma unroll
     for (int u = 0; u < V; ++u) {
