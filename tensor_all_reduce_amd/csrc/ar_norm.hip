@@ -483,12 +483,13 @@ hipError_t launch_reduce_norm(const Launch& L, const InPtrs& in, int P, const No
 
 namespace {
 
-// Four groups a lane (two or one for short rows) to have loads on their way;
-// 8 waves a CU, which the registers allow.
+// Two groups a lane up to 256 lanes a row (one in a single wave), four beyond,
+// to have loads on their way; 8 waves a CU, which the registers allow
+// ([1000 x 4096]: two groups 14.0 us, four 17.3; [16384 x 4096] 95 and 103;
+// [4096 x 5003] in 320 lanes of two 72, in 192 of four 56).
 RowShape bwd_shape(size_t cols) {
   const size_t groups = cdiv(cols, 8);
-  int v = 1;
-  while (v < 4 && cdiv(groups, v) > kWave) v *= 2;
+  int v = groups <= kWave ? 1 : cdiv(groups, 2) <= 256 ? 2 : 4;
   if (cdiv(groups, v) > 512) v = 8;
   return RowShape{(int)(cdiv(cdiv(groups, v), kWave) * kWave), v};
 }
