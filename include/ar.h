@@ -424,8 +424,8 @@ int ar_reduce_fp8(const uint8_t* const* codes, const uint8_t* const* scales, int
  * value(codes[i*ld + j]) * scale(i / block_rows, j / 128).
  *   codes      device pointer, 16-byte aligned
  *   ld         bytes from row to row: at least cols, a multiple of 16.  Bytes
- *              of a row after its cols-th are never read as values and never
- *              written.
+ *              of a row after its cols-th never count and are never written
+ *              (the aligned 16 that hold a row's last code are read whole).
  *   scales     device pointer, naturally aligned; the scale of block (i, j)
  *              is element i*scale_rs + j*scale_cs.  Of an output no two
  *              blocks may share an element.
@@ -520,7 +520,8 @@ int ar_quantize_block(const void* x, size_t ldx, size_t rows, size_t cols, const
  *             AR_FMT_F32, row m at c + m * ldc (elements), ldc >= N
  *   G         1..AR_MAX_RANKS
  *   workspace device memory, 16-byte aligned, zero before its first use; a
- *             call leaves its counters zero again.  With at least
+ *             call leaves its counters zero again, and calls of different
+ *             shapes may use one workspace in turn.  With at least
  *             ar_gemm_fp8_workspace(M, N, K, G) bytes, products with few
  *             rows and columns are split along K over the device; with less, or
  *             NULL, they are not.  Calls that overlap in time must not share

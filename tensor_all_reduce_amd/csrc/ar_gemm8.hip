@@ -821,9 +821,14 @@ bool few_rows(unsigned M, unsigned N, unsigned K, int G) {
   return tiles <= 192 || blocks_of(K) <= 2 || (tiles <= 1024 && tiles * blocks_of(K) <= 16384);
 }
 
-size_t counter_bytes(const Plan& p) { return cdiv(p.tiles * 8 * 4, 256) * 256; }  // at most 8 waves a tile
+// The counters' part of a workspace, the same for every shape, so that one
+// workspace serves products of all shapes in turn: 1024 counters, a wave each.
+// Cut into slices are at most 256 tiles of four waves or 128 of eight.
+constexpr size_t kCounterBytes = 1024 * 4;
+static_assert(kPlanCus <= 256, "counters for every wave of a product in slices");
+
 size_t few_bytes(const Plan& p) {
-  return p.slices > 1 ? counter_bytes(p) + p.tiles * p.slices * (p.mt * 256 * 16) : 0;
+  return p.slices > 1 ? kCounterBytes + p.tiles * p.slices * (p.mt * 256 * 16) : 0;
 }
 
 template <bool E8M0, bool BROWS, bool OUT32>
@@ -834,7 +839,7 @@ hipError_t gemm_few(const Launch& L, const GemmArgs& g, int G, void* ws) {
     p.per = blocks_of(g.K);
   }
   uint32_t* counters = static_cast<uint32_t*>(ws);
-  char* parts = static_cast<char*>(ws) + counter_bytes(p);
+  char* parts = static_cast<char*>(ws) + kCounterBytes;
   const dim3 grid((unsigned)cdiv(g.N, kFewCols), (unsigned)cdiv(g.M, 16 * p.mt), (unsigned)G * p.slices);
   const bool many = p.tiles * p.slices >= 4 * kPlanCus;
   auto k = p.mt == 4 ? k_gemm_few<4, 2, E8M0, BROWS, OUT32>
@@ -853,12 +858,12 @@ Plan plan_big(unsigned M, unsigned N, unsigned K, int G) {
   p.slices = (unsigned)cdiv(nk, p.per);
   return p;
 }
-size_t big_bytes(const Plan& p) { return p.slices > 1 ? counter_bytes(p) + p.tiles * p.slices * (128 * 256 * 4) : 0; }
+size_t big_bytes(const Plan& p) { return p.slices > 1 ? kCounterBytes + p.tiles * p.slices * (128 * 256 * 4) : 0; }
 
 template <int BM, bool E8M0, bool BROWS, bool OUT32, bool SPLIT>
 hipError_t gemm_tiles(const Launch& L, const GemmArgs& g, int G, const Plan& p, void* ws) {
   uint32_t* counters = static_cast<uint32_t*>(ws);
-  char* parts = static_cast<char*>(ws) + counter_bytes(p);
+  char* parts = static_cast<char*>(ws) + kCounterBytes;
   const unsigned tm = (unsigned)cdiv(g.M, BM), tn = (unsigned)cdiv(g.N, 256);
   const dim3 grid(SPLIT ? tm * tn : std::min(tm * tn * G, (unsigned)L.cus), 1, SPLIT ? (unsigned)G * p.slices : 1);
   return launch_k(k_gemm_big<BM, E8M0, BROWS, OUT32, SPLIT>, grid, dim3(512), 0, L.stream, g, tm, tn, G, (int)p.slices,

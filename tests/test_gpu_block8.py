@@ -319,3 +319,51 @@ def test_product_of_short_rows(M, N, K):
     for f32 in (True, False):
         got, = run([A], [B], 128, M, N, K, f32, 1, True)
         assert np.array_equal(got, want if f32 else ref.as_bf16(want))
+
+
+def test_one_workspace_for_products_of_different_shapes():
+    """Calls in stream order may share a workspace whatever their shapes: the
+    counters of one do not lie where another kept its parts."""
+    g = np.random.default_rng(41)
+    shapes = [(1, 128, 8192), (1, 8192, 8192), (40, 1000, 4096), (128, 8192, 8320), (1, 8192, 8192), (128, 8192, 8320)]
+    ws = torch.zeros(max(tar.gemm_fp8_workspace(*s) for s in shapes), dtype=torch.uint8, device=DEV)
+    todo = []
+    for M, N, K in shapes:
+        A, B = int_codes(g, M, K), int_codes(g, N, K)
+        one = lambda r: np.ones((r, K // 128), dtype=np.float32)    # noqa: E731
+        a, b = put(A, one(M)), put(B, one(-(-N // 128)))
+        todo.append((a, b, torch.full((M, N), 9.0, device=DEV), ref.E4M3[A].astype(np.float32) @ ref.E4M3[B].astype(np.float32).T))
+    note("one workspace, several shapes")
+    for _ in range(2):
+        for a, b, out, _w in todo:
+            tar.ar_gemm_fp8([a[0]], [a[1]], [b[0]], [b[1]], [out], workspace=ws)
+    torch.cuda.synchronize()
+    for i, (_a, _b, out, want) in enumerate(todo):
+        assert np.array_equal(out.cpu().numpy(), want), f"product {i}: {shapes[i]}"
+
+
+@pytest.mark.parametrize("e8m0", FMT)
+def test_product_with_a_short_last_slice(e8m0):
+    """65 blocks in slices of 9: the last has two, one of them with a tail."""
+    M, N, K = 128, 8192, 8300
+    g = np.random.default_rng(43)
+    k = [g.integers(-1, 2, size=(r, 65)) for r in (M, N // 128)]
+    s = [(v + 127).astype(np.uint8) if e8m0 else (2.0 ** v).astype(np.float32) for v in k]
+    A, B = (int_codes(g, M, K), s[0]), (int_codes(g, N, K), s[1])
+    want = ref.dequantise(*A, 1).astype(np.float32) @ ref.dequantise(*B, 128).astype(np.float32).T
+    note("product with a short last slice")
+    for f32 in (True, False):
+        got, = run([A], [B], 128, M, N, K, f32, 0, True)
+        assert np.array_equal(got, want if f32 else ref.as_bf16(want))
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 50, 300), (300, 4200, 700)])
+@pytest.mark.parametrize("f32", [False, True])
+def test_nan_scale_byte(M, N, K, f32):
+    g = np.random.default_rng(47)
+    A, B = int_codes(g, M, K), int_codes(g, N, K)
+    nb = -(-K // 128)
+    sa, sb = np.full((M, nb), 127, dtype=np.uint8), np.full((-(-N // 128), nb), 127, dtype=np.uint8)
+    sa[1, nb - 1] = 255
+    got, = run([(A, sa)], [(B, sb)], 128, M, N, K, f32, 0, True)
+    assert np.all(np.isnan(got[1])) and np.all(np.isfinite(got[0])) and np.all(np.isfinite(got[2:]))
