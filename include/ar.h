@@ -439,6 +439,10 @@ int ar_reduce_fp8(const uint8_t* const* codes, const uint8_t* const* scales, int
  *         x * 2^-k (exact),
  * each the nearest code (ties to even), 0x7F for a NaN or infinite element.
  * A matrix without rows or columns may have NULL pointers.
+ *
+ * The rank sum of ar_reduce_norm follows the convention above.  Row
+ * statistics, gradients and products also use fused multiply-adds, and their
+ * sums an order fixed by the sizes.
  */
 #define AR_BLOCK 128
 #define AR_SCALE_F32 0
@@ -510,8 +514,12 @@ int ar_quantize_block(const void* x, size_t ldx, size_t rows, size_t cols, const
  * of G ranks), in one call:
  *   C_g[m,n] = sum over blocks j of 128 along K of
  *              sa(m,j) * sb(n,j) * sum over k in block j of a[m,k] * b[n,k]
- * products and sums in binary32 (matrix cores), the result rounded once to
- * bf16 or kept.  Row-major a [M x K] with block_rows 1 (activations), b
+ * on the matrix cores, the result rounded once to bf16 or kept in binary32.
+ * Sums are binary32; within a block of a bf16 result the fp8 matrix
+ * instructions drop the low bits of terms far below the largest (about 2e-5
+ * of the result's size); a binary32 result takes the codes as bf16 instead
+ * and keeps binary32's precision, with E8M0 scales from 2^-117 to 2^118 (the
+ * scaled codes are bf16 values).  Row-major a [M x K] with block_rows 1 (activations), b
  * [N x K] with block_rows 128 (weights) or 1.
  *   a, b      host arrays of G matrices; ld, strides, scale_fmt and
  *             block_rows are the same for all of a, and for all of b, and

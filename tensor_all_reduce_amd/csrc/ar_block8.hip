@@ -3,7 +3,10 @@
 //
 // One 256-lane workgroup takes a 128 x 128 tile of x, which holds whole
 // blocks of every form, so each element is read once and its scale is known
-// before it is written.
+// before it is written.  Bound by memory: three bytes an element, [8192 x
+// 8192] in 128 x 128 blocks 36 us from memory (5.5 TB/s) and 33 from the
+// last-level cache, [4097 x 8192] transposed 23.8 us (4.2 TB/s; 2112 tiles
+// are a little more than the device holds at once).
 #include "ar_device.hpp"
 #include "ar_e4m3.hpp"
 #include "ar_internal.hpp"

@@ -2,6 +2,19 @@
 //   C[m,n] = sum over blocks j of  sa[m,j] * sb[n,j] * sum over k in j of a[m,k] b[n,k]
 // (sb of a row of b, or of 128 rows), accumulated in binary32, one rounding
 // to bf16 or none.
+//
+// A block of 128 is one matrix instruction deep (16 x 16 x 128), so scales
+// meet the products at its boundary:
+// - E8M0 scales are operands of the instruction and cost nothing;
+// - binary32 scales: the product of a block starts from zero and is scaled
+//   and added to the sum by four fused multiply-adds a lane, which run beside
+//   the next instructions of the matrix cores (alone, random operands: 4.2
+//   PFLOP/s, with the four 3.6);
+// - a binary32 result takes its products as bf16.  The fp8 instructions drop
+//   the low bits of terms far below the largest of their sum: 1.2e-5 to
+//   2.6e-5 of the result's size, far below bf16's rounding of 1.7e-3 but not
+//   below binary32's.  bf16 holds every code exactly, its products reach 1e-7
+//   at half the rate.
 #include "ar_device.hpp"
 #include "ar_internal.hpp"
 
@@ -202,6 +215,16 @@ __device__ __forceinline__ bool join_parts(f32x4 (&v)[Q], uint32_t* counter, cha
 // into the buffer of block k.  A workgroup takes tile after tile, and the
 // blocks of the next follow those of one without a gap.  SPLIT: it has one
 // tile and a slice of K, `per` blocks of it, and the parts are joined.
+//
+// Why this shape: 256 x 256 is the largest tile whose sums leave registers
+// for the fragments, two waves a SIMD, and whose two blocks fit LDS; each
+// byte copied serves 256 products.  b through registers straight from memory
+// was slower (a fragment's lanes are 16 rows apart in memory, and the vector
+// cache serves 16 bytes an access: 1446 us where this took 959).  Measured,
+// 16384 x 8192 x 8192: E8M0 820-890 us (2.5-2.7 PFLOP/s), binary32 scales
+// 890-940 (2.3-2.5); the same without its copies 700 and 782, with copies
+// that always hit the L2 785 and 882: what is left is the trip of each
+// block's first reader beyond the L2, for which there is no third buffer.
 template <int BM, bool E8M0, bool BROWS, bool OUT32, bool SPLIT>
 __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, unsigned tiles_n, int problems, int slices,
                                                   unsigned per, uint32_t* counters, char* parts) {
@@ -839,7 +862,7 @@ hipError_t gemm_few(const Launch& L, const GemmArgs& g, int G, void* ws) {
     p.per = blocks_of(g.K);
   }
   uint32_t* counters = static_cast<uint32_t*>(ws);
-  char* parts = static_cast<char*>(ws) + kCounterBytes;
+  char* parts = ws ? static_cast<char*>(ws) + kCounterBytes : nullptr;
   const dim3 grid((unsigned)cdiv(g.N, kFewCols), (unsigned)cdiv(g.M, 16 * p.mt), (unsigned)G * p.slices);
   const bool many = p.tiles * p.slices >= 4 * kPlanCus;
   auto k = p.mt == 4 ? k_gemm_few<4, 2, E8M0, BROWS, OUT32>
@@ -863,7 +886,7 @@ size_t big_bytes(const Plan& p) { return p.slices > 1 ? kCounterBytes + p.tiles 
 template <int BM, bool E8M0, bool BROWS, bool OUT32, bool SPLIT>
 hipError_t gemm_tiles(const Launch& L, const GemmArgs& g, int G, const Plan& p, void* ws) {
   uint32_t* counters = static_cast<uint32_t*>(ws);
-  char* parts = static_cast<char*>(ws) + kCounterBytes;
+  char* parts = ws ? static_cast<char*>(ws) + kCounterBytes : nullptr;
   const unsigned tm = (unsigned)cdiv(g.M, BM), tn = (unsigned)cdiv(g.N, 256);
   const dim3 grid(SPLIT ? tm * tn : std::min(tm * tn * G, (unsigned)L.cus), 1, SPLIT ? (unsigned)G * p.slices : 1);
   return launch_k(k_gemm_big<BM, E8M0, BROWS, OUT32, SPLIT>, grid, dim3(512), 0, L.stream, g, tm, tn, G, (int)p.slices,
