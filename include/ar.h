@@ -525,7 +525,8 @@ int ar_quantize_block(const void* x, size_t ldx, size_t rows, size_t cols, const
  *             block_rows are the same for all of a, and for all of b, and
  *             scale_fmt is the same for both
  *   c         host array of G device pointers, [M x N], out_fmt AR_FMT_BF16 or
- *             AR_FMT_F32, row m at c + m * ldc (elements), ldc >= N
+ *             AR_FMT_F32, row m at c + m * ldc (elements), ldc >= N; results
+ *             may lie side by side in one larger matrix
  *   G         1..AR_MAX_RANKS
  *   workspace device memory, 16-byte aligned, zero before its first use; a
  *             call leaves its counters zero again, and calls of different

@@ -302,6 +302,14 @@ int check_matrix(const ar_fp8_matrix& q, size_t rows, size_t cols, bool output, 
   return AR_OK;
 }
 
+// Whether two matrices of one shape and stride lie side by side (columns of
+// one larger matrix): their spans overlap, their elements do not.
+bool side_by_side(const void* p, const void* q, size_t pitch, size_t width) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  const size_t d = (a < b ? b - a : a - b) % pitch;
+  return d >= width && pitch - d >= width;
+}
+
 bool eps_ok(float eps) { return eps >= 0.0f && eps <= 3.402823466e38f; }
 
 int check_gain(const void* weight, int fmt, size_t cols, Span* s) {
@@ -840,7 +848,8 @@ int ar_gemm_fp8(const ar_fp8_matrix* a, const ar_fp8_matrix* b, void* const* c, 
   if (need) so[no++] = span_of(workspace, need);
   for (int o = 0; o < no; ++o) {
     if ((rc = check_disjoint(so[o], si, ni))) return rc;
-    if ((rc = check_disjoint(so[o], so + o + 1, no - o - 1))) return rc;
+    for (int q = o + 1; q < no; ++q)
+      if (overlap(so[o], so[q]) && !(q < G && side_by_side(c[o], c[q], ldc * es, N * es))) return AR_ERR_ALIAS;
   }
   g.lda = a[0].ld;
   g.ldb = b[0].ld;

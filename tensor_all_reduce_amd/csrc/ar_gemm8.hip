@@ -169,7 +169,7 @@ __device__ __forceinline__ bool join_parts(f32x4 (&v)[Q], uint32_t* counter, cha
     x.f = v[q];
     st16<2>(mine, bytes, (q * kWave + lane_id()) * 16, x.u);
   }
-  __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the part is out
   uint32_t before = 0;
   if (lane_id() == 0) before = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   before = __builtin_amdgcn_readfirstlane((int)before);

@@ -108,7 +108,8 @@ def test_product_refusals():
     assert gemm(a=[mat(A, 192, B, 1, 4)]) == INV and gemm(a=[mat(A, 200, B, 1, 4)]) == ALIGN
     assert gemm(a=[mat(A + 8, 256, B, 1, 4)]) == ALIGN and gemm(b=[mat(D, 256, E + 2, 1, 1, br=128)]) == ALIGN
     assert gemm(c=(A,)) == ALIAS and gemm(c=(E,)) == ALIAS
-    assert gemm(G=2, c=(C, C + 16)) == ALIAS
+    assert gemm(G=2, c=(C, C + 16)) == ALIAS and gemm(G=2, c=(C, C + 16), ldc=96) == ALIAS
+    assert gemm(G=2, c=(C, C + 192 - 16), ldc=96) == ALIAS               # 16 bytes short of the next row
     assert gemm(M=0) == OK and gemm(N=0) == OK
     assert tar.gemm_fp8_workspace(0, 5, 5) == 0 and tar.gemm_fp8_workspace(5, 5, 5, 9) == 0
 

@@ -367,3 +367,18 @@ def test_nan_scale_byte(M, N, K, f32):
     sa[1, nb - 1] = 255
     got, = run([(A, sa)], [(B, sb)], 128, M, N, K, f32, 0, True)
     assert np.all(np.isnan(got[1])) and np.all(np.isfinite(got[0])) and np.all(np.isfinite(got[2:]))
+
+
+@pytest.mark.parametrize("M,f32", [(3, True), (150, False), (400, False)])
+def test_results_side_by_side(M, f32):
+    """Two problems write the two halves of one matrix."""
+    N, K = 264, 700
+    g = np.random.default_rng(53)
+    A, B = [int_codes(g, M, K) for _ in range(2)], [int_codes(g, N, K) for _ in range(2)]
+    one = lambda r: np.ones((r, 6), dtype=np.float32)    # noqa: E731
+    a, b = [put(x, one(M)) for x in A], [put(x, one(3)) for x in B]
+    whole = torch.full((M, 2 * N), 9.0, dtype=torch.float32 if f32 else torch.bfloat16, device=DEV)
+    tar.ar_gemm_fp8([v[0] for v in a], [v[1] for v in a], [v[0] for v in b], [v[1] for v in b], [whole[:, :N], whole[:, N:]])
+    torch.cuda.synchronize()
+    want = np.concatenate([ref.E4M3[x] @ ref.E4M3[y].T for x, y in zip(A, B)], 1)
+    assert np.array_equal(whole.float().cpu().numpy(), want.astype(np.float32) if f32 else ref.as_bf16(want))
