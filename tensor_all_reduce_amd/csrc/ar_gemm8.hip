@@ -245,7 +245,11 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
   const int wm = (wave & 1) * (BM / 2), wn = (wave >> 1) * 64;
   const unsigned kb0 = SPLIT ? slice * per : 0;  // first block
   const unsigned K = SPLIT ? min(g.K - kb0 * kBK, per * kBK) : g.K;
-  const unsigned nk = (K + kBK - 1) / kBK;
+  const unsigned real = (K + kBK - 1) / kBK;
+  // 128-row tiles take any K: copies and scales run three blocks ahead, and
+  // blocks past K are masked (256-row tiles have no register for that: K > 256)
+  constexpr bool SHORT = BM == 128 && !SPLIT;
+  const unsigned nk = SHORT ? max(real, 3u) : real;
   const unsigned whole = K / kBK;            // K blocks without a tail
   const unsigned each_tiles = tiles_m * tiles_n, tiles = SPLIT ? each_tiles : each_tiles * (unsigned)problems;
 
@@ -287,7 +291,7 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
     unsigned row = min((is_a ? q.m0 : q.n0) + slane, slast);
     if (!BROWS && !is_a) row /= AR_BLOCK;
     const void* sbase = is_a ? g.sa[q.z] : g.sb[q.z];
-    const size_t i = (uint64_t)row * srs + (uint64_t)(kb0 + min(k, nk - 1)) * scs;
+    const size_t i = (uint64_t)row * srs + (uint64_t)(kb0 + min(k, real - 1)) * scs;
     if constexpr (E8M0) {
       const uint8_t b = static_cast<const uint8_t*>(sbase)[i];
       if constexpr (HW) return b;
@@ -544,7 +548,11 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
 #pragma unroll
       for (int j = 0; j < JT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     for (unsigned k = 0; k < whole; ++k) step(k, std::false_type{});
-    if (whole < nk) step(whole, std::true_type{});
+    if constexpr (SHORT) {
+      for (unsigned k = whole; k < nk; ++k) step(k, std::true_type{});
+    } else {
+      if (whole < nk) step(whole, std::true_type{});
+    }
     if constexpr (SPLIT) {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no copy outlives the workgroup's LDS
       const size_t w = ((size_t)now.z * tiles + id) * 8 + wave;
@@ -832,8 +840,7 @@ Plan plan_few(unsigned M, unsigned N, unsigned K, int G) {
 
 // Which kernel: few rows up to 192 of its 64 x 64 tiles, and beyond while a
 // workgroup for each is resident at once (1024) and tiles times blocks stay
-// within 16384, where large tiles, cut into slices, lose to their join; and
-// for K up to 256, which the large tiles' pipeline is too long for.  Either
+// within 16384, where large tiles, cut into slices, lose to their join.  Either
 // side, us, few rows first: N 8192, K 8192: M 64 21 and 32, M 128 30 and 33,
 // M 192 40 and 35; N 8192, K 1024: M 256 8 and 17, M 512 14 and 17, M 768 20
 // and 17; N 1024, K 8192: M 512 18 and 25, M 1024 30 and 30; N 4096, K 4096:
@@ -841,7 +848,7 @@ Plan plan_few(unsigned M, unsigned N, unsigned K, int G) {
 bool few_rows(unsigned M, unsigned N, unsigned K, int G) {
   const size_t tiles = cdiv(M, 64) * cdiv(N, kFewCols) * G;
   if (cdiv(M, 32) > 65535) return false;     // a launch's second axis
-  return tiles <= 192 || blocks_of(K) <= 2 || (tiles <= 1024 && tiles * blocks_of(K) <= 16384);
+  return tiles <= 192 || (tiles <= 1024 && tiles * blocks_of(K) <= 16384);
 }
 
 // The counters' part of a workspace, the same for every shape, so that one
@@ -900,9 +907,9 @@ hipError_t gemm_big(const Launch& L, const GemmArgs& g, int G, void* ws) {
   p.slices = 1;
   p.per = blocks_of(g.K);
   // 256 rows a tile unless registers do not hold it (products as bf16, a
-  // binary32 scale for each row of b) or it leaves CUs without one
+  // binary32 scale for each row of b), it leaves CUs without one, or K is short
   if constexpr (!OUT32 && (E8M0 || !BROWS))
-    if (cdiv(g.M, 256) * cdiv(g.N, 256) * G >= (size_t)L.cus / 2 || g.M % 256 == 0 || g.M % 256 > 128)
+    if (g.K > 256 && (cdiv(g.M, 256) * cdiv(g.N, 256) * G >= (size_t)L.cus / 2 || g.M % 256 == 0 || g.M % 256 > 128))
       return gemm_tiles<256, E8M0, BROWS, OUT32, false>(L, g, G, p, ws);
   return gemm_tiles<128, E8M0, BROWS, OUT32, false>(L, g, G, p, ws);
 }
@@ -912,7 +919,7 @@ hipError_t gemm_o(const Launch& L, const GemmArgs& g, int G, bool out_f32, void*
   const size_t wide = (g.lda | g.ldb) >> 23 | (g.sa_rs | g.sa_cs | g.sb_rs | g.sb_cs) >> 32;
   if (!wide && g.K > 0 && few_rows(g.M, g.N, g.K, G))
     return out_f32 ? gemm_few<E8M0, BROWS, true>(L, g, G, ws) : gemm_few<E8M0, BROWS, false>(L, g, G, ws);
-  if (!wide && g.K > 256)
+  if (!wide && g.K > 0)
     return out_f32 ? gemm_big<E8M0, BROWS, true>(L, g, G, ws) : gemm_big<E8M0, BROWS, false>(L, g, G, ws);
   const dim3 grid((unsigned)cdiv(g.M, 128), (unsigned)cdiv(g.N, 128), (unsigned)G);
   if (out_f32) return launch_k(k_gemm_tile<E8M0, BROWS, true>, grid, dim3(256), 0, L.stream, g);

@@ -382,3 +382,23 @@ def test_results_side_by_side(M, f32):
     torch.cuda.synchronize()
     want = np.concatenate([ref.E4M3[x] @ ref.E4M3[y].T for x, y in zip(A, B)], 1)
     assert np.array_equal(whole.float().cpu().numpy(), want.astype(np.float32) if f32 else ref.as_bf16(want))
+
+
+@pytest.mark.parametrize("e8m0", FMT)
+@pytest.mark.parametrize("brows", [1, 128])
+@pytest.mark.parametrize("K", [1, 100, 128, 200, 256, 300, 384])
+def test_large_tiles_of_few_blocks(K, brows, e8m0):
+    """K shorter than the large tiles' run ahead."""
+    M, N = 4170, 1100
+    g = np.random.default_rng([59, K])
+    note(f"large tiles K={K} brows={brows} e8m0={e8m0}")
+
+    def scales(rows, br):
+        k = g.integers(-1, 2, size=(-(-rows // br), -(-K // 128)))
+        return (k + 127).astype(np.uint8) if e8m0 else (2.0 ** k).astype(np.float32)
+
+    A, B = (int_codes(g, M, K), scales(M, 1)), (int_codes(g, N, K), scales(N, brows))
+    want = ref.dequantise(*A, 1).astype(np.float32) @ ref.dequantise(*B, brows).astype(np.float32).T
+    for f32 in (True, False):
+        got, = run([A], [B], brows, M, N, K, f32, 1, True)
+        assert np.array_equal(got, want if f32 else ref.as_bf16(want))
