@@ -578,8 +578,8 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
 // them on their way, and two to four workgroups a CU.  A group costs a barrier
 // and a chain of latencies, so two blocks a group are faster (48 x 4096 x
 // 8192: 14.7 us, one 16.2; 1 x 1024 x 1024: 5.3, 7.0) unless there are four
-// workgroups a CU to hide it (1 row, 8 problems of 8192 x 1024: 14.1, 12.5).  blockIdx: columns, rows, problem and slice
-// of K (`per` blocks each).
+// workgroups a CU to hide it (1 row, 8 problems of 8192 x 1024: 14.1, 12.5).
+// blockIdx: columns, rows, problem and slice of K (`per` blocks each).
 constexpr int kFewCols = 64, kFewBlocks = 16;  // columns; blocks whose scales are held at a time
 template <int MT, int BG, bool E8M0, bool BROWS, bool OUT32>
 __global__ __launch_bounds__(256) void k_gemm_few(GemmArgs g, int slices, unsigned per, uint32_t* counters, char* parts) {
@@ -743,51 +743,58 @@ __global__ __launch_bounds__(256) void k_gemm_tile(GemmArgs g) {
       lb[lds_at(r, c)] = load_chunk(B + rb * g.ldb, kb * kBK + c * 16, g.K);
     }
     __syncthreads();
-    i32x8 fa[4], fb[4];
+    Frag fa[4], fb[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int ra = wm + i * 16 + lr, rb = wn + i * 16 + lr;
-      union { u32x4 h[2]; i32x8 v; } u;
-      u.h[0] = la[lds_at(ra, 2 * lq)];
-      u.h[1] = la[lds_at(ra, 2 * lq + 1)];
-      fa[i] = u.v;
-      u.h[0] = lb[lds_at(rb, 2 * lq)];
-      u.h[1] = lb[lds_at(rb, 2 * lq + 1)];
-      fb[i] = u.v;
+      fa[i].h[0] = la[lds_at(ra, 2 * lq)];
+      fa[i].h[1] = la[lds_at(ra, 2 * lq + 1)];
+      fb[i].h[0] = lb[lds_at(rb, 2 * lq)];
+      fb[i].h[1] = lb[lds_at(rb, 2 * lq + 1)];
     }
-    if constexpr (E8M0) {
+    auto byte_of = [&](const void* p, size_t i) { return static_cast<const uint8_t*>(p)[i]; };
+    auto scale_of = [&](const void* p, size_t i) {
+      if constexpr (E8M0) return e8m0_f32(byte_of(p, i));
+      else return static_cast<const float*>(p)[i];
+    };
+    auto at_a = [&](unsigned m) { return (size_t)min(m, g.M - 1) * g.sa_rs + kb * g.sa_cs; };
+    auto at_b = [&](unsigned n) {
+      const size_t r = min(n, g.N - 1);
+      return (BROWS ? r : r / AR_BLOCK) * g.sb_rs + kb * g.sb_cs;
+    };
+    if constexpr (E8M0 && !OUT32) {
       int sa[4], sb[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const size_t m = min(m0 + wm + i * 16 + lr, g.M - 1);
-        const size_t n = min(n0 + wn + i * 16 + lr, g.N - 1);
-        sa[i] = static_cast<const uint8_t*>(g.sa[z])[m * g.sa_rs + kb * g.sa_cs];
-        sb[i] = static_cast<const uint8_t*>(g.sb[z])[(BROWS ? n : n / AR_BLOCK) * g.sb_rs + kb * g.sb_cs];
+        sa[i] = byte_of(g.sa[z], at_a(m0 + wm + i * 16 + lr));
+        sb[i] = byte_of(g.sb[z], at_b(n0 + wn + i * 16 + lr));
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[i], fa[j], acc[i][j], 0, 0, 0, sb[i], 0, sa[j]);
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[i].v, fa[j].v, acc[i][j], 0, 0, 0, sb[i], 0, sa[j]);
     } else {
       float sa[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const size_t m = min(m0 + wm + j * 16 + lr, g.M - 1);
-        sa[j] = static_cast<const float*>(g.sa[z])[m * g.sa_rs + kb * g.sa_cs];
-      }
+      for (int j = 0; j < 4; ++j) sa[j] = scale_of(g.sa[z], at_a(m0 + wm + j * 16 + lr));
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float sb[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const size_t n = min(n0 + wn + i * 16 + lq * 4 + r, g.N - 1);
-          sb[r] = static_cast<const float*>(g.sb[z])[(BROWS ? n : n / AR_BLOCK) * g.sb_rs + kb * g.sb_cs];
-        }
+        for (int r = 0; r < 4; ++r) sb[r] = scale_of(g.sb[z], at_b(n0 + wn + i * 16 + lq * 4 + r));
+        Wide wb;
+        if constexpr (OUT32) wb = widen(fb[i]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const f32x4 p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[i], fa[j], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0,
-                                                                        0, 0, 0);
+          f32x4 p = {0.f, 0.f, 0.f, 0.f};
+          if constexpr (OUT32) {
+            const Wide wa = widen(fa[j]);
+#pragma unroll
+            for (int h = 0; h < 4; ++h) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb.p[h], wa.p[h], p, 0, 0, 0);
+          } else {
+            p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[i].v, fa[j].v, p, 0, 0, 0, 0, 0, 0);
+          }
 #pragma unroll
           for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(p[r], sa[j] * sb[r], acc[i][j][r]);
         }

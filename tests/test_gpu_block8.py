@@ -402,3 +402,31 @@ def test_large_tiles_of_few_blocks(K, brows, e8m0):
     for f32 in (True, False):
         got, = run([A], [B], brows, M, N, K, f32, 1, True)
         assert np.array_equal(got, want if f32 else ref.as_bf16(want))
+
+
+@pytest.mark.parametrize("e8m0", FMT)
+@pytest.mark.parametrize("M,N,K,ld", [(8, 640, 700, None), (40, 300, 8192, None), (128, 8192, 8300, None), (4170, 1100, 700, None),
+                                      (3, 5, 700, (1 << 23) + 16)])
+def test_binary32_result_has_binary32_precision(M, N, K, ld, e8m0):
+    """Each way a product can go.  A sum of K products takes K / 32 matrix
+    instructions and as many scaled additions as blocks, each within 2^-24 of
+    a partial sum of the result's size or so, at random: sqrt(K / 32 +
+    K / 128) 2^-24, at most 1.1e-6 here; allowed is 2e-6 of the result's
+    norm.  (Products of fp8 instructions are 1e-5 off.)"""
+    g = np.random.default_rng([61, M, K])
+    A = ref.quantise(ref.as_bf16(g.standard_normal((M, K)) * np.exp(g.standard_normal(K))), 1, e8m0)
+    B = ref.quantise(ref.as_bf16(0.02 * g.standard_normal((N, K))), 1, e8m0)
+    note(f"binary32 result M={M} N={N} K={K} ld={ld} e8m0={e8m0}")
+    if ld is None:
+        got, = run([A], [B], 1, M, N, K, True, 0, True)
+    else:
+        big = torch.zeros(M + N, ld, dtype=torch.uint8, device=DEV)
+        big[:M, :K], big[M:, :K] = torch.from_numpy(A[0]).to(DEV), torch.from_numpy(B[0]).to(DEV)
+        out = torch.empty(M, N, device=DEV)
+        tar.ar_gemm_fp8([big[:M, :K]], [torch.from_numpy(A[1]).to(DEV)], [big[M:, :K]], [torch.from_numpy(B[1]).to(DEV)], [out],
+                        b_block_rows=1)
+        torch.cuda.synchronize()
+        got = out.cpu().numpy()
+    a, b = ref.dequantise(*A, 1), ref.dequantise(*B, 1)
+    want = a @ b.T
+    assert np.linalg.norm(got - want) <= 2e-6 * np.linalg.norm(want)
