@@ -127,18 +127,23 @@ __device__ __forceinline__ void each(F&& f) {
   each_of(f, std::make_integer_sequence<int, N>{});
 }
 
-// Copies 16 bytes a lane from byte `voff` + `soff` of a buffer to LDS, the
-// lanes of a wave side by side from byte address `lds`: no register holds
-// them on the way.  A lane beyond the buffer's end reads nothing.  The caller
-// waits for it (vmcnt) before a barrier.  Five wait states come before the copy:
-// the compiler may have written one of its scalar registers by a vector
-// instruction (v_readfirstlane, or v_readlane of a spilled one) right before,
-// and adds waits only to instructions that it emits itself.  M0 it keeps for
-// its own short uses and sets before each.
+// Copies 16 bytes a lane from byte `lane` + `at` of a buffer to LDS, the lanes
+// of a wave side by side from byte address `lds`: no register holds them on the
+// way.  A lane beyond the buffer's end reads nothing, which tiles past the last
+// row and blocks past the last of K rely on; the two parts are added in the
+// lane's register, whose check against the buffer's size is certain, and not in
+// the instruction, whose check of a scalar offset beyond that size is not.
+// (Added at each copy: sums kept over the loop would take registers.)  The
+// caller waits for the copy (vmcnt) before a barrier.  Five wait states come
+// before it: the compiler may have written one of its scalar registers by a
+// vector instruction (v_readfirstlane, or v_readlane of a spilled one) right
+// before, and adds waits only to instructions that it emits itself.  M0 it keeps
+// for its own short uses and sets before each.
 typedef uint32_t Resource __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ void copy_to_lds(Resource r, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-               :: "s"(lds), "v"(voff), "s"(r), "s"(soff) : "memory");
+__device__ __forceinline__ void copy_to_lds(Resource r, uint32_t lane, uint32_t at, uint32_t lds) {
+  asm("" : "+s"(at));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :: "s"(lds), "v"(lane + at), "s"(r) : "memory");
 }
 
 // `rows` rows of a code matrix from `p` on, as a bounded buffer.  (Word 3:

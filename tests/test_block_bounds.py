@@ -73,3 +73,14 @@ def test_copies_wait_for_their_scalar_registers(tmp_path):
         window = window[-7:] + [ins]
     assert copies > 100
     assert not early, f"{len(early)} of {copies} copies come too early: {early[:3]}"
+
+
+def test_copies_to_lds_have_no_scalar_offset(tmp_path):
+    """A buffer's size bounds what a copy reads: a tile's rows past the last,
+    and blocks past a slice of K, lie beyond it and have to read nothing.  The
+    check compares the lane's own offset with the size; how a scalar offset takes
+    part once it exceeds the size is another matter, so the lane's register
+    holds the whole offset."""
+    copies = [m.group(3) for m in map(COPY.search, instructions(tar.lib_path, tmp_path)) if m]
+    assert len(copies) > 100
+    assert set(copies) == {"0"}, f"{sum(c != '0' for c in copies)} of {len(copies)} copies use a scalar offset"
