@@ -100,6 +100,18 @@ __device__ __forceinline__ float wave_sum(float v) {
   return (row(0) + row(16)) + (row(32) + row(48));
 }
 
+// Means over a row are sums of terms times 2^-k, 2^k the power of two from the
+// row's length up, and a factor from 1 to 2: the power multiplies one of a
+// term's factors (exactly) before the fused multiply-add, so that no square and
+// no sum overflows unless the mean does.
+struct RowMean {
+  float part, rest;   // 2^-k, 2^k / cols
+};
+__device__ __forceinline__ RowMean row_mean(unsigned cols) {
+  const int k = cols > 1 ? 32 - __builtin_clz(cols - 1) : 0;
+  return RowMean{__builtin_ldexpf(1.0f, -k), __builtin_ldexpf(1.0f, k) / (float)cols};
+}
+
 constexpr int kMaxWaves = 16;
 
 // Sums of one value a wave, of up to 16 waves, kept in `part`: 16 slots, those
@@ -196,6 +208,7 @@ __global__ __launch_bounds__(1024) void k_reduce_norm(InPtrs in, NormArgs a) {
   // gains are fetched with the row where registers allow: after the row's sum
   // they would be one more trip to memory
   constexpr bool EARLY = V <= 2;
+  const RowMean mean = row_mean(cols);
   float h[V][8], w[V][8];
   float ss = 0.0f;
 #pragma unroll
@@ -228,17 +241,15 @@ __global__ __launch_bounds__(1024) void k_reduce_norm(InPtrs in, NormArgs a) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       if (!mine(g, j)) h[u][j] = 0.0f;
-      ss = __builtin_fmaf(h[u][j], h[u][j], ss);
+      ss = __builtin_fmaf(h[u][j], h[u][j] * mean.part, ss);
     }
   }
   if (!a.y && !a.codes) return;
   if (FORM == kRagged && a.codes)
     for (unsigned i = threadIdx.x; i < (cols + AR_BLOCK - 1) / AR_BLOCK; i += blockDim.x) top[i] = 0;
-  // a lane's sum is divided before lanes are added, so that only a mean
-  // square beyond binary32 overflows, not the sum of a whole row's squares
-  put_part(wave_sum(ss / (float)cols), part);
+  put_part(wave_sum(ss), part);
   __syncthreads();
-  const float r = 1.0f / sqrtf(sum_parts(part) + a.eps);
+  const float r = 1.0f / sqrtf(sum_parts(part) * mean.rest + a.eps);
 
   auto keep_scale = [&](size_t block, uint32_t kept) {
     const size_t k = row * a.scale_rs + block * a.scale_cs;
@@ -315,6 +326,7 @@ __global__ __launch_bounds__(V == 8 ? 1024 : 512) void k_norm_bwd(NormBwdArgs a)
   __shared__ __align__(16) float part[2][2][kMaxWaves];
   const unsigned cols = a.cols, groups = (cols + 7) / 8;
   constexpr bool AHEAD = V < 8, WHOLE = FORM != kRagged, NT = FORM == kStream;
+  const RowMean mean = row_mean(cols);
   struct Row {
     u32x4 h[V], dy[V], dres[V];
   };
@@ -352,18 +364,19 @@ __global__ __launch_bounds__(V == 8 ? 1024 : 512) void k_norm_bwd(NormBwdArgs a)
       widen(now.dy[u], dy);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        ss = __builtin_fmaf(h[j], h[j], ss);
-        gh = __builtin_fmaf(dy[j] * w[u][j], h[j], gh);
+        const float hp = h[j] * mean.part;
+        ss = __builtin_fmaf(h[j], hp, ss);
+        gh = __builtin_fmaf(dy[j] * w[u][j], hp, gh);
       }
     }
     // two sets of slots in turn: a wave may write the next row's sums while
     // another still reads this row's, and is held at the next barrier before
     // it could write these slots again
-    put_part(wave_sum(ss / (float)cols), part[flip][0]);
-    put_part(wave_sum(gh / (float)cols), part[flip][1]);
+    put_part(wave_sum(ss), part[flip][0]);
+    put_part(wave_sum(gh), part[flip][1]);
     __syncthreads();
-    const float r = 1.0f / sqrtf(sum_parts(part[flip][0]) + a.eps);
-    const float m = r * sum_parts(part[flip][1]);   // mean(g x)
+    const float r = 1.0f / sqrtf(sum_parts(part[flip][0]) * mean.rest + a.eps);
+    const float m = r * (sum_parts(part[flip][1]) * mean.rest);   // mean(g x)
 #pragma unroll
     for (int u = 0; u < V; ++u) {
       const unsigned g = u * blockDim.x + threadIdx.x;
