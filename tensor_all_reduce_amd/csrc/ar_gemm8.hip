@@ -585,11 +585,12 @@ __global__ __launch_bounds__(512) void k_gemm_big(GemmArgs g, unsigned tiles_m, 
 // codes of b are read once and there is little to compute on them, so the
 // kernel is a copy engine: a ring of groups of BG blocks in LDS, all but one of
 // them on their way, and two to four workgroups a CU.  A group costs a barrier
-// and a chain of latencies, so two blocks a group are faster (48 x 4096 x
-// 8192: 14.7 us, one 16.2; 1 x 1024 x 1024: 5.3, 7.0) unless there are four
-// workgroups a CU to hide it (1 row, 8 problems of 8192 x 1024: 14.1, 12.5).
+// and a chain of latencies, so a group has two blocks, unless rings of one,
+// which are smaller, save a second round of workgroups (gemm_few).
 // blockIdx: columns, rows, problem and slice of K (`per` blocks each).
 constexpr int kFewCols = 64, kFewBlocks = 16;  // columns; blocks whose scales are held at a time
+constexpr int few_ring(int mt, int bg) { return bg * (bg == 1 ? 3 : 2) * (16 * mt + kFewCols) * kBK; }  // bytes
+constexpr int few_scales(int mt, bool brows) { return kFewBlocks * 4 * (16 * mt + (brows ? kFewCols : 1)); }
 template <int MT, int BG, bool E8M0, bool BROWS, bool OUT32>
 __global__ __launch_bounds__(256) void k_gemm_few(GemmArgs g, int slices, unsigned per, uint32_t* counters, char* parts) {
   constexpr int BM = 16 * MT, NP = BG == 1 ? 3 : 2, ST = BG * NP;  // groups and blocks in the ring
@@ -597,6 +598,7 @@ __global__ __launch_bounds__(256) void k_gemm_few(GemmArgs g, int slices, unsign
   constexpr int kCopies = 2 + MT / 2;        // of a wave and block
   __shared__ __align__(16) char ring[ST][(BM + kFewCols) * kBK];  // rows of a, then of b
   __shared__ uint32_t lsa[kFewBlocks][BM], lsb[kFewBlocks][BROWS ? kFewCols : 1];
+  static_assert(sizeof(ring) == few_ring(MT, BG) && sizeof(lsa) + sizeof(lsb) == few_scales(MT, BROWS));
   const int z = blockIdx.z / slices, slice = blockIdx.z % slices, t = threadIdx.x, lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(t / kWave);
   const int lr = lane & 15, lq = lane >> 4;
@@ -830,6 +832,7 @@ __global__ __launch_bounds__(256) void k_gemm_tile(GemmArgs g) {
 // workgroups take.  Planned for the 256 CUs of the device, so that a
 // workspace's size does not depend on where it is asked for.
 constexpr unsigned kPlanCus = 256;
+constexpr unsigned kLdsBytes = 160 * 1024;  // of a CU
 struct Plan {
   int mt;           // few rows: fragments of 16 rows of a; 0: large tiles
   unsigned slices, per;
@@ -887,9 +890,18 @@ hipError_t gemm_few(const Launch& L, const GemmArgs& g, int G, void* ws) {
   uint32_t* counters = static_cast<uint32_t*>(ws);
   char* parts = ws ? static_cast<char*>(ws) + kCounterBytes : nullptr;
   const dim3 grid((unsigned)cdiv(g.N, kFewCols), (unsigned)cdiv(g.M, 16 * p.mt), (unsigned)G * p.slices);
-  const bool many = p.tiles * p.slices >= 4 * kPlanCus;
+  // Rings of one block where the workgroups of rings of two are more than the
+  // device's LDS holds at once and those of one are not: 769 to 1024, with
+  // scales for each row of b 513 to 768.  Us, one and two blocks, rows of
+  // 1024: 768 workgroups 10.4 and 10.4, 800 11.6 and 13.6, 896 11.8 and 13.8,
+  // 1024 12.3 and 14.4; with row scales 512 9.3 and 9.2, 516 9.4 and 12.1, 768
+  // 10.7 and 12.8, 896 14.8 and 13.6.
+  constexpr size_t held1 = kPlanCus * (kLdsBytes / (few_ring(2, 1) + few_scales(2, BROWS)));
+  constexpr size_t held2 = kPlanCus * (kLdsBytes / (few_ring(2, 2) + few_scales(2, BROWS)));
+  const size_t groups = p.tiles * p.slices;
+  const bool one = groups > held2 && groups <= held1;
   auto k = p.mt == 4 ? k_gemm_few<4, 2, E8M0, BROWS, OUT32>
-                     : many ? k_gemm_few<2, 1, E8M0, BROWS, OUT32> : k_gemm_few<2, 2, E8M0, BROWS, OUT32>;
+                     : one ? k_gemm_few<2, 1, E8M0, BROWS, OUT32> : k_gemm_few<2, 2, E8M0, BROWS, OUT32>;
   return launch_k(k, grid, dim3(256), 0, L.stream, g, (int)p.slices, p.per, counters, parts);
 }
 
