@@ -857,17 +857,22 @@ Plan plan_few(unsigned M, unsigned N, unsigned K, int G) {
   return p;
 }
 
-// Which kernel: few rows up to 192 of its 64 x 64 tiles, and beyond while a
-// workgroup for each is resident at once (1024) and tiles times blocks stay
-// within 16384, where large tiles, cut into slices, lose to their join.  Either
-// side, us, few rows first: N 8192, K 8192: M 64 21 and 32, M 128 30 and 33,
-// M 192 40 and 35; N 8192, K 1024: M 256 8 and 17, M 512 14 and 17, M 768 20
-// and 17; N 1024, K 8192: M 512 18 and 25, M 1024 30 and 30; N 4096, K 4096:
-// M 512 22 and 27, M 768 35 and 32.
+// Which kernel.  Few rows where
+// - its workgroups are all resident at once and read the codes of b once: up
+//   to 768 of 32 rows, 512 of 64;
+// - or there are up to 192 of its 64 x 64 tiles;
+// - or up to 1024, and tiles times blocks stay within 16384, where large tiles,
+//   cut into slices, lose to their join.
+// Either side, us, few rows first.  8192 columns of each of several problems,
+// K 8192: 1 row, 512 tiles 58 and 78, 768 81 and 95, 896 112 and 100; 64 rows,
+// 384 tiles 60 and 67, 512 69 and 80, 640 107 and 96.  One problem, N 8192, K
+// 8192: M 64 21 and 32, M 128 30 and 33, M 192 40 and 35; N 8192, K 1024: M 256
+// 8 and 17, M 512 14 and 17, M 768 20 and 17; N 1024, K 8192: M 512 18 and 25,
+// M 1024 30 and 30; N 4096, K 4096: M 512 22 and 27, M 768 35 and 32.
 bool few_rows(unsigned M, unsigned N, unsigned K, int G) {
   const size_t tiles = cdiv(M, 64) * cdiv(N, kFewCols) * G;
   if (cdiv(M, 32) > 65535) return false;     // a launch's second axis
-  return tiles <= 192 || (tiles <= 1024 && tiles * blocks_of(K) <= 16384);
+  return tiles <= (M <= 32 ? 768 : M <= 64 ? 512 : 192) || (tiles <= 1024 && tiles * blocks_of(K) <= 16384);
 }
 
 // The counters' part of a workspace, the same for every shape, so that one
@@ -905,8 +910,8 @@ hipError_t gemm_few(const Launch& L, const GemmArgs& g, int G, void* ws) {
   return launch_k(k, grid, dim3(256), 0, L.stream, g, (int)p.slices, p.per, counters, parts);
 }
 
-// More than 64 rows: large tiles, one workgroup a CU.  Where 128 x 256 tiles
-// fill half the CUs at most, they are cut into slices of at least 8 blocks.
+// Large tiles, one workgroup a CU.  Where 128 x 256 tiles fill half the CUs at
+// most, they are cut into slices of about 8 blocks or more.
 Plan plan_big(unsigned M, unsigned N, unsigned K, int G) {
   Plan p{};
   p.tiles = cdiv(M, 128) * cdiv(N, 256) * G;
@@ -935,9 +940,11 @@ hipError_t gemm_big(const Launch& L, const GemmArgs& g, int G, void* ws) {
   p.slices = 1;
   p.per = blocks_of(g.K);
   // 256 rows a tile unless registers do not hold it (products as bf16, a
-  // binary32 scale for each row of b), it leaves CUs without one, or K is short
+  // binary32 scale for each row of b), it leaves CUs without one, K is short,
+  // or 128 rows hold all (8 problems of 8192 columns, K 4096: 16 rows 57 us, in
+  // tiles of 256 rows 69; 128 rows 67 and 76)
   if constexpr (!OUT32 && (E8M0 || !BROWS))
-    if (g.K > 256 && (cdiv(g.M, 256) * cdiv(g.N, 256) * G >= (size_t)L.cus / 2 || g.M % 256 == 0 || g.M % 256 > 128))
+    if (g.K > 256 && g.M > 128 && (cdiv(g.M, 256) * cdiv(g.N, 256) * G >= (size_t)L.cus / 2 || g.M % 256 == 0 || g.M % 256 > 128))
       return gemm_tiles<256, E8M0, BROWS, OUT32, false>(L, g, G, p, ws);
   return gemm_tiles<128, E8M0, BROWS, OUT32, false>(L, g, G, p, ws);
 }
