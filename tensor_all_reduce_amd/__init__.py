@@ -473,6 +473,22 @@ def ar_reduce_fp8(codes: Sequence, scales: Sequence, outs: Sequence, n: int | No
 
 # ------------------------------------------- norm, block quantiser, fp8 product
 
+# Element types by what the kernels read them as: the type itself, or its bit
+# patterns in whole numbers.
+_BF16 = ("bfloat16", "int16", "uint16")
+_F32 = ("float32",)
+_E4M3 = ("float8_e4m3fn", "uint8", "int8")
+_E8M0 = ("float8_e8m0fnu", "uint8", "int8")
+
+
+def _typed(t, kinds, name: str) -> None:
+    """Refuses a tensor of another element type, which its bytes would be
+    misread as."""
+    dtype = getattr(t, "dtype", None)
+    if dtype is not None and str(dtype).rpartition(".")[2] not in kinds:
+        raise ValueError(f"{name} must have elements of type {' or '.join(kinds)}, not {dtype}")
+
+
 def _mat(t, elem_sizes, name: str, shape=None):
     """(pointer, row stride in elements) of a 2-D device tensor whose rows
     are contiguous."""
@@ -492,6 +508,7 @@ def _mat(t, elem_sizes, name: str, shape=None):
 def _rows_of(t, name: str, shape):
     """Pointer of a contiguous bf16 matrix of that shape."""
     ptr = _dev_ptr(t, 2, name)
+    _typed(t, _BF16, name)
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     return ptr
@@ -500,6 +517,7 @@ def _rows_of(t, name: str, shape):
 def _fp8_matrix(codes, scales, shape, block_rows: int, name: str) -> _Fp8Matrix:
     rows, cols = shape
     ptr, ld = _mat(codes, (1,), f"{name} codes", shape)
+    _typed(codes, _E4M3, f"{name} codes")
     if rows <= 1:
         ld = -(-cols // 16) * 16
     want = (-(-rows // block_rows), -(-cols // AR_BLOCK))
@@ -513,6 +531,7 @@ def _fp8_matrix(codes, scales, shape, block_rows: int, name: str) -> _Fp8Matrix:
         fmt = AR_SCALE_E8M0
     else:
         raise ValueError(f"{name} scales must be binary32 or power-of-two bytes")
+    _typed(scales, _F32 if fmt == AR_SCALE_F32 else _E8M0, f"{name} scales")
     # the stride of an axis of one block says nothing
     rs = scales.stride(0) if want[0] > 1 else 0
     cs = scales.stride(1) if want[1] > 1 else 0
@@ -527,6 +546,7 @@ def _gain(weight, cols: int):
     es = weight.element_size()
     if es not in (2, 4):
         raise ValueError("weight must be bf16 or binary32")
+    _typed(weight, _F32 if es == 4 else _BF16, "weight")
     return _dev_ptr(weight, es, "weight"), AR_FMT_F32 if es == 4 else AR_FMT_BF16
 
 
@@ -592,6 +612,7 @@ def ar_norm_bwd(dy, h, weight=None, dx=None, dres=None, dweight=None, workspace=
         if dweight.numel() != cols:
             raise ValueError(f"dweight holds {dweight.numel()} elements, {cols} needed")
         dp = _dev_ptr(dweight, 4, "dweight")
+        _typed(dweight, _F32, "dweight")
     sp, sb = _workspace(workspace)
     _call("ar_norm_bwd", yp, hp, wp, wf, rp, rows, cols, ctypes.c_float(eps), xp, dp, sp, sb, _stream(stream))
 
@@ -607,6 +628,7 @@ def ar_quantize_block(x, codes, scales, block_rows: int = 1, transpose: bool = F
     with a scale for each block of block_rows (1 or 128) x 128; transpose:
     codes and scales are those of x transposed."""
     xp, ldx = _mat(x, (2,), "x")
+    _typed(x, _BF16, "x")
     rows, cols = x.shape
     q = _fp8_matrix(codes, scales, (cols, rows) if transpose else (rows, cols), int(block_rows), "output")
     _call("ar_quantize_block", xp, ldx, rows, cols, ctypes.pointer(q), int(bool(transpose)), _stream(stream))
@@ -638,6 +660,7 @@ def ar_gemm_fp8(a_codes: Sequence, a_scales: Sequence, b_codes: Sequence, b_scal
         ptr, ld = _mat(t, (2, 4), f"outs[{i}]", (M, N))
         if t.element_size() != es or ld != _mat(outs[0], (2, 4), "outs[0]")[1]:
             raise ValueError("outs must share one element size and one row stride")
+        _typed(t, _F32 if es == 4 else _BF16, f"outs[{i}]")
         cp.append(ptr)
     sp, sb = _workspace(workspace)
     _call("ar_gemm_fp8", am, bm, _ptr_array(cp), G, M, N, K, ld, AR_FMT_F32 if es == 4 else AR_FMT_BF16, sp, sb,
