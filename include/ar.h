@@ -515,12 +515,17 @@ int ar_quantize_block(const void* x, size_t ldx, size_t rows, size_t cols, const
  *   C_g[m,n] = sum over blocks j of 128 along K of
  *              sa(m,j) * sb(n,j) * sum over k in block j of a[m,k] * b[n,k]
  * on the matrix cores, the result rounded once to bf16 or kept in binary32.
- * Sums are binary32; within a block of a bf16 result the fp8 matrix
- * instructions drop the low bits of terms far below the largest (about 2e-5
- * of the result's size); a binary32 result takes the codes as bf16 instead
- * and keeps binary32's precision, with E8M0 scales from 2^-117 to 2^118 (the
- * scaled codes are bf16 values).  Row-major a [M x K] with block_rows 1 (activations), b
- * [N x K] with block_rows 128 (weights) or 1.
+ * Sums are binary32.  Within a block of a bf16 result the fp8 matrix
+ * instructions drop the low bits of terms far below the block's largest (about
+ * 2e-5 of the result's size; more of a result whose terms cancel).  A binary32
+ * result takes the codes as bf16 instead and keeps binary32's precision, with
+ * E8M0 scales from 2^-117 to 2^118 (the scaled codes are bf16 values).
+ * Scales: the product sa * sb of a block is formed in binary32 by most kernels
+ * and belongs between 2^-126 and 2^128.  Below, it keeps fewer bits and is 0
+ * from 2^-150 down; beyond, results are infinities, and NaN where a sum of
+ * codes is 0.
+ * Row-major a [M x K] with block_rows 1 (activations), b [N x K] with
+ * block_rows 128 (weights) or 1.
  *   a, b      host arrays of G matrices; ld, strides, scale_fmt and
  *             block_rows are the same for all of a, and for all of b, and
  *             scale_fmt is the same for both
