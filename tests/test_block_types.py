@@ -86,3 +86,15 @@ def test_types_that_the_operators_take():
 def test_types_that_they_refuse(call, name, dtype):
     with pytest.raises(ValueError, match="must (have|be)"):
         call(**{name: dtype})
+
+
+def test_row_strides_that_the_codes_refuse():
+    """A stride of at least the row's length that is no multiple of 16, apart
+    from one that is shorter."""
+    def call(ld):
+        m = tar._Fp8Matrix(E, ld, F, 1, 64, 0, 1)
+        ins = (tar._vp * 1)(A)
+        return tar.lib().ar_reduce_norm(ins, 1, None, None, 0, 4, 200, 1e-6, C, None, tar.ctypes.byref(m), None)
+
+    assert call(200) == tar.AR_ERR_ALIGN and call(216) == tar.AR_ERR_ALIGN
+    assert call(192) == tar.AR_ERR_INVALID and call(0) == tar.AR_ERR_INVALID
