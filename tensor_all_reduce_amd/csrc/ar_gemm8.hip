@@ -728,13 +728,16 @@ __global__ __launch_bounds__(256) void k_gemm_few(GemmArgs g, int slices, unsign
 // 128 x 128 tile of C in a 256-lane workgroup, 64 x 64 a wave as 4 x 4
 // products of 16 x 16 x 128: any strides, any K (the other kernels address a
 // tile's rows in 32 bits).  b is the first operand, so a lane ends with four
-// consecutive n of one m.
+// consecutive n of one m.  blockIdx: rows, columns, and problem with the rows
+// beyond the first axis (HIP takes fewer than 2^32 lanes along one).
 template <bool E8M0, bool BROWS, bool OUT32>
-__global__ __launch_bounds__(256) void k_gemm_tile(GemmArgs g) {
+__global__ __launch_bounds__(256) void k_gemm_tile(GemmArgs g, int problems) {
   constexpr int BM = 128, BN = 128;
   __shared__ u32x4 la[BM * 8], lb[BN * 8];
-  const int z = blockIdx.z, t = threadIdx.x, lane = lane_id(), wave = t / kWave;
-  const unsigned m0 = blockIdx.x * BM, n0 = blockIdx.y * BN;
+  const int z = blockIdx.z % problems, t = threadIdx.x, lane = lane_id(), wave = t / kWave;
+  const size_t first = ((size_t)(blockIdx.z / problems) * gridDim.x + blockIdx.x) * BM;
+  if (first >= g.M) return;
+  const unsigned m0 = (unsigned)first, n0 = blockIdx.y * BN;
   const int wm = (wave & 1) * 64, wn = (wave >> 1) * 64;
   const int lr = lane & 15, lq = lane >> 4;
   const uint8_t *A = g.a[z], *B = g.b[z];
@@ -956,9 +959,10 @@ hipError_t gemm_o(const Launch& L, const GemmArgs& g, int G, bool out_f32, void*
     return out_f32 ? gemm_few<E8M0, BROWS, true>(L, g, G, ws) : gemm_few<E8M0, BROWS, false>(L, g, G, ws);
   if (!wide && g.K > 0)
     return out_f32 ? gemm_big<E8M0, BROWS, true>(L, g, G, ws) : gemm_big<E8M0, BROWS, false>(L, g, G, ws);
-  const dim3 grid((unsigned)cdiv(g.M, 128), (unsigned)cdiv(g.N, 128), (unsigned)G);
-  if (out_f32) return launch_k(k_gemm_tile<E8M0, BROWS, true>, grid, dim3(256), 0, L.stream, g);
-  return launch_k(k_gemm_tile<E8M0, BROWS, false>, grid, dim3(256), 0, L.stream, g);
+  const size_t tm = cdiv(g.M, 128), x = std::min<size_t>(tm, 1u << 20);
+  const dim3 grid((unsigned)x, (unsigned)cdiv(g.N, 128), (unsigned)(G * cdiv(tm, x)));
+  if (out_f32) return launch_k(k_gemm_tile<E8M0, BROWS, true>, grid, dim3(256), 0, L.stream, g, G);
+  return launch_k(k_gemm_tile<E8M0, BROWS, false>, grid, dim3(256), 0, L.stream, g, G);
 }
 
 }  // namespace

@@ -65,3 +65,17 @@ def test_rings_of_one_and_two_blocks(G, M, N, K, brows, e8m0, f32):
     (8, 128, 8192, 700, 128), (8, 129, 8192, 700, 128), (8, 100, 4300, 300, 1), (1, 65, 66000, 300, 128)])
 def test_kernels_of_few_rows(G, M, N, K, brows, e8m0, f32):
     check(G, M, N, K, brows, e8m0, f32)
+
+
+def test_most_rows_without_columns_of_k():
+    """K = 0 writes zeros, up to the largest M there is."""
+    M = 2 ** 31 - 1
+    note(f"product M={M} N=1 K=0")
+    out = torch.full((M, 1), 3.0, dtype=torch.bfloat16, device=DEV)
+    z = lambda r: (torch.empty(r, 0, dtype=torch.uint8, device=DEV), torch.empty(r, 0, device=DEV))  # noqa: E731
+    a, b = z(M), z(1)
+    tar.ar_gemm_fp8([a[0]], [a[1]], [b[0]], [b[1]], [out], b_block_rows=1)
+    torch.cuda.synchronize()
+    assert not bool(out.view(torch.int16).any())
+    del out
+    torch.cuda.empty_cache()
