@@ -727,7 +727,8 @@ __global__ __launch_bounds__(256) void k_gemm_few(GemmArgs g, int slices, unsign
 
 // 128 x 128 tile of C in a 256-lane workgroup, 64 x 64 a wave as 4 x 4
 // products of 16 x 16 x 128: any strides, any K (the other kernels address a
-// tile's rows in 32 bits).  b is the first operand, so a lane ends with four
+// tile's rows in 32 bits, and are faster: 4096 x 4096 x 4096 278 us here, 65
+// in large tiles).  b is the first operand, so a lane ends with four
 // consecutive n of one m.  blockIdx: rows, columns, and problem with the rows
 // beyond the first axis (HIP takes fewer than 2^32 lanes along one).
 template <bool E8M0, bool BROWS, bool OUT32>
@@ -847,8 +848,8 @@ unsigned blocks_of(unsigned K) { return (K + kBK - 1) / kBK; }
 // 32 or 64 rows of a and 64 columns a workgroup; slices of at least 8 blocks
 // until there are two workgroups a CU.  A join costs 3 to 5 us (parts out to
 // memory, a counter, parts back), so more slices lose what they gain: 48 x
-// 4096 x 8192 took 16.3 us in 8 slices, 21.0 in 16; 1 x 1024 x 8192 10.6 in 8
-// and 11.9 in 16.
+// 4096 x 8192 takes 15.1 us in 4 slices, 15.4 in 8 and 20.1 in 16; 1 x 1024 x
+// 8192 10.0, 9.2 and 11.3.
 Plan plan_few(unsigned M, unsigned N, unsigned K, int G) {
   Plan p{};
   p.mt = M <= 32 ? 2 : 4;
