@@ -12,9 +12,9 @@
 // Both kernels are bound by memory.  A row stays in registers between the sum
 // of its squares and its result, so every input is read once and every output
 // written once; the two passes over a row that the formulas ask for cost no
-// traffic.  Measured: 8 ranks, [16384 x 8192], fp8 result, 464-472 us, 6.0
-// TB/s; a single row 4.7 us, where an empty call takes 3.4; gradient of
-// [16384 x 16384] 363 us, 5.9 TB/s.
+// traffic.  Measured: 8 ranks, [16384 x 8192], fp8 result, 464-476 us, 6.0
+// TB/s; a single row 4.7-4.8 us, where an empty call takes 3.4; gradient of
+// [16384 x 16384] 358-370 us, 5.9 TB/s.
 #include "ar_device.hpp"
 #include "ar_e4m3.hpp"
 #include "ar_internal.hpp"
