@@ -548,6 +548,166 @@ int ar_gemm_fp8(const ar_fp8_matrix* a, const ar_fp8_matrix* b, void* const* c, 
                 size_t ldc, int out_fmt, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * The attention of a transformer block: what lies between its query, key and
+ * value projection and its output projection.
+ *
+ * Queries, keys, values and results are matrices [tokens][heads][dim] of bf16,
+ * dim contiguous:
+ *   data        device pointer, 16-byte aligned; NULL where a matrix may be
+ *               left out
+ *   token_stride, head_stride   elements, multiples of 8 (the heads of a token
+ *               may lie side by side in one projection's result)
+ * dim is a multiple of 16 up to AR_ATTN_MAX_DIM.  Query head h uses key head
+ * h / (hq / hkv); hq is a multiple of hkv.
+ *
+ * A sequence's keys lie in rows of a matrix or in the pages of a cache:
+ *   k, v        page 0's first element: bf16 (AR_FMT_BF16), or E4M3 codes
+ *               (AR_FMT_E4M3) that stand for value(code) * scale
+ *   page_stride, token_stride, head_stride   of k and of v, elements;
+ *               multiples of 8 (bf16) or 16 (codes)
+ *   k_scales, v_scales   AR_FMT_E4M3: binary32, one for each token and head,
+ *               with strides of their own (any)
+ *   pages, page_size   pages in the cache, tokens in a page (any, below 2^31
+ *               together)
+ *   heads, dim
+ * Key j of sequence b is token j % page_size of page
+ * table[b * table_stride + j / page_size] (int32).
+ *
+ * Masks.  A sequence's queries are its last positions: query i of n_q has
+ * position p = n_k - n_q + i and sees key j if
+ *   j <= p  and  (window == 0  or  j > p - window  or  j < sinks).
+ * Pages of keys that no query sees are not looked up.  What masked places hold
+ * never counts, be it infinite or NaN.  A query without a visible key (also:
+ * only scores of -infinity) has a result of zeros and an lse of -infinity.
+ *   out[i] = sum_j softmax_j(scale * q_i . k_j) v_j
+ *   lse[i] = log(sum_j exp(scale * q_i . k_j))      binary32
+ * Scores, maxima and sums are binary32; the softmax's numerators, and what
+ * multiplies a matrix in the gradients, are rounded to bf16 for their
+ * products.
+ *
+ * Numbers on the device (lengths, offsets, positions, page numbers, slots) are
+ * not known to the caller's thread and not refused: lengths and offsets are
+ * held within the buffers (a length below 0 is 0), and a page number outside
+ * [0, pages) makes the results that read that page NaN.
+ */
+#define AR_FMT_E4M3 2
+#define AR_ATTN_MAX_DIM 128
+
+typedef struct ar_heads {
+  void* data;
+  size_t token_stride, head_stride;
+} ar_heads;
+
+typedef struct ar_kv_cache {
+  void *k, *v;
+  float *k_scales, *v_scales;
+  size_t pages, page_size, heads, dim;
+  size_t page_stride, token_stride, head_stride;
+  size_t scale_page_stride, scale_token_stride, scale_head_stride;
+  int fmt;
+} ar_kv_cache;
+
+/*
+ * Rotates queries and keys by their positions and puts keys and values into a
+ * cache.  With c and s the cosine and sine of the token's position and of the
+ * pair,  (a, b) -> (a c - b s, b c + a s)  for rot / 2 pairs of a head's first
+ * rot elements: elements i and i + rot / 2, or 2 i and 2 i + 1 with
+ * AR_ROPE_PAIRS.  AR_ROPE_INVERSE rotates back (s negated), which is the
+ * gradient's way.  Arithmetic is binary32, each result rounded once.
+ *   q, q_out    [tokens][hq][dim]; q_out may be exactly q.  Both may be NULL
+ *               (hq 0)
+ *   k, k_out    [tokens][hkv][dim]; k_out may be exactly k, or NULL.  k may be
+ *               NULL (hkv 0)
+ *   v           [tokens][hkv][dim], only read into the cache; may be NULL
+ *               without one
+ *   cos_sin     [table_rows][rot] binary32: rot / 2 cosines, then the sines.
+ *               rot is a multiple of 16 up to dim
+ *   positions   int32[tokens], held within [0, table_rows)
+ *   cache       NULL: none.  E4M3 scales are max(largest finite magnitude of
+ *               the token's head / 448, 2^-126), codes as in
+ *               ar_quantize_block
+ *   slots       int64[tokens]: token t goes to place slots[t] % page_size of
+ *               page slots[t] / page_size; any slot outside the cache (-1)
+ *               goes nowhere.  Of tokens with one slot any may be kept, and
+ *               E4M3 codes of one with another's scale
+ * Outputs may lie side by side with inputs in one larger matrix of the same
+ * token_stride.
+ */
+#define AR_ROPE_PAIRS 1
+#define AR_ROPE_INVERSE 2
+int ar_rope_kv(const ar_heads* q, const ar_heads* k, const ar_heads* v, size_t tokens, size_t hq, size_t hkv, size_t dim,
+               const float* cos_sin, size_t table_rows, size_t rot, const int32_t* positions, const ar_heads* q_out,
+               const ar_heads* k_out, const ar_kv_cache* cache, const int64_t* slots, int flags, void* stream);
+
+/*
+ * Attention of one new token a sequence over a cache that holds the token's
+ * own key already.
+ *   q, out      [seqs][hq][dim]; out may be exactly q
+ *   table, table_stride, table_pages   page table: rows of table_pages entries
+ *   lens        int32[seqs], keys of each sequence, held within
+ *               [0, table_pages * page_size]
+ *   scale       finite, above 0
+ *   lse         element (i, h) at lse[i * lse_ts + h * lse_hs], or NULL
+ *   workspace   device memory, 16-byte aligned, zero before its first use; a
+ *               call leaves its counters zero again, and calls of other
+ *               shapes may use one workspace in turn.  With at least
+ *               ar_attn_decode_workspace(seqs, hq, hkv, dim) bytes the keys are
+ *               spread evenly over the device whatever the lengths; with less,
+ *               or NULL, each sequence and key head is one workgroup's work.
+ *               Calls that overlap in time must not share it.
+ * With given lengths and workspace results repeat bit for bit.
+ */
+size_t ar_attn_decode_workspace(size_t seqs, size_t hq, size_t hkv, size_t dim);
+int ar_attn_decode(const ar_heads* q, const ar_kv_cache* cache, const int32_t* table, size_t table_stride,
+                   size_t table_pages, const int32_t* lens, size_t seqs, size_t hq, float scale, size_t window,
+                   size_t sinks, const ar_heads* out, float* lse, size_t lse_ts, size_t lse_hs, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/*
+ * Attention of ragged prompts.  Rows cu_q[b] .. cu_q[b + 1] - 1 of q and out
+ * are sequence b's queries; rows that belong to no sequence are left as they
+ * are.
+ *   ar_attn        keys and values in rows cu_k[b] .. cu_k[b + 1] - 1 of k, v
+ *   ar_attn_paged  in a cache, lens[b] of them (as in ar_attn_decode)
+ *   q, out      [rows_q][hq][dim]; out may be exactly q
+ *   k, v        [rows_k][hkv][dim]
+ *   cu_q, cu_k  int32[seqs + 1], ascending
+ * rows_q and rows_k at most 2^30 (AR_ERR_UNSUPPORTED).
+ */
+int ar_attn(const ar_heads* q, const ar_heads* k, const ar_heads* v, const int32_t* cu_q, const int32_t* cu_k, size_t seqs,
+            size_t rows_q, size_t rows_k, size_t hq, size_t hkv, size_t dim, float scale, size_t window, size_t sinks,
+            const ar_heads* out, float* lse, size_t lse_ts, size_t lse_hs, void* stream);
+int ar_attn_paged(const ar_heads* q, const ar_kv_cache* cache, const int32_t* table, size_t table_stride,
+                  size_t table_pages, const int32_t* lens, const int32_t* cu_q, size_t seqs, size_t rows_q, size_t hq,
+                  float scale, size_t window, size_t sinks, const ar_heads* out, float* lse, size_t lse_ts, size_t lse_hs,
+                  void* stream);
+
+/*
+ * Gradient of ar_attn.  With P = exp(scale q k - lse) on visible keys,
+ *   dv = P^T d_out,   dS = P (d_out v^T - rowsum(d_out * out)),
+ *   dq = scale dS k,  dk = scale dS^T q,
+ * dk and dv summed over the query heads of a key head.
+ *   out, lse    what ar_attn wrote
+ *   d_out       [rows_q][hq][dim], the gradient of out
+ *   dq          [rows_q][hq][dim], or NULL
+ *   dk, dv      [rows_k][hkv][dim], or both NULL
+ *   workspace   ar_attn_bwd_workspace(...) bytes, 16-byte aligned; no
+ *               particular contents
+ * Rows of dq, dk and dv that belong to no sequence are left as they are.  No
+ * output may overlap an input (they may lie side by side in a larger matrix).
+ * The sums' order is fixed by the sizes, offsets and mask: results repeat bit
+ * for bit.  Masked places: a value that is no number reaches its own
+ * sequence's gradients only.
+ */
+size_t ar_attn_bwd_workspace(size_t rows_q, size_t rows_k, size_t seqs, size_t hq, size_t hkv, size_t dim, size_t window,
+                             size_t sinks);
+int ar_attn_bwd(const ar_heads* q, const ar_heads* k, const ar_heads* v, const ar_heads* out, const float* lse,
+                size_t lse_ts, size_t lse_hs, const ar_heads* d_out, const int32_t* cu_q, const int32_t* cu_k, size_t seqs,
+                size_t rows_q, size_t rows_k, size_t hq, size_t hkv, size_t dim, float scale, size_t window, size_t sinks,
+                const ar_heads* dq, const ar_heads* dk, const ar_heads* dv, void* workspace, size_t workspace_bytes,
+                void* stream);
+
+/*
  * Initialise an error record for ar_unpack_fused / ar_rd_schedule on
  * `stream`: d_err[0] = 0, d_err[1] = UINT64_MAX.  Uses a one-thread kernel,
  * not a memset, so it may be recorded in a HIP graph.

@@ -41,6 +41,9 @@ __all__ = [
     "ar_reduce_norm", "ar_norm_bwd", "ar_quantize_block", "ar_gemm_fp8", "norm_bwd_workspace", "gemm_fp8_workspace",
     "fp8_codes_empty", "fp8_scales_empty",
     "AR_BLOCK", "AR_SCALE_F32", "AR_SCALE_E8M0", "AR_FMT_BF16", "AR_FMT_F32", "AR_NORM_MAX_COLS",
+    "ar_rope_kv", "ar_attn_decode", "ar_attn", "ar_attn_paged", "ar_attn_bwd", "attn_decode_workspace",
+    "attn_bwd_workspace", "kv_cache_empty", "rope_table",
+    "AR_FMT_E4M3", "AR_ATTN_MAX_DIM", "AR_ROPE_PAIRS", "AR_ROPE_INVERSE",
 ]
 
 AR_OK = 0
@@ -87,6 +90,10 @@ AR_SCALE_E8M0 = 1
 AR_FMT_BF16 = 0
 AR_FMT_F32 = 1
 AR_NORM_MAX_COLS = 65536
+AR_FMT_E4M3 = 2
+AR_ATTN_MAX_DIM = 128
+AR_ROPE_PAIRS = 1
+AR_ROPE_INVERSE = 2
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_HERE, "libarcore.so")
@@ -101,6 +108,18 @@ class _Fp8Matrix(ctypes.Structure):
     """ar_fp8_matrix"""
     _fields_ = [("codes", _vp), ("ld", _sz), ("scales", _vp), ("scale_rs", _sz), ("scale_cs", _sz),
                 ("scale_fmt", ctypes.c_int), ("block_rows", ctypes.c_int)]
+
+
+class _Heads(ctypes.Structure):
+    """ar_heads"""
+    _fields_ = [("data", _vp), ("token_stride", _sz), ("head_stride", _sz)]
+
+
+class _KVCache(ctypes.Structure):
+    """ar_kv_cache"""
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scales", _vp), ("v_scales", _vp)] + [
+        (n, _sz) for n in ("pages", "page_size", "heads", "dim", "page_stride", "token_stride", "head_stride",
+                           "scale_page_stride", "scale_token_stride", "scale_head_stride")] + [("fmt", ctypes.c_int)]
 
 
 class ARError(RuntimeError):
@@ -170,6 +189,24 @@ def lib():
         L.ar_gemm_fp8.restype = ctypes.c_int
         L.ar_gemm_fp8.argtypes = [mp, mp, ctypes.POINTER(_vp), ctypes.c_int, _sz, _sz, _sz, _sz, ctypes.c_int, _vp,
                                   _sz, _vp]
+        hp, cp = ctypes.POINTER(_Heads), ctypes.POINTER(_KVCache)
+        tail = [_sz, _sz]                       # window, sinks
+        res = [hp, _vp, _sz, _sz]               # out, lse and its strides
+        L.ar_rope_kv.restype = ctypes.c_int
+        L.ar_rope_kv.argtypes = [hp, hp, hp, _sz, _sz, _sz, _sz, _vp, _sz, _sz, _vp, hp, hp, cp, _vp, ctypes.c_int, _vp]
+        L.ar_attn_decode_workspace.restype = _sz
+        L.ar_attn_decode_workspace.argtypes = [_sz] * 4
+        L.ar_attn_decode.restype = ctypes.c_int
+        L.ar_attn_decode.argtypes = [hp, cp, _vp, _sz, _sz, _vp, _sz, _sz, f32, *tail, *res, _vp, _sz, _vp]
+        L.ar_attn.restype = ctypes.c_int
+        L.ar_attn.argtypes = [hp, hp, hp, _vp, _vp] + [_sz] * 6 + [f32, *tail, *res, _vp]
+        L.ar_attn_paged.restype = ctypes.c_int
+        L.ar_attn_paged.argtypes = [hp, cp, _vp, _sz, _sz, _vp, _vp, _sz, _sz, _sz, f32, *tail, *res, _vp]
+        L.ar_attn_bwd_workspace.restype = _sz
+        L.ar_attn_bwd_workspace.argtypes = [_sz] * 8
+        L.ar_attn_bwd.restype = ctypes.c_int
+        L.ar_attn_bwd.argtypes = [hp, hp, hp, hp, _vp, _sz, _sz, hp, _vp, _vp] + [_sz] * 6 + [f32, *tail, hp, hp, hp, _vp,
+                                                                                             _sz, _vp]
         L.ar_set_launch_shape.restype = ctypes.c_int
         L.ar_set_launch_shape.argtypes = [ctypes.c_int] * 6
         ip = ctypes.POINTER(ctypes.c_int)
@@ -253,7 +290,7 @@ def prepare(func, *args, **kwargs) -> Prepared:
     step's all-reduce): a wrapper call spends about 0.45 us per tensor in
     checks and pointer lookups, a prepared call none.  ``func`` is one of the
     device calls of this module."""
-    if func not in _PREPARABLE and func not in _PREPARABLE_BLOCK:
+    if func not in _PREPARABLE and func not in _PREPARABLE_BLOCK and func not in _PREPARABLE_ATTN:
         raise ValueError(f"prepare() takes a device call of this module, not {func!r}")
     slot = []
     _tls.capture = slot
@@ -667,6 +704,264 @@ def ar_gemm_fp8(a_codes: Sequence, a_scales: Sequence, b_codes: Sequence, b_scal
           _stream(stream))
 
 
+# ------------------------------------------------------------------ attention
+
+_I32 = ("int32",)
+_I64 = ("int64",)
+
+
+def _here(tensors) -> None:
+    """Refuses tensors that are not all on the current device, on which the
+    call's work is queued."""
+    import torch
+    where = {t.device for t in tensors if t is not None and getattr(t, "device", None) is not None}
+    if len(where) > 1 or (where and next(iter(where)).index != torch.cuda.current_device()):
+        raise ValueError("all tensors of a call must be on the current device")
+
+
+def _heads(t, name: str, shape=None):
+    """ar_heads of a [tokens, heads, dim] tensor whose dim is contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dim() != 3 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} must have shape {'(tokens, heads, dim)' if shape is None else tuple(shape)}, "
+                         f"not {tuple(t.shape)}")
+    _typed(t, _BF16, name)
+    if t.element_size() != 2:
+        raise ValueError(f"{name} must have 2-byte elements")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name} must have contiguous heads")
+    # the stride of an axis of one element says nothing
+    return ctypes.pointer(_Heads(t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0))
+
+
+def _ints(t, kinds, name: str, count: int):
+    if t.dim() != 1 or t.shape[0] != count:
+        raise ValueError(f"{name} must have shape ({count},), not {tuple(t.shape)}")
+    _typed(t, kinds, name)
+    return _dev_ptr(t, 8 if kinds is _I64 else 4, name)
+
+
+def _kv_cache(cache):
+    """ar_kv_cache of (keys, values) or (keys, values, their scales)."""
+    if len(cache) not in (2, 4):
+        raise ValueError("a cache is (k, v), or (k, v, k_scales, v_scales) of E4M3 codes")
+    k, v = cache[:2]
+    small = len(cache) == 4
+    for t, name in ((k, "cache keys"), (v, "cache values")):
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a device tensor")
+        if t.dim() != 4 or tuple(t.shape) != tuple(k.shape):
+            raise ValueError(f"{name} must have shape (pages, page_size, heads, dim), both the same")
+        _typed(t, _E4M3 if small else _BF16, name)
+        if t.element_size() != (1 if small else 2):
+            raise ValueError(f"{name} must have {1 if small else 2}-byte elements")
+        if t.shape[3] > 1 and t.stride(3) != 1:
+            raise ValueError(f"{name} must have contiguous heads")
+        if _steps(t, 3) != _steps(k, 3):
+            raise ValueError("cache keys and values must have the same strides")
+    steps, ptrs = _steps(k, 3), [None, None]
+    scale_steps = (0, 0, 0)
+    if small:
+        scale_steps = _steps(cache[2], 3)
+        for i, (t, name) in enumerate(zip(cache[2:], ("cache k_scales", "cache v_scales"))):
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a device tensor")
+            if tuple(t.shape) != tuple(k.shape[:3]):
+                raise ValueError(f"{name} must have shape {tuple(k.shape[:3])}, not {tuple(t.shape)}")
+            _typed(t, _F32, name)
+            if _steps(t, 3) != scale_steps:
+                raise ValueError("cache scales must have the same strides")
+            ptrs[i] = t.data_ptr()
+    return ctypes.pointer(_KVCache(k.data_ptr(), v.data_ptr(), *ptrs, *k.shape, *steps, *scale_steps,
+                                   AR_FMT_E4M3 if small else AR_FMT_BF16))
+
+
+def _steps(t, n: int) -> tuple:
+    """The first n strides; 0 of an axis of one element."""
+    return tuple(t.stride(i) if t.shape[i] > 1 else 0 for i in range(n))
+
+
+def _lse(lse, shape):
+    if lse is None:
+        return None, 0, 0
+    if not lse.is_cuda:
+        raise ValueError("lse must be a device tensor")
+    if tuple(lse.shape) != tuple(shape):
+        raise ValueError(f"lse must have shape {tuple(shape)}, not {tuple(lse.shape)}")
+    _typed(lse, _F32, "lse")
+    return (lse.data_ptr(), *_steps(lse, 2))
+
+
+def _mask(scale, dim: int, window: int, sinks: int):
+    if window < 0 or sinks < 0:
+        raise ValueError("window and sinks must not be negative")
+    return ctypes.c_float(dim ** -0.5 if scale is None else scale), int(window), int(sinks)
+
+
+def kv_cache_empty(pages: int, page_size: int, heads: int, dim: int, device, e4m3: bool = False):
+    """An uninitialised cache: (k, v) of shape [pages, page_size, heads, dim]
+    in bf16, or (k, v, k_scales, v_scales) with E4M3 codes."""
+    import torch
+    shape = (int(pages), int(page_size), int(heads), int(dim))
+    kv = tuple(torch.empty(shape, device=device, dtype=torch.float8_e4m3fn if e4m3 else torch.bfloat16) for _ in range(2))
+    return kv + tuple(torch.empty(shape[:3], device=device, dtype=torch.float32) for _ in range(2)) if e4m3 else kv
+
+
+def rope_table(positions: int, rot: int, theta: float = 10000.0, device="cuda"):
+    """cos_sin of ar_rope_kv for positions 0 ... positions - 1: the angle of
+    pair i is position * theta^(-2 i / rot), formed in 64 bits."""
+    import torch
+    freq = float(theta) ** (-torch.arange(0, int(rot), 2, device=device, dtype=torch.float64) / int(rot))
+    angle = torch.arange(int(positions), device=device, dtype=torch.float64)[:, None] * freq
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+def ar_rope_kv(q, k, v, cos_sin, positions, q_out=None, k_out=None, cache=None, slots=None, pairs: bool = False,
+               inverse: bool = False, stream=None) -> None:
+    """Rotates q and k [tokens, heads, dim] by their positions (int32) into
+    q_out and k_out (each may be its input) and puts rotated keys and v into
+    the cache's slots (int64, page * page_size + place; -1: nowhere).
+    cos_sin [positions, rot] binary32: rot / 2 cosines, then the sines
+    (rope_table).  pairs: neighbours are rotated together, not elements half
+    of rot apart.  inverse: the rotation back, which is the gradient.  q, or
+    k and v, may be None."""
+    some = q if q is not None else k
+    if some is None:
+        raise ValueError("need q or k")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    if (cache is None) != (slots is None):
+        raise ValueError("cache and slots come together")
+    if some.dim() != 3:
+        raise ValueError("q and k must have shape (tokens, heads, dim)")
+    tokens, _, dim = some.shape
+    hq = 0 if q is None else int(q.shape[1])
+    hkv = 0 if k is None else int(k.shape[1])
+    qp = None if q is None else _heads(q, "q", (tokens, hq, dim))
+    qo = None if q is None else _heads(q_out, "q_out", (tokens, hq, dim))
+    kp = None if k is None else _heads(k, "k", (tokens, hkv, dim))
+    vp = None if v is None else _heads(v, "v", (tokens, hkv, dim))
+    ko = None if k_out is None else _heads(k_out, "k_out", (tokens, hkv, dim))
+    if cos_sin.dim() != 2:
+        raise ValueError("cos_sin must have shape (positions, rot)")
+    rows, rot = cos_sin.shape
+    _typed(cos_sin, _F32, "cos_sin")
+    tp = _dev_ptr(cos_sin, 4, "cos_sin")
+    pp = _ints(positions, _I32, "positions", tokens)
+    cp = sp = None
+    if cache is not None:
+        cp, sp = _kv_cache(cache), _ints(slots, _I64, "slots", tokens)
+    _here([q, k, v, cos_sin, positions, q_out, k_out, slots, *(cache or ())])
+    _call("ar_rope_kv", qp, kp, vp, tokens, hq, hkv, dim, tp, rows, rot, pp, qo, ko, cp, sp,
+          (AR_ROPE_PAIRS if pairs else 0) | (AR_ROPE_INVERSE if inverse else 0), _stream(stream))
+
+
+def attn_decode_workspace(seqs: int, hq: int, hkv: int, dim: int) -> int:
+    """Bytes of workspace with which ar_attn_decode spreads its keys over the
+    device (zero-initialised once by the caller)."""
+    return int(lib().ar_attn_decode_workspace(int(seqs), int(hq), int(hkv), int(dim)))
+
+
+def _table(table, seqs: int):
+    if table.dim() != 2 or table.shape[0] != seqs:
+        raise ValueError(f"table must have shape ({seqs}, pages), not {tuple(table.shape)}")
+    _typed(table, _I32, "table")
+    ptr, ld = _mat(table, (4,), "table")
+    return ptr, ld, int(table.shape[1])
+
+
+def ar_attn_decode(q, cache, table, lens, out, scale=None, window: int = 0, sinks: int = 0, lse=None, workspace=None,
+                   stream=None) -> None:
+    """Attention of one new token a sequence: q and out [seqs, hq, dim], the
+    sequence's keys (its own among them) in the cache's pages `table[seq]`
+    (int32), lens[seq] of them.  window 0: no window; scale None: dim ** -0.5.
+    attn_decode_workspace(...) zeroed bytes spread the keys over the device."""
+    qp = _heads(q, "q")
+    seqs, hq, dim = q.shape
+    op = _heads(out, "out", (seqs, hq, dim))
+    cp = _kv_cache(cache)
+    if int(cache[0].shape[3]) != dim:
+        raise ValueError(f"the cache's dim is {int(cache[0].shape[3])}, q's {dim}")
+    tp, ld, pages = _table(table, seqs)
+    np_ = _ints(lens, _I32, "lens", seqs)
+    sp, sb = _workspace(workspace)
+    _here([q, table, lens, out, lse, workspace, *cache])
+    _call("ar_attn_decode", qp, cp, tp, ld, pages, np_, seqs, hq, *_mask(scale, dim, window, sinks), op,
+          *_lse(lse, (seqs, hq)), sp, sb, _stream(stream))
+
+
+def ar_attn(q, k, v, cu_q, cu_k, out, scale=None, window: int = 0, sinks: int = 0, lse=None, stream=None) -> None:
+    """Attention of ragged sequences: q and out [rows, hq, dim], k and v
+    [rows, hkv, dim]; rows cu_q[b] ... cu_q[b + 1] - 1 (int32) are sequence
+    b's.  A query sees the keys up to its own position, within `window` (0:
+    all) or among the first `sinks`.  lse [rows, hq] binary32, any strides."""
+    qp, kp = _heads(q, "q"), _heads(k, "k")
+    (rows, hq, dim), (rows_k, hkv) = q.shape, k.shape[:2]
+    vp, op = _heads(v, "v", (rows_k, hkv, dim)), _heads(out, "out", (rows, hq, dim))
+    if k.shape[2] != dim:
+        raise ValueError(f"k must have heads of {dim}, not {k.shape[2]}")
+    seqs = int(cu_q.shape[0]) - 1 if cu_q.dim() == 1 else -1
+    if seqs < 0:
+        raise ValueError("cu_q must have shape (seqs + 1,)")
+    qc, kc = _ints(cu_q, _I32, "cu_q", seqs + 1), _ints(cu_k, _I32, "cu_k", seqs + 1)
+    _here([q, k, v, cu_q, cu_k, out, lse])
+    _call("ar_attn", qp, kp, vp, qc, kc, seqs, rows, rows_k, hq, hkv, dim, *_mask(scale, dim, window, sinks), op,
+          *_lse(lse, (rows, hq)), _stream(stream))
+
+
+def ar_attn_paged(q, cache, table, lens, cu_q, out, scale=None, window: int = 0, sinks: int = 0, lse=None,
+                  stream=None) -> None:
+    """ar_attn with the keys in a cache's pages (as in ar_attn_decode): the
+    queries are the last of each sequence's lens[b] positions."""
+    qp = _heads(q, "q")
+    rows, hq, dim = q.shape
+    op = _heads(out, "out", (rows, hq, dim))
+    cp = _kv_cache(cache)
+    if int(cache[0].shape[3]) != dim:
+        raise ValueError(f"the cache's dim is {int(cache[0].shape[3])}, q's {dim}")
+    seqs = int(cu_q.shape[0]) - 1 if cu_q.dim() == 1 else -1
+    if seqs < 0:
+        raise ValueError("cu_q must have shape (seqs + 1,)")
+    tp, ld, pages = _table(table, seqs)
+    np_, qc = _ints(lens, _I32, "lens", seqs), _ints(cu_q, _I32, "cu_q", seqs + 1)
+    _here([q, table, lens, cu_q, out, lse, *cache])
+    _call("ar_attn_paged", qp, cp, tp, ld, pages, np_, qc, seqs, rows, hq, *_mask(scale, dim, window, sinks), op,
+          *_lse(lse, (rows, hq)), _stream(stream))
+
+
+def attn_bwd_workspace(rows_q: int, rows_k: int, seqs: int, hq: int, hkv: int, dim: int, window: int = 0,
+                       sinks: int = 0) -> int:
+    """Bytes of workspace that ar_attn_bwd needs."""
+    return int(lib().ar_attn_bwd_workspace(int(rows_q), int(rows_k), int(seqs), int(hq), int(hkv), int(dim), int(window),
+                                           int(sinks)))
+
+
+def ar_attn_bwd(q, k, v, out, lse, d_out, cu_q, cu_k, dq=None, dk=None, dv=None, workspace=None, scale=None,
+                window: int = 0, sinks: int = 0, stream=None) -> None:
+    """Gradient of ar_attn: dq, and / or dk and dv (summed over the query heads
+    of a key head), from out and lse of ar_attn and the gradient d_out.  Needs
+    attn_bwd_workspace(...) bytes."""
+    qp, kp = _heads(q, "q"), _heads(k, "k")
+    (rows, hq, dim), (rows_k, hkv) = q.shape, k.shape[:2]
+    shape_q, shape_k = (rows, hq, dim), (rows_k, hkv, dim)
+    kp, vp = _heads(k, "k", shape_k), _heads(v, "v", shape_k)
+    op, gp = _heads(out, "out", shape_q), _heads(d_out, "d_out", shape_q)
+    if lse is None:
+        raise ValueError("lse is needed")
+    dqp = None if dq is None else _heads(dq, "dq", shape_q)
+    dkp = None if dk is None else _heads(dk, "dk", shape_k)
+    dvp = None if dv is None else _heads(dv, "dv", shape_k)
+    seqs = int(cu_q.shape[0]) - 1 if cu_q.dim() == 1 else -1
+    if seqs < 0:
+        raise ValueError("cu_q must have shape (seqs + 1,)")
+    qc, kc = _ints(cu_q, _I32, "cu_q", seqs + 1), _ints(cu_k, _I32, "cu_k", seqs + 1)
+    sp, sb = _workspace(workspace)
+    _here([q, k, v, out, lse, d_out, cu_q, cu_k, dq, dk, dv, workspace])
+    _call("ar_attn_bwd", qp, kp, vp, op, *_lse(lse, (rows, hq)), gp, qc, kc, seqs, rows, rows_k, hq, hkv, dim,
+          *_mask(scale, dim, window, sinks), dqp, dkp, dvp, sp, sb, _stream(stream))
+
+
 def ar_err_init(d_err, stream=None) -> None:
     (ep,) = _bufs([d_err], 8, "d_err", 2)
     _call("ar_err_init", ep, _stream(stream))
@@ -692,3 +987,4 @@ _PREPARABLE = frozenset([ar_reduce_oneshot, ar_reduce_2stage, ar_reduce_2stage_s
                          ar_unpack_fused, ar_unpack_fused_wait, ar_rd_schedule, ar_reduce_ubatch,
                          ar_reduce_ubatch_flags, ar_quantize_fp8, ar_reduce_fp8, ar_err_init])
 _PREPARABLE_BLOCK = frozenset([ar_reduce_norm, ar_norm_bwd, ar_quantize_block, ar_gemm_fp8])
+_PREPARABLE_ATTN = frozenset([ar_rope_kv, ar_attn_decode, ar_attn, ar_attn_paged, ar_attn_bwd])

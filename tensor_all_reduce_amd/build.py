@@ -16,7 +16,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libarcore.so")
 BENCH_LIB = os.path.join(HERE, "libarbench.so")
 SOURCES = ["ar_api.hip", "ar_reduce.hip", "ar_fused.hip", "ar_fp8.hip", "ar_norm.hip", "ar_block8.hip",
-           "ar_gemm8.hip"]
+           "ar_gemm8.hip", "ar_rope.hip", "ar_attn.hip", "ar_attn_decode.hip", "ar_attn_bwd.hip"]
 BENCH_SOURCES = ["ar_bench.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -61,7 +61,7 @@ def _link(objs, out, extra, verbose):
     os.replace(tmp, out)
 
 
-def build(verbose: bool = False, jobs: int = 4) -> str:
+def build(verbose: bool = False, jobs: int = 8) -> str:
     """Compile libarcore.so (the library) and libarbench.so (timing helpers
     and a copy kernel used only by bench.py; linked against libarcore.so)."""
     objs = _compile(SOURCES + BENCH_SOURCES, verbose, jobs)

@@ -17,6 +17,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
+#include <utility>
 
 #include "ar.h"
 #include "ar_internal.hpp"
@@ -308,6 +309,212 @@ bool side_by_side(const void* p, const void* q, size_t pitch, size_t width) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
   const size_t d = (a < b ? b - a : a - b) % pitch;
   return d >= width && pitch - d >= width;
+}
+
+// ---- attention --------------------------------------------------------------
+
+// A strided array of up to four axes, the innermost of `width` bytes; strides
+// in bytes.  Axes of one element have no stride.
+struct Grid {
+  uintptr_t at;
+  size_t n[3], stride[3], width;
+};
+
+Grid grid_of(const void* p, size_t elem, size_t width, const size_t (&n)[3], const size_t (&stride)[3]) {
+  Grid g{reinterpret_cast<uintptr_t>(p), {}, {}, width * elem};
+  int k = 0;
+  for (int i = 0; i < 3; ++i)
+    if (n[i] > 1) {
+      g.n[k] = n[i];
+      g.stride[k++] = stride[i] * elem;
+    }
+  for (int i = k; i < 3; ++i) g.n[i] = 1;
+  // widest stride first
+  for (int i = 0; i < k; ++i)
+    for (int j = i + 1; j < k; ++j)
+      if (g.stride[j] > g.stride[i]) {
+        std::swap(g.stride[i], g.stride[j]);
+        std::swap(g.n[i], g.n[j]);
+      }
+  return g;
+}
+
+// Bytes from the first to the last of axes i and inwards, or false if they
+// are more than the address space holds.
+bool reach(const Grid& g, int i, size_t* bytes) {
+  size_t w = g.width;
+  for (; i < 3; ++i) {
+    if (g.n[i] == 1) continue;
+    if (mul_overflows(g.n[i] - 1, g.stride[i])) return false;
+    const size_t x = (g.n[i] - 1) * g.stride[i];
+    if (w + x < w) return false;
+    w += x;
+  }
+  *bytes = w;
+  return true;
+}
+
+// Whether every element of an output has a place of its own.
+bool distinct(const Grid& g) {
+  for (int i = 0; i < 3; ++i) {
+    size_t w;
+    if (g.n[i] > 1 && (!reach(g, i + 1, &w) || g.stride[i] < w)) return false;
+  }
+  return true;
+}
+
+bool same_grid(const Grid& a, const Grid& b) {
+  if (a.at != b.at || a.width != b.width) return false;
+  for (int i = 0; i < 3; ++i)
+    if (a.n[i] != b.n[i] || (a.n[i] > 1 && a.stride[i] != b.stride[i])) return false;
+  return true;
+}
+
+// Whether two arrays share no byte: their spans do not meet, or they lie side
+// by side within the steps of a stride that both have and of which both's
+// wider strides are multiples.
+bool apart(const Grid& a, const Grid& b) {
+  size_t wa, wb;
+  if (!reach(a, 0, &wa) || !reach(b, 0, &wb)) return false;
+  const Span x{a.at, a.at + wa < a.at ? ~(uintptr_t)0 : a.at + wa}, y{b.at, b.at + wb < b.at ? ~(uintptr_t)0 : b.at + wb};
+  if (!overlap(x, y)) return true;
+  for (int i = 0; i < 3 && a.n[i] > 1; ++i)
+    for (int j = 0; j < 3 && b.n[j] > 1; ++j) {
+      const size_t s = a.stride[i];
+      if (s == 0 || s != b.stride[j]) continue;
+      bool fits = true;
+      for (int k = 0; k < i; ++k) fits &= a.stride[k] % s == 0;
+      for (int k = 0; k < j; ++k) fits &= b.stride[k] % s == 0;
+      if (!fits || !reach(a, i + 1, &wa) || !reach(b, j + 1, &wb)) continue;
+      // b begins d bytes after a, modulo the stride
+      const size_t d = a.at <= b.at ? (b.at - a.at) % s : (s - (a.at - b.at) % s) % s;
+      if (d >= wa && s - d >= wb) return true;
+    }
+  return false;
+}
+
+constexpr size_t kMaxRows = (size_t)1 << 30;
+
+// Checks a matrix [tokens][heads][dim] and gives its grid.
+int check_heads(const ar_heads* m, size_t tokens, size_t heads, size_t dim, bool output, Grid* g) {
+  if (!m || !m->data) return AR_ERR_INVALID;
+  if (!aligned16(m->data) || ((tokens > 1 ? m->token_stride : 0) & 7u) || ((heads > 1 ? m->head_stride : 0) & 7u))
+    return AR_ERR_ALIGN;
+  if (mul_overflows(m->token_stride, 2) || mul_overflows(m->head_stride, 2)) return AR_ERR_INVALID;
+  *g = grid_of(m->data, 2, dim, {tokens, heads, 1}, {m->token_stride, m->head_stride, 0});
+  size_t w;
+  if (!reach(*g, 0, &w)) return AR_ERR_INVALID;
+  return output && !distinct(*g) ? AR_ERR_ALIAS : AR_OK;
+}
+
+ar::HeadRows rows_arg(const ar_heads* m) {
+  return m ? ar::HeadRows{static_cast<const uint16_t*>(m->data), m->token_stride, m->head_stride} : ar::HeadRows{};
+}
+ar::HeadOut out_arg(const ar_heads* m) {
+  return m ? ar::HeadOut{static_cast<uint16_t*>(m->data), m->token_stride, m->head_stride} : ar::HeadOut{};
+}
+
+// Checks a cache; grids of keys, values and scales (ng of them).
+int check_cache(const ar_kv_cache& c, bool output, ar::Pages* p, Grid* g, int* ng) {
+  if (c.fmt != AR_FMT_BF16 && c.fmt != AR_FMT_E4M3) return AR_ERR_INVALID;
+  const bool small = c.fmt == AR_FMT_E4M3;
+  if (!c.k || !c.v || (small && (!c.k_scales || !c.v_scales))) return AR_ERR_INVALID;
+  if (c.pages == 0 || c.page_size == 0 || c.heads == 0 || mul_overflows(c.pages, c.page_size)) return AR_ERR_INVALID;
+  if (c.pages * c.page_size >> 31 || c.heads >> 16) return AR_ERR_UNSUPPORTED;
+  const size_t n[3] = {c.pages, c.page_size, c.heads}, es = small ? 1 : 2, odd = small ? 15 : 7;
+  const size_t s[3] = {c.page_stride, c.token_stride, c.head_stride};
+  const size_t ss[3] = {c.scale_page_stride, c.scale_token_stride, c.scale_head_stride};
+  for (int i = 0; i < 3; ++i) {
+    if (n[i] > 1 && (s[i] & odd)) return AR_ERR_ALIGN;
+    if (mul_overflows(s[i], 4) || (small && mul_overflows(ss[i], 4))) return AR_ERR_INVALID;
+  }
+  if (!aligned16(c.k) || !aligned16(c.v)) return AR_ERR_ALIGN;
+  *ng = 0;
+  g[(*ng)++] = grid_of(c.k, es, c.dim, n, s);
+  g[(*ng)++] = grid_of(c.v, es, c.dim, n, s);
+  if (small) {
+    if ((reinterpret_cast<uintptr_t>(c.k_scales) | reinterpret_cast<uintptr_t>(c.v_scales)) & 3u) return AR_ERR_ALIGN;
+    g[(*ng)++] = grid_of(c.k_scales, 4, 1, n, ss);
+    g[(*ng)++] = grid_of(c.v_scales, 4, 1, n, ss);
+  }
+  for (int i = 0; i < *ng; ++i) {
+    size_t w;
+    if (!reach(g[i], 0, &w)) return AR_ERR_INVALID;
+    if (!output) continue;
+    if (!distinct(g[i])) return AR_ERR_ALIAS;
+    for (int j = 0; j < i; ++j)
+      if (!apart(g[i], g[j])) return AR_ERR_ALIAS;
+  }
+  unsigned shift = 32, magic = 0;
+  if (c.page_size > 1) {
+    // x / d = (x m) >> (31 + l) with 2^(l-1) < d <= 2^l, m = ceil(2^(31+l) / d), for x < 2^31
+    unsigned l = 1;
+    while (((size_t)1 << l) < c.page_size) ++l;
+    magic = (unsigned)((((uint64_t)1 << (31 + l)) + c.page_size - 1) / c.page_size);
+    shift = l - 1;
+  }
+  *p = ar::Pages{c.k, c.v, c.k_scales, c.v_scales, c.page_stride, c.token_stride, c.head_stride, c.scale_page_stride,
+                 c.scale_token_stride, c.scale_head_stride, (unsigned)c.pages, (unsigned)c.page_size, magic, shift};
+  return AR_OK;
+}
+
+bool dim_ok(size_t dim) { return dim >= 16 && dim % 16 == 0; }
+
+// Checks heads, mask and scale, and fills them in.
+int check_mask(size_t hq, size_t hkv, size_t dim, float scale, size_t window, size_t sinks, ar::AttnArgs* a) {
+  if (hq == 0 || hkv == 0 || hq % hkv || !dim_ok(dim)) return AR_ERR_INVALID;
+  if (!(scale > 0.0f && scale <= 3.402823466e38f)) return AR_ERR_INVALID;
+  if (dim > AR_ATTN_MAX_DIM || hq >> 16) return AR_ERR_UNSUPPORTED;
+  a->hq = (unsigned)hq;
+  a->hkv = (unsigned)hkv;
+  a->dim = (unsigned)dim;
+  a->scale = scale;
+  a->window = window == 0 || window > kMaxRows ? 0x7FFFFFFFu : (unsigned)window;
+  a->sinks = (unsigned)(sinks < kMaxRows ? sinks : kMaxRows);
+  return AR_OK;
+}
+
+// int32 numbers on the device.
+int check_ints(const int32_t* p, size_t n, Grid* g) {
+  if (!p) return AR_ERR_INVALID;
+  if (reinterpret_cast<uintptr_t>(p) & 3u) return AR_ERR_ALIGN;
+  if (mul_overflows(n, 4)) return AR_ERR_INVALID;
+  *g = grid_of(p, 4, n, {1, 1, 1}, {0, 0, 0});
+  return AR_OK;
+}
+
+int check_table(const int32_t* table, size_t stride, size_t pages, size_t seqs, const ar_kv_cache& c, ar::AttnArgs* a, Grid* g) {
+  if (!table || pages == 0 || (seqs > 1 && stride < pages)) return AR_ERR_INVALID;
+  if (reinterpret_cast<uintptr_t>(table) & 3u) return AR_ERR_ALIGN;
+  if (mul_overflows(stride, 4) || mul_overflows(pages, 4)) return AR_ERR_INVALID;
+  *g = grid_of(table, 4, pages, {seqs, 1, 1}, {stride, 0, 0});
+  size_t w;
+  if (!reach(*g, 0, &w)) return AR_ERR_INVALID;
+  a->table = table;
+  a->table_ld = stride;
+  const size_t most = pages > kMaxRows / c.page_size ? kMaxRows : pages * c.page_size;
+  a->capacity = (unsigned)most;
+  return AR_OK;
+}
+
+int check_lse(const float* lse, size_t ts, size_t hs, size_t rows, size_t heads, Grid* g) {
+  if (reinterpret_cast<uintptr_t>(lse) & 3u) return AR_ERR_ALIGN;
+  if (mul_overflows(ts, 4) || mul_overflows(hs, 4)) return AR_ERR_INVALID;
+  *g = grid_of(lse, 4, 1, {rows, heads, 1}, {ts, hs, 0});
+  size_t w;
+  return reach(*g, 0, &w) ? AR_OK : AR_ERR_INVALID;
+}
+
+// An output shares no byte with an input (but may be exactly `twin`) nor with
+// another output.
+int check_apart(const Grid* in, int ni, const Grid* out, int no, int twin_in = -1, int twin_out = -1) {
+  for (int o = 0; o < no; ++o) {
+    for (int i = 0; i < ni; ++i)
+      if (!(i == twin_in && o == twin_out && same_grid(in[i], out[o])) && !apart(in[i], out[o])) return AR_ERR_ALIAS;
+    for (int q = 0; q < o; ++q)
+      if (!apart(out[q], out[o])) return AR_ERR_ALIAS;
+  }
+  return AR_OK;
 }
 
 bool eps_ok(float eps) { return eps >= 0.0f && eps <= 3.402823466e38f; }
@@ -865,6 +1072,267 @@ int ar_gemm_fp8(const ar_fp8_matrix* a, const ar_fp8_matrix* b, void* const* c, 
   if ((rc = resolve(&L, stream))) return rc;
   return hip_status(ar::launch_gemm_fp8(L, g, G, b[0].scale_fmt == AR_SCALE_E8M0, b[0].block_rows == 1,
                                         out_fmt == AR_FMT_F32, need ? workspace : nullptr));
+}
+
+int ar_rope_kv(const ar_heads* q, const ar_heads* k, const ar_heads* v, size_t tokens, size_t hq, size_t hkv, size_t dim,
+               const float* cos_sin, size_t table_rows, size_t rot, const int32_t* positions, const ar_heads* q_out,
+               const ar_heads* k_out, const ar_kv_cache* cache, const int64_t* slots, int flags, void* stream) {
+  if (flags & ~(AR_ROPE_PAIRS | AR_ROPE_INVERSE) || !dim_ok(dim) || rot % 16 || rot > dim) return AR_ERR_INVALID;
+  if ((hq != 0) != (q != nullptr) || (q != nullptr) != (q_out != nullptr) || (hkv != 0) != (k != nullptr)) return AR_ERR_INVALID;
+  if ((k && !k_out && !cache) || (k_out && !k) || (cache && (!k || !v || cache->heads != hkv || cache->dim != dim)))
+    return AR_ERR_INVALID;
+  if (dim > AR_ATTN_MAX_DIM || tokens > kMaxRows || hq >> 16 || hkv >> 16) return AR_ERR_UNSUPPORTED;
+  if (tokens == 0 || hq + hkv == 0) return AR_OK;
+  if (rot && (!cos_sin || table_rows == 0 || !positions)) return AR_ERR_INVALID;
+  if (cache && !slots) return AR_ERR_INVALID;
+  if (table_rows >> 31 || tokens * (hq + 2 * hkv) > 0x7FFFFFFF) return AR_ERR_UNSUPPORTED;
+  if ((rot && !aligned16(cos_sin)) || (reinterpret_cast<uintptr_t>(positions) & 3u) ||
+      (cache && (reinterpret_cast<uintptr_t>(slots) & 7u)))
+    return AR_ERR_ALIGN;
+  // inputs 0 and 1 may be outputs 0 and 1
+  Grid in[6], out[6];
+  int ni = 0, no = 0, rc;
+  ar::RopeArgs a{};
+  const Grid none = grid_of(nullptr, 1, 0, {1, 1, 1}, {0, 0, 0});
+  in[0] = in[1] = out[0] = out[1] = none;
+  if (q && ((rc = check_heads(q, tokens, hq, dim, false, &in[0])) || (rc = check_heads(q_out, tokens, hq, dim, true, &out[0]))))
+    return rc;
+  if (k && (rc = check_heads(k, tokens, hkv, dim, false, &in[1]))) return rc;
+  if (k_out && (rc = check_heads(k_out, tokens, hkv, dim, true, &out[1]))) return rc;
+  ni = no = 2;
+  if (cache) {
+    if ((rc = check_heads(v, tokens, hkv, dim, false, &in[ni++]))) return rc;
+    int ng;
+    if ((rc = check_cache(*cache, true, &a.cache, out + no, &ng))) return rc;
+    no += ng;
+    in[ni++] = grid_of(slots, 8, tokens, {1, 1, 1}, {0, 0, 0});
+  }
+  if (rot) {
+    if (mul3_overflows(table_rows, rot, 4)) return AR_ERR_INVALID;
+    in[ni++] = grid_of(cos_sin, 4, table_rows * rot, {1, 1, 1}, {0, 0, 0});
+    in[ni++] = grid_of(positions, 4, tokens, {1, 1, 1}, {0, 0, 0});
+  }
+  for (int o = 0; o < no; ++o) {
+    if (out[o].at == 0) continue;
+    for (int i = 0; i < ni; ++i)
+      if (in[i].at && !(i == o && i < 2 && same_grid(in[i], out[o])) && !apart(in[i], out[o])) return AR_ERR_ALIAS;
+    for (int p = 0; p < o; ++p)
+      if (out[p].at && !apart(out[p], out[o])) return AR_ERR_ALIAS;
+  }
+  a.q = rows_arg(q);
+  a.k = rows_arg(k);
+  a.v = rows_arg(v);
+  a.q_out = out_arg(q_out);
+  a.k_out = out_arg(k_out);
+  a.cos_sin = cos_sin;
+  a.positions = positions;
+  a.slots = slots;
+  a.tokens = tokens;
+  a.table_rows = (unsigned)table_rows;
+  a.hq = (unsigned)hq;
+  a.hkv = (unsigned)hkv;
+  a.dim = (unsigned)dim;
+  a.rot = (unsigned)rot;
+  a.pairs = (flags & AR_ROPE_PAIRS) != 0;
+  a.inverse = (flags & AR_ROPE_INVERSE) != 0;
+  a.e4m3 = cache && cache->fmt == AR_FMT_E4M3;
+  ar::Launch L;
+  if ((rc = resolve(&L, stream))) return rc;
+  return hip_status(ar::launch_rope_kv(L, a));
+}
+
+size_t ar_attn_decode_workspace(size_t seqs, size_t hq, size_t hkv, size_t dim) {
+  if (seqs == 0 || seqs > kMaxRows || hq == 0 || hkv == 0 || hq % hkv || hq >> 16 || !dim_ok(dim) || dim > AR_ATTN_MAX_DIM) return 0;
+  return ar::attn_decode_workspace(seqs, hq, hkv, dim);
+}
+
+int ar_attn_decode(const ar_heads* q, const ar_kv_cache* cache, const int32_t* table, size_t table_stride,
+                   size_t table_pages, const int32_t* lens, size_t seqs, size_t hq, float scale, size_t window,
+                   size_t sinks, const ar_heads* out, float* lse, size_t lse_ts, size_t lse_hs, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+  if (!cache) return AR_ERR_INVALID;
+  ar::AttnArgs a{};
+  int rc = check_mask(hq, cache->heads, cache->dim, scale, window, sinks, &a);
+  if (rc) return rc;
+  if (seqs == 0) return AR_OK;
+  if (seqs > kMaxRows) return AR_ERR_UNSUPPORTED;
+  Grid in[8], og[3];
+  int ni = 0, no = 0, ng;
+  if ((rc = check_heads(q, seqs, hq, cache->dim, false, &in[ni++])) ||
+      (rc = check_cache(*cache, false, &a.cache, in + ni, &ng)))
+    return rc;
+  ni += ng;
+  if ((rc = check_table(table, table_stride, table_pages, seqs, *cache, &a, &in[ni++])) ||
+      (rc = check_ints(lens, seqs, &in[ni++])) || (rc = check_heads(out, seqs, hq, cache->dim, true, &og[no++])))
+    return rc;
+  if (lse) {
+    if ((rc = check_lse(lse, lse_ts, lse_hs, seqs, hq, &og[no]))) return rc;
+    if (!distinct(og[no++])) return AR_ERR_ALIAS;
+  }
+  if (!aligned16(workspace)) return AR_ERR_ALIGN;
+  size_t need = ar_attn_decode_workspace(seqs, hq, cache->heads, cache->dim);
+  if (!workspace || workspace_bytes < need) need = 0;
+  if (need) og[no++] = grid_of(workspace, 1, need, {1, 1, 1}, {0, 0, 0});
+  if ((rc = check_apart(in, ni, og, no, 0, 0))) return rc;
+  // the row of all tiles is counted in 32 bits
+  const size_t tiles = a.capacity / 128 + 3, heads = cache->heads * (((hq / cache->heads) + 15) / 16);
+  if (mul3_overflows(tiles, heads, seqs) || tiles * heads * seqs >> 32) return AR_ERR_UNSUPPORTED;
+  a.q = rows_arg(q);
+  a.out = out_arg(out);
+  a.lens = lens;
+  a.lse = lse;
+  a.lse_ts = lse_ts;
+  a.lse_hs = lse_hs;
+  a.seqs = (unsigned)seqs;
+  ar::Launch L;
+  if ((rc = resolve(&L, stream))) return rc;
+  return hip_status(ar::launch_attn_decode(L, a, cache->fmt == AR_FMT_E4M3, need ? workspace : nullptr));
+}
+
+}  // extern "C"
+
+namespace {
+
+// What ar_attn and ar_attn_paged have in common: grids in[0..ni) are their
+// keys' and values' by now.
+int attn_impl(const ar_heads* q, const int32_t* cu_q, size_t seqs, size_t rows_q, size_t hq, size_t dim, const ar_heads* out,
+              float* lse, size_t lse_ts, size_t lse_hs, void* stream, ar::KeySource src, ar::AttnArgs& a, Grid* in, int ni) {
+  Grid og[2];
+  int rc, no = 0;
+  const int twin = ni;
+  if ((rc = check_heads(q, rows_q, hq, dim, false, &in[ni++])) || (rc = check_ints(cu_q, seqs + 1, &in[ni++])) ||
+      (rc = check_heads(out, rows_q, hq, dim, true, &og[no++])))
+    return rc;
+  if (lse) {
+    if ((rc = check_lse(lse, lse_ts, lse_hs, rows_q, hq, &og[no]))) return rc;
+    if (!distinct(og[no++])) return AR_ERR_ALIAS;
+  }
+  if ((rc = check_apart(in, ni, og, no, twin, 0))) return rc;
+  if (!ar::attn_fits(rows_q, seqs, hq)) return AR_ERR_UNSUPPORTED;
+  a.q = rows_arg(q);
+  a.out = out_arg(out);
+  a.cu_q = cu_q;
+  a.lse = lse;
+  a.lse_ts = lse_ts;
+  a.lse_hs = lse_hs;
+  a.rows_q = (unsigned)rows_q;
+  a.seqs = (unsigned)seqs;
+  ar::Launch L;
+  if ((rc = resolve(&L, stream))) return rc;
+  return hip_status(ar::launch_attn(L, a, src));
+}
+
+}  // namespace
+
+extern "C" {
+
+int ar_attn(const ar_heads* q, const ar_heads* k, const ar_heads* v, const int32_t* cu_q, const int32_t* cu_k, size_t seqs,
+            size_t rows_q, size_t rows_k, size_t hq, size_t hkv, size_t dim, float scale, size_t window, size_t sinks,
+            const ar_heads* out, float* lse, size_t lse_ts, size_t lse_hs, void* stream) {
+  ar::AttnArgs a{};
+  int rc = check_mask(hq, hkv, dim, scale, window, sinks, &a);
+  if (rc) return rc;
+  if (rows_q > kMaxRows || rows_k > kMaxRows || seqs > kMaxRows) return AR_ERR_UNSUPPORTED;
+  if (seqs == 0 || rows_q == 0) return AR_OK;
+  Grid in[5];
+  int ni = 0;
+  if (rows_k && ((rc = check_heads(k, rows_k, hkv, dim, false, &in[ni++])) ||
+                 (rc = check_heads(v, rows_k, hkv, dim, false, &in[ni++]))))
+    return rc;
+  if ((rc = check_ints(cu_k, seqs + 1, &in[ni++]))) return rc;
+  a.k = rows_arg(k);
+  a.v = rows_arg(v);
+  a.cu_k = cu_k;
+  a.rows_k = (unsigned)rows_k;
+  return attn_impl(q, cu_q, seqs, rows_q, hq, dim, out, lse, lse_ts, lse_hs, stream, ar::kKeyRows, a, in, ni);
+}
+
+int ar_attn_paged(const ar_heads* q, const ar_kv_cache* cache, const int32_t* table, size_t table_stride,
+                  size_t table_pages, const int32_t* lens, const int32_t* cu_q, size_t seqs, size_t rows_q, size_t hq,
+                  float scale, size_t window, size_t sinks, const ar_heads* out, float* lse, size_t lse_ts, size_t lse_hs,
+                  void* stream) {
+  if (!cache) return AR_ERR_INVALID;
+  ar::AttnArgs a{};
+  int rc = check_mask(hq, cache->heads, cache->dim, scale, window, sinks, &a);
+  if (rc) return rc;
+  if (rows_q > kMaxRows || seqs > kMaxRows) return AR_ERR_UNSUPPORTED;
+  if (seqs == 0 || rows_q == 0) return AR_OK;
+  Grid in[8];
+  int ni;
+  if ((rc = check_cache(*cache, false, &a.cache, in, &ni)) ||
+      (rc = check_table(table, table_stride, table_pages, seqs, *cache, &a, &in[ni++])) ||
+      (rc = check_ints(lens, seqs, &in[ni++])))
+    return rc;
+  a.lens = lens;
+  return attn_impl(q, cu_q, seqs, rows_q, hq, cache->dim, out, lse, lse_ts, lse_hs, stream,
+                   cache->fmt == AR_FMT_E4M3 ? ar::kKeyPagesE4M3 : ar::kKeyPages, a, in, ni);
+}
+
+size_t ar_attn_bwd_workspace(size_t rows_q, size_t rows_k, size_t seqs, size_t hq, size_t hkv, size_t dim, size_t window,
+                             size_t sinks) {
+  ar::AttnArgs a{};
+  if (check_mask(hq, hkv, dim, 1.0f, window, sinks, &a)) return 0;
+  if (rows_q > kMaxRows || rows_k > kMaxRows || seqs > kMaxRows || seqs == 0) return 0;
+  return ar::attn_bwd_workspace(rows_q, rows_k, seqs, hq, hkv, dim, a.window, a.sinks);
+}
+
+int ar_attn_bwd(const ar_heads* q, const ar_heads* k, const ar_heads* v, const ar_heads* out, const float* lse,
+                size_t lse_ts, size_t lse_hs, const ar_heads* d_out, const int32_t* cu_q, const int32_t* cu_k, size_t seqs,
+                size_t rows_q, size_t rows_k, size_t hq, size_t hkv, size_t dim, float scale, size_t window, size_t sinks,
+                const ar_heads* dq, const ar_heads* dk, const ar_heads* dv, void* workspace, size_t workspace_bytes,
+                void* stream) {
+  ar::AttnBwdArgs b{};
+  ar::AttnArgs& a = b.f;
+  int rc = check_mask(hq, hkv, dim, scale, window, sinks, &a);
+  if (rc) return rc;
+  if ((dk != nullptr) != (dv != nullptr) || (!dq && !dk)) return AR_ERR_INVALID;
+  if (rows_q > kMaxRows || rows_k > kMaxRows || seqs > kMaxRows) return AR_ERR_UNSUPPORTED;
+  if (seqs == 0 || rows_q + rows_k == 0) return AR_OK;
+  Grid in[8], og[4];
+  int ni = 0, no = 0;
+  if (rows_q) {
+    if ((rc = check_heads(q, rows_q, hq, dim, false, &in[ni++])) || (rc = check_heads(out, rows_q, hq, dim, false, &in[ni++])) ||
+        (rc = check_heads(d_out, rows_q, hq, dim, false, &in[ni++])))
+      return rc;
+    if (!lse) return AR_ERR_INVALID;
+    if ((rc = check_lse(lse, lse_ts, lse_hs, rows_q, hq, &in[ni++]))) return rc;
+    if (dq && (rc = check_heads(dq, rows_q, hq, dim, true, &og[no++]))) return rc;
+  }
+  if (rows_k) {
+    if ((rc = check_heads(k, rows_k, hkv, dim, false, &in[ni++])) || (rc = check_heads(v, rows_k, hkv, dim, false, &in[ni++])))
+      return rc;
+    if (dk && ((rc = check_heads(dk, rows_k, hkv, dim, true, &og[no++])) || (rc = check_heads(dv, rows_k, hkv, dim, true, &og[no++]))))
+      return rc;
+  }
+  if ((rc = check_ints(cu_q, seqs + 1, &in[ni++])) || (rc = check_ints(cu_k, seqs + 1, &in[ni++]))) return rc;
+  const size_t need = ar_attn_bwd_workspace(rows_q, rows_k, seqs, hq, hkv, dim, window, sinks);
+  if (need) {
+    if (!workspace || workspace_bytes < need) return AR_ERR_INVALID;
+    if (!aligned16(workspace)) return AR_ERR_ALIGN;
+    og[no++] = grid_of(workspace, 1, need, {1, 1, 1}, {0, 0, 0});
+  }
+  if ((rc = check_apart(in, ni, og, no))) return rc;
+  if (!ar::attn_fits(rows_q, seqs, hq) || !ar::attn_fits(rows_k, seqs, hq)) return AR_ERR_UNSUPPORTED;
+  a.q = rows_arg(q);
+  a.k = rows_arg(k);
+  a.v = rows_arg(v);
+  a.cu_q = cu_q;
+  a.cu_k = cu_k;
+  a.lse = const_cast<float*>(lse);
+  a.lse_ts = lse_ts;
+  a.lse_hs = lse_hs;
+  a.rows_q = (unsigned)rows_q;
+  a.rows_k = (unsigned)rows_k;
+  a.seqs = (unsigned)seqs;
+  b.out = rows_arg(out);
+  b.d_out = rows_arg(d_out);
+  b.dq = out_arg(dq);
+  b.dk = out_arg(dk);
+  b.dv = out_arg(dv);
+  b.workspace = workspace;
+  ar::Launch L;
+  if ((rc = resolve(&L, stream))) return rc;
+  return hip_status(ar::launch_attn_bwd(L, b));
 }
 
 int ar_err_init(uint64_t* d_err, void* stream) {

@@ -1,0 +1,491 @@
+// Attention of one new token a sequence over a paged cache.
+//
+// Bound by memory: a key and its value are read once for all query heads that
+// share them.  A workgroup takes 128 keys of one key head at a time, a wave
+// 32 of them; scores S^T = K Q^T and results O^T = V^T P^T are 16 x 16 x 32
+// products whose columns are the (up to 16) query heads of the key head.
+//
+// The keys of all sequences and key heads are one long row of tiles, which
+// is cut into equal runs, one a workgroup, whatever the lengths are.  A
+// sequence that is cut is joined by the last workgroup that arrives with a
+// part, which adds all parts in their order, so that the result does not
+// depend on which one was last.
+//
+// Keys and values are copied to LDS past the registers, two steps of a wave
+// ahead: 64 to 128 KiB a CU are on their way, which is what its share of the
+// memory's rate takes over the memory's latency.  The page numbers of a step
+// come the same way, two steps before its keys.
+#include "ar_attn.hpp"
+
+namespace ar {
+namespace {
+
+constexpr int kWaves = 4, kStep = 32, kTileKeys = kWaves * kStep;
+constexpr unsigned kWorkers = 256;             // one a CU: the LDS of a workgroup fills it
+constexpr unsigned kHeads = 16;                // query heads of a tile
+
+// Dynamic: what is in LDS of one wave.
+template <int DP, bool E4M3>
+struct Ring {
+  static constexpr int kRow = E4M3 ? DP : DP * 2;              // bytes
+  static constexpr int kKeys = kStep * kRow;                   // bytes of a step's keys, or values
+  static constexpr int kScales = E4M3 ? 2 * kStep * 4 : 0;     // of the keys, then of the values
+  static constexpr int kStage = 2 * kKeys + kScales;
+  static constexpr int kIds = 4 * kWave * 4;                   // page numbers of four steps
+  static constexpr int kBytes = 2 * kStage + kIds;
+  static constexpr int kCopies = kKeys / 1024 * 2 + (E4M3 ? 1 : 0) + 1;  // instructions of a step
+};
+
+template <int RB>
+__device__ __forceinline__ int swizzle_bytes(int r) {
+  if constexpr (RB == 256) return swizzle<128>(r);
+  else if constexpr (RB == 128) return swizzle<64>(r);
+  else return (r >> 2) & 3;
+}
+template <int RB>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) { return (uint32_t)(r * RB + ((c ^ swizzle_bytes<RB>(r)) * 16)); }
+
+__device__ __forceinline__ void copy4_to_lds(const void* from, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dword %1, off" :: "s"(lds), "v"(from) : "memory");
+}
+
+// What a sequence's keys are cut into.
+struct Cut {
+  int len, lo, sunk;            // keys; the window's first; sinks before it
+  int ts, n;                    // tiles of sinks, of all (at least 1)
+};
+__device__ __forceinline__ Cut cut_of(const AttnArgs& a, int len) {
+  Cut c;
+  c.len = (int)min((unsigned)max(len, 0), a.capacity);
+  c.lo = window_start(c.len - 1, a.window);
+  c.sunk = min((int)a.sinks, c.lo);
+  c.ts = (c.sunk + kTileKeys - 1) / kTileKeys;
+  c.n = max(c.ts + (c.len - c.lo + kTileKeys - 1) / kTileKeys, 1);
+  return c;
+}
+
+// One tile of a workgroup's run.
+struct Step {
+  int seq, hx;                  // sequence; key head and its tile of query heads
+  int j0, end;                  // first key of the tile, end of its keys
+  unsigned seq_u, seq_n;        // the sequence's first tile in the row of all, number of its tiles
+  int first, last;              // of the sequence's tiles in this run
+};
+
+template <int DP, bool E4M3>
+__global__ __launch_bounds__(kWaves * 64, 1) void k_attn_decode(AttnArgs a, unsigned head_tiles, uint32_t* counters, float* parts,
+                                                                bool split) {
+  using R = Ring<DP, E4M3>;
+  constexpr int RB = R::kRow, KS = DP / 32, DT = DP / 16;
+  __shared__ __align__(1024) char ring[kWaves * R::kBytes];
+  __shared__ __align__(16) float lo_[kWaves][kHeads][36];      // 32 columns of each wave's result
+  __shared__ float lm[kWaves][kHeads], ll[kWaves][kHeads];
+  __shared__ unsigned lcount;
+  const int t = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(t / kWave);
+  const int hd = lane & 15, g = lane >> 4;
+  const unsigned group = a.hq / a.hkv;
+
+  // this workgroup's run of tiles
+  unsigned N = 0;
+  for (unsigned s0 = 0; s0 < a.seqs; s0 += kWave) {
+    const unsigned n = s0 + lane < a.seqs ? (unsigned)cut_of(a, a.lens[s0 + lane]).n : 0;
+    N += __shfl(wave_scan(n), kWave - 1);
+  }
+  N = __builtin_amdgcn_readfirstlane((int)N);
+  const unsigned heads = a.hkv * head_tiles;
+  const uint64_t all = (uint64_t)N * heads;
+  const unsigned per = split ? (unsigned)((all + kWorkers - 1) / kWorkers) : 0;
+  uint64_t u, u_end;
+  int hx, seq;
+  unsigned into;                               // tile of the sequence
+  if (split) {
+    u = (uint64_t)blockIdx.x * per;
+    u_end = u + per < all ? u + per : all;
+    if (u >= all) return;
+    hx = (int)(u / N);
+    unsigned at = (unsigned)(u % N);
+    seq = 0;
+    into = 0;
+    for (unsigned s0 = 0; s0 < a.seqs; s0 += kWave) {
+      const unsigned n = s0 + lane < a.seqs ? (unsigned)cut_of(a, a.lens[s0 + lane]).n : 0;
+      const unsigned upto = wave_scan(n), here = __shfl(upto, kWave - 1);
+      if (at < here) {
+        const int who = __builtin_ctzll(__ballot(upto > at));
+        seq = (int)s0 + who;
+        into = at - (__shfl(upto, who) - __shfl(n, who));
+        break;
+      }
+      at -= here;
+    }
+    seq = __builtin_amdgcn_readfirstlane(seq);
+    into = __builtin_amdgcn_readfirstlane((int)into);
+  } else {                                     // a sequence and head each
+    seq = (int)(blockIdx.x % a.seqs);
+    hx = (int)(blockIdx.x / a.seqs);
+    into = 0;
+    u = 0;
+    u_end = (uint64_t)cut_of(a, a.lens[seq]).n;
+  }
+
+  // walks over the run's tiles, some steps ahead of what is computed
+  typedef const __attribute__((address_space(4))) int32_t* Scalar;
+  const Scalar lens = (Scalar)(uintptr_t)a.lens;
+  uint64_t ahead = u;                          // tile that the walk is at
+  Cut cut = cut_of(a, lens[seq]);
+  bool begun = true;                           // the walk's tile is the run's first of its sequence
+  auto walk = [&]() -> Step {
+    Step s;
+    s.seq = seq;
+    s.hx = hx;
+    const bool sink = (int)into < cut.ts;
+    s.j0 = sink ? (int)into * kTileKeys : cut.lo + ((int)into - cut.ts) * kTileKeys;
+    s.end = sink ? cut.sunk : cut.len;
+    s.seq_u = (unsigned)(ahead - into);
+    s.seq_n = (unsigned)cut.n;
+    s.first = begun;
+    s.last = ahead + 1 >= u_end || (int)into + 1 >= cut.n;
+    begun = false;
+    if (ahead < u_end) ++ahead;
+    if (ahead < u_end && (int)++into >= cut.n) {
+      begun = true;
+      into = 0;
+      if (++seq >= (int)a.seqs) {
+        seq = 0;
+        ++hx;
+      }
+      cut = cut_of(a, lens[seq]);
+    }
+    return s;
+  };
+
+  char* mine = ring + wave * R::kBytes;
+  const uint32_t lmine = __builtin_amdgcn_readfirstlane((int)lds_addr(mine));
+  const uint32_t lids = lmine + 2 * R::kStage;
+  const uint32_t* ids = reinterpret_cast<const uint32_t*>(mine + 2 * R::kStage);
+  if (a.dim < DP) {                            // places that no copy fills
+    for (int o = lane * 16; o < 2 * R::kStage; o += kWave * 16) *reinterpret_cast<u32x4*>(mine + o) = u32x4{0, 0, 0, 0};
+    __syncthreads();
+  }
+
+  // key of the wave's row r, held within the step's keys
+  auto key_of = [&](const Step& s, int r) { return max(min(s.j0 + wave * kStep + r, s.end - 1), 0); };
+  auto fetch_ids = [&](const Step& s, int slot) {
+    const unsigned pg = page_of((unsigned)key_of(s, lane & 31), a.cache);
+    copy4_to_lds(a.table + (size_t)s.seq * a.table_ld + pg, lids + slot * kWave * 4);
+  };
+  constexpr int RPC = 1024 / RB, CPR = RB / 16, ES = E4M3 ? 1 : 2;
+  auto fetch = [&](const Step& s, const Step& later, int stage, int slot) {
+    const unsigned kvh = (unsigned)s.hx / head_tiles;
+    const uint32_t to = lmine + stage * R::kStage;
+    auto token = [&](int r, size_t ps, size_t ts, size_t hs) -> size_t {
+      const unsigned j = (unsigned)key_of(s, r), pg = page_of(j, a.cache), in = j - pg * a.cache.size;
+      uint32_t id = ids[slot * kWave + r];
+      if (id >= a.cache.pages) id = 0;         // found again when the step is computed
+      return (size_t)id * ps + (size_t)in * ts + kvh * hs;
+    };
+#pragma unroll
+    for (int i = 0; i < kStep / RPC; ++i) {
+      const int r = i * RPC + lane / CPR, ch = (lane % CPR) ^ swizzle_bytes<RB>(r);
+      const size_t o = token(r, a.cache.page, a.cache.ts, a.cache.hs) * ES + ch * 16;
+      if (ch * 16 < (int)a.dim * ES) {
+        copy16_to_lds(static_cast<const char*>(a.cache.k) + o, to + i * 1024);
+        copy16_to_lds(static_cast<const char*>(a.cache.v) + o, to + R::kKeys + i * 1024);
+      }
+    }
+    if constexpr (E4M3) {
+      const size_t o = token(lane & 31, a.cache.spage, a.cache.sts, a.cache.shs);
+      copy4_to_lds((lane < 32 ? a.cache.k_scales : a.cache.v_scales) + o, to + 2 * R::kKeys);
+    }
+    fetch_ids(later, (slot + 2) & 3);
+  };
+
+  Step s0 = walk(), s1 = walk(), s2 = walk(), s3 = walk();
+  fetch_ids(s0, 0);
+  fetch_ids(s1, 1);
+  wait_copies();
+  fetch(s0, s2, 0, 0);
+  fetch(s1, s3, 1, 1);
+
+  Frag8 q[KS];
+  f32x4 o[DT];
+  float m = AR_NEG_INF, l = 0.f;
+  const float c = a.scale * kLog2e;
+  int stage = 0, slot = 0;
+  for (; u < u_end; ++u) {
+    // the step's copies are done when only the next step's are left
+    asm volatile("s_waitcnt vmcnt(%0)" :: "n"(R::kCopies) : "memory");
+    const unsigned kvh = (unsigned)s0.hx / head_tiles, ht = (unsigned)s0.hx % head_tiles;
+    const unsigned here = min(group - ht * kHeads, kHeads), head0 = kvh * group + ht * kHeads;
+    if (s0.first) {
+      m = AR_NEG_INF;
+      l = 0.f;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+      // columns past the last head are those of the last; their results are not kept
+      const uint16_t* qp = a.q.p + (size_t)s0.seq * a.q.ts + (head0 + min((unsigned)hd, here - 1)) * a.q.hs;
+#pragma unroll
+      for (int x = 0; x < KS; ++x) {
+        const unsigned d = E4M3 ? 64 * (x / 2) + 16 * g + 8 * (x & 1) : 32 * x + 8 * g;
+        q[x].u = d < a.dim ? *reinterpret_cast<const u32x4*>(qp + d) : u32x4{0, 0, 0, 0};
+      }
+    }
+    const int keys = min(s0.end - s0.j0 - wave * kStep, kStep);   // of this wave's step
+    if (keys > 0) {
+      if (__any((lane & 31) < keys && ids[slot * kWave + lane] >= a.cache.pages)) l = __uint_as_float(0x7FC00000u);
+      const char* lk = mine + stage * R::kStage;
+      const uint32_t lv = lmine + stage * R::kStage + R::kKeys;
+      f32x4 s[2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        s[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if constexpr (E4M3) {
+#pragma unroll
+          for (int x = 0; x < KS / 2; ++x) {
+            const u32x4 w = *reinterpret_cast<const u32x4*>(lk + chunk_at<RB>(16 * b + hd, 4 * x + g));
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              Frag8 k;
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                union { b16x2 b; uint32_t u; } lo, hi;
+                lo.b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[2 * y + e], 1.0f, false);
+                hi.b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[2 * y + e], 1.0f, true);
+                k.w[2 * e] = lo.u;
+                k.w[2 * e + 1] = hi.u;
+              }
+              s[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k.b, q[2 * x + y].b, s[b], 0, 0, 0);
+            }
+          }
+          const f32x4 f = *reinterpret_cast<const f32x4*>(lk + 2 * R::kKeys + (16 * b + 4 * g) * 4);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) s[b][r] *= f[r];
+        } else {
+#pragma unroll
+          for (int x = 0; x < KS; ++x) {
+            Frag8 k;
+            k.u = *reinterpret_cast<const u32x4*>(lk + chunk_at<RB>(16 * b + hd, 4 * x + g));
+            s[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k.b, q[x].b, s[b], 0, 0, 0);
+          }
+        }
+      }
+      // register r of block b is key 16 b + 4 g + r of the step
+      if (keys < kStep) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) s[b][r] = 16 * b + 4 * g + r < keys ? s[b][r] : AR_NEG_INF;
+      }
+      float top = AR_NEG_INF;
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) top = fmaxf(top, s[b][r]);
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32)) * c;
+      if (__any(top > m + 8.0f)) {
+        const float up = fmaxf(m, top), f = up == AR_NEG_INF ? 1.0f : exp2_fast(m - up);
+        m = up;
+        l *= f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[d] *= f;
+      }
+      const float base = m == AR_NEG_INF ? 0.f : m;
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          s[b][r] = exp2_fast(__builtin_fmaf(s[b][r], c, -base));
+          l += s[b][r];
+        }
+      if constexpr (E4M3) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const f32x4 f = *reinterpret_cast<const f32x4*>(lk + 2 * R::kKeys + (kStep + 16 * b + 4 * g) * 4);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) s[b][r] = 16 * b + 4 * g + r < keys ? s[b][r] * f[r] : 0.f;
+        }
+      }
+      Frag8 p;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        p.w[2 * b] = cvt_bf16x2(s[b][0], s[b][1]);
+        p.w[2 * b + 1] = cvt_bf16x2(s[b][2], s[b][3]);
+      }
+      // whether element e of the lane's eight values is of a key of the step:
+      // 0 times what a masked place holds must be 0
+      const int beyond = keys - 4 * g;         // of keys 4 g + ...; 16 less for the second four
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        Frag8 v;
+        if constexpr (E4M3) {
+          const int e = (lane & 15) / 2, r = 4 * g + (e & 3) + (e >= 4 ? 16 : 0);
+          const i32x2 w = read_tr8(lv + chunk_at<RB>(r, d) + (lane & 1) * 8);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            union { b16x2 b; uint32_t u; } lo, hi;
+            lo.b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[x], 1.0f, false);
+            hi.b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[x], 1.0f, true);
+            v.w[2 * x] = lo.u;
+            v.w[2 * x + 1] = hi.u;
+          }
+        } else {
+          const int r = 4 * g + (lane & 15) / 4, ch = 2 * d + (lane & 3) / 2;
+          v.s[0] = read_tr16(lv + chunk_at<RB>(r, ch) + (lane & 1) * 8);
+          v.s[1] = read_tr16(lv + chunk_at<RB>(r + 16, ch) + (lane & 1) * 8);
+        }
+        if (keys < kStep) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if ((e & 3) + (e >= 4 ? 16 : 0) >= beyond) v.w[e / 2] &= e & 1 ? 0xFFFFu : 0xFFFF0000u;
+        }
+        o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v.b, p.b, o[d], 0, 0, 0);
+      }
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the stage has been read
+    const Step s4 = walk();
+    fetch(s2, s4, stage, (slot + 2) & 3);
+    stage ^= 1;
+    slot = (slot + 1) & 3;
+
+    if (s0.last) {
+      // the waves' results are one
+      l += __shfl_xor(l, 16);
+      l += __shfl_xor(l, 32);
+      if (lane < 16) {
+        lm[wave][hd] = m;
+        ll[wave][hd] = l;
+      }
+      __syncthreads();
+      float M = AR_NEG_INF, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) M = fmaxf(M, lm[w][hd]);
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w)
+        sum += lm[w][hd] == AR_NEG_INF ? ll[w][hd] : ll[w][hd] * exp2_fast(lm[w][hd] - M);
+      const float f = m == AR_NEG_INF ? 0.f : exp2_fast(m - M);
+      const unsigned begin = split ? s0.seq_u / per : 0, finish = split ? (s0.seq_u + s0.seq_n - 1) / per : 0;
+      const unsigned count = finish - begin + 1;   // runs that hold parts of the sequence
+      const float inv = sum > 0.f ? 1.0f / sum : sum;   // no key: zeros; NaN stays
+      // results of a part: 16 maxima, 16 sums, then rows of a head's columns
+      constexpr unsigned kPart = 2 * kHeads + kHeads * DP;
+      float* part = count > 1 ? parts + (size_t)(blockIdx.x * 2 + (blockIdx.x == begin ? 1 : 0)) * kPart : nullptr;
+      const unsigned oh = t / 16, od = (t % 16) * 2;
+      const float oinv = __shfl(inv, (int)oh & 15);
+#pragma unroll
+      for (int d2 = 0; d2 < DT / 2; ++d2) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          f32x4 v = o[2 * d2 + x];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[r] *= f;
+          *reinterpret_cast<f32x4*>(&lo_[wave][hd][16 * x + 4 * g]) = v;
+        }
+        __syncthreads();
+        float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+          a0 += lo_[w][oh][od];
+          a1 += lo_[w][oh][od + 1];
+        }
+        const unsigned at = 32 * d2 + od;
+        if (oh < here && at < a.dim) {
+          if (part) {
+            __hip_atomic_store(reinterpret_cast<uint64_t*>(part + 2 * kHeads + oh * DP + at),
+                               (uint64_t)__float_as_uint(a0) | (uint64_t)__float_as_uint(a1) << 32, __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
+          } else {
+            uint16_t* op = a.out.p + (size_t)s0.seq * a.out.ts + (head0 + oh) * a.out.hs + at;
+            *reinterpret_cast<uint32_t*>(op) = result_bf16x2(a0 * oinv, a1 * oinv);
+          }
+        }
+        __syncthreads();
+      }
+      if (part) {
+        if (t < (int)kHeads) {
+          __hip_atomic_store(part + t, M, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          __hip_atomic_store(part + kHeads + t, sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the part is out
+        __syncthreads();
+        uint32_t* counter = counters + (size_t)s0.hx * a.seqs + s0.seq;
+        if (t == 0) lcount = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        if (lcount == count - 1) {
+          __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+          if (t == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          const unsigned h = t / 16;
+          auto part_of = [&](unsigned i) { return parts + (size_t)((begin + i) * 2 + (i == 0 ? 1 : 0)) * kPart; };
+          if (h < here) {
+            float M2 = AR_NEG_INF, L2 = 0.f;
+            for (unsigned i = 0; i < count; ++i) M2 = fmaxf(M2, part_of(i)[h]);
+            f32x4 acc[DP / 64];
+#pragma unroll
+            for (int x = 0; x < DP / 64; ++x) acc[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+            for (unsigned i = 0; i < count; ++i) {
+              const float* p = part_of(i);
+              const float w = p[h] == AR_NEG_INF ? 0.f : exp2_fast(p[h] - M2);
+              L2 = p[h] == AR_NEG_INF ? L2 + p[kHeads + h] : __builtin_fmaf(p[kHeads + h], w, L2);
+#pragma unroll
+              for (int x = 0; x < DP / 64; ++x) {
+                const unsigned d = 64 * x + (t % 16) * 4;
+                if (d < a.dim) {
+                  const f32x4 v = *reinterpret_cast<const f32x4*>(p + 2 * kHeads + h * DP + d);
+#pragma unroll
+                  for (int r = 0; r < 4; ++r) acc[x][r] = __builtin_fmaf(v[r], w, acc[x][r]);
+                }
+              }
+            }
+            const float i2 = L2 > 0.f ? 1.0f / L2 : L2;
+            uint16_t* op = a.out.p + (size_t)s0.seq * a.out.ts + (head0 + h) * a.out.hs;
+#pragma unroll
+            for (int x = 0; x < DP / 64; ++x) {
+              const unsigned d = 64 * x + (t % 16) * 4;
+              if (d < a.dim)
+                *reinterpret_cast<u32x2*>(op + d) =
+                    u32x2{result_bf16x2(acc[x][0] * i2, acc[x][1] * i2), result_bf16x2(acc[x][2] * i2, acc[x][3] * i2)};
+            }
+            if (a.lse && t % 16 == 0)
+              a.lse[(size_t)s0.seq * a.lse_ts + (head0 + h) * a.lse_hs] =
+                  L2 > 0.f ? (M2 + __builtin_amdgcn_logf(L2)) * kLn2 : L2 == 0.f ? AR_NEG_INF : L2;
+          }
+        }
+        __syncthreads();
+      } else if (a.lse && t < (int)here) {
+        a.lse[(size_t)s0.seq * a.lse_ts + (head0 + t) * a.lse_hs] =
+            sum > 0.f ? (M + __builtin_amdgcn_logf(sum)) * kLn2 : sum == 0.f ? AR_NEG_INF : sum;
+      }
+    }
+    s0 = s1;
+    s1 = s2;
+    s2 = s3;
+    s3 = s4;
+  }
+  wait_copies();                               // LDS is not given up under a copy
+}
+
+unsigned head_tiles_of(size_t hq, size_t hkv) { return (unsigned)cdiv(hq / hkv, kHeads); }
+size_t counters_bytes(size_t seqs, size_t hq, size_t hkv) { return cdiv(seqs * hkv * head_tiles_of(hq, hkv) * 4, 256) * 256; }
+
+template <int DP, bool E4M3>
+hipError_t launch(const Launch& L, const AttnArgs& a, void* ws) {
+  const unsigned ht = head_tiles_of(a.hq, a.hkv);
+  uint32_t* counters = static_cast<uint32_t*>(ws);
+  float* parts = ws ? reinterpret_cast<float*>(static_cast<char*>(ws) + counters_bytes(a.seqs, a.hq, a.hkv)) : nullptr;
+  const unsigned grid = ws ? kWorkers : a.seqs * a.hkv * ht;
+  return launch_k(k_attn_decode<DP, E4M3>, dim3(grid), dim3(kWaves * 64), 0, L.stream, a, ht, counters, parts, ws != nullptr);
+}
+
+}  // namespace
+
+size_t attn_decode_workspace(size_t seqs, size_t hq, size_t hkv, size_t dim) {
+  const size_t dp = dim > 64 ? 128 : 64;
+  return counters_bytes(seqs, hq, hkv) + (size_t)kWorkers * 2 * (2 * kHeads + kHeads * dp) * 4;
+}
+
+hipError_t launch_attn_decode(const Launch& L, const AttnArgs& a, bool e4m3, void* ws) {
+  if (a.dim > 64) return e4m3 ? launch<128, true>(L, a, ws) : launch<128, false>(L, a, ws);
+  return e4m3 ? launch<64, true>(L, a, ws) : launch<64, false>(L, a, ws);
+}
+
+}  // namespace ar

@@ -187,6 +187,68 @@ size_t gemm_fp8_workspace(size_t M, size_t N, size_t K, int G);
 hipError_t launch_gemm_fp8(const Launch& L, const GemmArgs& g, int G, bool e8m0, bool b_rows, bool out_f32,
                            void* workspace);  // gemm_fp8_workspace bytes, or nullptr
 
+// Operands of the rotation and of attention, checked by the API layer.
+// Strides are in elements.
+struct HeadRows {              // [tokens][heads][dim], dim contiguous
+  const uint16_t* p;
+  size_t ts, hs;
+};
+struct HeadOut {
+  uint16_t* p;
+  size_t ts, hs;
+};
+struct Pages {                 // a paged cache of keys and values
+  void *k, *v;                 // bf16, or E4M3 codes
+  float *k_scales, *v_scales;  // E4M3: one for each token and head
+  size_t page, ts, hs;         // strides of k and v
+  size_t spage, sts, shs;      // strides of the scales
+  unsigned pages, size;        // number of pages, tokens in one
+  unsigned magic, shift;       // x / size = mulhi(x, magic) >> shift for x < 2^31 (shift 32: size is 1)
+};
+struct RopeArgs {
+  HeadRows q, k, v;            // p nullptr: none
+  HeadOut q_out, k_out;
+  Pages cache;                 // k nullptr: none
+  const float* cos_sin;        // [table_rows][rot]: rot / 2 cosines, then as many sines
+  const int32_t* positions;
+  const int64_t* slots;
+  size_t tokens;
+  unsigned table_rows, hq, hkv, dim, rot;
+  int pairs, inverse, e4m3;
+};
+hipError_t launch_rope_kv(const Launch& L, const RopeArgs& a);
+
+struct AttnArgs {
+  HeadRows q, k, v;            // k, v: unless the keys are in pages
+  Pages cache;
+  const int32_t *table, *lens; // [seqs][table_ld] page numbers; keys of each sequence
+  const int32_t *cu_q, *cu_k;  // [seqs + 1] first rows
+  HeadOut out;
+  float* lse;                  // nullptr: not written
+  size_t table_ld, lse_ts, lse_hs;
+  unsigned capacity;           // keys that a table row has room for
+  unsigned rows_q, rows_k;     // rows of q and of k, v
+  unsigned seqs, hq, hkv, dim;
+  float scale;                 // of the scores, finite and positive
+  unsigned window, sinks;      // window at least 1
+};
+enum KeySource { kKeyRows = 0, kKeyPages, kKeyPagesE4M3 };
+hipError_t launch_attn(const Launch& L, const AttnArgs& a, KeySource src);
+bool attn_fits(size_t rows_q, size_t seqs, size_t hq);  // whether its grid fits a launch
+
+size_t attn_decode_workspace(size_t seqs, size_t hq, size_t hkv, size_t dim);
+hipError_t launch_attn_decode(const Launch& L, const AttnArgs& a, bool e4m3, void* workspace);
+
+struct AttnBwdArgs {
+  AttnArgs f;                  // q, k, v, cu_q, cu_k, lse and the mask of the forward pass
+  HeadRows out, d_out;
+  HeadOut dq, dk, dv;          // p nullptr: not written (dk and dv both or neither)
+  void* workspace;
+};
+size_t attn_bwd_workspace(size_t rows_q, size_t rows_k, size_t seqs, size_t hq, size_t hkv, size_t dim, size_t window,
+                          size_t sinks);
+hipError_t launch_attn_bwd(const Launch& L, const AttnBwdArgs& a);
+
 hipError_t launch_pack(const Launch& L, const void* x, uint64_t* w, size_t n, uint32_t seq);
 hipError_t launch_unpack(const Launch& L, const uint64_t* w, void* x, size_t n, uint32_t seq,
                          uint64_t* d_err);

@@ -1,0 +1,128 @@
+// Rotation of queries and keys by their positions, and the append of keys and
+// values to a paged cache.
+//   u = a c - b s,  w = b c + a s
+// for the pairs (a, b) of a head's first `rot` values, a and b `rot` / 2
+// apart or neighbours, with the cosine and sine of the token's position; the
+// gradient is the rotation back (s negated).
+//
+// Bound by memory.  A lane takes 16 values of a head: 8 pairs as two groups
+// of 8, so that every access is 16 bytes wide and both values of a pair are
+// in one lane; the lanes of a head lie side by side, and a head's largest
+// magnitude (E4M3) is found by exchanges between them.
+#include "ar_attn.hpp"
+#include "ar_e4m3.hpp"
+
+namespace ar {
+namespace {
+
+__device__ __forceinline__ void unpack8(u32x4 v, float* f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = lo_f32(v[i]);
+    f[2 * i + 1] = hi_f32(v[i]);
+  }
+}
+__device__ __forceinline__ u32x4 pack8(const float* f) {
+  u32x4 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = result_bf16x2(f[2 * i], f[2 * i + 1]);
+  return v;
+}
+
+// One workgroup row is a token; 2^lg lanes a head, the rest of the workgroup's
+// lanes over the token's heads: queries, keys, then values.
+template <bool E4M3, bool PAIRS>
+__global__ __launch_bounds__(256) void k_rope_kv(RopeArgs a, int lg, unsigned heads) {
+  const unsigned lanes = 1u << lg, i = threadIdx.x & (lanes - 1);
+  const unsigned work = blockIdx.x * (256 >> lg) + (threadIdx.x >> lg);   // (token, head)
+  const uint64_t token = work / heads;
+  const unsigned head = work % heads;
+  const bool on = token < a.tokens && i < a.dim / 16;
+  const bool is_q = head < a.hq, is_v = head >= a.hq + a.hkv;
+  const unsigned h = is_q ? head : is_v ? head - a.hq - a.hkv : head - a.hq;
+  const HeadRows src = is_q ? a.q : is_v ? a.v : a.k;
+  const bool turn = on && !is_v && i < a.rot / 16;
+  // the lane's two groups of 8
+  unsigned g0, g1;
+  if (!is_v && i < a.rot / 16 && !PAIRS) {
+    g0 = 8 * i;
+    g1 = a.rot / 2 + 8 * i;
+  } else {
+    g0 = 16 * i;
+    g1 = 16 * i + 8;
+  }
+  float x[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) x[e] = 0.f;
+  if (on) {
+    const uint16_t* p = src.p + token * src.ts + h * src.hs;
+    unpack8(*reinterpret_cast<const u32x4*>(p + g0), x);
+    unpack8(*reinterpret_cast<const u32x4*>(p + g1), x + 8);
+  }
+  if (turn) {
+    const unsigned pos = min((unsigned)max(a.positions[token], 0), a.table_rows - 1);
+    const float* row = a.cos_sin + (size_t)pos * a.rot + 8 * i;
+    float c[8], s[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      c[e] = row[e];
+      s[e] = a.inverse ? -row[a.rot / 2 + e] : row[a.rot / 2 + e];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      constexpr int step = PAIRS ? 2 : 1;
+      const int at = step * e, bt = PAIRS ? at + 1 : at + 8;
+      const float u = x[at], w = x[bt];
+      x[at] = __builtin_fmaf(u, c[e], -(w * s[e]));
+      x[bt] = __builtin_fmaf(w, c[e], u * s[e]);
+    }
+  }
+  const HeadOut dst = is_q ? a.q_out : is_v ? HeadOut{nullptr, 0, 0} : a.k_out;
+  if (on && dst.p) {
+    uint16_t* p = dst.p + token * dst.ts + h * dst.hs;
+    *reinterpret_cast<u32x4*>(p + g0) = pack8(x);
+    *reinterpret_cast<u32x4*>(p + g1) = pack8(x + 8);
+  }
+  if (!a.cache.k) return;
+  uint32_t amax = 0;
+  if constexpr (E4M3) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) amax = max(amax, finite_mag(x[e]));
+    for (unsigned d = 1; d < lanes; d *= 2) amax = max(amax, (uint32_t)__shfl_xor((int)amax, d));
+  }
+  if (!on || is_q) return;
+  const int64_t slot = a.slots[token];
+  if (slot < 0 || slot >= (int64_t)a.cache.pages * a.cache.size) return;
+  const size_t page = (size_t)slot / a.cache.size, in = (size_t)slot % a.cache.size;
+  const size_t at = page * a.cache.page + in * a.cache.ts + h * a.cache.hs;
+  void* base = is_v ? a.cache.v : a.cache.k;
+  if constexpr (E4M3) {
+    const BlockScale s = block_scale<false>(amax);
+    uint8_t* p = static_cast<uint8_t*>(base) + at;
+    *reinterpret_cast<u32x2*>(p + g0) = u32x2{codes4_scaled(x, s.inv), codes4_scaled(x + 4, s.inv)};
+    *reinterpret_cast<u32x2*>(p + g1) = u32x2{codes4_scaled(x + 8, s.inv), codes4_scaled(x + 12, s.inv)};
+    if (i == 0)
+      (is_v ? a.cache.v_scales : a.cache.k_scales)[page * a.cache.spage + in * a.cache.sts + h * a.cache.shs] =
+          __uint_as_float(s.kept);
+  } else {
+    uint16_t* p = static_cast<uint16_t*>(base) + at;
+    *reinterpret_cast<u32x4*>(p + g0) = pack8(x);
+    *reinterpret_cast<u32x4*>(p + g1) = pack8(x + 8);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_rope_kv(const Launch& L, const RopeArgs& a) {
+  // heads of a token that have work: values only with a cache
+  const unsigned heads = a.hq + a.hkv + (a.cache.k ? a.hkv : 0);
+  int lg = 0;
+  while ((16u << lg) < a.dim) ++lg;
+  const size_t work = a.tokens * heads, per = 256u >> lg;
+  auto* k = a.e4m3 ? (a.pairs ? k_rope_kv<true, true> : k_rope_kv<true, false>)
+                   : (a.pairs ? k_rope_kv<false, true> : k_rope_kv<false, false>);
+  return launch_k(k, dim3((unsigned)cdiv(work, per)), dim3(256), 0, L.stream, a,
+                  lg, heads);
+}
+
+}  // namespace ar
