@@ -11,8 +11,6 @@
 // of the values' own sum to bf16 costs once more.
 #include "ar_attn.hpp"
 
-#include <utility>
-
 namespace ar {
 namespace {
 
@@ -33,22 +31,20 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
   const unsigned rank = blockIdx.x / a.hq, hi = blockIdx.x % a.hq;
   const unsigned kvh = hi % a.hkv, head = kvh * (a.hq / a.hkv) + hi / a.hkv;
   Tile tile;
-  if (!find_tile(a.cu_q, a.seqs, a.rows_q, BM, rank, &tile)) return;
-  const Rows rq = rows_of(a.cu_q, tile.seq, a.rows_q);
+  if (!find_tile<true>(a.cu_q, a.seqs, a.rows_q, BM, rank, &tile)) return;
+  const Rows rq = rows_at(a.cu_q, tile.seq, a.rows_q);
   unsigned nk, k_first = 0;
   if constexpr (SRC == kKeyRows) {
-    const Rows rk = rows_of(a.cu_k, tile.seq, a.rows_k);
+    const Rows rk = rows_at(a.cu_k, tile.seq, a.rows_k);
     nk = rk.count;
     k_first = rk.first;
   } else {
-    nk = min((unsigned)max(a.lens[tile.seq], 0), a.capacity);
+    nk = (unsigned)uniform((int)min((unsigned)max(a.lens[tile.seq], 0), a.capacity));
   }
   const int shift = (int)nk - (int)rq.count;   // position of the sequence's first query
   const int last = (int)rq.count - 1;
   const int p0 = shift + (int)tile.row, p1 = shift + min((int)tile.row + BM - 1, last);
-  // keys of the tile: the sinks before its window, then from its window's start
-  const int lo = window_start(p0, a.window), sunk = min((int)min(a.sinks, 0x7FFFFFFFu), lo), end = p1 + 1;
-  const int ts = (sunk + kBN - 1) / kBN, nt = end > lo ? ts + (end - lo + kBN - 1) / kBN : 0;
+  const KeyRange keys = key_range(p0, p1, a.window, a.sinks, kBN);
   // this lane's query, and the wave's
   const int row = (int)tile.row + wave * 32 + col, p = shift + min(row, last), start = window_start(p, a.window);
   const int wp0 = shift + min((int)tile.row + wave * 32, last), wp1 = shift + min((int)tile.row + wave * 32 + 31, last);
@@ -71,13 +67,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
     __syncthreads();
   }
 
-  // the tile's rows that this lane copies: a wave copies 1 KiB at a time
-  constexpr int RPC = 1024 / (DP * 2), COPIES = kBN / RPC / NW, CPR = DP / 8;
-  const int crow = lane / CPR;
   unsigned bad = 0;                            // a page number out of range was met
-  auto key_at = [&](int n) {                   // first key and number of keys of tile n
-    return n < ts ? std::pair<int, int>{n * kBN, sunk} : std::pair<int, int>{lo + (n - ts) * kBN, end};
-  };
   auto page_base = [&](int j, unsigned& in) {  // page of key j, its place in the page
     const unsigned pg = page_of((unsigned)j, a.cache);
     in = (unsigned)j - pg * a.cache.size;
@@ -88,27 +78,24 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
     }
     return id;
   };
+  const TileCopy<DP, NW> copy_rows(a.k.ts, a.v.ts, a.dim, wave, lane);
+  const uint16_t *kb = a.k.p + (size_t)k_first * a.k.ts + kvh * a.k.hs, *vb = a.v.p + (size_t)k_first * a.v.ts + kvh * a.v.hs;
   auto copy = [&](int n, int buf) {
-    const std::pair<int, int> k = key_at(n);
+    const KeyStep k = key_step(keys, n, kBN);
+    const uint32_t to = lbase + buf * 2 * kTile;
+    if constexpr (SRC == kKeyRows) {
+      copy_rows(kb, a.k.ts, vb, a.v.ts, k.j0, k.end - 1, to);
+    } else {
 #pragma unroll
-    for (int i = 0; i < COPIES; ++i) {
-      const int r = (i * NW + wave) * RPC + crow;
-      const int j = min(k.first + r, k.second - 1);
-      const int ch = (lane % CPR) ^ swizzle<DP>(r);
-      const uint16_t *kp, *vp;
-      if constexpr (SRC == kKeyRows) {
-        kp = a.k.p + (size_t)(k_first + j) * a.k.ts + kvh * a.k.hs;
-        vp = a.v.p + (size_t)(k_first + j) * a.v.ts + kvh * a.v.hs;
-      } else {
+      for (int i = 0; i < copy_rows.COPIES; ++i) {
+        const int j = min(k.j0 + i * NW * copy_rows.RPC + copy_rows.row, k.end - 1);
         unsigned in;
         const size_t at = (size_t)page_base(j, in) * a.cache.page + (size_t)in * a.cache.ts + kvh * a.cache.hs;
-        kp = static_cast<const uint16_t*>(a.cache.k) + at;
-        vp = static_cast<const uint16_t*>(a.cache.v) + at;
-      }
-      const uint32_t to = lbase + buf * 2 * kTile + (i * NW + wave) * 1024;
-      if (ch * 8 < (int)a.dim) {
-        copy16_to_lds(kp + ch * 8, __builtin_amdgcn_readfirstlane((int)to));
-        copy16_to_lds(vp + ch * 8, __builtin_amdgcn_readfirstlane((int)(to + kTile)));
+        if (copy_rows.on) {
+          const uint32_t here = to + (i * NW + wave) * 1024;
+          copy16_to_lds(reinterpret_cast<const char*>(static_cast<const uint16_t*>(a.cache.k) + at) + copy_rows.chunk, here);
+          copy16_to_lds(reinterpret_cast<const char*>(static_cast<const uint16_t*>(a.cache.v) + at) + copy_rows.chunk, here + kTile);
+        }
       }
     }
   };
@@ -117,12 +104,12 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
   u32x4 ck[CHUNKS], cv[CHUNKS];
   float cs = 0.f;
   auto fetch = [&](int n) {
-    const std::pair<int, int> k = key_at(n);
+    const KeyStep k = key_step(keys, n, kBN);
 #pragma unroll
     for (int i = 0; i < CHUNKS; ++i) {
       const int at = i * NW * 64 + t, r = at / (DP / 16), ch = at % (DP / 16);
       unsigned in;
-      const size_t pg = page_base(min(k.first + r, k.second - 1), in);
+      const size_t pg = page_base(min(k.j0 + r, k.end - 1), in);
       const size_t o = pg * a.cache.page + (size_t)in * a.cache.ts + kvh * a.cache.hs + ch * 16;
       ck[i] = cv[i] = u32x4{0, 0, 0, 0};
       if (at < ALL && ch * 16 < (int)a.dim) {
@@ -132,7 +119,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
     }
     if (t < 2 * kBN) {
       unsigned in;
-      const size_t pg = page_base(min(k.first + t % kBN, k.second - 1), in);
+      const size_t pg = page_base(min(k.j0 + t % kBN, k.end - 1), in);
       cs = (t < kBN ? a.cache.k_scales : a.cache.v_scales)[pg * a.cache.spage + (size_t)in * a.cache.sts + kvh * a.cache.shs];
     }
   };
@@ -161,14 +148,46 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
     if (t < 2 * kBN) lscale[buf * 2 * kBN + t] = cs;
   };
 
-  // addresses in a tile: of this lane's chunks of keys, and of the 8-byte
-  // pieces that the transposing reads of values take
-  const uint32_t va = (uint32_t)(4 * hh + (lane & 15) / 4);       // row, of 16 s + ...
-  const int vch = 2 * ((lane >> 4) & 1) + (lane & 3) / 2;         // chunk, of 4 dt + ...
-  const uint32_t vhalf = (lane & 1) * 8;
-
   f32x16 o[DT];
   float m, l;
+  // o += V^T P^T where infinities and NaN of masked places must not count: 0 in
+  // their place, and a count of each kind that a query sees
+  auto add_with_care = [&](const LaneAddr<DP>& from, const Frag8 (&pf)[4], auto& seen) {
+#pragma unroll 1
+    for (int kind = -1; kind < 3; ++kind) {    // -1: the numbers; infinities; NaN
+      const uint32_t like = kind == 0 ? 0x7F80u : 0xFF80u;
+      const float add = kind == 0 ? __builtin_huge_valf() : kind == 1 ? AR_NEG_INF : __uint_as_float(0x7FC00000u);
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        f32x16 sum;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) sum[r] = 0.f;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          Frag8 v = from.columns(kBN + 16 * n, d), w = pf[n];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t out = 0;
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const uint32_t x = (v.w[e] >> (16 * z)) & 0xFFFFu, size = x & 0x7FFFu;
+              const uint32_t y = kind < 0 ? (size < 0x7F80u ? x : 0u) : (kind < 2 ? x == like : size > 0x7F80u) ? 0x3F80u : 0u;
+              out |= y << (16 * z);
+            }
+            v.w[e] = out;
+            const int r = n % 2 * 8 + 2 * e;
+            asm volatile("" : "+v"(v.w[e]));   // one word after the other: not all masks at once
+            if (kind >= 0) w.w[e] = (seen(n / 2, r) ? 0x3F80u : 0u) | (seen(n / 2, r + 1) ? 0x3F800000u : 0u);
+          }
+          sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v.b, w.b, sum, 0, 0, 0);
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (kind < 0) o[d][r] += sum[r];
+          else if (sum[r] > 0.f) o[d][r] += add;
+      }
+    }
+  };
   // Values that are no numbers under masked scores: such a score counts 0,
   // but 0 times them is NaN.  So where a result is no number the pass is made
   // again with care: tiles with masked scores put 0 for such values and add
@@ -181,158 +200,130 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
     for (int d = 0; d < DT; ++d)
 #pragma unroll
       for (int r = 0; r < 16; ++r) o[d][r] = 0.f;
-    if (nt > 0) {
+    if (keys.steps > 0) {
       if constexpr (SRC == kKeyPagesE4M3) fetch(0);
       else copy(0, 0);
     }
-    for (int n = 0; n < nt; ++n) {
+    for (int n = 0; n < keys.steps; ++n) {
       const int buf = n & 1;
       if constexpr (SRC == kKeyPagesE4M3) put(buf);
       else wait_copies();
       __syncthreads();
-      if (n + 1 < nt) {
+      if (n + 1 < keys.steps) {
         if constexpr (SRC == kKeyPagesE4M3) fetch(n + 1);
         else copy(n + 1, buf ^ 1);
       }
-      const std::pair<int, int> kr = key_at(n);
-      const int j0 = kr.first, jend = kr.second;
+      const KeyStep k = key_step(keys, n, kBN);
+      const int j0 = k.j0;
       // no key of the tile is visible to the wave's queries
-      if ((int)tile.row + wave * 32 > last || j0 > wp1 || (j0 + kBN <= wstart0 && j0 >= (int)a.sinks)) continue;
-      const bool whole = j0 + kBN <= jend && j0 + kBN - 1 <= wp0 && j0 >= wstart1;
-      const char* tk = lds + buf * 2 * kTile;
-      const uint32_t tv = lbase + buf * 2 * kTile + kTile;
-
-      f32x16 s[2];
+      if ((int)tile.row + wave * 32 > last || j0 > wp1 || (!k.sinks && j0 + kBN <= wstart0)) continue;
+      const bool whole = j0 + kBN - 1 <= min(wp0, k.end - 1) && (k.sinks || j0 >= wstart1);
+      // of the tile's keys, less 4 hh, those that the lane's query sees
+      const Interval view((k.sinks ? 0 : start) - j0 - 4 * hh, min(p, k.end - 1) - j0 - 4 * hh);
+      const LaneAddr<DP> from(lbase + buf * 2 * kTile, lane);
+      // register r of block b: key 32 b + 8 (r / 4) + 4 hh + r % 4
+      auto seen = [&](int b, int r) { return view.has(32 * b + 8 * (r / 4) + r % 4); };
+      auto scales = [&](int x, int b, f32x16& f) {   // E4M3: of keys (x 0), of values (x 1)
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
+        for (int g = 0; g < 4; ++g) {
+          const f32x4 v = *reinterpret_cast<const f32x4*>(&lscale[(buf * 2 + x) * kBN + 32 * b + 8 * g + 4 * hh]);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) s[b][r] = 0.f;
-#pragma unroll
-        for (int x = 0; x < KS; ++x) {
-          Frag8 k;
-          k.u = *reinterpret_cast<const u32x4*>(tk + chunk_addr<DP>(32 * b + col, 2 * x + hh));
-          s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k.b, q[x].b, s[b], 0, 0, 0);
+          for (int e = 0; e < 4; ++e) f[4 * g + e] = v[e];
         }
-      }
-      // register r of block b is key 32 b + 8 (r / 4) + 4 hh + r % 4 of the tile
-      if constexpr (SRC == kKeyPagesE4M3) {
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const f32x4 f = *reinterpret_cast<const f32x4*>(&lscale[buf * 2 * kBN + 32 * b + 8 * g + 4 * hh]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[b][4 * g + e] *= f[e];
-          }
-      }
-      auto seen = [&](int b, int r) {
-        const int j = j0 + 32 * b + 8 * (r / 4) + 4 * hh + r % 4;
-        return j <= p && j < jend && (j >= start || j < (int)a.sinks);
       };
-      if (!whole) {
+      auto tile_step = [&](auto masked) {
+        constexpr bool MASK = decltype(masked)::value;
+        constexpr int AHEAD = 4, ALL = 2 * KS + 4 * DT;
+        // products 0 .. 2 KS - 1: scores of 32 keys, then of 32 more; then
+        // values of 16 keys each, DT at a time
+        Frag8 f[AHEAD], pf[4];
+        f32x16 s[2];
+        auto load = [&](auto ii) {
+          constexpr int i = decltype(ii)::value;
+          if constexpr (i < 2 * KS) f[i % AHEAD].u = from.rows(i / KS * 32, i % KS);
+          else f[i % AHEAD] = from.columns(kBN + (i - 2 * KS) / DT * 16, (i - 2 * KS) % DT);
+        };
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-          for (int r = 0; r < 16; ++r) s[b][r] = seen(b, r) ? s[b][r] : AR_NEG_INF;
-      }
-      float top = AR_NEG_INF;
+          for (int r = 0; r < 16; ++r) s[b][r] = 0.f;
+        auto fit = [&](int b) {                // scales and mask of a block of scores
+          if constexpr (SRC == kKeyPagesE4M3) {
+            f32x16 f;
+            scales(0, b, f);
+            s[b] *= f;
+          }
+          if constexpr (MASK) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+            for (int r = 0; r < 16; ++r) s[b][r] = seen(b, r) ? s[b][r] : AR_NEG_INF;
+          }
+        };
+        auto largest = [&](int b, float top) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) top = fmaxf(top, s[b][r]);
-      top = max_halves(top) * c;
-      // the running maximum follows only where it falls behind by 2^8: sums
-      // stay far below binary32's range, and most tiles change nothing
-      if (__any(top > m + 8.0f)) {
-        const float up = fmaxf(m, top), f = up == AR_NEG_INF ? 1.0f : exp2_fast(m - up);
-        m = up;
-        l *= f;
+          for (int r = 0; r < 16; ++r) top = fmaxf(top, s[b][r]);
+          return top;
+        };
+        steps<AHEAD>(load);
+        float top = AR_NEG_INF;
+        steps<2 * KS>([&](auto ii) {
+          constexpr int i = decltype(ii)::value;
+          s[i / KS] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[i % AHEAD].b, q[i % KS].b, s[i / KS], 0, 0, 0);
+          load(SPc<i + AHEAD>{});
+          if constexpr (i == KS + KS / 2) {
+            fit(0);
+            top = largest(0, top);
+          }
+          keep_order();
+        });
+        fit(1);
+        top = max_halves(largest(1, top)) * c;
+        // the running maximum follows only where it falls behind by 2^8: sums
+        // stay far below binary32's range, and most tiles change nothing
+        if (__any(top > m + 8.0f)) {
+          const float up = fmaxf(m, top), f = up == AR_NEG_INF ? 1.0f : exp2_fast(m - up);
+          m = up;
+          l *= f;
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) o[d][r] *= f;
-      }
-      const float base = m == AR_NEG_INF ? 0.f : m;
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          s[b][r] = exp2_fast(__builtin_fmaf(s[b][r], c, -base));
-          l += s[b][r];
+          for (int d = 0; d < DT; ++d) o[d] *= f;
         }
-      if constexpr (SRC == kKeyPagesE4M3) {
+        const float base = m == AR_NEG_INF ? 0.f : m;
+        float more = 0.f;
+        auto weigh = [&](int b, int r, int n) {   // numerators of n scores, as bf16
+          f32x16 f;
+          if constexpr (SRC == kKeyPagesE4M3) scales(1, b, f);
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+          for (int x = r; x < r + n; x += 2) {
+            float w[2];
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const f32x4 f = *reinterpret_cast<const f32x4*>(&lscale[buf * 2 * kBN + kBN + 32 * b + 8 * g + 4 * hh]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[b][4 * g + e] = whole || seen(b, 4 * g + e) ? s[b][4 * g + e] * f[e] : 0.f;
-          }
-      }
-      auto values = [&](int b, int x, int d) {   // of 16 keys, 32 columns
-        Frag8 v;
-        const int r0 = 32 * b + 16 * x + (int)va;
-        v.s[0] = read_tr16(tv + chunk_addr<DP>(r0, 4 * d + vch) + vhalf);
-        v.s[1] = read_tr16(tv + chunk_addr<DP>(r0 + 8, 4 * d + vch) + vhalf);
-        return v;
-      };
-      const bool sift = care && !whole;
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          Frag8 pf;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) pf.w[e] = cvt_bf16x2(s[b][8 * x + 2 * e], s[b][8 * x + 2 * e + 1]);
-#pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            Frag8 v = values(b, x, d);
-            if (sift) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if ((v.w[e] & 0x7F80u) == 0x7F80u) v.w[e] &= 0xFFFF0000u;
-                if ((v.w[e] & 0x7F800000u) == 0x7F800000u) v.w[e] &= 0xFFFFu;
-              }
+            for (int e = 0; e < 2; ++e) {
+              w[e] = exp2_fast(__builtin_fmaf(s[b][x + e], c, -base));
+              if (e) more += w[e];
+              else l += w[e];
+              if constexpr (SRC == kKeyPagesE4M3) w[e] = !MASK || seen(b, x + e) ? w[e] * f[x + e] : 0.f;
             }
-            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v.b, pf.b, o[d], 0, 0, 0);
+            pf[2 * b + x / 8].w[x % 8 / 2] = cvt_bf16x2(w[0], w[1]);
+          }
+        };
+        weigh(0, 0, 16);
+        if constexpr (MASK) {
+          weigh(1, 0, 16);
+          if (care) {
+            add_with_care(from, pf, seen);
+            l += more;
+            return;
           }
         }
-      if (sift) {
-        // infinities and NaN of the tile: how many of a kind each query sees
-        for (int kind = 0; kind < 3; ++kind) {
-          const uint32_t like = kind == 0 ? 0x7F80u : kind == 1 ? 0xFF80u : 0u;
-          const float add = kind == 0 ? __builtin_huge_valf() : kind == 1 ? AR_NEG_INF : __uint_as_float(0x7FC00000u);
-#pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            f32x16 count;
-#pragma unroll
-            for (int r = 0; r < 16; ++r) count[r] = 0.f;
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                Frag8 v = values(b, x, d), pf;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  uint32_t is = 0;
-#pragma unroll
-                  for (int z = 0; z < 2; ++z) {
-                    const uint32_t w = (v.w[e] >> (16 * z)) & 0xFFFFu;
-                    const bool hit = kind < 2 ? w == like : (w & 0x7FFFu) > 0x7F80u;
-                    is |= hit ? 0x3F80u << (16 * z) : 0u;
-                  }
-                  v.w[e] = is;
-                  pf.w[e] = (seen(b, 8 * x + 2 * e) ? 0x3F80u : 0u) | (seen(b, 8 * x + 2 * e + 1) ? 0x3F800000u : 0u);
-                }
-                count = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v.b, pf.b, count, 0, 0, 0);
-              }
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-              if (count[r] > 0.f) o[d][r] += add;
-          }
-        }
-      }
+        steps<4 * DT>([&](auto ii) {
+          constexpr int n = decltype(ii)::value, i = n + 2 * KS;
+          o[n % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[i % AHEAD].b, pf[n / DT].b, o[n % DT], 0, 0, 0);
+          if constexpr (i + AHEAD < ALL) load(SPc<i + AHEAD>{});
+          if constexpr (!MASK && n < 2 * DT) weigh(1, n * 8 / DT, 8 / DT);
+          keep_order();
+        });
+        l += more;
+      };
+      if (whole) tile_step(std::false_type{});
+      else tile_step(std::true_type{});
     }
     float odd = 0.f;   // NaN if any result is no number
 #pragma unroll
@@ -344,7 +335,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
     if (odd != 0.f) lflag[0] = 1;              // true of NaN
     if (bad) lflag[1] = 1;
     __syncthreads();
-    if (care || lflag[0] == 0) break;
+    if (care || uniform(lflag[0]) == 0) break;
     care = true;
   }
 

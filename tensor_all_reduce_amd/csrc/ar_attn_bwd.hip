@@ -17,7 +17,8 @@
 namespace ar {
 namespace {
 
-constexpr int kWavesB = 8, kRowsB = kWavesB * 32;  // rows of a workgroup: of queries, or of keys
+constexpr int kWavesQ = 8, kQueries = kWavesQ * 32;  // queries of a workgroup
+constexpr int kWavesK = 4, kKeysB = kWavesK * 32;    // keys of a workgroup
 constexpr int kBT = 64;                            // rows of the other side at a time
 constexpr unsigned kFar = 2048;                    // queries of a run
 
@@ -41,27 +42,8 @@ __global__ __launch_bounds__(256) void k_attn_delta(HeadRows out, HeadRows d_out
   if (row < rows && i == 0) delta[(size_t)head * rows + row] = sum;
 }
 
-// Copies rows first .. of two matrices to LDS, kBT rows each; rows past `last`
-// are copies of it.
-template <int DP>
-__device__ __forceinline__ void copy_tiles(const uint16_t* x, size_t xs, const uint16_t* y, size_t ys, int first, int last,
-                                           unsigned dim, uint32_t lds, int wave, int lane) {
-  constexpr int RPC = 1024 / (DP * 2), CPR = DP / 8, COPIES = kBT / RPC / kWavesB;
-#pragma unroll
-  for (int i = 0; i < COPIES; ++i) {
-    const int r = (i * kWavesB + wave) * RPC + lane / CPR, j = min(first + r, last);
-    const int ch = (lane % CPR) ^ swizzle<DP>(r);
-    const uint32_t to = (uint32_t)__builtin_amdgcn_readfirstlane((int)(lds + (i * kWavesB + wave) * 1024));
-    if (ch * 8 < (int)dim) {
-      copy16_to_lds(x + (size_t)j * xs + ch * 8, to);
-      copy16_to_lds(y + (size_t)j * ys + ch * 8, to + kBT * DP * 2);
-    }
-  }
-}
-
-template <int DP>
 __device__ __forceinline__ void zero_lds(char* lds, int bytes) {
-  for (int o = threadIdx.x * 16; o < bytes; o += kWavesB * 64 * 16) *reinterpret_cast<u32x4*>(lds + o) = u32x4{0, 0, 0, 0};
+  for (int o = threadIdx.x * 16; o < bytes; o += blockDim.x * 16) *reinterpret_cast<u32x4*>(lds + o) = u32x4{0, 0, 0, 0};
   __syncthreads();
 }
 
@@ -72,42 +54,6 @@ __device__ __forceinline__ void load_row(Frag8 (&f)[KS], const uint16_t* p, int 
   for (int s = 0; s < KS; ++s) {
     const unsigned d = 16 * s + 8 * hh;
     f[s].u = d < dim ? *reinterpret_cast<const u32x4*>(p + d) : u32x4{0, 0, 0, 0};
-  }
-}
-
-// 32 rows of LDS (from row r0) times the rows held in f.
-template <int DP>
-__device__ __forceinline__ f32x16 times_rows(const char* tile, int r0, int col, int hh, const Frag8 (&f)[DP / 16]) {
-  f32x16 s;
-#pragma unroll
-  for (int r = 0; r < 16; ++r) s[r] = 0.f;
-#pragma unroll
-  for (int x = 0; x < DP / 16; ++x) {
-    Frag8 k;
-    k.u = *reinterpret_cast<const u32x4*>(tile + chunk_addr<DP>(r0 + col, 2 * x + hh));
-    s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k.b, f[x].b, s, 0, 0, 0);
-  }
-  return s;
-}
-
-// acc += (32 rows of LDS from r0, transposed) times the 32 x 32 values s.
-template <int DP>
-__device__ __forceinline__ void add_columns(f32x16 (&acc)[DP / 32], uint32_t tile, int r0, int lane, const f32x16& s) {
-  const int va = 4 * (lane >> 5) + (lane & 15) / 4, vch = 2 * ((lane >> 4) & 1) + (lane & 3) / 2;
-  const uint32_t vhalf = (lane & 1) * 8;
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    Frag8 p;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) p.w[e] = cvt_bf16x2(s[8 * x + 2 * e], s[8 * x + 2 * e + 1]);
-#pragma unroll
-    for (int d = 0; d < DP / 32; ++d) {
-      Frag8 v;
-      const int r = r0 + 16 * x + va;
-      v.s[0] = read_tr16(tile + chunk_addr<DP>(r, 4 * d + vch) + vhalf);
-      v.s[1] = read_tr16(tile + chunk_addr<DP>(r + 8, 4 * d + vch) + vhalf);
-      acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v.b, p.b, acc[d], 0, 0, 0);
-    }
   }
 }
 
@@ -144,12 +90,12 @@ __device__ __forceinline__ void store_row(float* p, const f32x16 (&o)[DT], int h
     }
 }
 
-// What an exponent subtracts: lse in powers of two; of a query without keys 0.
-__device__ __forceinline__ float lse2_of(float lse) { return lse == AR_NEG_INF ? 0.f : lse * kLog2e; }
+// lse, of a query without keys 0.
+__device__ __forceinline__ float finite_lse(float lse) { return lse == AR_NEG_INF ? 0.f : lse; }
 
 // dQ: 256 queries of one head, 64 keys at a time.
 template <int DP>
-__global__ __launch_bounds__(kWavesB * 64, 2) void k_attn_dq(AttnBwdArgs b, const float* delta) {
+__global__ __launch_bounds__(kWavesQ * 64, 2) void k_attn_dq(AttnBwdArgs b, const float* delta) {
   constexpr int KS = DP / 16, DT = DP / 32;
   constexpr uint32_t kTile = kBT * DP * 2;
   __shared__ __align__(1024) char lds[4 * kTile];
@@ -159,57 +105,96 @@ __global__ __launch_bounds__(kWavesB * 64, 2) void k_attn_dq(AttnBwdArgs b, cons
   const unsigned rank = blockIdx.x / a.hq, hi = blockIdx.x % a.hq;
   const unsigned kvh = hi % a.hkv, head = kvh * (a.hq / a.hkv) + hi / a.hkv;
   Tile tile;
-  if (!find_tile(a.cu_q, a.seqs, a.rows_q, kRowsB, rank, &tile)) return;
-  const Rows rq = rows_of(a.cu_q, tile.seq, a.rows_q), rk = rows_of(a.cu_k, tile.seq, a.rows_k);
+  if (!find_tile<true>(a.cu_q, a.seqs, a.rows_q, kQueries, rank, &tile)) return;
+  const Rows rq = rows_at(a.cu_q, tile.seq, a.rows_q), rk = rows_at(a.cu_k, tile.seq, a.rows_k);
   const int shift = (int)rk.count - (int)rq.count, last = (int)rq.count - 1;
-  const int p0 = shift + (int)tile.row, p1 = shift + min((int)tile.row + kRowsB - 1, last);
-  const int lo = window_start(p0, a.window), sunk = min((int)a.sinks, lo), end = p1 + 1;
-  const int ts = (sunk + kBT - 1) / kBT, nt = end > lo ? ts + (end - lo + kBT - 1) / kBT : 0;
+  const int p0 = shift + (int)tile.row, p1 = shift + min((int)tile.row + kQueries - 1, last);
+  const KeyRange keys = key_range(p0, p1, a.window, a.sinks, kBT);
   const int row = (int)tile.row + wave * 32 + col, p = shift + min(row, last), start = window_start(p, a.window);
   const int wp0 = shift + min((int)tile.row + wave * 32, last), wp1 = shift + min((int)tile.row + wave * 32 + 31, last);
   const int wstart0 = window_start(wp0, a.window), wstart1 = window_start(wp1, a.window);
 
-  if (a.dim < DP) zero_lds<DP>(lds, 4 * kTile);
+  if (a.dim < DP) zero_lds(lds, 4 * kTile);
   const size_t at = rq.first + min(row, last);
   Frag8 q[KS], g[KS];
   load_row(q, a.q.p + at * a.q.ts + head * a.q.hs, hh, a.dim);
   load_row(g, b.d_out.p + at * b.d_out.ts + head * b.d_out.hs, hh, a.dim);
-  const float lse2 = lse2_of(a.lse[at * a.lse_ts + head * a.lse_hs]), dl = delta[(size_t)head * a.rows_q + at];
+  const float lse2 = finite_lse(a.lse[at * a.lse_ts + head * a.lse_hs]) * kLog2e, dl = delta[(size_t)head * a.rows_q + at];
   const float c = a.scale * kLog2e;
   const uint16_t* kb = a.k.p + (size_t)rk.first * a.k.ts + kvh * a.k.hs;
   const uint16_t* vb = a.v.p + (size_t)rk.first * a.v.ts + kvh * a.v.hs;
   const uint32_t lbase = lds_addr(lds);
+  const TileCopy<DP, kWavesQ> copy_rows(a.k.ts, a.v.ts, a.dim, wave, lane);
   auto copy = [&](int n, int buf) {
-    copy_tiles<DP>(kb, a.k.ts, vb, a.v.ts, n < ts ? n * kBT : lo + (n - ts) * kBT, (n < ts ? sunk : end) - 1, a.dim,
-                   lbase + buf * 2 * kTile, wave, lane);
+    const KeyStep k = key_step(keys, n, kBT);
+    copy_rows(kb, a.k.ts, vb, a.v.ts, k.j0, k.end - 1, lbase + buf * 2 * kTile);
   };
   f32x16 o[DT];
   clear(o);
-  if (nt > 0) copy(0, 0);
-  for (int n = 0; n < nt; ++n) {
+  if (keys.steps > 0) copy(0, 0);
+  for (int n = 0; n < keys.steps; ++n) {
     const int buf = n & 1;
     wait_copies();
     __syncthreads();
-    if (n + 1 < nt) copy(n + 1, buf ^ 1);
-    const int j0 = n < ts ? n * kBT : lo + (n - ts) * kBT, jend = n < ts ? sunk : end;
-    if ((int)tile.row + wave * 32 > last || j0 > wp1 || (j0 + kBT <= wstart0 && j0 >= (int)a.sinks)) continue;
-    const bool whole = j0 + kBT <= jend && j0 + kBT - 1 <= wp0 && j0 >= wstart1;
-    const char* tk = lds + buf * 2 * kTile;
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      f32x16 s = times_rows<DP>(tk, 32 * x, col, hh, q);
-      const f32x16 d = times_rows<DP>(tk + kTile, 32 * x, col, hh, g);
-#pragma unroll
-      for (int r = 0; r < 16; ++r) s[r] = exp2_fast(__builtin_fmaf(s[r], c, -lse2)) * (d[r] - dl);
-      if (!whole) {
+    if (n + 1 < keys.steps) copy(n + 1, buf ^ 1);
+    const KeyStep k = key_step(keys, n, kBT);
+    const int j0 = k.j0;
+    if ((int)tile.row + wave * 32 > last || j0 > wp1 || (!k.sinks && j0 + kBT <= wstart0)) continue;
+    const bool whole = j0 + kBT - 1 <= min(wp0, k.end - 1) && (k.sinks || j0 >= wstart1);
+    const Interval view((k.sinks ? 0 : start) - j0 - 4 * hh, min(p, k.end - 1) - j0 - 4 * hh);
+    const LaneAddr<DP> at_k(lbase + buf * 2 * kTile, lane);
+    auto tile_step = [&](auto masked) {
+      constexpr bool MASK = decltype(masked)::value;
+#pragma unroll 1
+      for (int r0 = 0; r0 < kBT; r0 += 32) {
+        const LaneAddr<DP> from = {at_k, (uint32_t)(r0 * DP * 2)};
+        // products 0 .. KS - 1: scores; then dP; then dQ
+        constexpr int ALL = 2 * KS + 2 * DT, AHEAD = 4;
+        Frag8 f[AHEAD], pd[2];
+        f32x16 s, d;
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          const int j = j0 + 32 * x + 8 * (r / 4) + 4 * hh + r % 4;
-          s[r] = j <= p && j < jend && (j >= start || j < (int)a.sinks) ? s[r] : 0.f;
+          s[r] = 0.f;
+          d[r] = -dl;                          // dP - delta
         }
+        auto load = [&](auto ii) {
+          constexpr int i = decltype(ii)::value;
+          Frag8& x = f[i % AHEAD];
+          if constexpr (i < KS) x.u = from.rows(0, i);
+          else if constexpr (i < 2 * KS) x.u = from.rows(kBT, i - KS);
+          else x = from.columns((i - 2 * KS) / DT * 16, (i - 2 * KS) % DT);
+        };
+        steps<AHEAD>(load);
+        steps<ALL>([&](auto ii) {
+          constexpr int i = decltype(ii)::value;
+          const Frag8& x = f[i % AHEAD];
+          if constexpr (i < KS) s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x.b, q[i].b, s, 0, 0, 0);
+          else if constexpr (i < 2 * KS) d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x.b, g[i - KS].b, d, 0, 0, 0);
+          else o[i % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x.b, pd[(i - 2 * KS) / DT].b, o[i % DT], 0, 0, 0);
+          if constexpr (i + AHEAD < ALL) load(SPc<i + AHEAD>{});
+          if constexpr (i >= KS && i < 2 * KS) {   // beside the products of dP
+            constexpr int per = 16 / KS, a0 = (i - KS) * per;
+#pragma unroll
+            for (int r = a0; r < a0 + per; ++r) s[r] = exp2_fast(__builtin_fmaf(s[r], c, -lse2));
+          }
+          if constexpr (i == 2 * KS - 1) {
+#pragma unroll
+            for (int r = 0; r < 16; r += 2) {
+              float y[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                y[e] = s[r + e] * d[r + e];
+                if (MASK) y[e] = view.has(r0 + 8 * (r / 4) + r % 4 + e) ? y[e] : 0.f;
+              }
+              pd[r / 8].w[r % 8 / 2] = cvt_bf16x2(y[0], y[1]);
+            }
+          }
+          keep_order();
+        });
       }
-      add_columns<DP>(o, lbase + buf * 2 * kTile, 32 * x, lane, s);
-    }
+    };
+    if (whole) tile_step(std::false_type{});
+    else tile_step(std::true_type{});
   }
   if (row <= last) store_row(b.dq.p + at * b.dq.ts + head * b.dq.hs, o, a.scale, hh, a.dim);
 }
@@ -221,7 +206,7 @@ struct Band {
   int lo, hi;                  // first query, first beyond
 };
 __device__ __forceinline__ Band band_of(const AttnArgs& a, int j0, int shift, int nq) {
-  const long long wide = (long long)j0 + kRowsB - 1 + a.window - shift;
+  const long long wide = (long long)j0 + kKeysB - 1 + a.window - shift;
   Band r;
   r.lo = min(max(j0 - shift, 0), nq);
   r.hi = (int)min((long long)nq, max(wide, (long long)r.lo));
@@ -229,16 +214,24 @@ __device__ __forceinline__ Band band_of(const AttnArgs& a, int j0, int shift, in
   return r;
 }
 
+// Where sums of (dK, dV) go that are to be joined.  `near`: [sets][rows_k][dim]
+// of dK, then of dV; `far`: [run][tile with sinks][set][dK, dV][kKeysB][dim].
 struct KeySums {
-  float *near, *far;           // sums of (dK, dV) before they are joined; nullptr: results are written
+  float *near, *far;           // nullptr: results are written; there are no runs
+  unsigned per, sets;          // query heads of a workgroup; hq / per
   unsigned sink_tiles;         // tiles of a sequence that may have runs
   unsigned runs;               // at most, of all sequences
 };
 
-// dK, dV of 256 keys for one query head, 64 queries at a time; FAR: one run
-// of queries for a tile with sinks.
-template <int DP, bool FAR>
-__global__ __launch_bounds__(kWavesB * 64, 2) void k_attn_dkv(AttnBwdArgs b, const float* delta, KeySums sums) {
+// dK, dV of 128 keys for some query heads of their key head, 64 queries at a
+// time; the first workgroups take the runs of queries beyond tiles with sinks.
+//
+// One wave a SIMD: the sums (128 registers), the operands of its 32 keys (64)
+// and two 32 x 32 tiles leave no room for a second, so within the wave the
+// arithmetic of P and dS is spread over the products that do not need it, and
+// operands are read from LDS eight products ahead.
+template <int DP>
+__global__ __launch_bounds__(kWavesK * 64, DP == 64 ? 2 : 1) void k_attn_dkv(AttnBwdArgs b, const float* delta, KeySums sums) {
   constexpr int KS = DP / 16, DT = DP / 32;
   constexpr uint32_t kTile = kBT * DP * 2;
   __shared__ __align__(1024) char lds[4 * kTile];
@@ -246,28 +239,29 @@ __global__ __launch_bounds__(kWavesB * 64, 2) void k_attn_dkv(AttnBwdArgs b, con
   const AttnArgs& a = b.f;
   const int t = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(t / kWave);
   const int col = lane & 31, hh = lane >> 5;
-  unsigned rank = blockIdx.x / a.hq;
-  const unsigned hi = blockIdx.x % a.hq;
-  const unsigned kvh = hi % a.hkv, head = kvh * (a.hq / a.hkv) + hi / a.hkv;
+  unsigned rank = blockIdx.x / sums.sets;
+  const unsigned hi = blockIdx.x % sums.sets;   // sets of one key head on one XCD, if there are eight heads
+  const unsigned kvh = hi % a.hkv, set = kvh * (sums.sets / a.hkv) + hi / a.hkv, head0 = set * sums.per;
+  const unsigned far_tiles = sums.runs * sums.sink_tiles;
+  const bool far = rank < far_tiles;
   Tile tile;
   int j0, q_lo, q_hi;
   Rows rq, rk;
-  if constexpr (FAR) {
+  if (far) {
     const unsigned st = rank % sums.sink_tiles;
-    rank /= sums.sink_tiles;
     // (offsets that do not ascend can ask for more runs than there is room for)
-    if (!find_tile<true>(a.cu_q, a.seqs, a.rows_q, kFar, rank, &tile) || tile.at >= sums.runs) return;
-    rq = rows_of(a.cu_q, tile.seq, a.rows_q);
-    rk = rows_of(a.cu_k, tile.seq, a.rows_k);
-    j0 = (int)(st * kRowsB);
+    if (!find_tile<true, true>(a.cu_q, a.seqs, a.rows_q, kFar, rank / sums.sink_tiles, &tile) || tile.at >= sums.runs) return;
+    rq = rows_at(a.cu_q, tile.seq, a.rows_q);
+    rk = rows_at(a.cu_k, tile.seq, a.rows_k);
+    j0 = (int)(st * kKeysB);
     if (j0 >= (int)rk.count) return;
     q_lo = max((int)tile.row, band_of(a, j0, (int)rk.count - (int)rq.count, (int)rq.count).hi);
     q_hi = min((int)(tile.row + kFar), (int)rq.count);
     if (q_lo >= q_hi) return;
   } else {
-    if (!find_tile(a.cu_k, a.seqs, a.rows_k, kRowsB, rank, &tile)) return;
-    rq = rows_of(a.cu_q, tile.seq, a.rows_q);
-    rk = rows_of(a.cu_k, tile.seq, a.rows_k);
+    if (!find_tile<false>(a.cu_k, a.seqs, a.rows_k, kKeysB, rank - far_tiles, &tile)) return;
+    rq = rows_at(a.cu_q, tile.seq, a.rows_q);
+    rk = rows_at(a.cu_k, tile.seq, a.rows_k);
     j0 = (int)tile.row;
     const Band band = band_of(a, j0, (int)rk.count - (int)rq.count, (int)rq.count);
     q_lo = band.lo;
@@ -276,86 +270,138 @@ __global__ __launch_bounds__(kWavesB * 64, 2) void k_attn_dkv(AttnBwdArgs b, con
   const int shift = (int)rk.count - (int)rq.count, klast = (int)rk.count - 1;
   const int key = j0 + wave * 32 + col, w0 = j0 + wave * 32;
   const bool sinks = key < (int)a.sinks;
-  const int nt = (q_hi - q_lo + kBT - 1) / kBT;
+  const int nt = max((q_hi - q_lo + kBT - 1) / kBT, 0), all = nt * (int)sums.per;   // tiles of a head, of all
 
-  if (a.dim < DP) zero_lds<DP>(lds, 4 * kTile);
+  if (a.dim < DP) zero_lds(lds, 4 * kTile);
   const size_t at = rk.first + min(key, klast);
   Frag8 k[KS], v[KS];
   load_row(k, a.k.p + at * a.k.ts + kvh * a.k.hs, hh, a.dim);
   load_row(v, a.v.p + at * a.v.ts + kvh * a.v.hs, hh, a.dim);
   const float c = a.scale * kLog2e;
-  const uint16_t* qb = a.q.p + (size_t)rq.first * a.q.ts + head * a.q.hs;
-  const uint16_t* gb = b.d_out.p + (size_t)rq.first * b.d_out.ts + head * b.d_out.hs;
+  const uint16_t* qb = a.q.p + (size_t)rq.first * a.q.ts + head0 * a.q.hs;
+  const uint16_t* gb = b.d_out.p + (size_t)rq.first * b.d_out.ts + head0 * b.d_out.hs;
   const uint32_t lbase = lds_addr(lds);
+  const float inv_scale = 1.0f / a.scale;
   float stat = 0.f;                            // of the tile's query t: lse, or delta
-  auto copy = [&](int n, int buf) {
-    copy_tiles<DP>(qb, a.q.ts, gb, b.d_out.ts, q_lo + n * kBT, q_hi - 1, a.dim, lbase + buf * 2 * kTile, wave, lane);
+  const TileCopy<DP, kWavesK> copy_rows(a.q.ts, b.d_out.ts, a.dim, wave, lane);
+  int next = 0, next_head = 0;                 // tile that is copied next
+  auto copy = [&](int buf) {
+    const int first = q_lo + next * kBT;
+    copy_rows(qb + next_head * a.q.hs, a.q.ts, gb + next_head * b.d_out.hs, b.d_out.ts, first, q_hi - 1, lbase + buf * 2 * kTile);
     if (t < 2 * kBT) {
-      const size_t i = rq.first + min(q_lo + n * kBT + t % kBT, q_hi - 1);
-      stat = t < kBT ? lse2_of(a.lse[i * a.lse_ts + head * a.lse_hs]) : delta[(size_t)head * a.rows_q + i];
+      const size_t i = rq.first + min(first + t % kBT, q_hi - 1), head = head0 + next_head;
+      // what the sums start from: S - lse / scale, dP - delta
+      stat = t < kBT ? -finite_lse(a.lse[i * a.lse_ts + head * a.lse_hs]) * inv_scale : -delta[head * a.rows_q + i];
+    }
+    if (++next == nt) {
+      next = 0;
+      ++next_head;
     }
   };
   f32x16 dk[DT], dv[DT];
   clear(dk);
   clear(dv);
-  if (nt > 0) copy(0, 0);
-  for (int n = 0; n < nt; ++n) {
+  int now = 0;
+  if (all > 0) copy(0);
+  for (int n = 0; n < all; ++n) {
     const int buf = n & 1;
     wait_copies();
     if (t < 2 * kBT) lrow[buf][t / kBT][t % kBT] = stat;
     __syncthreads();
-    if (n + 1 < nt) copy(n + 1, buf ^ 1);
-    const int i0 = q_lo + n * kBT, p0 = shift + i0, pn = shift + min(i0 + kBT, q_hi) - 1;
+    if (n + 1 < all) copy(buf ^ 1);
+    const int i0 = q_lo + now * kBT, p0 = shift + i0, pn = shift + min(i0 + kBT, q_hi) - 1;
+    now = now + 1 == nt ? 0 : now + 1;
     const int wfar = window_start(p0, a.window);   // first key that a query of the tile has in its window
     if (w0 > klast || w0 > pn || (w0 + 31 < wfar && w0 >= (int)a.sinks)) continue;
     const bool whole = i0 + kBT <= q_hi && w0 + 31 <= p0 && w0 + 31 <= klast &&
                        (w0 >= window_start(pn, a.window) || w0 + 31 < (int)a.sinks);
-    const char* tq = lds + buf * 2 * kTile;
+    // of the tile's queries, less 4 hh, those that see the lane's key
+    const int far_end = sinks ? q_hi - 1 : (int)min((long long)q_hi - 1, (long long)key + a.window - 1 - shift);
+    const Interval view(key - shift - i0 - 4 * hh, (key <= klast ? far_end : -0x40000000) - i0 - 4 * hh);
+    const LaneAddr<DP> at_q(lbase + buf * 2 * kTile, lane);
+    auto tile_step = [&](auto masked) {
+      constexpr bool MASK = decltype(masked)::value;
+#pragma unroll 1
+      for (int r0 = 0; r0 < kBT; r0 += 32) {
+        const LaneAddr<DP> from = {at_q, (uint32_t)(r0 * DP * 2)};
+        f32x16 s, d;
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      f32x16 s = times_rows<DP>(tq, 32 * x, col, hh, k);
+        for (int g = 0; g < 4; ++g) {
+          const f32x4 l = *reinterpret_cast<const f32x4*>(&lrow[buf][0][r0 + 8 * g + 4 * hh]);
+          const f32x4 e = *reinterpret_cast<const f32x4*>(&lrow[buf][1][r0 + 8 * g + 4 * hh]);
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const f32x4 l = *reinterpret_cast<const f32x4*>(&lrow[buf][0][32 * x + 8 * g + 4 * hh]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[4 * g + e] = exp2_fast(__builtin_fmaf(s[4 * g + e], c, -l[e]));
-      }
-      uint32_t seen = 0xFFFFu;
-      if (!whole) {
-        seen = 0;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int i = i0 + 32 * x + 8 * (r / 4) + 4 * hh + r % 4, p = shift + i;
-          if (i < q_hi && key <= p && key <= klast && (key >= window_start(p, a.window) || sinks)) seen |= 1u << r;
+          for (int x = 0; x < 4; ++x) {
+            s[4 * g + x] = l[x];
+            d[4 * g + x] = e[x];
+          }
         }
+        // products 0 .. KS - 1: scores; then dP; dV; dK, 2 DT each
+        constexpr int ALL = 2 * KS + 4 * DT, AHEAD = 8;
+        Frag8 f[AHEAD];
+        auto load = [&](auto ii) {
+          constexpr int i = decltype(ii)::value;
+          Frag8& o = f[i % AHEAD];
+          if constexpr (i < KS) o.u = from.rows(0, i);
+          else if constexpr (i < 2 * KS) o.u = from.rows(kBT, i - KS);
+          else if constexpr (i < 2 * KS + 2 * DT) o = from.columns(kBT + (i - 2 * KS) / DT * 16, (i - 2 * KS) % DT);
+          else o = from.columns((i - 2 * KS - 2 * DT) / DT * 16, (i - 2 * KS - 2 * DT) % DT);
+        };
+        Frag8 pp[2], pd[2];
+        auto seen = [&](int r) { return view.has(r0 + 8 * (r / 4) + r % 4); };
+        steps<AHEAD>(load);
+        steps<ALL>([&](auto ii) {
+          constexpr int i = decltype(ii)::value;
+          const Frag8& o = f[i % AHEAD];
+          if constexpr (i < KS) {
+            s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(o.b, k[i].b, s, 0, 0, 0);
+          } else if constexpr (i < 2 * KS) {
+            d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(o.b, v[i - KS].b, d, 0, 0, 0);
+          } else if constexpr (i < 2 * KS + 2 * DT) {
+            constexpr int n = i - 2 * KS;
+            dv[n % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(o.b, pp[n / DT].b, dv[n % DT], 0, 0, 0);
+          } else {
+            constexpr int n = i - 2 * KS - 2 * DT;
+            dk[n % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(o.b, pd[n / DT].b, dk[n % DT], 0, 0, 0);
+          }
+          if constexpr (i + AHEAD < ALL) load(SPc<i + AHEAD>{});
+          // beside the products of dP, P; beside those of dV, dS
+          if constexpr (i >= KS && i < 2 * KS) {
+            constexpr int per = 16 / KS, r0_ = (i - KS) * per;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) s[r] = seen >> r & 1 ? s[r] : 0.f;
+            for (int r = r0_; r < r0_ + per; r += 2) {
+#pragma unroll
+              for (int x = r; x < r + 2; ++x) {
+                s[x] = exp2_fast(s[x] * c);
+                if (MASK) s[x] = seen(x) ? s[x] : 0.f;
+              }
+              pp[r / 8].w[r % 8 / 2] = cvt_bf16x2(s[r], s[r + 1]);
+            }
+          }
+          if constexpr (i >= 2 * KS && i < 2 * KS + 2 * DT) {
+            constexpr int per = 16 / (2 * DT), r0_ = (i - 2 * KS) * per;
+#pragma unroll
+            for (int r = r0_; r < r0_ + per; r += 2) {
+              const float x = s[r] * d[r], y = s[r + 1] * d[r + 1];
+              pd[r / 8].w[r % 8 / 2] = MASK ? cvt_bf16x2(s[r] == 0.f ? 0.f : x, s[r + 1] == 0.f ? 0.f : y) : cvt_bf16x2(x, y);
+            }
+          }
+          keep_order();
+        });
       }
-      add_columns<DP>(dv, lbase + buf * 2 * kTile + kTile, 32 * x, lane, s);
-      const f32x16 d = times_rows<DP>(tq + kTile, 32 * x, col, hh, v);
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const f32x4 l = *reinterpret_cast<const f32x4*>(&lrow[buf][1][32 * x + 8 * g + 4 * hh]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[4 * g + e] *= d[4 * g + e] - l[e];
-      }
-      if (!whole) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) s[r] = seen >> r & 1 ? s[r] : 0.f;
-      }
-      add_columns<DP>(dk, lbase + buf * 2 * kTile, 32 * x, lane, s);
-    }
+    };
+    if (whole) tile_step(std::false_type{});
+    else tile_step(std::true_type{});
   }
   if (key > klast) return;
-  if constexpr (FAR) {
-    const size_t slot = ((size_t)tile.at * sums.sink_tiles + j0 / kRowsB) * a.hq + head;
-    float* o = sums.far + (slot * 2 * kRowsB + wave * 32 + col) * a.dim;
+  if (far) {
+    const size_t slot = ((size_t)tile.at * sums.sink_tiles + j0 / kKeysB) * sums.sets + set;
+    float* o = sums.far + (slot * 2 * kKeysB + wave * 32 + col) * a.dim;
     store_row(o, dk, hh, a.dim);
-    store_row(o + (size_t)kRowsB * a.dim, dv, hh, a.dim);
+    store_row(o + (size_t)kKeysB * a.dim, dv, hh, a.dim);
   } else if (sums.near) {
-    float* o = sums.near + ((size_t)head * a.rows_k + at) * a.dim;
+    float* o = sums.near + ((size_t)set * a.rows_k + at) * a.dim;
     store_row(o, dk, hh, a.dim);
-    store_row(o + (size_t)a.hq * a.rows_k * a.dim, dv, hh, a.dim);
+    store_row(o + (size_t)sums.sets * a.rows_k * a.dim, dv, hh, a.dim);
   } else {
     store_row(b.dk.p + at * b.dk.ts + kvh * b.dk.hs, dk, a.scale, hh, a.dim);
     store_row(b.dv.p + at * b.dv.ts + kvh * b.dv.hs, dv, 1.0f, hh, a.dim);
@@ -366,15 +412,15 @@ __global__ __launch_bounds__(kWavesB * 64, 2) void k_attn_dkv(AttnBwdArgs b, con
 // one key head, dK then dV.
 __global__ __launch_bounds__(256) void k_attn_join(AttnBwdArgs b, KeySums sums) {
   const AttnArgs& a = b.f;
-  const unsigned kvh = blockIdx.x % a.hkv, rank = blockIdx.x / a.hkv, group = a.hq / a.hkv;
+  const unsigned kvh = blockIdx.x % a.hkv, rank = blockIdx.x / a.hkv, group = sums.sets / a.hkv;   // sets of a key head
   Tile tile;
-  if (!find_tile(a.cu_k, a.seqs, a.rows_k, 64, rank, &tile)) return;
-  const Rows rq = rows_of(a.cu_q, tile.seq, a.rows_q), rk = rows_of(a.cu_k, tile.seq, a.rows_k);
-  const int j0 = (int)(tile.row / kRowsB * kRowsB);   // of the rows' tile of keys
+  if (!find_tile<true>(a.cu_k, a.seqs, a.rows_k, 64, rank, &tile)) return;
+  const Rows rq = rows_at(a.cu_q, tile.seq, a.rows_q), rk = rows_at(a.cu_k, tile.seq, a.rows_k);
+  const int j0 = (int)(tile.row / kKeysB * kKeysB);   // of the rows' tile of keys
   // runs of the sequence: numbers first .. first + runs - 1, queries from (1 + i) kFar on
   unsigned first = 0, runs = 0;
   Band band{0, 0};
-  if (sums.sink_tiles && j0 < (int)a.sinks && (unsigned)(j0 / kRowsB) < sums.sink_tiles && rq.count > kFar) {
+  if (sums.sink_tiles && j0 < (int)a.sinks && (unsigned)(j0 / kKeysB) < sums.sink_tiles && rq.count > kFar) {
     runs = (rq.count - 1) / kFar;
     for (unsigned s0 = 0; s0 < tile.seq; s0 += kWave) {
       const unsigned s = s0 + lane_id(), n = s < tile.seq ? rows_of(a.cu_q, s, a.rows_q).count : 0;
@@ -390,15 +436,15 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnBwdArgs b, KeySums sums) 
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
       f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-      const float* near = sums.near + (size_t)which * a.hq * a.rows_k * a.dim + at * a.dim + d;
+      const float* near = sums.near + (size_t)which * sums.sets * a.rows_k * a.dim + at * a.dim + d;
 #pragma unroll 4
       for (unsigned h = 0; h < group; ++h)
         sum += *reinterpret_cast<const f32x4*>(near + (size_t)(kvh * group + h) * a.rows_k * a.dim);
       for (unsigned n = 0; n < runs && first + n < sums.runs; ++n) {
         if ((int)min((n + 2) * kFar, rq.count) <= band.hi) continue;   // all of the run's queries were near
-        const size_t slot = ((size_t)(first + n) * sums.sink_tiles + j0 / kRowsB) * a.hq + kvh * group;
-        const float* far = sums.far + ((slot * 2 + which) * kRowsB + tile.row - j0 + r) * a.dim + d;
-        for (unsigned h = 0; h < group; ++h) sum += *reinterpret_cast<const f32x4*>(far + (size_t)h * 2 * kRowsB * a.dim);
+        const size_t slot = ((size_t)(first + n) * sums.sink_tiles + j0 / kKeysB) * sums.sets + kvh * group;
+        const float* far = sums.far + ((slot * 2 + which) * kKeysB + tile.row - j0 + r) * a.dim + d;
+        for (unsigned h = 0; h < group; ++h) sum += *reinterpret_cast<const f32x4*>(far + (size_t)h * 2 * kKeysB * a.dim);
       }
       const float f = which ? 1.0f : a.scale;
       const HeadOut& o = which ? b.dv : b.dk;
@@ -410,18 +456,27 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnBwdArgs b, KeySums sums) 
 
 struct Room {
   size_t delta, near, far;     // binary32 values
-  unsigned sink_tiles, runs;
+  unsigned per, sets, sink_tiles, runs;
 };
 Room room_of(size_t rows_q, size_t rows_k, size_t hq, size_t hkv, size_t dim, size_t window, size_t sinks) {
   Room r{};
   r.delta = cdiv(rows_q * hq, 64) * 64;
+  // Query heads of a key head that one workgroup takes one after the other:
+  // as many as leave two workgroups a CU.  Each spares a write and a read of
+  // its sums and a start.
+  const size_t group = hq / hkv, tiles = cdiv(rows_k ? rows_k : 1, kKeysB) * hkv;
+  size_t per = group;
+  while (per > 1 && (group % per || tiles * (group / per) < 512)) --per;
+  r.per = (unsigned)per;
+  r.sets = (unsigned)(hq / per);
   if (window < rows_k && sinks) {
-    r.sink_tiles = (unsigned)cdiv(sinks < rows_k ? sinks : rows_k, kRowsB);
+    r.sink_tiles = (unsigned)cdiv(sinks < rows_k ? sinks : rows_k, kKeysB);
     r.runs = (unsigned)(rows_q / kFar);
     if (r.runs == 0) r.sink_tiles = 0;
   }
-  if (hq > hkv || r.sink_tiles) r.near = 2 * hq * rows_k * dim;
-  r.far = (size_t)r.runs * r.sink_tiles * hq * 2 * kRowsB * dim;
+  if (r.sets > hkv || r.sink_tiles) r.near = 2 * r.sets * rows_k * dim;
+  r.far = (size_t)r.runs * r.sink_tiles * r.sets * 2 * kKeysB * dim;
+  if (r.far == 0) r.runs = r.sink_tiles = 0;
   return r;
 }
 
@@ -436,19 +491,16 @@ hipError_t launch(const Launch& L, const AttnBwdArgs& b) {
                  a.rows_q, a.hq, a.dim);
     if (e != hipSuccess) return e;
     if (b.dq.p) {
-      const unsigned tiles = a.rows_q / kRowsB + a.seqs;
-      e = launch_k(k_attn_dq<DP>, dim3(tiles * a.hq), dim3(kWavesB * 64), 0, L.stream, b, delta);
+      const unsigned tiles = a.rows_q / kQueries + a.seqs;
+      e = launch_k(k_attn_dq<DP>, dim3(tiles * a.hq), dim3(kWavesQ * 64), 0, L.stream, b, delta);
       if (e != hipSuccess) return e;
     }
   }
   if (!b.dk.p || a.rows_k == 0) return hipSuccess;
   const KeySums sums{room.near ? delta + room.delta : nullptr, room.far ? delta + room.delta + room.near : nullptr,
-                     room.sink_tiles, room.runs};
-  if (room.far) {
-    e = launch_k(k_attn_dkv<DP, true>, dim3(room.runs * room.sink_tiles * a.hq), dim3(kWavesB * 64), 0, L.stream, b, delta, sums);
-    if (e != hipSuccess) return e;
-  }
-  e = launch_k(k_attn_dkv<DP, false>, dim3((a.rows_k / kRowsB + a.seqs) * a.hq), dim3(kWavesB * 64), 0, L.stream, b, delta, sums);
+                     room.per, room.sets, room.sink_tiles, room.runs};
+  const unsigned tiles = room.runs * room.sink_tiles + a.rows_k / kKeysB + a.seqs;
+  e = launch_k(k_attn_dkv<DP>, dim3(tiles * room.sets), dim3(kWavesK * 64), 0, L.stream, b, delta, sums);
   if (e != hipSuccess || !sums.near) return e;
   return launch_k(k_attn_join, dim3((a.rows_k / 64 + a.seqs) * a.hkv), dim3(256), 0, L.stream, b, sums);
 }
