@@ -150,48 +150,10 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
 
   f32x16 o[DT];
   float m, l;
-  // o += V^T P^T where infinities and NaN of masked places must not count: 0 in
-  // their place, and a count of each kind that a query sees
-  auto add_with_care = [&](const LaneAddr<DP>& from, const Frag8 (&pf)[4], auto& seen) {
-#pragma unroll 1
-    for (int kind = -1; kind < 3; ++kind) {    // -1: the numbers; infinities; NaN
-      const uint32_t like = kind == 0 ? 0x7F80u : 0xFF80u;
-      const float add = kind == 0 ? __builtin_huge_valf() : kind == 1 ? AR_NEG_INF : __uint_as_float(0x7FC00000u);
-#pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        f32x16 sum;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) sum[r] = 0.f;
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          Frag8 v = from.columns(kBN + 16 * n, d), w = pf[n];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t out = 0;
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const uint32_t x = (v.w[e] >> (16 * z)) & 0xFFFFu, size = x & 0x7FFFu;
-              const uint32_t y = kind < 0 ? (size < 0x7F80u ? x : 0u) : (kind < 2 ? x == like : size > 0x7F80u) ? 0x3F80u : 0u;
-              out |= y << (16 * z);
-            }
-            v.w[e] = out;
-            const int r = n % 2 * 8 + 2 * e;
-            asm volatile("" : "+v"(v.w[e]));   // one word after the other: not all masks at once
-            if (kind >= 0) w.w[e] = (seen(n / 2, r) ? 0x3F80u : 0u) | (seen(n / 2, r + 1) ? 0x3F800000u : 0u);
-          }
-          sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v.b, w.b, sum, 0, 0, 0);
-        }
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (kind < 0) o[d][r] += sum[r];
-          else if (sum[r] > 0.f) o[d][r] += add;
-      }
-    }
-  };
   // Values that are no numbers under masked scores: such a score counts 0,
   // but 0 times them is NaN.  So where a result is no number the pass is made
-  // again with care: tiles with masked scores put 0 for such values and add
-  // them where they are visible.
+  // again with care: such values are added where they are visible, and are 0
+  // in the product.
   bool care = false;
   for (;;) {
     m = AR_NEG_INF;
@@ -215,11 +177,33 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
       }
       const KeyStep k = key_step(keys, n, kBN);
       const int j0 = k.j0;
+      // of the tile's keys, less 4 hh, those that the lane's query sees
+      const Interval view((k.sinks ? 0 : start) - j0 - 4 * hh, min(p, k.end - 1) - j0 - 4 * hh);
+      if (care) {
+        char* tv = lds + (buf * 2 + 1) * kTile;
+#pragma unroll 1
+        for (int r = 0; r < kBN; ++r) {
+          const bool sees = view.has(r - 4 * hh);
+#pragma unroll
+          for (int x = 0; x < DT * 4; ++x) {
+            const u32x2 w = *reinterpret_cast<const u32x2*>(tv + chunk_addr<DP>(r, x) + 8 * hh);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float v = e & 1 ? hi_f32(w[e / 2]) : lo_f32(w[e / 2]);
+              if (sees && !(__builtin_fabsf(v) < __builtin_huge_valf())) o[x / 4][x % 4 * 4 + e] += v;
+            }
+          }
+        }
+        __syncthreads();
+        for (uint32_t at = t * 4; at < kTile; at += NW * 64 * 4) {
+          uint32_t& w = *reinterpret_cast<uint32_t*>(tv + at);
+          w &= ((w & 0x7F80u) == 0x7F80u ? 0xFFFF0000u : ~0u) & ((w & 0x7F800000u) == 0x7F800000u ? 0xFFFFu : ~0u);
+        }
+        __syncthreads();
+      }
       // no key of the tile is visible to the wave's queries
       if ((int)tile.row + wave * 32 > last || j0 > wp1 || (!k.sinks && j0 + kBN <= wstart0)) continue;
       const bool whole = j0 + kBN - 1 <= min(wp0, k.end - 1) && (k.sinks || j0 >= wstart1);
-      // of the tile's keys, less 4 hh, those that the lane's query sees
-      const Interval view((k.sinks ? 0 : start) - j0 - 4 * hh, min(p, k.end - 1) - j0 - 4 * hh);
       const LaneAddr<DP> from(lbase + buf * 2 * kTile, lane);
       // register r of block b: key 32 b + 8 (r / 4) + 4 hh + r % 4
       auto seen = [&](int b, int r) { return view.has(32 * b + 8 * (r / 4) + r % 4); };
@@ -243,10 +227,6 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
           if constexpr (i < 2 * KS) f[i % AHEAD].u = from.rows(i / KS * 32, i % KS);
           else f[i % AHEAD] = from.columns(kBN + (i - 2 * KS) / DT * 16, (i - 2 * KS) % DT);
         };
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) s[b][r] = 0.f;
         auto fit = [&](int b) {                // scales and mask of a block of scores
           if constexpr (SRC == kKeyPagesE4M3) {
             f32x16 f;
@@ -267,7 +247,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
         float top = AR_NEG_INF;
         steps<2 * KS>([&](auto ii) {
           constexpr int i = decltype(ii)::value;
-          s[i / KS] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[i % AHEAD].b, q[i % KS].b, s[i / KS], 0, 0, 0);
+          s[i / KS] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[i % AHEAD].b, q[i % KS].b, i % KS ? s[i / KS] : f32x16{}, 0, 0, 0);
           load(SPc<i + AHEAD>{});
           if constexpr (i == KS + KS / 2) {
             fit(0);
@@ -280,7 +260,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
         // the running maximum follows only where it falls behind by 2^8: sums
         // stay far below binary32's range, and most tiles change nothing
         if (__any(top > m + 8.0f)) {
-          const float up = fmaxf(m, top), f = up == AR_NEG_INF ? 1.0f : exp2_fast(m - up);
+          const float up = fmaxf(m, top), f = m == AR_NEG_INF ? 1.0f : exp2_fast(m - up);   // (all is 0 before a first score)
           m = up;
           l *= f;
 #pragma unroll
@@ -305,14 +285,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
           }
         };
         weigh(0, 0, 16);
-        if constexpr (MASK) {
-          weigh(1, 0, 16);
-          if (care) {
-            add_with_care(from, pf, seen);
-            l += more;
-            return;
-          }
-        }
+        if constexpr (MASK) weigh(1, 0, 16);
         steps<4 * DT>([&](auto ii) {
           constexpr int n = decltype(ii)::value, i = n + 2 * KS;
           o[n % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[i % AHEAD].b, pf[n / DT].b, o[n % DT], 0, 0, 0);
