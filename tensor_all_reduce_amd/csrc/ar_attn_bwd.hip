@@ -18,7 +18,7 @@ namespace ar {
 namespace {
 
 constexpr int kWavesQ = 8, kQueries = kWavesQ * 32;  // queries of a workgroup
-constexpr int kWavesK = 4, kKeysB = kWavesK * 32;    // keys of a workgroup
+constexpr int kWavesK = 8, kKeysB = kWavesK / 2 * 32;  // keys of a workgroup, each wave half of a tile's queries
 constexpr int kBT = 64;                            // rows of the other side at a time
 constexpr unsigned kFar = 2048;                    // queries of a run
 
@@ -226,15 +226,18 @@ struct KeySums {
 // dK, dV of 128 keys for some query heads of their key head, 64 queries at a
 // time; the first workgroups take the runs of queries beyond tiles with sinks.
 //
-// One wave a SIMD: the sums (128 registers), the operands of its 32 keys (64)
-// and two 32 x 32 tiles leave no room for a second, so within the wave the
-// arithmetic of P and dS is spread over the products that do not need it, and
-// operands are read from LDS eight products ahead.
+// A wave has 32 of the keys and half of a tile's queries, and its partner's
+// sums are added at the end.  Two waves a SIMD hold their sums (128 registers)
+// and two 32 x 32 tiles in registers only because the keys and values stay in
+// LDS, too: with them in registers there is room for one wave a SIMD, which
+// measured slower though it reads a third less from LDS (2 x 4096 tokens, 64
+// heads of 128: 1437 us, this 1190).  The arithmetic of P and dS is spread
+// over the products that do not need it.
 template <int DP>
-__global__ __launch_bounds__(kWavesK * 64, DP == 64 ? 2 : 1) void k_attn_dkv(AttnBwdArgs b, const float* delta, KeySums sums) {
+__global__ __launch_bounds__(kWavesK * 64, 2) void k_attn_dkv(AttnBwdArgs b, const float* delta, KeySums sums) {
   constexpr int KS = DP / 16, DT = DP / 32;
   constexpr uint32_t kTile = kBT * DP * 2;
-  __shared__ __align__(1024) char lds[4 * kTile];
+  __shared__ __align__(1024) char lds[8 * kTile];  // two tiles of queries; the keys and values, 64 at a time
   __shared__ __align__(16) float lrow[2][2][kBT];  // lse, delta
   const AttnArgs& a = b.f;
   const int t = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(t / kWave);
@@ -268,15 +271,12 @@ __global__ __launch_bounds__(kWavesK * 64, DP == 64 ? 2 : 1) void k_attn_dkv(Att
     q_hi = band.hi;
   }
   const int shift = (int)rk.count - (int)rq.count, klast = (int)rk.count - 1;
-  const int key = j0 + wave * 32 + col, w0 = j0 + wave * 32;
+  const int w0 = j0 + (wave & 3) * 32, key = w0 + col, r0 = (wave >> 2) * 32;   // the wave's keys, its rows of a tile
   const bool sinks = key < (int)a.sinks;
   const int nt = max((q_hi - q_lo + kBT - 1) / kBT, 0), all = nt * (int)sums.per;   // tiles of a head, of all
 
-  if (a.dim < DP) zero_lds(lds, 4 * kTile);
+  if (a.dim < DP) zero_lds(lds, 8 * kTile);
   const size_t at = rk.first + min(key, klast);
-  Frag8 k[KS], v[KS];
-  load_row(k, a.k.p + at * a.k.ts + kvh * a.k.hs, hh, a.dim);
-  load_row(v, a.v.p + at * a.v.ts + kvh * a.v.hs, hh, a.dim);
   const float c = a.scale * kLog2e;
   const uint16_t* qb = a.q.p + (size_t)rq.first * a.q.ts + head0 * a.q.hs;
   const uint16_t* gb = b.d_out.p + (size_t)rq.first * b.d_out.ts + head0 * b.d_out.hs;
@@ -284,15 +284,17 @@ __global__ __launch_bounds__(kWavesK * 64, DP == 64 ? 2 : 1) void k_attn_dkv(Att
   const float inv_scale = 1.0f / a.scale;
   float stat = 0.f;                            // of the tile's query t: lse, or delta
   const TileCopy<DP, kWavesK> copy_rows(a.q.ts, b.d_out.ts, a.dim, wave, lane);
+  // from the last tile on: there the workgroups of a sequence's keys begin together, and share
+  // what they read in the L2
   int next = 0, next_head = 0;                 // tile that is copied next
   auto copy = [&](int buf) {
-    const int first = q_lo + next * kBT;
-    copy_rows(qb + next_head * a.q.hs, a.q.ts, gb + next_head * b.d_out.hs, b.d_out.ts, first, q_hi - 1, lbase + buf * 2 * kTile);
+    const int first = q_lo + (nt - 1 - next) * kBT;
     if (t < 2 * kBT) {
       const size_t i = rq.first + min(first + t % kBT, q_hi - 1), head = head0 + next_head;
       // what the sums start from: S - lse / scale, dP - delta
       stat = t < kBT ? -finite_lse(a.lse[i * a.lse_ts + head * a.lse_hs]) * inv_scale : -delta[head * a.rows_q + i];
     }
+    copy_rows(qb + next_head * a.q.hs, a.q.ts, gb + next_head * b.d_out.hs, b.d_out.ts, first, q_hi - 1, lbase + buf * 2 * kTile);
     if (++next == nt) {
       next = 0;
       ++next_head;
@@ -302,28 +304,31 @@ __global__ __launch_bounds__(kWavesK * 64, DP == 64 ? 2 : 1) void k_attn_dkv(Att
   clear(dk);
   clear(dv);
   int now = 0;
-  if (all > 0) copy(0);
+  if (all > 0) {
+    const TileCopy<DP, kWavesK> copy_keys(a.k.ts, a.v.ts, a.dim, wave, lane);
+    const uint16_t *kb = a.k.p + (size_t)rk.first * a.k.ts + kvh * a.k.hs, *vb = a.v.p + (size_t)rk.first * a.v.ts + kvh * a.v.hs;
+    for (int x = 0; x < 2; ++x) copy_keys(kb, a.k.ts, vb, a.v.ts, j0 + 64 * x, klast, lbase + (4 + 2 * x) * kTile);
+    copy(0);
+  }
+  const uint32_t lkeys = lbase + (4 + (wave >> 1 & 1) * 2) * kTile + (wave & 1) * 32 * DP * 2;
   for (int n = 0; n < all; ++n) {
     const int buf = n & 1;
     wait_copies();
     if (t < 2 * kBT) lrow[buf][t / kBT][t % kBT] = stat;
     __syncthreads();
     if (n + 1 < all) copy(buf ^ 1);
-    const int i0 = q_lo + now * kBT, p0 = shift + i0, pn = shift + min(i0 + kBT, q_hi) - 1;
+    const int i0 = q_lo + (nt - 1 - now) * kBT + r0, p0 = shift + i0, pn = shift + min(i0 + 32, q_hi) - 1;   // the wave's queries
     now = now + 1 == nt ? 0 : now + 1;
-    const int wfar = window_start(p0, a.window);   // first key that a query of the tile has in its window
-    if (w0 > klast || w0 > pn || (w0 + 31 < wfar && w0 >= (int)a.sinks)) continue;
-    const bool whole = i0 + kBT <= q_hi && w0 + 31 <= p0 && w0 + 31 <= klast &&
+    const int wfar = window_start(p0, a.window);   // first key that one of them has in its window
+    if (i0 >= q_hi || w0 > klast || w0 > pn || (w0 + 31 < wfar && w0 >= (int)a.sinks)) continue;
+    const bool whole = i0 + 32 <= q_hi && w0 + 31 <= p0 && w0 + 31 <= klast &&
                        (w0 >= window_start(pn, a.window) || w0 + 31 < (int)a.sinks);
-    // of the tile's queries, less 4 hh, those that see the lane's key
+    // of the wave's queries, less 4 hh, those that see the lane's key
     const int far_end = sinks ? q_hi - 1 : (int)min((long long)q_hi - 1, (long long)key + a.window - 1 - shift);
     const Interval view(key - shift - i0 - 4 * hh, (key <= klast ? far_end : -0x40000000) - i0 - 4 * hh);
-    const LaneAddr<DP> at_q(lbase + buf * 2 * kTile, lane);
+    const LaneAddr<DP> from(lbase + buf * 2 * kTile + r0 * DP * 2, lane), keys(lkeys, lane);
     auto tile_step = [&](auto masked) {
       constexpr bool MASK = decltype(masked)::value;
-#pragma unroll 1
-      for (int r0 = 0; r0 < kBT; r0 += 32) {
-        const LaneAddr<DP> from = {at_q, (uint32_t)(r0 * DP * 2)};
         f32x16 s, d;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
@@ -336,26 +341,28 @@ __global__ __launch_bounds__(kWavesK * 64, DP == 64 ? 2 : 1) void k_attn_dkv(Att
           }
         }
         // products 0 .. KS - 1: scores; then dP; dV; dK, 2 DT each
-        constexpr int ALL = 2 * KS + 4 * DT, AHEAD = 8;
-        Frag8 f[AHEAD];
+        constexpr int ALL = 2 * KS + 4 * DT, AHEAD = 3;
+        Frag8 f[AHEAD], fk[AHEAD];
         auto load = [&](auto ii) {
           constexpr int i = decltype(ii)::value;
           Frag8& o = f[i % AHEAD];
-          if constexpr (i < KS) o.u = from.rows(0, i);
-          else if constexpr (i < 2 * KS) o.u = from.rows(kBT, i - KS);
+          if constexpr (i < 2 * KS) {
+            o.u = from.rows(i / KS * kBT, i % KS);
+            fk[i % AHEAD].u = keys.rows(i / KS * kBT, i % KS);
+          }
           else if constexpr (i < 2 * KS + 2 * DT) o = from.columns(kBT + (i - 2 * KS) / DT * 16, (i - 2 * KS) % DT);
           else o = from.columns((i - 2 * KS - 2 * DT) / DT * 16, (i - 2 * KS - 2 * DT) % DT);
         };
         Frag8 pp[2], pd[2];
-        auto seen = [&](int r) { return view.has(r0 + 8 * (r / 4) + r % 4); };
+        auto seen = [&](int r) { return view.has(8 * (r / 4) + r % 4); };
         steps<AHEAD>(load);
         steps<ALL>([&](auto ii) {
           constexpr int i = decltype(ii)::value;
           const Frag8& o = f[i % AHEAD];
           if constexpr (i < KS) {
-            s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(o.b, k[i].b, s, 0, 0, 0);
+            s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(o.b, fk[i % AHEAD].b, s, 0, 0, 0);
           } else if constexpr (i < 2 * KS) {
-            d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(o.b, v[i - KS].b, d, 0, 0, 0);
+            d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(o.b, fk[i % AHEAD].b, d, 0, 0, 0);
           } else if constexpr (i < 2 * KS + 2 * DT) {
             constexpr int n = i - 2 * KS;
             dv[n % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(o.b, pp[n / DT].b, dv[n % DT], 0, 0, 0);
@@ -387,71 +394,97 @@ __global__ __launch_bounds__(kWavesK * 64, DP == 64 ? 2 : 1) void k_attn_dkv(Att
           }
           keep_order();
         });
-      }
     };
     if (whole) tile_step(std::false_type{});
     else tile_step(std::true_type{});
   }
-  if (key > klast) return;
-  if (far) {
-    const size_t slot = ((size_t)tile.at * sums.sink_tiles + j0 / kKeysB) * sums.sets + set;
-    float* o = sums.far + (slot * 2 * kKeysB + wave * 32 + col) * a.dim;
-    store_row(o, dk, hh, a.dim);
-    store_row(o + (size_t)kKeysB * a.dim, dv, hh, a.dim);
-  } else if (sums.near) {
-    float* o = sums.near + ((size_t)set * a.rows_k + at) * a.dim;
-    store_row(o, dk, hh, a.dim);
-    store_row(o + (size_t)sums.sets * a.rows_k * a.dim, dv, hh, a.dim);
+  // The sums of both halves: a wave gives its partner dK or dV, and takes the other.
+  __syncthreads();
+  const bool upper = wave >= 4;
+  f32x4* lsum = reinterpret_cast<f32x4*>(lds) + lane;
+  auto give = [&](const f32x16 (&sum)[DT]) {
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        lsum[((wave * DT + d) * 4 + g) * kWave] = f32x4{sum[d][4 * g], sum[d][4 * g + 1], sum[d][4 * g + 2], sum[d][4 * g + 3]};
+  };
+  auto take = [&](f32x16 (&sum)[DT]) {
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x4 x = lsum[(((wave ^ 4) * DT + d) * 4 + g) * kWave];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[d][4 * g + e] += x[e];
+        keep_order();
+      }
+  };
+  auto store = [&](f32x16 (&sum)[DT], const HeadOut& out, float f) {
+    if (key > klast) return;
+    if (far) {
+      const size_t slot = ((size_t)tile.at * sums.sink_tiles + j0 / kKeysB) * sums.sets + set;
+      store_row(sums.far + ((slot * 2 + upper) * kKeysB + key - j0) * a.dim, sum, hh, a.dim);
+    } else if (sums.near) {
+      store_row(sums.near + (((size_t)upper * sums.sets + set) * a.rows_k + at) * a.dim, sum, hh, a.dim);
+    } else {
+      store_row(out.p + at * out.ts + kvh * out.hs, sum, f, hh, a.dim);
+    }
+  };
+  if (upper) give(dk);
+  else give(dv);
+  __syncthreads();
+  if (upper) {
+    take(dv);
+    store(dv, b.dv, 1.0f);
   } else {
-    store_row(b.dk.p + at * b.dk.ts + kvh * b.dk.hs, dk, a.scale, hh, a.dim);
-    store_row(b.dv.p + at * b.dv.ts + kvh * b.dv.hs, dv, 1.0f, hh, a.dim);
+    take(dk);
+    store(dk, b.dk, a.scale);
   }
 }
 
-// Joins the sums of a key's query heads and runs: a workgroup takes 64 rows of
-// one key head, dK then dV.
+// Joins the sums of a key's query heads and runs: a workgroup takes 8 rows of
+// one key head of dK, or of dV.
+constexpr int kJoinRows = 8;
 __global__ __launch_bounds__(256) void k_attn_join(AttnBwdArgs b, KeySums sums) {
   const AttnArgs& a = b.f;
-  const unsigned kvh = blockIdx.x % a.hkv, rank = blockIdx.x / a.hkv, group = sums.sets / a.hkv;   // sets of a key head
+  const unsigned which = blockIdx.x & 1, kvh = (blockIdx.x >> 1) % a.hkv, rank = (blockIdx.x >> 1) / a.hkv;
+  const unsigned group = sums.sets / a.hkv;    // sets of a key head
   Tile tile;
-  if (!find_tile<true>(a.cu_k, a.seqs, a.rows_k, 64, rank, &tile)) return;
+  if (!find_tile<true>(a.cu_k, a.seqs, a.rows_k, kJoinRows, rank, &tile)) return;
   const Rows rq = rows_at(a.cu_q, tile.seq, a.rows_q), rk = rows_at(a.cu_k, tile.seq, a.rows_k);
   const int j0 = (int)(tile.row / kKeysB * kKeysB);   // of the rows' tile of keys
   // runs of the sequence: numbers first .. first + runs - 1, queries from (1 + i) kFar on
-  unsigned first = 0, runs = 0;
-  Band band{0, 0};
+  unsigned first = 0, runs = 0, skip = 0;
   if (sums.sink_tiles && j0 < (int)a.sinks && (unsigned)(j0 / kKeysB) < sums.sink_tiles && rq.count > kFar) {
     runs = (rq.count - 1) / kFar;
     for (unsigned s0 = 0; s0 < tile.seq; s0 += kWave) {
       const unsigned s = s0 + lane_id(), n = s < tile.seq ? rows_of(a.cu_q, s, a.rows_q).count : 0;
       first += __shfl(wave_scan(n ? (n - 1) / kFar : 0), kWave - 1);
     }
-    band = band_of(a, j0, (int)rk.count - (int)rq.count, (int)rq.count);
+    runs = first < sums.runs ? min(runs, sums.runs - first) : 0;
+    // the first runs' queries may all have been near
+    const Band band = band_of(a, j0, (int)rk.count - (int)rq.count, (int)rq.count);
+    while (skip < runs && (int)min((skip + 2) * kFar, rq.count) <= band.hi) ++skip;
   }
-  const unsigned per = a.dim / 4;              // groups of 4 columns
-  const unsigned rows = min(64u, rk.count - tile.row);
-  for (unsigned i = threadIdx.x; i < rows * per; i += 256) {
-    const unsigned r = i / per, d = i % per * 4;
-    const size_t at = rk.first + tile.row + r;
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-      const float* near = sums.near + (size_t)which * sums.sets * a.rows_k * a.dim + at * a.dim + d;
+  const unsigned per = a.dim / 4, i = threadIdx.x;   // groups of 4 columns
+  const unsigned r = i / per, d = i % per * 4;
+  if (i >= kJoinRows * per || tile.row + r >= rk.count) return;
+  const size_t at = rk.first + tile.row + r;
+  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+  const float* near = sums.near + (((size_t)which * sums.sets + kvh * group) * a.rows_k + at) * a.dim + d;
 #pragma unroll 4
-      for (unsigned h = 0; h < group; ++h)
-        sum += *reinterpret_cast<const f32x4*>(near + (size_t)(kvh * group + h) * a.rows_k * a.dim);
-      for (unsigned n = 0; n < runs && first + n < sums.runs; ++n) {
-        if ((int)min((n + 2) * kFar, rq.count) <= band.hi) continue;   // all of the run's queries were near
-        const size_t slot = ((size_t)(first + n) * sums.sink_tiles + j0 / kKeysB) * sums.sets + kvh * group;
-        const float* far = sums.far + ((slot * 2 + which) * kKeysB + tile.row - j0 + r) * a.dim + d;
-        for (unsigned h = 0; h < group; ++h) sum += *reinterpret_cast<const f32x4*>(far + (size_t)h * 2 * kKeysB * a.dim);
-      }
-      const float f = which ? 1.0f : a.scale;
-      const HeadOut& o = which ? b.dv : b.dk;
-      *reinterpret_cast<u32x2*>(o.p + at * o.ts + kvh * o.hs + d) =
-          u32x2{result_bf16x2(sum[0] * f, sum[1] * f), result_bf16x2(sum[2] * f, sum[3] * f)};
-    }
+  for (unsigned h = 0; h < group; ++h) sum += *reinterpret_cast<const f32x4*>(near + (size_t)h * a.rows_k * a.dim);
+  for (unsigned n = skip; n < runs; ++n) {
+    const size_t slot = ((size_t)(first + n) * sums.sink_tiles + j0 / kKeysB) * sums.sets + kvh * group;
+    const float* far = sums.far + ((slot * 2 + which) * kKeysB + tile.row - j0 + r) * a.dim + d;
+#pragma unroll 4
+    for (unsigned h = 0; h < group; ++h) sum += *reinterpret_cast<const f32x4*>(far + (size_t)h * 2 * kKeysB * a.dim);
   }
+  const float f = which ? 1.0f : a.scale;
+  const HeadOut& o = which ? b.dv : b.dk;
+  *reinterpret_cast<u32x2*>(o.p + at * o.ts + kvh * o.hs + d) =
+      u32x2{result_bf16x2(sum[0] * f, sum[1] * f), result_bf16x2(sum[2] * f, sum[3] * f)};
 }
 
 struct Room {
@@ -502,7 +535,7 @@ hipError_t launch(const Launch& L, const AttnBwdArgs& b) {
   const unsigned tiles = room.runs * room.sink_tiles + a.rows_k / kKeysB + a.seqs;
   e = launch_k(k_attn_dkv<DP>, dim3(tiles * room.sets), dim3(kWavesK * 64), 0, L.stream, b, delta, sums);
   if (e != hipSuccess || !sums.near) return e;
-  return launch_k(k_attn_join, dim3((a.rows_k / 64 + a.seqs) * a.hkv), dim3(256), 0, L.stream, b, sums);
+  return launch_k(k_attn_join, dim3((a.rows_k / kJoinRows + a.seqs) * a.hkv * 2), dim3(256), 0, L.stream, b, sums);
 }
 
 }  // namespace
