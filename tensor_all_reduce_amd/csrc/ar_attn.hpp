@@ -99,16 +99,18 @@ __device__ __forceinline__ unsigned page_of(unsigned x, const Pages& c) {
   return c.shift == 32 ? x : __umulhi(x, c.magic) >> c.shift;
 }
 
-// A wave's inclusive sums over its lanes.
+// A wave's inclusive sums over its lanes, which are all switched on: within
+// rows of 16 by DPP shifts, then a row's last lane to the rows after it.
 __device__ __forceinline__ unsigned wave_scan(unsigned v) {
-  const int lane = lane_id();
-#pragma unroll
-  for (int d = 1; d < kWave; d *= 2) {
-    const unsigned u = __shfl_up(v, d);
-    if (lane >= d) v += u;
-  }
+  v += (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, false);
+  v += (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, false);
+  v += (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, false);
+  v += (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, false);
+  v += (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false);
+  v += (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false);
   return v;
 }
+__device__ __forceinline__ unsigned last_lane(unsigned v) { return (unsigned)__builtin_amdgcn_readlane((int)v, kWave - 1); }
 
 // Rows first .. first + count - 1 of sequence s out of the offsets cu.  Any
 // contents of cu give rows below `rows`.
@@ -144,12 +146,12 @@ __device__ __forceinline__ bool find_tile(const int32_t* cu, unsigned seqs, unsi
     return SKIP ? (n ? (n - 1) / bm : 0) : (n + bm - 1) / bm;
   };
   unsigned total = 0;
-  for (unsigned s0 = 0; s0 < seqs; s0 += kWave) total += __shfl(wave_scan(tiles_of(s0 + lane)), kWave - 1);
+  for (unsigned s0 = 0; s0 < seqs; s0 += kWave) total += last_lane(wave_scan(tiles_of(s0 + lane)));
   if (rank >= total) return false;
   unsigned at = DOWN ? total - 1 - rank : rank;
   t->at = at;
   for (unsigned s0 = 0; s0 < seqs; s0 += kWave) {
-    const unsigned tiles = tiles_of(s0 + lane), upto = wave_scan(tiles), here = __shfl(upto, kWave - 1);
+    const unsigned tiles = tiles_of(s0 + lane), upto = wave_scan(tiles), here = last_lane(upto);
     if (at < here) {
       const uint64_t past = __ballot(upto > at);
       const int who = __builtin_ctzll(past);

@@ -460,7 +460,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnBwdArgs b, KeySums sums) 
     runs = (rq.count - 1) / kFar;
     for (unsigned s0 = 0; s0 < tile.seq; s0 += kWave) {
       const unsigned s = s0 + lane_id(), n = s < tile.seq ? rows_of(a.cu_q, s, a.rows_q).count : 0;
-      first += __shfl(wave_scan(n ? (n - 1) / kFar : 0), kWave - 1);
+      first += last_lane(wave_scan(n ? (n - 1) / kFar : 0));
     }
     runs = first < sums.runs ? min(runs, sums.runs - first) : 0;
     // the first runs' queries may all have been near

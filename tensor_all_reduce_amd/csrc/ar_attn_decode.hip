@@ -1,9 +1,10 @@
 // Attention of one new token a sequence over a paged cache.
 //
 // Bound by memory: a key and its value are read once for all query heads that
-// share them.  A workgroup takes 128 keys of one key head at a time, a wave
-// 32 of them; scores S^T = K Q^T and results O^T = V^T P^T are 16 x 16 x 32
-// products whose columns are the (up to 16) query heads of the key head.
+// share them.  A workgroup takes a tile of keys of one key head at a time, each
+// of its eight waves a step of 16 or 32 keys; scores S^T = K Q^T and results
+// O^T = V^T P^T are 16 x 16 products whose columns are the (up to 16) query
+// heads of the key head.
 //
 // The keys of all sequences and key heads are one long row of tiles, which
 // is cut into equal runs, one a workgroup, whatever the lengths are.  A
@@ -20,14 +21,16 @@
 namespace ar {
 namespace {
 
-constexpr int kWaves = 4, kStep = 32, kTileKeys = kWaves * kStep;
+constexpr int kWaves = 8;
 constexpr unsigned kWorkers = 256;             // one a CU: the LDS of a workgroup fills it
 constexpr unsigned kHeads = 16;                // query heads of a tile
 
-// Dynamic: what is in LDS of one wave.
+// What a wave has in LDS: two steps' keys and values, four steps' page numbers.
 template <int DP, bool E4M3>
 struct Ring {
   static constexpr int kRow = E4M3 ? DP : DP * 2;              // bytes
+  static constexpr int kStep = kRow == 256 ? 16 : 32;          // keys of a wave's step: two steps of eight waves fit LDS
+  static constexpr int kTileKeys = kWaves * kStep;
   static constexpr int kKeys = kStep * kRow;                   // bytes of a step's keys, or values
   static constexpr int kScales = E4M3 ? 2 * kStep * 4 : 0;     // of the keys, then of the values
   static constexpr int kStage = 2 * kKeys + kScales;
@@ -54,6 +57,7 @@ struct Cut {
   int len, lo, sunk;            // keys; the window's first; sinks before it
   int ts, n;                    // tiles of sinks, of all (at least 1)
 };
+template <int kTileKeys>
 __device__ __forceinline__ Cut cut_of(const AttnArgs& a, int len) {
   Cut c;
   c.len = (int)min((unsigned)max(len, 0), a.capacity);
@@ -68,15 +72,15 @@ __device__ __forceinline__ Cut cut_of(const AttnArgs& a, int len) {
 struct Step {
   int seq, hx;                  // sequence; key head and its tile of query heads
   int j0, end;                  // first key of the tile, end of its keys
-  unsigned seq_u, seq_n;        // the sequence's first tile in the row of all, number of its tiles
-  int first, last;              // of the sequence's tiles in this run
+  unsigned into, n;             // the tile's number in the sequence, number of the sequence's tiles
+  bool first, last;             // of the sequence's tiles in this run
 };
 
 template <int DP, bool E4M3>
-__global__ __launch_bounds__(kWaves * 64, 1) void k_attn_decode(AttnArgs a, unsigned head_tiles, uint32_t* counters, float* parts,
+__global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsigned head_tiles, uint32_t* counters, float* parts,
                                                                 bool split) {
   using R = Ring<DP, E4M3>;
-  constexpr int RB = R::kRow, KS = DP / 32, DT = DP / 16;
+  constexpr int RB = R::kRow, KS = DP / 32, DT = DP / 16, STEP = R::kStep, TILE = R::kTileKeys, NB = STEP / 16;
   __shared__ __align__(1024) char ring[kWaves * R::kBytes];
   __shared__ __align__(16) float lo_[kWaves][kHeads][36];      // 32 columns of each wave's result
   __shared__ float lm[kWaves][kHeads], ll[kWaves][kHeads];
@@ -85,81 +89,69 @@ __global__ __launch_bounds__(kWaves * 64, 1) void k_attn_decode(AttnArgs a, unsi
   const int hd = lane & 15, g = lane >> 4;
   const unsigned group = a.hq / a.hkv;
 
-  // this workgroup's run of tiles
-  unsigned N = 0;
-  for (unsigned s0 = 0; s0 < a.seqs; s0 += kWave) {
-    const unsigned n = s0 + lane < a.seqs ? (unsigned)cut_of(a, a.lens[s0 + lane]).n : 0;
-    N += __shfl(wave_scan(n), kWave - 1);
-  }
-  N = __builtin_amdgcn_readfirstlane((int)N);
-  const unsigned heads = a.hkv * head_tiles;
-  const uint64_t all = (uint64_t)N * heads;
-  const unsigned per = split ? (unsigned)((all + kWorkers - 1) / kWorkers) : 0;
-  uint64_t u, u_end;
+  // this workgroup's run of tiles: u .. u_end - 1 of all (split), or of a
+  // sequence's own
+  auto tiles_of = [&](unsigned s) { return s < a.seqs ? (unsigned)cut_of<TILE>(a, a.lens[s]).n : 0u; };
+  uint64_t u = 0, u_end;
   int hx, seq;
-  unsigned into;                               // tile of the sequence
+  unsigned into = 0, per = 0;                  // tile of the sequence; tiles of a run
   if (split) {
+    unsigned N = 0;
+    for (unsigned s0 = 0; s0 < a.seqs; s0 += kWave) N += last_lane(wave_scan(tiles_of(s0 + lane)));
+    const uint64_t all = (uint64_t)N * a.hkv * head_tiles;
+    per = (unsigned)((all + kWorkers - 1) / kWorkers);
     u = (uint64_t)blockIdx.x * per;
     u_end = u + per < all ? u + per : all;
     if (u >= all) return;
     hx = (int)(u / N);
     unsigned at = (unsigned)(u % N);
     seq = 0;
-    into = 0;
     for (unsigned s0 = 0; s0 < a.seqs; s0 += kWave) {
-      const unsigned n = s0 + lane < a.seqs ? (unsigned)cut_of(a, a.lens[s0 + lane]).n : 0;
-      const unsigned upto = wave_scan(n), here = __shfl(upto, kWave - 1);
+      const unsigned n = tiles_of(s0 + lane), upto = wave_scan(n), here = last_lane(upto);
       if (at < here) {
         const int who = __builtin_ctzll(__ballot(upto > at));
         seq = (int)s0 + who;
-        into = at - (__shfl(upto, who) - __shfl(n, who));
+        into = at - (unsigned)(__builtin_amdgcn_readlane((int)upto, who) - __builtin_amdgcn_readlane((int)n, who));
         break;
       }
       at -= here;
     }
-    seq = __builtin_amdgcn_readfirstlane(seq);
-    into = __builtin_amdgcn_readfirstlane((int)into);
-  } else {                                     // a sequence and head each
+    seq = uniform(seq);
+    into = (unsigned)uniform((int)into);
+  } else {
     seq = (int)(blockIdx.x % a.seqs);
     hx = (int)(blockIdx.x / a.seqs);
-    into = 0;
-    u = 0;
-    u_end = (uint64_t)cut_of(a, a.lens[seq]).n;
+    u_end = (uint64_t)uniform((int)tiles_of((unsigned)seq));
   }
 
   // walks over the run's tiles, some steps ahead of what is computed
   typedef const __attribute__((address_space(4))) int32_t* Scalar;
   const Scalar lens = (Scalar)(uintptr_t)a.lens;
-  uint64_t ahead = u;                          // tile that the walk is at
-  Cut cut = cut_of(a, lens[seq]);
+  unsigned left = (unsigned)(u_end - u);       // tiles that the walk has yet to give
+  Cut cut = cut_of<TILE>(a, lens[seq]);
   bool begun = true;                           // the walk's tile is the run's first of its sequence
-  auto walk = [&]() -> Step {
-    Step s;
-    s.seq = seq;
-    s.hx = hx;
+  auto walk = [&]() -> Step {                  // (after the run's end its last tile again)
     const bool sink = (int)into < cut.ts;
-    s.j0 = sink ? (int)into * kTileKeys : cut.lo + ((int)into - cut.ts) * kTileKeys;
-    s.end = sink ? cut.sunk : cut.len;
-    s.seq_u = (unsigned)(ahead - into);
-    s.seq_n = (unsigned)cut.n;
-    s.first = begun;
-    s.last = ahead + 1 >= u_end || (int)into + 1 >= cut.n;
+    const Step s{seq, hx, sink ? (int)into * TILE : cut.lo + ((int)into - cut.ts) * TILE, sink ? cut.sunk : cut.len,
+                 into, (unsigned)cut.n, begun, left <= 1 || (int)into + 1 >= cut.n};
     begun = false;
-    if (ahead < u_end) ++ahead;
-    if (ahead < u_end && (int)++into >= cut.n) {
-      begun = true;
-      into = 0;
-      if (++seq >= (int)a.seqs) {
-        seq = 0;
-        ++hx;
+    if (left > 1) {
+      --left;
+      if ((int)++into >= cut.n) {
+        begun = true;
+        into = 0;
+        if (++seq >= (int)a.seqs) {
+          seq = 0;
+          ++hx;
+        }
+        cut = cut_of<TILE>(a, lens[seq]);
       }
-      cut = cut_of(a, lens[seq]);
     }
     return s;
   };
 
   char* mine = ring + wave * R::kBytes;
-  const uint32_t lmine = __builtin_amdgcn_readfirstlane((int)lds_addr(mine));
+  const uint32_t lmine = (uint32_t)uniform((int)lds_addr(mine));
   const uint32_t lids = lmine + 2 * R::kStage;
   const uint32_t* ids = reinterpret_cast<const uint32_t*>(mine + 2 * R::kStage);
   if (a.dim < DP) {                            // places that no copy fills
@@ -167,33 +159,44 @@ __global__ __launch_bounds__(kWaves * 64, 1) void k_attn_decode(AttnArgs a, unsi
     __syncthreads();
   }
 
-  // key of the wave's row r, held within the step's keys
-  auto key_of = [&](const Step& s, int r) { return max(min(s.j0 + wave * kStep + r, s.end - 1), 0); };
+  // key of the wave's row r, held within the tile's keys
+  auto key_of = [&](const Step& s, int r) { return (unsigned)max(min(s.j0 + wave * STEP + r, s.end - 1), 0); };
   auto fetch_ids = [&](const Step& s, int slot) {
-    const unsigned pg = page_of((unsigned)key_of(s, lane & 31), a.cache);
+    const unsigned pg = page_of(key_of(s, lane & (STEP - 1)), a.cache);
     copy4_to_lds(a.table + (size_t)s.seq * a.table_ld + pg, lids + slot * kWave * 4);
   };
-  constexpr int RPC = 1024 / RB, CPR = RB / 16, ES = E4M3 ? 1 : 2;
+  constexpr int RPC = 1024 / RB, CPR = RB / 16, ES = E4M3 ? 1 : 2, COPIES = STEP / RPC;
+  const int crow = lane / CPR;
+  const uint32_t chunk = (uint32_t)((lane % CPR) ^ swizzle_bytes<RB>(crow)) * 16;
+  // (a page number out of range is found again when the step is computed)
+  const unsigned top_page = a.cache.pages - 1;
   auto fetch = [&](const Step& s, const Step& later, int stage, int slot) {
     const unsigned kvh = (unsigned)s.hx / head_tiles;
     const uint32_t to = lmine + stage * R::kStage;
-    auto token = [&](int r, size_t ps, size_t ts, size_t hs) -> size_t {
-      const unsigned j = (unsigned)key_of(s, r), pg = page_of(j, a.cache), in = j - pg * a.cache.size;
-      uint32_t id = ids[slot * kWave + r];
-      if (id >= a.cache.pages) id = 0;         // found again when the step is computed
-      return (size_t)id * ps + (size_t)in * ts + kvh * hs;
-    };
+    uint32_t id[COPIES];
 #pragma unroll
-    for (int i = 0; i < kStep / RPC; ++i) {
-      const int r = i * RPC + lane / CPR, ch = (lane % CPR) ^ swizzle_bytes<RB>(r);
-      const size_t o = token(r, a.cache.page, a.cache.ts, a.cache.hs) * ES + ch * 16;
-      if (ch * 16 < (int)a.dim * ES) {
-        copy16_to_lds(static_cast<const char*>(a.cache.k) + o, to + i * 1024);
-        copy16_to_lds(static_cast<const char*>(a.cache.v) + o, to + R::kKeys + i * 1024);
+    for (int i = 0; i < COPIES; ++i) id[i] = ids[slot * kWave + i * RPC + crow];
+    const size_t head = kvh * a.cache.hs * ES;
+    const char *kb = static_cast<const char*>(a.cache.k) + head, *vb = static_cast<const char*>(a.cache.v) + head;
+    auto rows = [&](auto whole) {
+#pragma unroll
+      for (int i = 0; i < COPIES; ++i) {
+        // the chunk of row crow is that of row i RPC + crow but for the rows' swizzle
+        const uint32_t ch = chunk ^ (uint32_t)((swizzle_bytes<RB>(i * RPC + crow) ^ swizzle_bytes<RB>(crow)) * 16);
+        const unsigned j = key_of(s, i * RPC + crow), pg = page_of(j, a.cache), in = j - pg * a.cache.size;
+        const size_t o = ((size_t)min(id[i], top_page) * a.cache.page + (size_t)in * a.cache.ts) * ES + ch;
+        if (decltype(whole)::value || ch < a.dim * ES) {
+          copy16_to_lds(kb + o, to + i * 1024);
+          copy16_to_lds(vb + o, to + R::kKeys + i * 1024);
+        }
       }
-    }
+    };
+    if (a.dim == DP) rows(std::true_type{});
+    else rows(std::false_type{});
     if constexpr (E4M3) {
-      const size_t o = token(lane & 31, a.cache.spage, a.cache.sts, a.cache.shs);
+      const unsigned j = key_of(s, lane & 31), pg = page_of(j, a.cache), in = j - pg * a.cache.size;
+      const size_t o = (size_t)min(ids[slot * kWave + (lane & 31)], top_page) * a.cache.spage + (size_t)in * a.cache.sts +
+                       kvh * a.cache.shs;
       copy4_to_lds((lane < 32 ? a.cache.k_scales : a.cache.v_scales) + o, to + 2 * R::kKeys);
     }
     fetch_ids(later, (slot + 2) & 3);
@@ -212,8 +215,6 @@ __global__ __launch_bounds__(kWaves * 64, 1) void k_attn_decode(AttnArgs a, unsi
   const float c = a.scale * kLog2e;
   int stage = 0, slot = 0;
   for (; u < u_end; ++u) {
-    // the step's copies are done when only the next step's are left
-    asm volatile("s_waitcnt vmcnt(%0)" :: "n"(R::kCopies) : "memory");
     const unsigned kvh = (unsigned)s0.hx / head_tiles, ht = (unsigned)s0.hx % head_tiles;
     const unsigned here = min(group - ht * kHeads, kHeads), head0 = kvh * group + ht * kHeads;
     if (s0.first) {
@@ -228,15 +229,19 @@ __global__ __launch_bounds__(kWaves * 64, 1) void k_attn_decode(AttnArgs a, unsi
         const unsigned d = E4M3 ? 64 * (x / 2) + 16 * g + 8 * (x & 1) : 32 * x + 8 * g;
         q[x].u = d < a.dim ? *reinterpret_cast<const u32x4*>(qp + d) : u32x4{0, 0, 0, 0};
       }
+      wait_copies();                           // the queries are here (and the copies before them)
     }
-    const int keys = min(s0.end - s0.j0 - wave * kStep, kStep);   // of this wave's step
+    // the step's copies are done when only the next step's are left
+    asm volatile("s_waitcnt vmcnt(%0)" :: "n"(R::kCopies) : "memory");
+    const int keys = min(s0.end - s0.j0 - wave * STEP, STEP);   // of this wave's step
     if (keys > 0) {
-      if (__any((lane & 31) < keys && ids[slot * kWave + lane] >= a.cache.pages)) l = __uint_as_float(0x7FC00000u);
+      if (__any((lane & (STEP - 1)) < keys && ids[slot * kWave + (lane & (STEP - 1))] >= a.cache.pages))
+        l = __uint_as_float(0x7FC00000u);
       const char* lk = mine + stage * R::kStage;
       const uint32_t lv = lmine + stage * R::kStage + R::kKeys;
-      f32x4 s[2];
+      f32x4 s[NB];
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
+      for (int b = 0; b < NB; ++b) {
         s[b] = f32x4{0.f, 0.f, 0.f, 0.f};
         if constexpr (E4M3) {
 #pragma unroll
@@ -269,21 +274,21 @@ __global__ __launch_bounds__(kWaves * 64, 1) void k_attn_decode(AttnArgs a, unsi
         }
       }
       // register r of block b is key 16 b + 4 g + r of the step
-      if (keys < kStep) {
+      if (keys < STEP) {
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
           for (int r = 0; r < 4; ++r) s[b][r] = 16 * b + 4 * g + r < keys ? s[b][r] : AR_NEG_INF;
       }
       float top = AR_NEG_INF;
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int r = 0; r < 4; ++r) top = fmaxf(top, s[b][r]);
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32)) * c;
       if (__any(top > m + 8.0f)) {
-        const float up = fmaxf(m, top), f = up == AR_NEG_INF ? 1.0f : exp2_fast(m - up);
+        const float up = fmaxf(m, top), f = m == AR_NEG_INF ? 1.0f : exp2_fast(m - up);
         m = up;
         l *= f;
 #pragma unroll
@@ -291,7 +296,7 @@ __global__ __launch_bounds__(kWaves * 64, 1) void k_attn_decode(AttnArgs a, unsi
       }
       const float base = m == AR_NEG_INF ? 0.f : m;
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           s[b][r] = exp2_fast(__builtin_fmaf(s[b][r], c, -base));
@@ -299,24 +304,24 @@ __global__ __launch_bounds__(kWaves * 64, 1) void k_attn_decode(AttnArgs a, unsi
         }
       if constexpr (E4M3) {
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const f32x4 f = *reinterpret_cast<const f32x4*>(lk + 2 * R::kKeys + (kStep + 16 * b + 4 * g) * 4);
+        for (int b = 0; b < NB; ++b) {
+          const f32x4 f = *reinterpret_cast<const f32x4*>(lk + 2 * R::kKeys + (STEP + 16 * b + 4 * g) * 4);
 #pragma unroll
           for (int r = 0; r < 4; ++r) s[b][r] = 16 * b + 4 * g + r < keys ? s[b][r] * f[r] : 0.f;
         }
       }
       Frag8 p;
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
+      for (int b = 0; b < NB; ++b) {
         p.w[2 * b] = cvt_bf16x2(s[b][0], s[b][1]);
         p.w[2 * b + 1] = cvt_bf16x2(s[b][2], s[b][3]);
       }
-      // whether element e of the lane's eight values is of a key of the step:
-      // 0 times what a masked place holds must be 0
+      // whether element e of the lane's values is of a key of the step: 0
+      // times what a masked place holds must be 0
       const int beyond = keys - 4 * g;         // of keys 4 g + ...; 16 less for the second four
+      Frag8 v[DT];
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
-        Frag8 v;
         if constexpr (E4M3) {
           const int e = (lane & 15) / 2, r = 4 * g + (e & 3) + (e >= 4 ? 16 : 0);
           const i32x2 w = read_tr8(lv + chunk_at<RB>(r, d) + (lane & 1) * 8);
@@ -325,20 +330,26 @@ __global__ __launch_bounds__(kWaves * 64, 1) void k_attn_decode(AttnArgs a, unsi
             union { b16x2 b; uint32_t u; } lo, hi;
             lo.b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[x], 1.0f, false);
             hi.b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[x], 1.0f, true);
-            v.w[2 * x] = lo.u;
-            v.w[2 * x + 1] = hi.u;
+            v[d].w[2 * x] = lo.u;
+            v[d].w[2 * x + 1] = hi.u;
           }
         } else {
           const int r = 4 * g + (lane & 15) / 4, ch = 2 * d + (lane & 3) / 2;
-          v.s[0] = read_tr16(lv + chunk_at<RB>(r, ch) + (lane & 1) * 8);
-          v.s[1] = read_tr16(lv + chunk_at<RB>(r + 16, ch) + (lane & 1) * 8);
-        }
-        if (keys < kStep) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if ((e & 3) + (e >= 4 ? 16 : 0) >= beyond) v.w[e / 2] &= e & 1 ? 0xFFFFu : 0xFFFF0000u;
+          for (int b = 0; b < NB; ++b) v[d].s[b] = read_tr16(lv + chunk_at<RB>(r + 16 * b, ch) + (lane & 1) * 8);
         }
-        o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v.b, p.b, o[d], 0, 0, 0);
+      }
+      if (keys < STEP) {
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int e = 0; e < 4 * NB; ++e)
+            if ((e & 3) + (e >= 4 ? 16 : 0) >= beyond) v[d].w[e / 2] &= e & 1 ? 0xFFFFu : 0xFFFF0000u;
+      }
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        if constexpr (NB == 2) o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[d].b, p.b, o[d], 0, 0, 0);
+        else o[d] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(v[d].s[0], p.s[0], o[d], 0, 0, 0);
       }
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the stage has been read
@@ -363,14 +374,15 @@ __global__ __launch_bounds__(kWaves * 64, 1) void k_attn_decode(AttnArgs a, unsi
       for (int w = 0; w < kWaves; ++w)
         sum += lm[w][hd] == AR_NEG_INF ? ll[w][hd] : ll[w][hd] * exp2_fast(lm[w][hd] - M);
       const float f = m == AR_NEG_INF ? 0.f : exp2_fast(m - M);
-      const unsigned begin = split ? s0.seq_u / per : 0, finish = split ? (s0.seq_u + s0.seq_n - 1) / per : 0;
+      const uint64_t seq_u = u - s0.into;
+      const unsigned begin = split ? (unsigned)(seq_u / per) : 0, finish = split ? (unsigned)((seq_u + s0.n - 1) / per) : 0;
       const unsigned count = finish - begin + 1;   // runs that hold parts of the sequence
       const float inv = sum > 0.f ? 1.0f / sum : sum;   // no key: zeros; NaN stays
       // results of a part: 16 maxima, 16 sums, then rows of a head's columns
       constexpr unsigned kPart = 2 * kHeads + kHeads * DP;
       float* part = count > 1 ? parts + (size_t)(blockIdx.x * 2 + (blockIdx.x == begin ? 1 : 0)) * kPart : nullptr;
-      const unsigned oh = t / 16, od = (t % 16) * 2;
-      const float oinv = __shfl(inv, (int)oh & 15);
+      const unsigned oh = t / 32, od = t % 32;     // this lane's head and column of 32
+      const float oinv = __shfl(inv, (int)oh);
 #pragma unroll
       for (int d2 = 0; d2 < DT / 2; ++d2) {
 #pragma unroll
@@ -381,22 +393,13 @@ __global__ __launch_bounds__(kWaves * 64, 1) void k_attn_decode(AttnArgs a, unsi
           *reinterpret_cast<f32x4*>(&lo_[wave][hd][16 * x + 4 * g]) = v;
         }
         __syncthreads();
-        float a0 = 0.f, a1 = 0.f;
+        float sum2 = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-          a0 += lo_[w][oh][od];
-          a1 += lo_[w][oh][od + 1];
-        }
+        for (int w = 0; w < kWaves; ++w) sum2 += lo_[w][oh][od];
         const unsigned at = 32 * d2 + od;
         if (oh < here && at < a.dim) {
-          if (part) {
-            __hip_atomic_store(reinterpret_cast<uint64_t*>(part + 2 * kHeads + oh * DP + at),
-                               (uint64_t)__float_as_uint(a0) | (uint64_t)__float_as_uint(a1) << 32, __ATOMIC_RELAXED,
-                               __HIP_MEMORY_SCOPE_AGENT);
-          } else {
-            uint16_t* op = a.out.p + (size_t)s0.seq * a.out.ts + (head0 + oh) * a.out.hs + at;
-            *reinterpret_cast<uint32_t*>(op) = result_bf16x2(a0 * oinv, a1 * oinv);
-          }
+          if (part) __hip_atomic_store(part + 2 * kHeads + oh * DP + at, sum2, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          else a.out.p[(size_t)s0.seq * a.out.ts + (head0 + oh) * a.out.hs + at] = to_bf16(sum2 * oinv);
         }
         __syncthreads();
       }
@@ -405,7 +408,7 @@ __global__ __launch_bounds__(kWaves * 64, 1) void k_attn_decode(AttnArgs a, unsi
           __hip_atomic_store(part + t, M, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
           __hip_atomic_store(part + kHeads + t, sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the part is out
+        wait_copies();                         // the part is out
         __syncthreads();
         uint32_t* counter = counters + (size_t)s0.hx * a.seqs + s0.seq;
         if (t == 0) lcount = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -413,39 +416,46 @@ __global__ __launch_bounds__(kWaves * 64, 1) void k_attn_decode(AttnArgs a, unsi
         if (lcount == count - 1) {
           __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
           if (t == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-          const unsigned h = t / 16;
+          // 32 lanes a head; 4 columns each
           auto part_of = [&](unsigned i) { return parts + (size_t)((begin + i) * 2 + (i == 0 ? 1 : 0)) * kPart; };
+          const unsigned h = oh, lane32 = t % 32, d = lane32 * 4;
           if (h < here) {
             float M2 = AR_NEG_INF, L2 = 0.f;
-            for (unsigned i = 0; i < count; ++i) M2 = fmaxf(M2, part_of(i)[h]);
-            f32x4 acc[DP / 64];
+            for (unsigned i = lane32; i < count; i += 32) M2 = fmaxf(M2, part_of(i)[h]);
 #pragma unroll
-            for (int x = 0; x < DP / 64; ++x) acc[x] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-            for (unsigned i = 0; i < count; ++i) {
-              const float* p = part_of(i);
-              const float w = p[h] == AR_NEG_INF ? 0.f : exp2_fast(p[h] - M2);
-              L2 = p[h] == AR_NEG_INF ? L2 + p[kHeads + h] : __builtin_fmaf(p[kHeads + h], w, L2);
+            for (int x = 1; x < 32; x *= 2) M2 = fmaxf(M2, __shfl_xor(M2, x));
+            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+            for (unsigned i0 = 0; i0 < count; i0 += 32) {
+              // lane i's part: what it weighs, and its sum
+              float w = 0.f, s = 0.f;
+              if (i0 + lane32 < count) {
+                const float pm = part_of(i0 + lane32)[h], pl = part_of(i0 + lane32)[kHeads + h];
+                w = pm == AR_NEG_INF ? 0.f : exp2_fast(pm - M2);
+                s = pm == AR_NEG_INF ? pl : pl * w;
+              }
+              // eight parts at a time are on their way at once
+              for (unsigned i1 = 0; i1 < min(32u, count - i0); i1 += 8) {
+                f32x4 v[8];
 #pragma unroll
-              for (int x = 0; x < DP / 64; ++x) {
-                const unsigned d = 64 * x + (t % 16) * 4;
-                if (d < a.dim) {
-                  const f32x4 v = *reinterpret_cast<const f32x4*>(p + 2 * kHeads + h * DP + d);
+                for (unsigned i = 0; i < 8; ++i)
+                  v[i] = *reinterpret_cast<const f32x4*>(part_of(min(i0 + i1 + i, count - 1)) + 2 * kHeads + h * DP + min(d, (unsigned)DP - 4));
 #pragma unroll
-                  for (int r = 0; r < 4; ++r) acc[x][r] = __builtin_fmaf(v[r], w, acc[x][r]);
+                for (unsigned i = 0; i < 8; ++i) {
+                  const int from = (int)((lane & 32) + i1 + i);
+                  const float wi = __shfl(w, from);
+                  L2 += __shfl(s, from);
+                  if (i0 + i1 + i < count) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(v[i][r], wi, acc[r]);
+                  }
                 }
               }
             }
             const float i2 = L2 > 0.f ? 1.0f / L2 : L2;
-            uint16_t* op = a.out.p + (size_t)s0.seq * a.out.ts + (head0 + h) * a.out.hs;
-#pragma unroll
-            for (int x = 0; x < DP / 64; ++x) {
-              const unsigned d = 64 * x + (t % 16) * 4;
-              if (d < a.dim)
-                *reinterpret_cast<u32x2*>(op + d) =
-                    u32x2{result_bf16x2(acc[x][0] * i2, acc[x][1] * i2), result_bf16x2(acc[x][2] * i2, acc[x][3] * i2)};
-            }
-            if (a.lse && t % 16 == 0)
+            if (d < a.dim)
+              *reinterpret_cast<u32x2*>(a.out.p + (size_t)s0.seq * a.out.ts + (head0 + h) * a.out.hs + d) =
+                  u32x2{result_bf16x2(acc[0] * i2, acc[1] * i2), result_bf16x2(acc[2] * i2, acc[3] * i2)};
+            if (a.lse && lane32 == 0)
               a.lse[(size_t)s0.seq * a.lse_ts + (head0 + h) * a.lse_hs] =
                   L2 > 0.f ? (M2 + __builtin_amdgcn_logf(L2)) * kLn2 : L2 == 0.f ? AR_NEG_INF : L2;
           }
