@@ -1174,9 +1174,9 @@ int ar_attn_decode(const ar_heads* q, const ar_kv_cache* cache, const int32_t* t
   if (!workspace || workspace_bytes < need) need = 0;
   if (need) og[no++] = grid_of(workspace, 1, need, {1, 1, 1}, {0, 0, 0});
   if ((rc = check_apart(in, ni, og, no, 0, 0))) return rc;
-  // the row of all tiles is counted in 32 bits
-  const size_t tiles = a.capacity / 128 + 3, heads = cache->heads * (((hq / cache->heads) + 15) / 16);
-  if (mul3_overflows(tiles, heads, seqs) || tiles * heads * seqs >> 32) return AR_ERR_UNSUPPORTED;
+  // the row of all tiles is counted in 32 bits (of tiles of 128 keys at least, each sequence with a few more)
+  const size_t tiles = a.capacity / 128 + 6, heads = cache->heads * (((hq / cache->heads) + 15) / 16);
+  if (mul3_overflows(tiles, heads, seqs) || tiles * heads * seqs >> 31) return AR_ERR_UNSUPPORTED;
   a.q = rows_arg(q);
   a.out = out_arg(out);
   a.lens = lens;

@@ -68,11 +68,11 @@ __device__ __forceinline__ i32x2 read_tr8(uint32_t addr) {
 // Copies 16 bytes a lane from `from` to LDS, the lanes of a wave side by side
 // from byte address `lds`, past the registers; a lane that is switched off
 // copies nothing and leaves its place as it is.  The caller waits (vmcnt) and
-// meets a barrier before the data are read.  The wait states cover the write
+// meets a barrier before the data are read.  The wait state covers the write
 // of M0 before the copy reads it.
 __device__ __forceinline__ void copy16_to_lds(const void* from, uint32_t lds) {
   lds = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds);
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, off" :: "s"(lds), "v"(from) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" :: "s"(lds), "v"(from) : "memory");
 }
 
 // The same from a base that the wave shares and an offset of the lane's own.
@@ -306,8 +306,17 @@ struct TileCopy {
   }
 };
 
-// The larger of a value and its counterpart 32 lanes away; the sum of both.
-__device__ __forceinline__ float max_halves(float x) { return fmaxf(x, __shfl_xor(x, 32)); }
-__device__ __forceinline__ float add_halves(float x) { return x + __shfl_xor(x, 32); }
+// The larger of a value and its counterpart 32 (16) lanes away, and the sum of
+// both, by the instructions that swap halves (rows of 16) of two registers.
+__device__ __forceinline__ u32x2 swap32(float x) {
+  return __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+}
+__device__ __forceinline__ u32x2 swap16(float x) {
+  return __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+}
+__device__ __forceinline__ float max_of(u32x2 p) { return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1])); }
+__device__ __forceinline__ float sum_of(u32x2 p) { return __uint_as_float(p[0]) + __uint_as_float(p[1]); }
+__device__ __forceinline__ float max_halves(float x) { return max_of(swap32(x)); }
+__device__ __forceinline__ float add_halves(float x) { return sum_of(swap32(x)); }
 
 }  // namespace ar

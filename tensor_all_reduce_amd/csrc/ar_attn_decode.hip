@@ -49,8 +49,13 @@ template <int RB>
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) { return (uint32_t)(r * RB + ((c ^ swizzle_bytes<RB>(r)) * 16)); }
 
 __device__ __forceinline__ void copy4_to_lds(const void* from, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dword %1, off" :: "s"(lds), "v"(from) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" :: "s"(lds), "v"(from) : "memory");
 }
+
+// What a sequence costs beside its tiles, in tiles: the join of its waves and
+// the start of the next.  (48 sequences of 100 to 16384 keys: @@ us, without
+// it @@.)
+constexpr unsigned kEnd = 2;
 
 // What a sequence's keys are cut into.
 struct Cut {
@@ -72,8 +77,9 @@ __device__ __forceinline__ Cut cut_of(const AttnArgs& a, int len) {
 struct Step {
   int seq, hx;                  // sequence; key head and its tile of query heads
   int j0, end;                  // first key of the tile, end of its keys
-  unsigned into, n;             // the tile's number in the sequence, number of the sequence's tiles
+  unsigned seq_u, n;            // where the sequence begins in the row of all, number of its tiles
   bool first, last;             // of the sequence's tiles in this run
+  bool live;                    // within the run
 };
 
 template <int DP, bool E4M3>
@@ -89,22 +95,26 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
   const int hd = lane & 15, g = lane >> 4;
   const unsigned group = a.hq / a.hkv;
 
-  // this workgroup's run of tiles: u .. u_end - 1 of all (split), or of a
-  // sequence's own
-  auto tiles_of = [&](unsigned s) { return s < a.seqs ? (unsigned)cut_of<TILE>(a, a.lens[s]).n : 0u; };
-  uint64_t u = 0, u_end;
+  // This workgroup's run of the row of all tiles, each sequence's followed by
+  // kEnd empty ones; or (split false) one sequence's.
+  auto tiles_of = [&](unsigned s) { return s < a.seqs ? (unsigned)cut_of<TILE>(a, a.lens[s]).n + kEnd : 0u; };
+  unsigned u = 0, u_end, per = 0;              // tiles of a run
   int hx, seq;
-  unsigned into = 0, per = 0;                  // tile of the sequence; tiles of a run
+  unsigned into = 0;                           // tile of the sequence
   if (split) {
     unsigned N = 0;
     for (unsigned s0 = 0; s0 < a.seqs; s0 += kWave) N += last_lane(wave_scan(tiles_of(s0 + lane)));
-    const uint64_t all = (uint64_t)N * a.hkv * head_tiles;
-    per = (unsigned)((all + kWorkers - 1) / kWorkers);
-    u = (uint64_t)blockIdx.x * per;
-    u_end = u + per < all ? u + per : all;
-    if (u >= all) return;
-    hx = (int)(u / N);
-    unsigned at = (unsigned)(u % N);
+    // Runs of whole key heads where that leaves few workgroups idle: the heads
+    // of a token, which lie side by side in memory, are then read at one time.
+    const unsigned heads = a.hkv * head_tiles, each = kWorkers / heads;
+    const bool aligned = each * heads * 10 >= kWorkers * 9;
+    per = aligned ? (N + each - 1) / each : (N * heads + kWorkers - 1) / kWorkers;
+    const unsigned wide = aligned ? per * each : N;   // a head's share of the row
+    u = blockIdx.x * per;
+    hx = (int)(u / wide);
+    unsigned at = u % wide;
+    if (hx >= (int)heads || at >= N) return;
+    u_end = min(u + per, aligned ? hx * wide + N : N * heads);
     seq = 0;
     for (unsigned s0 = 0; s0 < a.seqs; s0 += kWave) {
       const unsigned n = tiles_of(s0 + lane), upto = wave_scan(n), here = last_lane(upto);
@@ -121,31 +131,36 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
   } else {
     seq = (int)(blockIdx.x % a.seqs);
     hx = (int)(blockIdx.x / a.seqs);
-    u_end = (uint64_t)uniform((int)tiles_of((unsigned)seq));
+    u_end = (unsigned)uniform((int)tiles_of((unsigned)seq)) - kEnd;
   }
 
   // walks over the run's tiles, some steps ahead of what is computed
   typedef const __attribute__((address_space(4))) int32_t* Scalar;
   const Scalar lens = (Scalar)(uintptr_t)a.lens;
-  unsigned left = (unsigned)(u_end - u);       // tiles that the walk has yet to give
   Cut cut = cut_of<TILE>(a, lens[seq]);
+  unsigned at = u;                             // of the walk, in the row of all
   bool begun = true;                           // the walk's tile is the run's first of its sequence
-  auto walk = [&]() -> Step {                  // (after the run's end its last tile again)
+  auto advance = [&]() {                       // past the sequence's end
+    at += (unsigned)cut.n + kEnd - into;
+    into = 0;
+    begun = true;
+    if (at >= u_end) return;
+    if (++seq >= (int)a.seqs) {
+      seq = 0;
+      ++hx;
+    }
+    cut = cut_of<TILE>(a, lens[seq]);
+  };
+  if ((int)into >= cut.n) advance();
+  if (at >= u_end) return;
+  auto walk = [&]() -> Step {                  // (after the run's end some tile of it again)
     const bool sink = (int)into < cut.ts;
     const Step s{seq, hx, sink ? (int)into * TILE : cut.lo + ((int)into - cut.ts) * TILE, sink ? cut.sunk : cut.len,
-                 into, (unsigned)cut.n, begun, left <= 1 || (int)into + 1 >= cut.n};
-    begun = false;
-    if (left > 1) {
-      --left;
-      if ((int)++into >= cut.n) {
-        begun = true;
-        into = 0;
-        if (++seq >= (int)a.seqs) {
-          seq = 0;
-          ++hx;
-        }
-        cut = cut_of<TILE>(a, lens[seq]);
-      }
+                 at - into, (unsigned)cut.n, begun, at + 1 >= u_end || (int)into + 1 >= cut.n, at < u_end};
+    if (at < u_end) {
+      begun = false;
+      ++at;
+      if ((int)++into >= cut.n) advance();
     }
     return s;
   };
@@ -170,12 +185,15 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
   const uint32_t chunk = (uint32_t)((lane % CPR) ^ swizzle_bytes<RB>(crow)) * 16;
   // (a page number out of range is found again when the step is computed)
   const unsigned top_page = a.cache.pages - 1;
+  uint32_t id[COPIES], id_scale = 0;           // page numbers of the step that is fetched next
+  auto read_ids = [&](int slot) {
+#pragma unroll
+    for (int i = 0; i < COPIES; ++i) id[i] = ids[slot * kWave + i * RPC + crow];
+    if constexpr (E4M3) id_scale = ids[slot * kWave + (lane & 31)];
+  };
   auto fetch = [&](const Step& s, const Step& later, int stage, int slot) {
     const unsigned kvh = (unsigned)s.hx / head_tiles;
     const uint32_t to = lmine + stage * R::kStage;
-    uint32_t id[COPIES];
-#pragma unroll
-    for (int i = 0; i < COPIES; ++i) id[i] = ids[slot * kWave + i * RPC + crow];
     const size_t head = kvh * a.cache.hs * ES;
     const char *kb = static_cast<const char*>(a.cache.k) + head, *vb = static_cast<const char*>(a.cache.v) + head;
     auto rows = [&](auto whole) {
@@ -195,7 +213,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
     else rows(std::false_type{});
     if constexpr (E4M3) {
       const unsigned j = key_of(s, lane & 31), pg = page_of(j, a.cache), in = j - pg * a.cache.size;
-      const size_t o = (size_t)min(ids[slot * kWave + (lane & 31)], top_page) * a.cache.spage + (size_t)in * a.cache.sts +
+      const size_t o = (size_t)min(id_scale, top_page) * a.cache.spage + (size_t)in * a.cache.sts +
                        kvh * a.cache.shs;
       copy4_to_lds((lane < 32 ? a.cache.k_scales : a.cache.v_scales) + o, to + 2 * R::kKeys);
     }
@@ -206,7 +224,9 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
   fetch_ids(s0, 0);
   fetch_ids(s1, 1);
   wait_copies();
+  read_ids(0);
   fetch(s0, s2, 0, 0);
+  read_ids(1);
   fetch(s1, s3, 1, 1);
 
   Frag8 q[KS];
@@ -214,7 +234,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
   float m = AR_NEG_INF, l = 0.f;
   const float c = a.scale * kLog2e;
   int stage = 0, slot = 0;
-  for (; u < u_end; ++u) {
+  while (s0.live) {
     const unsigned kvh = (unsigned)s0.hx / head_tiles, ht = (unsigned)s0.hx % head_tiles;
     const unsigned here = min(group - ht * kHeads, kHeads), head0 = kvh * group + ht * kHeads;
     if (s0.first) {
@@ -233,12 +253,28 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
     }
     // the step's copies are done when only the next step's are left
     asm volatile("s_waitcnt vmcnt(%0)" :: "n"(R::kCopies) : "memory");
+    read_ids((slot + 2) & 3);
     const int keys = min(s0.end - s0.j0 - wave * STEP, STEP);   // of this wave's step
     if (keys > 0) {
       if (__any((lane & (STEP - 1)) < keys && ids[slot * kWave + (lane & (STEP - 1))] >= a.cache.pages))
         l = __uint_as_float(0x7FC00000u);
       const char* lk = mine + stage * R::kStage;
       const uint32_t lv = lmine + stage * R::kStage + R::kKeys;
+      // values are read first: they arrive while the scores are formed
+      Frag8 v[DT];
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        if constexpr (E4M3) {
+          const int e = (lane & 15) / 2, r = 4 * g + (e & 3) + (e >= 4 ? 16 : 0);
+          const i32x2 w = read_tr8(lv + chunk_at<RB>(r, d) + (lane & 1) * 8);
+          v[d].w[0] = (uint32_t)w[0];
+          v[d].w[1] = (uint32_t)w[1];
+        } else {
+          const int r = 4 * g + (lane & 15) / 4, ch = 2 * d + (lane & 3) / 2;
+#pragma unroll
+          for (int b = 0; b < NB; ++b) v[d].s[b] = read_tr16(lv + chunk_at<RB>(r + 16 * b, ch) + (lane & 1) * 8);
+        }
+      }
       f32x4 s[NB];
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
@@ -285,8 +321,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
       for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int r = 0; r < 4; ++r) top = fmaxf(top, s[b][r]);
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32)) * c;
+      top = max_of(swap32(max_of(swap16(top)))) * c;
       if (__any(top > m + 8.0f)) {
         const float up = fmaxf(m, top), f = m == AR_NEG_INF ? 1.0f : exp2_fast(m - up);
         m = up;
@@ -319,12 +354,10 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
       // whether element e of the lane's values is of a key of the step: 0
       // times what a masked place holds must be 0
       const int beyond = keys - 4 * g;         // of keys 4 g + ...; 16 less for the second four
-      Frag8 v[DT];
+      if constexpr (E4M3) {
 #pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        if constexpr (E4M3) {
-          const int e = (lane & 15) / 2, r = 4 * g + (e & 3) + (e >= 4 ? 16 : 0);
-          const i32x2 w = read_tr8(lv + chunk_at<RB>(r, d) + (lane & 1) * 8);
+        for (int d = 0; d < DT; ++d) {
+          const i32x2 w = {(int)v[d].w[0], (int)v[d].w[1]};
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             union { b16x2 b; uint32_t u; } lo, hi;
@@ -333,10 +366,6 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
             v[d].w[2 * x] = lo.u;
             v[d].w[2 * x + 1] = hi.u;
           }
-        } else {
-          const int r = 4 * g + (lane & 15) / 4, ch = 2 * d + (lane & 3) / 2;
-#pragma unroll
-          for (int b = 0; b < NB; ++b) v[d].s[b] = read_tr16(lv + chunk_at<RB>(r + 16 * b, ch) + (lane & 1) * 8);
         }
       }
       if (keys < STEP) {
@@ -360,8 +389,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
 
     if (s0.last) {
       // the waves' results are one
-      l += __shfl_xor(l, 16);
-      l += __shfl_xor(l, 32);
+      l = sum_of(swap32(sum_of(swap16(l))));
       if (lane < 16) {
         lm[wave][hd] = m;
         ll[wave][hd] = l;
@@ -374,8 +402,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
       for (int w = 0; w < kWaves; ++w)
         sum += lm[w][hd] == AR_NEG_INF ? ll[w][hd] : ll[w][hd] * exp2_fast(lm[w][hd] - M);
       const float f = m == AR_NEG_INF ? 0.f : exp2_fast(m - M);
-      const uint64_t seq_u = u - s0.into;
-      const unsigned begin = split ? (unsigned)(seq_u / per) : 0, finish = split ? (unsigned)((seq_u + s0.n - 1) / per) : 0;
+      const unsigned begin = split ? s0.seq_u / per : 0, finish = split ? (s0.seq_u + s0.n - 1) / per : 0;
       const unsigned count = finish - begin + 1;   // runs that hold parts of the sequence
       const float inv = sum > 0.f ? 1.0f / sum : sum;   // no key: zeros; NaN stays
       // results of a part: 16 maxima, 16 sums, then rows of a head's columns
