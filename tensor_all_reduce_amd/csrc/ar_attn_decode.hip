@@ -73,13 +73,11 @@ __device__ __forceinline__ Cut cut_of(const AttnArgs& a, int len) {
   return c;
 }
 
-// One tile of a workgroup's run.
-struct Step {
+// A sequence's tiles in a workgroup's run.
+struct Part {
   int seq, hx;                  // sequence; key head and its tile of query heads
-  int j0, end;                  // first key of the tile, end of its keys
-  unsigned seq_u, n;            // where the sequence begins in the row of all, number of its tiles
-  bool first, last;             // of the sequence's tiles in this run
-  bool live;                    // within the run
+  unsigned seq_u, into, count;  // where the sequence begins in the row of all; first tile, number of tiles
+  Cut cut;
 };
 
 template <int DP, bool E4M3>
@@ -134,36 +132,25 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
     u_end = (unsigned)uniform((int)tiles_of((unsigned)seq)) - kEnd;
   }
 
-  // walks over the run's tiles, some steps ahead of what is computed
   typedef const __attribute__((address_space(4))) int32_t* Scalar;
   const Scalar lens = (Scalar)(uintptr_t)a.lens;
-  Cut cut = cut_of<TILE>(a, lens[seq]);
-  unsigned at = u;                             // of the walk, in the row of all
-  bool begun = true;                           // the walk's tile is the run's first of its sequence
-  auto advance = [&]() {                       // past the sequence's end
-    at += (unsigned)cut.n + kEnd - into;
-    into = 0;
-    begun = true;
-    if (at >= u_end) return;
-    if (++seq >= (int)a.seqs) {
-      seq = 0;
-      ++hx;
+  Part now{seq, hx, u - into, into, 0, cut_of<TILE>(a, lens[seq])};
+  // The run's next sequence; false at the run's end.
+  auto follow = [&](Part& p) {
+    const unsigned at = p.seq_u + (unsigned)p.cut.n + kEnd;
+    if (at >= u_end) return false;
+    if (++p.seq >= (int)a.seqs) {
+      p.seq = 0;
+      ++p.hx;
     }
-    cut = cut_of<TILE>(a, lens[seq]);
+    p.cut = cut_of<TILE>(a, lens[p.seq]);
+    p.seq_u = at;
+    p.into = 0;
+    p.count = min((unsigned)p.cut.n, u_end - at);
+    return true;
   };
-  if ((int)into >= cut.n) advance();
-  if (at >= u_end) return;
-  auto walk = [&]() -> Step {                  // (after the run's end some tile of it again)
-    const bool sink = (int)into < cut.ts;
-    const Step s{seq, hx, sink ? (int)into * TILE : cut.lo + ((int)into - cut.ts) * TILE, sink ? cut.sunk : cut.len,
-                 at - into, (unsigned)cut.n, begun, at + 1 >= u_end || (int)into + 1 >= cut.n, at < u_end};
-    if (at < u_end) {
-      begun = false;
-      ++at;
-      if ((int)++into >= cut.n) advance();
-    }
-    return s;
-  };
+  if ((int)into < now.cut.n) now.count = min((unsigned)now.cut.n - into, u_end - u);
+  else if (!follow(now)) return;
 
   char* mine = ring + wave * R::kBytes;
   const uint32_t lmine = (uint32_t)uniform((int)lds_addr(mine));
@@ -174,11 +161,19 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
     __syncthreads();
   }
 
+  // first key of a part's tile i, end of its keys
+  struct Keys {
+    int j0, end;
+  };
+  auto keys_of = [&](const Part& p, unsigned i) {
+    const int n = (int)(p.into + i), ts = p.cut.ts;
+    return n < ts ? Keys{n * TILE, p.cut.sunk} : Keys{p.cut.lo + (n - ts) * TILE, p.cut.len};
+  };
   // key of the wave's row r, held within the tile's keys
-  auto key_of = [&](const Step& s, int r) { return (unsigned)max(min(s.j0 + wave * STEP + r, s.end - 1), 0); };
-  auto fetch_ids = [&](const Step& s, int slot) {
-    const unsigned pg = page_of(key_of(s, lane & (STEP - 1)), a.cache);
-    copy4_to_lds(a.table + (size_t)s.seq * a.table_ld + pg, lids + slot * kWave * 4);
+  auto key_of = [&](Keys k, int r) { return (unsigned)max(min(k.j0 + wave * STEP + r, k.end - 1), 0); };
+  auto fetch_ids = [&](const Part& p, unsigned i, int slot) {
+    const unsigned pg = page_of(key_of(keys_of(p, i), lane & (STEP - 1)), a.cache);
+    copy4_to_lds(a.table + (size_t)p.seq * a.table_ld + pg, lids + slot * kWave * 4);
   };
   constexpr int RPC = 1024 / RB, CPR = RB / 16, ES = E4M3 ? 1 : 2, COPIES = STEP / RPC;
   const int crow = lane / CPR;
@@ -191,9 +186,11 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
     for (int i = 0; i < COPIES; ++i) id[i] = ids[slot * kWave + i * RPC + crow];
     if constexpr (E4M3) id_scale = ids[slot * kWave + (lane & 31)];
   };
-  auto fetch = [&](const Step& s, const Step& later, int stage, int slot) {
-    const unsigned kvh = (unsigned)s.hx / head_tiles;
+  // Starts tile i's copies, and those of the page numbers of tile i + 2.
+  auto fetch = [&](const Part& p, unsigned i, int stage, int slot) {
+    const unsigned kvh = (unsigned)p.hx / head_tiles;
     const uint32_t to = lmine + stage * R::kStage;
+    const Keys keys = keys_of(p, i);
     const size_t head = kvh * a.cache.hs * ES;
     const char *kb = static_cast<const char*>(a.cache.k) + head, *vb = static_cast<const char*>(a.cache.v) + head;
     auto rows = [&](auto whole) {
@@ -201,7 +198,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
       for (int i = 0; i < COPIES; ++i) {
         // the chunk of row crow is that of row i RPC + crow but for the rows' swizzle
         const uint32_t ch = chunk ^ (uint32_t)((swizzle_bytes<RB>(i * RPC + crow) ^ swizzle_bytes<RB>(crow)) * 16);
-        const unsigned j = key_of(s, i * RPC + crow), pg = page_of(j, a.cache), in = j - pg * a.cache.size;
+        const unsigned j = key_of(keys, i * RPC + crow), pg = page_of(j, a.cache), in = j - pg * a.cache.size;
         const size_t o = ((size_t)min(id[i], top_page) * a.cache.page + (size_t)in * a.cache.ts) * ES + ch;
         if (decltype(whole)::value || ch < a.dim * ES) {
           copy16_to_lds(kb + o, to + i * 1024);
@@ -212,49 +209,56 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
     if (a.dim == DP) rows(std::true_type{});
     else rows(std::false_type{});
     if constexpr (E4M3) {
-      const unsigned j = key_of(s, lane & 31), pg = page_of(j, a.cache), in = j - pg * a.cache.size;
-      const size_t o = (size_t)min(id_scale, top_page) * a.cache.spage + (size_t)in * a.cache.sts +
-                       kvh * a.cache.shs;
+      const unsigned j = key_of(keys, lane & 31), pg = page_of(j, a.cache), in = j - pg * a.cache.size;
+      const size_t o = (size_t)min(id_scale, top_page) * a.cache.spage + (size_t)in * a.cache.sts + kvh * a.cache.shs;
       copy4_to_lds((lane < 32 ? a.cache.k_scales : a.cache.v_scales) + o, to + 2 * R::kKeys);
     }
-    fetch_ids(later, (slot + 2) & 3);
+    fetch_ids(p, min(i + 2, p.count - 1), (slot + 2) & 3);
+  };
+  // Starts a part's first two tiles: slots 0 and 1, stages 0 and 1.
+  auto start = [&](const Part& p) {
+    fetch_ids(p, 0, 0);
+    fetch_ids(p, min(1u, p.count - 1), 1);
+    wait_copies();
+    read_ids(0);
+    fetch(p, 0, 0, 0);
+    if (p.count > 1) {
+      read_ids(1);
+      fetch(p, 1, 1, 1);
+    }
   };
 
-  Step s0 = walk(), s1 = walk(), s2 = walk(), s3 = walk();
-  fetch_ids(s0, 0);
-  fetch_ids(s1, 1);
-  wait_copies();
-  read_ids(0);
-  fetch(s0, s2, 0, 0);
-  read_ids(1);
-  fetch(s1, s3, 1, 1);
-
+  start(now);
   Frag8 q[KS];
   f32x4 o[DT];
   float m = AR_NEG_INF, l = 0.f;
   const float c = a.scale * kLog2e;
-  int stage = 0, slot = 0;
-  while (s0.live) {
-    const unsigned kvh = (unsigned)s0.hx / head_tiles, ht = (unsigned)s0.hx % head_tiles;
+  for (;;) {
+    const unsigned kvh = (unsigned)now.hx / head_tiles, ht = (unsigned)now.hx % head_tiles;
     const unsigned here = min(group - ht * kHeads, kHeads), head0 = kvh * group + ht * kHeads;
-    if (s0.first) {
-      m = AR_NEG_INF;
-      l = 0.f;
+    m = AR_NEG_INF;
+    l = 0.f;
 #pragma unroll
-      for (int d = 0; d < DT; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int d = 0; d < DT; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+    {
       // columns past the last head are those of the last; their results are not kept
-      const uint16_t* qp = a.q.p + (size_t)s0.seq * a.q.ts + (head0 + min((unsigned)hd, here - 1)) * a.q.hs;
+      const uint16_t* qp = a.q.p + (size_t)now.seq * a.q.ts + (head0 + min((unsigned)hd, here - 1)) * a.q.hs;
 #pragma unroll
       for (int x = 0; x < KS; ++x) {
         const unsigned d = E4M3 ? 64 * (x / 2) + 16 * g + 8 * (x & 1) : 32 * x + 8 * g;
         q[x].u = d < a.dim ? *reinterpret_cast<const u32x4*>(qp + d) : u32x4{0, 0, 0, 0};
       }
-      wait_copies();                           // the queries are here (and the copies before them)
     }
-    // the step's copies are done when only the next step's are left
-    asm volatile("s_waitcnt vmcnt(%0)" :: "n"(R::kCopies) : "memory");
-    read_ids((slot + 2) & 3);
-    const int keys = min(s0.end - s0.j0 - wave * STEP, STEP);   // of this wave's step
+    wait_copies();                             // the queries are here (and the copies before them)
+#pragma unroll 1
+    for (unsigned i = 0; i < now.count; ++i) {
+    const int stage = i & 1, slot = i & 3;
+    // the tile's copies are done when only the next one's are left
+    if (i + 1 < now.count) asm volatile("s_waitcnt vmcnt(%0)" :: "n"(R::kCopies) : "memory");
+    else wait_copies();
+    if (i + 2 < now.count) read_ids((slot + 2) & 3);
+    const Keys tile = keys_of(now, i);
+    const int keys = min(tile.end - tile.j0 - wave * STEP, STEP);   // of this wave's step
     if (keys > 0) {
       if (__any((lane & (STEP - 1)) < keys && ids[slot * kWave + (lane & (STEP - 1))] >= a.cache.pages))
         l = __uint_as_float(0x7FC00000u);
@@ -382,12 +386,14 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
       }
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the stage has been read
-    const Step s4 = walk();
-    fetch(s2, s4, stage, (slot + 2) & 3);
-    stage ^= 1;
-    slot = (slot + 1) & 3;
+    if (i + 2 < now.count) fetch(now, i + 2, stage, (slot + 2) & 3);
+    }
 
-    if (s0.last) {
+    // the run's next sequence is on its way while this one's results are joined
+    const Part s0 = now;
+    const bool more = follow(now);
+    if (more) start(now);
+    {
       // the waves' results are one
       l = sum_of(swap32(sum_of(swap16(l))));
       if (lane < 16) {
@@ -402,7 +408,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
       for (int w = 0; w < kWaves; ++w)
         sum += lm[w][hd] == AR_NEG_INF ? ll[w][hd] : ll[w][hd] * exp2_fast(lm[w][hd] - M);
       const float f = m == AR_NEG_INF ? 0.f : exp2_fast(m - M);
-      const unsigned begin = split ? s0.seq_u / per : 0, finish = split ? (s0.seq_u + s0.n - 1) / per : 0;
+      const unsigned begin = split ? s0.seq_u / per : 0, finish = split ? (s0.seq_u + (unsigned)s0.cut.n - 1) / per : 0;
       const unsigned count = finish - begin + 1;   // runs that hold parts of the sequence
       const float inv = sum > 0.f ? 1.0f / sum : sum;   // no key: zeros; NaN stays
       // results of a part: 16 maxima, 16 sums, then rows of a head's columns
@@ -493,12 +499,8 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
             sum > 0.f ? (M + __builtin_amdgcn_logf(sum)) * kLn2 : sum == 0.f ? AR_NEG_INF : sum;
       }
     }
-    s0 = s1;
-    s1 = s2;
-    s2 = s3;
-    s3 = s4;
+    if (!more) break;
   }
-  wait_copies();                               // LDS is not given up under a copy
 }
 
 unsigned head_tiles_of(size_t hq, size_t hkv) { return (unsigned)cdiv(hq / hkv, kHeads); }
