@@ -68,18 +68,33 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
   }
 
   unsigned bad = 0;                            // a page number out of range was met
-  auto page_base = [&](int j, unsigned& in) {  // page of key j, its place in the page
-    const unsigned pg = page_of((unsigned)j, a.cache);
-    in = (unsigned)j - pg * a.cache.size;
-    unsigned id = (unsigned)a.table[tile.seq * a.table_ld + pg];
+  const TileCopy<DP, NW> copy_rows(a.k.ts, a.v.ts, a.dim, wave, lane);
+  const uint16_t *kb = a.k.p + (size_t)k_first * a.k.ts + kvh * a.k.hs, *vb = a.v.p + (size_t)k_first * a.v.ts + kvh * a.v.hs;
+  // Pages: the numbers of a tile's pages are read one tile before its keys.
+  constexpr int ALL = kBN * DP / 16, CHUNKS = SRC == kKeyPagesE4M3 ? (ALL + NW * 64 - 1) / (NW * 64) : 1;  // of 16 codes
+  constexpr int IDS = SRC == kKeyPagesE4M3 ? CHUNKS + 1 : copy_rows.COPIES;
+  unsigned ids[IDS];
+  auto id_row = [&](int i) {                   // the tile's row that number i is for
+    if constexpr (SRC == kKeyPagesE4M3) return i < CHUNKS ? (i * NW * 64 + t) / (DP / 16) : t % kBN;
+    else return i * NW * copy_rows.RPC + copy_rows.row;
+  };
+  auto look_up = [&](int n) {
+    if constexpr (SRC != kKeyRows) {
+      const KeyStep k = key_step(keys, n, kBN);
+#pragma unroll
+      for (int i = 0; i < IDS; ++i)
+        ids[i] = (unsigned)a.table[tile.seq * a.table_ld + page_of((unsigned)min(k.j0 + id_row(i), k.end - 1), a.cache)];
+    }
+  };
+  // Element of row r's token: in page `id` for strides ps of pages, ts of tokens.
+  auto token = [&](const KeyStep& k, int r, unsigned id, size_t ps, size_t ts) {
+    const unsigned j = (unsigned)min(k.j0 + r, k.end - 1), in = j - page_of(j, a.cache) * a.cache.size;
     if (id >= a.cache.pages) {
       bad = 1;
       id = 0;
     }
-    return id;
+    return (size_t)id * ps + (size_t)in * ts;
   };
-  const TileCopy<DP, NW> copy_rows(a.k.ts, a.v.ts, a.dim, wave, lane);
-  const uint16_t *kb = a.k.p + (size_t)k_first * a.k.ts + kvh * a.k.hs, *vb = a.v.p + (size_t)k_first * a.v.ts + kvh * a.v.hs;
   auto copy = [&](int n, int buf) {
     const KeyStep k = key_step(keys, n, kBN);
     const uint32_t to = lbase + buf * 2 * kTile;
@@ -88,9 +103,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
     } else {
 #pragma unroll
       for (int i = 0; i < copy_rows.COPIES; ++i) {
-        const int j = min(k.j0 + i * NW * copy_rows.RPC + copy_rows.row, k.end - 1);
-        unsigned in;
-        const size_t at = (size_t)page_base(j, in) * a.cache.page + (size_t)in * a.cache.ts + kvh * a.cache.hs;
+        const size_t at = token(k, i * NW * copy_rows.RPC + copy_rows.row, ids[SRC == kKeyPages ? i : 0], a.cache.page, a.cache.ts) + kvh * a.cache.hs;
         if (copy_rows.on) {
           const uint32_t here = to + (i * NW + wave) * 1024;
           copy16_to_lds(reinterpret_cast<const char*>(static_cast<const uint16_t*>(a.cache.k) + at) + copy_rows.chunk, here);
@@ -100,7 +113,6 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
     }
   };
   // E4M3: codes through registers, which are the same values in bf16
-  constexpr int ALL = kBN * DP / 16, CHUNKS = SRC == kKeyPagesE4M3 ? (ALL + NW * 64 - 1) / (NW * 64) : 1;  // of 16 codes
   u32x4 ck[CHUNKS], cv[CHUNKS];
   float cs = 0.f;
   auto fetch = [&](int n) {
@@ -108,20 +120,15 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
 #pragma unroll
     for (int i = 0; i < CHUNKS; ++i) {
       const int at = i * NW * 64 + t, r = at / (DP / 16), ch = at % (DP / 16);
-      unsigned in;
-      const size_t pg = page_base(min(k.j0 + r, k.end - 1), in);
-      const size_t o = pg * a.cache.page + (size_t)in * a.cache.ts + kvh * a.cache.hs + ch * 16;
+      const size_t o = token(k, r, ids[SRC == kKeyPagesE4M3 ? i : 0], a.cache.page, a.cache.ts) + kvh * a.cache.hs + ch * 16;
       ck[i] = cv[i] = u32x4{0, 0, 0, 0};
       if (at < ALL && ch * 16 < (int)a.dim) {
         ck[i] = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(a.cache.k) + o);
         cv[i] = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(a.cache.v) + o);
       }
     }
-    if (t < 2 * kBN) {
-      unsigned in;
-      const size_t pg = page_base(min(k.j0 + t % kBN, k.end - 1), in);
-      cs = (t < kBN ? a.cache.k_scales : a.cache.v_scales)[pg * a.cache.spage + (size_t)in * a.cache.sts + kvh * a.cache.shs];
-    }
+    if (t < 2 * kBN)
+      cs = (t < kBN ? a.cache.k_scales : a.cache.v_scales)[token(k, t % kBN, ids[IDS - 1], a.cache.spage, a.cache.sts) + kvh * a.cache.shs];
   };
   auto put = [&](int buf) {
 #pragma unroll
@@ -163,8 +170,10 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) o[d][r] = 0.f;
     if (keys.steps > 0) {
+      look_up(0);
       if constexpr (SRC == kKeyPagesE4M3) fetch(0);
       else copy(0, 0);
+      if (keys.steps > 1) look_up(1);
     }
     for (int n = 0; n < keys.steps; ++n) {
       const int buf = n & 1;
@@ -174,6 +183,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
       if (n + 1 < keys.steps) {
         if constexpr (SRC == kKeyPagesE4M3) fetch(n + 1);
         else copy(n + 1, buf ^ 1);
+        if (n + 2 < keys.steps) look_up(n + 2);
       }
       const KeyStep k = key_step(keys, n, kBN);
       const int j0 = k.j0;
@@ -256,7 +266,8 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
           keep_order();
         });
         fit(1);
-        top = max_halves(largest(1, top)) * c;
+        top = largest(1, top);
+        top = fmaxf(top, __shfl_xor(top, 32)) * c;
         // the running maximum follows only where it falls behind by 2^8: sums
         // stay far below binary32's range, and most tiles change nothing
         if (__any(top > m + 8.0f)) {
@@ -312,7 +323,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
     care = true;
   }
 
-  l = add_halves(l);
+  l += __shfl_xor(l, 32);
   if (row > last) return;
   float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;   // no visible key: zeros; NaN stays
   if (SRC != kKeyRows && lflag[1]) inv = __uint_as_float(0x7FC00000u);
@@ -339,9 +350,14 @@ hipError_t launch(const Launch& L, const AttnArgs& a) {
   return launch_k(k_attn<DP, NW, SRC>, dim3(tiles * a.hq), dim3(NW * 64), 0, L.stream, a);
 }
 
+// 256 queries a workgroup where that gives every CU two, else 128, of which
+// two share a CU.  (16384 tokens, 64 heads of 128: 4187 us and 4391; 647 tokens,
+// 6 heads of 64: 15.4 and 11.9.)
 template <KeySource SRC>
 hipError_t launch_src(const Launch& L, const AttnArgs& a) {
-  return a.dim > 64 ? launch<128, 8, SRC>(L, a) : launch<64, 8, SRC>(L, a);
+  const bool wide = (size_t)a.rows_q * a.hq >= (size_t)2 * L.cus * 256;
+  if (a.dim > 64) return wide ? launch<128, 8, SRC>(L, a) : launch<128, 4, SRC>(L, a);
+  return wide ? launch<64, 8, SRC>(L, a) : launch<64, 4, SRC>(L, a);
 }
 
 }  // namespace

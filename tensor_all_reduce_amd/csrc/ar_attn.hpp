@@ -131,7 +131,8 @@ __device__ __forceinline__ Rows rows_at(const int32_t* cu, unsigned s, unsigned 
 
 // Tile `rank` of all sequences' tiles of `bm` rows, those with the most work of
 // a causal sequence first: of queries the last (DOWN), of keys the first.
-// False if there are fewer.  SKIP: without each sequence's first tile.  Every
+// False if there are fewer.  (Counts go through lane exchanges: with scalar
+// ones, and so a scalar exit, the compiler spills 25 registers of k_attn.)  SKIP: without each sequence's first tile.  Every
 // lane of the wave takes part and gets the same answer.
 struct Tile {
   unsigned seq, row;            // sequence, its row at which the tile begins
@@ -146,12 +147,12 @@ __device__ __forceinline__ bool find_tile(const int32_t* cu, unsigned seqs, unsi
     return SKIP ? (n ? (n - 1) / bm : 0) : (n + bm - 1) / bm;
   };
   unsigned total = 0;
-  for (unsigned s0 = 0; s0 < seqs; s0 += kWave) total += last_lane(wave_scan(tiles_of(s0 + lane)));
+  for (unsigned s0 = 0; s0 < seqs; s0 += kWave) total += __shfl(wave_scan(tiles_of(s0 + lane)), kWave - 1);
   if (rank >= total) return false;
   unsigned at = DOWN ? total - 1 - rank : rank;
   t->at = at;
   for (unsigned s0 = 0; s0 < seqs; s0 += kWave) {
-    const unsigned tiles = tiles_of(s0 + lane), upto = wave_scan(tiles), here = last_lane(upto);
+    const unsigned tiles = tiles_of(s0 + lane), upto = wave_scan(tiles), here = __shfl(upto, kWave - 1);
     if (at < here) {
       const uint64_t past = __ballot(upto > at);
       const int who = __builtin_ctzll(past);
@@ -316,7 +317,5 @@ __device__ __forceinline__ u32x2 swap16(float x) {
 }
 __device__ __forceinline__ float max_of(u32x2 p) { return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1])); }
 __device__ __forceinline__ float sum_of(u32x2 p) { return __uint_as_float(p[0]) + __uint_as_float(p[1]); }
-__device__ __forceinline__ float max_halves(float x) { return max_of(swap32(x)); }
-__device__ __forceinline__ float add_halves(float x) { return sum_of(swap32(x)); }
 
 }  // namespace ar

@@ -95,14 +95,13 @@ __device__ __forceinline__ float finite_lse(float lse) { return lse == AR_NEG_IN
 
 // dQ: 256 queries of one head, 64 keys at a time.
 template <int DP>
-__global__ __launch_bounds__(kWavesQ * 64, 2) void k_attn_dq(AttnBwdArgs b, const float* delta) {
+__device__ __forceinline__ void queries_pass(const AttnBwdArgs& b, const float* delta, unsigned block, char* lds) {
   constexpr int KS = DP / 16, DT = DP / 32;
   constexpr uint32_t kTile = kBT * DP * 2;
-  __shared__ __align__(1024) char lds[4 * kTile];
   const AttnArgs& a = b.f;
   const int t = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(t / kWave);
   const int col = lane & 31, hh = lane >> 5;
-  const unsigned rank = blockIdx.x / a.hq, hi = blockIdx.x % a.hq;
+  const unsigned rank = block / a.hq, hi = block % a.hq;
   const unsigned kvh = hi % a.hkv, head = kvh * (a.hq / a.hkv) + hi / a.hkv;
   Tile tile;
   if (!find_tile<true>(a.cu_q, a.seqs, a.rows_q, kQueries, rank, &tile)) return;
@@ -234,16 +233,16 @@ struct KeySums {
 // heads of 128: 1437 us, this 1190).  The arithmetic of P and dS is spread
 // over the products that do not need it.
 template <int DP>
-__global__ __launch_bounds__(kWavesK * 64, 2) void k_attn_dkv(AttnBwdArgs b, const float* delta, KeySums sums) {
+__device__ __forceinline__ void keys_pass(const AttnBwdArgs& b, const float* delta, const KeySums& sums, unsigned block,
+                                          char* lds, float (*lrow)[2][kBT]) {
   constexpr int KS = DP / 16, DT = DP / 32;
   constexpr uint32_t kTile = kBT * DP * 2;
-  __shared__ __align__(1024) char lds[8 * kTile];  // two tiles of queries; the keys and values, 64 at a time
-  __shared__ __align__(16) float lrow[2][2][kBT];  // lse, delta
+  // lds: two tiles of queries; the keys and values, 64 at a time.  lrow: lse, delta of the queries
   const AttnArgs& a = b.f;
   const int t = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(t / kWave);
   const int col = lane & 31, hh = lane >> 5;
-  unsigned rank = blockIdx.x / sums.sets;
-  const unsigned hi = blockIdx.x % sums.sets;   // sets of one key head on one XCD, if there are eight heads
+  unsigned rank = block / sums.sets;
+  const unsigned hi = block % sums.sets;   // sets of one key head on one XCD, if there are eight heads
   const unsigned kvh = hi % a.hkv, set = kvh * (sums.sets / a.hkv) + hi / a.hkv, head0 = set * sums.per;
   const unsigned far_tiles = sums.runs * sums.sink_tiles;
   const bool far = rank < far_tiles;
@@ -443,6 +442,17 @@ __global__ __launch_bounds__(kWavesK * 64, 2) void k_attn_dkv(AttnBwdArgs b, con
   }
 }
 
+// Both passes in one launch, the keys' first, whose workgroups have more to do:
+// short batches wait for one of them only, and long ones end together.
+template <int DP>
+__global__ __launch_bounds__(kWavesQ * 64, 2) void k_attn_bwd(AttnBwdArgs b, const float* delta, KeySums sums, unsigned key_blocks) {
+  static_assert(kWavesQ == kWavesK, "both passes have one workgroup size");
+  __shared__ __align__(1024) char lds[8 * kBT * DP * 2];
+  __shared__ __align__(16) float lrow[2][2][kBT];
+  if (blockIdx.x < key_blocks) keys_pass<DP>(b, delta, sums, blockIdx.x, lds, lrow);
+  else queries_pass<DP>(b, delta, blockIdx.x - key_blocks, lds);
+}
+
 // Joins the sums of a key's query heads and runs: a workgroup takes 8 rows of
 // one key head of dK, or of dV.
 constexpr int kJoinRows = 8;
@@ -494,9 +504,9 @@ struct Room {
 Room room_of(size_t rows_q, size_t rows_k, size_t hq, size_t hkv, size_t dim, size_t window, size_t sinks) {
   Room r{};
   r.delta = cdiv(rows_q * hq, 64) * 64;
-  // Query heads of a key head that one workgroup takes one after the other:
-  // as many as leave two workgroups a CU.  Each spares a write and a read of
-  // its sums and a start.
+  // Query heads of a key head that one workgroup takes one after the other, each
+  // of which spares a write and a read of its sums and a start: as many as
+  // leave two workgroups a CU.
   const size_t group = hq / hkv, tiles = cdiv(rows_k ? rows_k : 1, kKeysB) * hkv;
   size_t per = group;
   while (per > 1 && (group % per || tiles * (group / per) < 512)) --per;
@@ -523,18 +533,16 @@ hipError_t launch(const Launch& L, const AttnBwdArgs& b) {
     e = launch_k(k_attn_delta, dim3((unsigned)cdiv((size_t)a.rows_q * a.hq, 16)), dim3(256), 0, L.stream, b.out, b.d_out, delta,
                  a.rows_q, a.hq, a.dim);
     if (e != hipSuccess) return e;
-    if (b.dq.p) {
-      const unsigned tiles = a.rows_q / kQueries + a.seqs;
-      e = launch_k(k_attn_dq<DP>, dim3(tiles * a.hq), dim3(kWavesQ * 64), 0, L.stream, b, delta);
-      if (e != hipSuccess) return e;
-    }
   }
-  if (!b.dk.p || a.rows_k == 0) return hipSuccess;
   const KeySums sums{room.near ? delta + room.delta : nullptr, room.far ? delta + room.delta + room.near : nullptr,
                      room.per, room.sets, room.sink_tiles, room.runs};
+  const bool keys = b.dk.p && a.rows_k;
   const unsigned tiles = room.runs * room.sink_tiles + a.rows_k / kKeysB + a.seqs;
-  e = launch_k(k_attn_dkv<DP>, dim3(tiles * room.sets), dim3(kWavesK * 64), 0, L.stream, b, delta, sums);
-  if (e != hipSuccess || !sums.near) return e;
+  const unsigned key_blocks = keys ? tiles * room.sets : 0;
+  const unsigned query_blocks = b.dq.p && a.rows_q ? (a.rows_q / kQueries + a.seqs) * a.hq : 0;
+  if (key_blocks + query_blocks == 0) return hipSuccess;
+  e = launch_k(k_attn_bwd<DP>, dim3(key_blocks + query_blocks), dim3(kWavesQ * 64), 0, L.stream, b, delta, sums, key_blocks);
+  if (e != hipSuccess || !keys || !sums.near) return e;
   return launch_k(k_attn_join, dim3((a.rows_k / kJoinRows + a.seqs) * a.hkv * 2), dim3(256), 0, L.stream, b, sums);
 }
 
