@@ -646,7 +646,7 @@ int ar_rope_kv(const ar_heads* q, const ar_heads* k, const ar_heads* v, size_t t
  *   table, table_stride, table_pages   page table: rows of table_pages entries
  *   lens        int32[seqs], keys of each sequence, held within
  *               [0, table_pages * page_size]
- *   scale       finite, above 0
+ *   scale       above 0; 2^-64 to 2^64 (AR_ERR_UNSUPPORTED)
  *   lse         element (i, h) at lse[i * lse_ts + h * lse_hs], or NULL
  *   workspace   device memory, 16-byte aligned, zero before its first use; a
  *               call leaves its counters zero again, and calls of other

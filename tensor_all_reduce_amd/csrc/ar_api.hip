@@ -464,7 +464,7 @@ bool dim_ok(size_t dim) { return dim >= 16 && dim % 16 == 0; }
 int check_mask(size_t hq, size_t hkv, size_t dim, float scale, size_t window, size_t sinks, ar::AttnArgs* a) {
   if (hq == 0 || hkv == 0 || hq % hkv || !dim_ok(dim)) return AR_ERR_INVALID;
   if (!(scale > 0.0f && scale <= 3.402823466e38f)) return AR_ERR_INVALID;
-  if (dim > AR_ATTN_MAX_DIM || hq >> 16) return AR_ERR_UNSUPPORTED;
+  if (dim > AR_ATTN_MAX_DIM || hq >> 16 || scale < 0x1p-64f || scale > 0x1p64f) return AR_ERR_UNSUPPORTED;
   a->hq = (unsigned)hq;
   a->hkv = (unsigned)hkv;
   a->dim = (unsigned)dim;
@@ -1143,7 +1143,7 @@ int ar_rope_kv(const ar_heads* q, const ar_heads* k, const ar_heads* v, size_t t
 
 size_t ar_attn_decode_workspace(size_t seqs, size_t hq, size_t hkv, size_t dim) {
   if (seqs == 0 || seqs > kMaxRows || hq == 0 || hkv == 0 || hq % hkv || hq >> 16 || !dim_ok(dim) || dim > AR_ATTN_MAX_DIM) return 0;
-  return ar::attn_decode_workspace(seqs, hq, hkv, dim);
+  return ar::attn_decode_workspace(seqs, hq, hkv);
 }
 
 int ar_attn_decode(const ar_heads* q, const ar_kv_cache* cache, const int32_t* table, size_t table_stride,
@@ -1312,7 +1312,7 @@ int ar_attn_bwd(const ar_heads* q, const ar_heads* k, const ar_heads* v, const a
     og[no++] = grid_of(workspace, 1, need, {1, 1, 1}, {0, 0, 0});
   }
   if ((rc = check_apart(in, ni, og, no))) return rc;
-  if (!ar::attn_fits(rows_q, seqs, hq) || !ar::attn_fits(rows_k, seqs, hq)) return AR_ERR_UNSUPPORTED;
+  if (!ar::attn_bwd_fits(rows_q, rows_k, seqs, hq, hkv, dim, a.window, a.sinks)) return AR_ERR_UNSUPPORTED;
   a.q = rows_arg(q);
   a.k = rows_arg(k);
   a.v = rows_arg(v);

@@ -554,6 +554,13 @@ size_t attn_bwd_workspace(size_t rows_q, size_t rows_k, size_t seqs, size_t hq, 
   return (r.delta + r.near + r.far) * sizeof(float);
 }
 
+bool attn_bwd_fits(size_t rows_q, size_t rows_k, size_t seqs, size_t hq, size_t hkv, size_t dim, size_t window, size_t sinks) {
+  const Room r = room_of(rows_q, rows_k, hq, hkv, dim, window, sinks);
+  const size_t blocks = ((size_t)r.runs * r.sink_tiles + rows_k / kKeysB + seqs) * r.sets + (rows_q / kQueries + seqs) * hq;
+  const size_t join = (rows_k / kJoinRows + seqs) * hkv * 2;
+  return (rows_q * hq) / 16 < 0x7FFFFFFF && blocks <= 0x7FFFFFFF && join <= 0x7FFFFFFF;
+}
+
 hipError_t launch_attn_bwd(const Launch& L, const AttnBwdArgs& b) {
   return b.f.dim > 64 ? launch<128>(L, b) : launch<64>(L, b);
 }

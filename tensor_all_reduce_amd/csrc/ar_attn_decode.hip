@@ -504,23 +504,23 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
 }
 
 unsigned head_tiles_of(size_t hq, size_t hkv) { return (unsigned)cdiv(hq / hkv, kHeads); }
+// The parts come first, with room for the widest heads, so that the counters
+// lie in one place for every shape.
+constexpr size_t kPartsBytes = (size_t)kWorkers * 2 * (2 * kHeads + kHeads * AR_ATTN_MAX_DIM) * 4;
 size_t counters_bytes(size_t seqs, size_t hq, size_t hkv) { return cdiv(seqs * hkv * head_tiles_of(hq, hkv) * 4, 256) * 256; }
 
 template <int DP, bool E4M3>
 hipError_t launch(const Launch& L, const AttnArgs& a, void* ws) {
   const unsigned ht = head_tiles_of(a.hq, a.hkv);
-  uint32_t* counters = static_cast<uint32_t*>(ws);
-  float* parts = ws ? reinterpret_cast<float*>(static_cast<char*>(ws) + counters_bytes(a.seqs, a.hq, a.hkv)) : nullptr;
+  float* parts = static_cast<float*>(ws);
+  uint32_t* counters = ws ? reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + kPartsBytes) : nullptr;
   const unsigned grid = ws ? kWorkers : a.seqs * a.hkv * ht;
   return launch_k(k_attn_decode<DP, E4M3>, dim3(grid), dim3(kWaves * 64), 0, L.stream, a, ht, counters, parts, ws != nullptr);
 }
 
 }  // namespace
 
-size_t attn_decode_workspace(size_t seqs, size_t hq, size_t hkv, size_t dim) {
-  const size_t dp = dim > 64 ? 128 : 64;
-  return counters_bytes(seqs, hq, hkv) + (size_t)kWorkers * 2 * (2 * kHeads + kHeads * dp) * 4;
-}
+size_t attn_decode_workspace(size_t seqs, size_t hq, size_t hkv) { return kPartsBytes + counters_bytes(seqs, hq, hkv); }
 
 hipError_t launch_attn_decode(const Launch& L, const AttnArgs& a, bool e4m3, void* ws) {
   if (a.dim > 64) return e4m3 ? launch<128, true>(L, a, ws) : launch<128, false>(L, a, ws);

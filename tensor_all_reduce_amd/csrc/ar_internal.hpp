@@ -236,7 +236,7 @@ enum KeySource { kKeyRows = 0, kKeyPages, kKeyPagesE4M3 };
 hipError_t launch_attn(const Launch& L, const AttnArgs& a, KeySource src);
 bool attn_fits(size_t rows_q, size_t seqs, size_t hq);  // whether its grid fits a launch
 
-size_t attn_decode_workspace(size_t seqs, size_t hq, size_t hkv, size_t dim);
+size_t attn_decode_workspace(size_t seqs, size_t hq, size_t hkv);
 hipError_t launch_attn_decode(const Launch& L, const AttnArgs& a, bool e4m3, void* workspace);
 
 struct AttnBwdArgs {
@@ -247,6 +247,8 @@ struct AttnBwdArgs {
 };
 size_t attn_bwd_workspace(size_t rows_q, size_t rows_k, size_t seqs, size_t hq, size_t hkv, size_t dim, size_t window,
                           size_t sinks);
+bool attn_bwd_fits(size_t rows_q, size_t rows_k, size_t seqs, size_t hq, size_t hkv, size_t dim, size_t window,
+                   size_t sinks);  // whether its grids fit a launch
 hipError_t launch_attn_bwd(const Launch& L, const AttnBwdArgs& a);
 
 hipError_t launch_pack(const Launch& L, const void* x, uint64_t* w, size_t n, uint32_t seq);
