@@ -29,59 +29,58 @@ __device__ __forceinline__ u32x4 pack8(const float* f) {
   return v;
 }
 
-// One workgroup row is a token; 2^lg lanes a head, the rest of the workgroup's
-// lanes over the token's heads: queries, keys, then values.
-template <bool E4M3, bool PAIRS>
+// 2^lg lanes a head, 256 >> lg heads a workgroup: of a token's queries, keys,
+// then values, token after token.  NT: past the caches, of what is too much
+// for them.
+template <bool E4M3, bool PAIRS, bool NT>
 __global__ __launch_bounds__(256) void k_rope_kv(RopeArgs a, int lg, unsigned heads) {
   const unsigned lanes = 1u << lg, i = threadIdx.x & (lanes - 1);
   const unsigned work = blockIdx.x * (256 >> lg) + (threadIdx.x >> lg);   // (token, head)
-  const uint64_t token = work / heads;
-  const unsigned head = work % heads;
+  const unsigned token = work / heads, head = work - token * heads;
   const bool on = token < a.tokens && i < a.dim / 16;
   const bool is_q = head < a.hq, is_v = head >= a.hq + a.hkv;
   const unsigned h = is_q ? head : is_v ? head - a.hq - a.hkv : head - a.hq;
   const HeadRows src = is_q ? a.q : is_v ? a.v : a.k;
   const bool turn = on && !is_v && i < a.rot / 16;
   // the lane's two groups of 8
-  unsigned g0, g1;
-  if (!is_v && i < a.rot / 16 && !PAIRS) {
-    g0 = 8 * i;
-    g1 = a.rot / 2 + 8 * i;
-  } else {
-    g0 = 16 * i;
-    g1 = 16 * i + 8;
-  }
-  float x[16];
-#pragma unroll
-  for (int e = 0; e < 16; ++e) x[e] = 0.f;
+  const bool apart = turn && !PAIRS;
+  const unsigned g0 = apart ? 8 * i : 16 * i, g1 = apart ? a.rot / 2 + 8 * i : 16 * i + 8;
+  u32x4 r0 = {0, 0, 0, 0}, r1 = r0;
+  float c[8], s[8];
+  int64_t slot = -1;
   if (on) {
     const uint16_t* p = src.p + token * src.ts + h * src.hs;
-    unpack8(*reinterpret_cast<const u32x4*>(p + g0), x);
-    unpack8(*reinterpret_cast<const u32x4*>(p + g1), x + 8);
+    r0 = ld4<NT>(reinterpret_cast<const u32x4*>(p + g0));
+    r1 = ld4<NT>(reinterpret_cast<const u32x4*>(p + g1));
+    if (a.cache.k && !is_q) slot = a.slots[token];
   }
   if (turn) {
     const unsigned pos = min((unsigned)max(a.positions[token], 0), a.table_rows - 1);
-    const float* row = a.cos_sin + (size_t)pos * a.rot + 8 * i;
-    float c[8], s[8];
+    const f32x4* row = reinterpret_cast<const f32x4*>(a.cos_sin + (size_t)pos * a.rot + 8 * i);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      c[e] = row[e];
-      s[e] = a.inverse ? -row[a.rot / 2 + e] : row[a.rot / 2 + e];
+      c[e] = row[e / 4][e % 4];
+      s[e] = row[a.rot / 8 + e / 4][e % 4];
     }
+  }
+  float x[16];
+  unpack8(r0, x);
+  unpack8(r1, x + 8);
+  if (turn) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       constexpr int step = PAIRS ? 2 : 1;
       const int at = step * e, bt = PAIRS ? at + 1 : at + 8;
-      const float u = x[at], w = x[bt];
-      x[at] = __builtin_fmaf(u, c[e], -(w * s[e]));
-      x[bt] = __builtin_fmaf(w, c[e], u * s[e]);
+      const float u = x[at], w = x[bt], sn = a.inverse ? -s[e] : s[e];
+      x[at] = __builtin_fmaf(u, c[e], -(w * sn));
+      x[bt] = __builtin_fmaf(w, c[e], u * sn);
     }
   }
   const HeadOut dst = is_q ? a.q_out : is_v ? HeadOut{nullptr, 0, 0} : a.k_out;
   if (on && dst.p) {
     uint16_t* p = dst.p + token * dst.ts + h * dst.hs;
-    *reinterpret_cast<u32x4*>(p + g0) = pack8(x);
-    *reinterpret_cast<u32x4*>(p + g1) = pack8(x + 8);
+    st4<NT>(reinterpret_cast<u32x4*>(p + g0), pack8(x));
+    st4<NT>(reinterpret_cast<u32x4*>(p + g1), pack8(x + 8));
   }
   if (!a.cache.k) return;
   uint32_t amax = 0;
@@ -91,9 +90,8 @@ __global__ __launch_bounds__(256) void k_rope_kv(RopeArgs a, int lg, unsigned he
     for (unsigned d = 1; d < lanes; d *= 2) amax = max(amax, (uint32_t)__shfl_xor((int)amax, d));
   }
   if (!on || is_q) return;
-  const int64_t slot = a.slots[token];
   if (slot < 0 || slot >= (int64_t)a.cache.pages * a.cache.size) return;
-  const size_t page = (size_t)slot / a.cache.size, in = (size_t)slot % a.cache.size;
+  const unsigned page = page_of((unsigned)slot, a.cache), in = (unsigned)slot - page * a.cache.size;
   const size_t at = page * a.cache.page + in * a.cache.ts + h * a.cache.hs;
   void* base = is_v ? a.cache.v : a.cache.k;
   if constexpr (E4M3) {
@@ -119,10 +117,16 @@ hipError_t launch_rope_kv(const Launch& L, const RopeArgs& a) {
   int lg = 0;
   while ((16u << lg) < a.dim) ++lg;
   const size_t work = a.tokens * heads, per = 256u >> lg;
-  auto* k = a.e4m3 ? (a.pairs ? k_rope_kv<true, true> : k_rope_kv<true, false>)
-                   : (a.pairs ? k_rope_kv<false, true> : k_rope_kv<false, false>);
-  return launch_k(k, dim3((unsigned)cdiv(work, per)), dim3(256), 0, L.stream, a,
-                  lg, heads);
+  // (16384 tokens of 80 heads of 128: 126 us through the caches, 111 past them)
+  const bool nt = a.tokens * (2 * a.hq + 2 * a.hkv) * a.dim * 2 > (size_t)256 << 20;
+  auto pick = [&](auto e4m3, auto pairs) {
+    constexpr bool E = decltype(e4m3)::value, P = decltype(pairs)::value;
+    return nt ? k_rope_kv<E, P, true> : k_rope_kv<E, P, false>;
+  };
+  const std::true_type yes;
+  const std::false_type no;
+  auto* k = a.e4m3 ? (a.pairs ? pick(yes, yes) : pick(yes, no)) : (a.pairs ? pick(no, yes) : pick(no, no));
+  return launch_k(k, dim3((unsigned)cdiv(work, per)), dim3(256), 0, L.stream, a, lg, heads);
 }
 
 }  // namespace ar
