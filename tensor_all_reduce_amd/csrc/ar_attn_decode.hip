@@ -48,6 +48,12 @@ __device__ __forceinline__ int swizzle_bytes(int r) {
 template <int RB>
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) { return (uint32_t)(r * RB + ((c ^ swizzle_bytes<RB>(r)) * 16)); }
 
+// As copy16_to_lds, with the hint that the data are not read again.
+__device__ __forceinline__ void stream16_to_lds(const void* from, uint32_t lds) {
+  lds = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off nt" :: "s"(lds), "v"(from) : "memory");
+}
+
 __device__ __forceinline__ void copy4_to_lds(const void* from, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" :: "s"(lds), "v"(from) : "memory");
 }
@@ -201,8 +207,8 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
         const unsigned j = key_of(keys, i * RPC + crow), pg = page_of(j, a.cache), in = j - pg * a.cache.size;
         const size_t o = ((size_t)min(id[i], top_page) * a.cache.page + (size_t)in * a.cache.ts) * ES + ch;
         if (decltype(whole)::value || ch < a.dim * ES) {
-          copy16_to_lds(kb + o, to + i * 1024);
-          copy16_to_lds(vb + o, to + R::kKeys + i * 1024);
+          stream16_to_lds(kb + o, to + i * 1024);
+          stream16_to_lds(vb + o, to + R::kKeys + i * 1024);
         }
       }
     };
