@@ -101,13 +101,18 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
 
   // This workgroup's run of the row of all tiles, each sequence's followed by
   // kEnd empty ones; or (split false) one sequence's.
-  auto tiles_of = [&](unsigned s) { return s < a.seqs ? (unsigned)cut_of<TILE>(a, a.lens[s]).n + kEnd : 0u; };
+  auto tiles_of = [&](unsigned s, int& len) {
+    if (s >= a.seqs) return 0u;
+    len = a.lens[s];
+    return (unsigned)cut_of<TILE>(a, len).n + kEnd;
+  };
+  int len = 0;
   unsigned u = 0, u_end, per = 0;              // tiles of a run
   int hx, seq;
   unsigned into = 0;                           // tile of the sequence
   if (split) {
     unsigned N = 0;
-    for (unsigned s0 = 0; s0 < a.seqs; s0 += kWave) N += last_lane(wave_scan(tiles_of(s0 + lane)));
+    for (unsigned s0 = 0; s0 < a.seqs; s0 += kWave) N += last_lane(wave_scan(tiles_of(s0 + lane, len)));
     // Runs of whole key heads where that leaves few workgroups idle: the heads
     // of a token, which lie side by side in memory, are then read at one time.
     const unsigned heads = a.hkv * head_tiles, each = kWorkers / heads;
@@ -121,26 +126,29 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
     u_end = min(u + per, aligned ? hx * wide + N : N * heads);
     seq = 0;
     for (unsigned s0 = 0; s0 < a.seqs; s0 += kWave) {
-      const unsigned n = tiles_of(s0 + lane), upto = wave_scan(n), here = last_lane(upto);
+      const unsigned n = tiles_of(s0 + lane, len), upto = wave_scan(n), here = last_lane(upto);
       if (at < here) {
         const int who = __builtin_ctzll(__ballot(upto > at));
         seq = (int)s0 + who;
         into = at - (unsigned)(__builtin_amdgcn_readlane((int)upto, who) - __builtin_amdgcn_readlane((int)n, who));
+        len = __builtin_amdgcn_readlane(len, who);
         break;
       }
       at -= here;
     }
     seq = uniform(seq);
     into = (unsigned)uniform((int)into);
+    len = uniform(len);
   } else {
     seq = (int)(blockIdx.x % a.seqs);
     hx = (int)(blockIdx.x / a.seqs);
-    u_end = (unsigned)uniform((int)tiles_of((unsigned)seq)) - kEnd;
+    u_end = (unsigned)uniform((int)tiles_of((unsigned)seq, len)) - kEnd;
+    len = uniform(len);
   }
 
   typedef const __attribute__((address_space(4))) int32_t* Scalar;
   const Scalar lens = (Scalar)(uintptr_t)a.lens;
-  Part now{seq, hx, u - into, into, 0, cut_of<TILE>(a, lens[seq])};
+  Part now{seq, hx, u - into, into, 0, cut_of<TILE>(a, len)};
   // The run's next sequence; false at the run's end.
   auto follow = [&](Part& p) {
     const unsigned at = p.seq_u + (unsigned)p.cut.n + kEnd;
@@ -186,39 +194,46 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
   const uint32_t chunk = (uint32_t)((lane % CPR) ^ swizzle_bytes<RB>(crow)) * 16;
   // (a page number out of range is found again when the step is computed)
   const unsigned top_page = a.cache.pages - 1;
-  uint32_t id[COPIES], id_scale = 0;           // page numbers of the step that is fetched next
-  auto read_ids = [&](int slot) {
+  // Where the step that is fetched next lies: its rows' chunks, and (E4M3) the
+  // lane's scale.
+  size_t from[COPIES], from_scale = 0;
+  auto locate = [&](const Part& p, unsigned i, int slot) {
+    uint32_t id[COPIES], id_scale = 0;
 #pragma unroll
-    for (int i = 0; i < COPIES; ++i) id[i] = ids[slot * kWave + i * RPC + crow];
+    for (int x = 0; x < COPIES; ++x) id[x] = ids[slot * kWave + x * RPC + crow];
     if constexpr (E4M3) id_scale = ids[slot * kWave + (lane & 31)];
+    const Keys keys = keys_of(p, i);
+    const unsigned kvh = (unsigned)p.hx / head_tiles;
+#pragma unroll
+    for (int x = 0; x < COPIES; ++x) {
+      // the chunk of row crow is that of row x RPC + crow but for the rows' swizzle
+      const uint32_t ch = chunk ^ (uint32_t)((swizzle_bytes<RB>(x * RPC + crow) ^ swizzle_bytes<RB>(crow)) * 16);
+      const unsigned j = key_of(keys, x * RPC + crow), in = j - page_of(j, a.cache) * a.cache.size;
+      from[x] = ((size_t)min(id[x], top_page) * a.cache.page + (size_t)in * a.cache.ts + kvh * a.cache.hs) * ES + ch;
+    }
+    if constexpr (E4M3) {
+      const unsigned j = key_of(keys, lane & 31), in = j - page_of(j, a.cache) * a.cache.size;
+      from_scale = (size_t)min(id_scale, top_page) * a.cache.spage + (size_t)in * a.cache.sts + kvh * a.cache.shs;
+    }
   };
   // Starts tile i's copies, and those of the page numbers of tile i + 2.
   auto fetch = [&](const Part& p, unsigned i, int stage, int slot) {
-    const unsigned kvh = (unsigned)p.hx / head_tiles;
     const uint32_t to = lmine + stage * R::kStage;
-    const Keys keys = keys_of(p, i);
-    const size_t head = kvh * a.cache.hs * ES;
-    const char *kb = static_cast<const char*>(a.cache.k) + head, *vb = static_cast<const char*>(a.cache.v) + head;
+    const char *kb = static_cast<const char*>(a.cache.k), *vb = static_cast<const char*>(a.cache.v);
     auto rows = [&](auto whole) {
 #pragma unroll
-      for (int i = 0; i < COPIES; ++i) {
-        // the chunk of row crow is that of row i RPC + crow but for the rows' swizzle
-        const uint32_t ch = chunk ^ (uint32_t)((swizzle_bytes<RB>(i * RPC + crow) ^ swizzle_bytes<RB>(crow)) * 16);
-        const unsigned j = key_of(keys, i * RPC + crow), pg = page_of(j, a.cache), in = j - pg * a.cache.size;
-        const size_t o = ((size_t)min(id[i], top_page) * a.cache.page + (size_t)in * a.cache.ts) * ES + ch;
+      for (int x = 0; x < COPIES; ++x) {
+        const uint32_t ch = chunk ^ (uint32_t)((swizzle_bytes<RB>(x * RPC + crow) ^ swizzle_bytes<RB>(crow)) * 16);
         if (decltype(whole)::value || ch < a.dim * ES) {
-          stream16_to_lds(kb + o, to + i * 1024);
-          stream16_to_lds(vb + o, to + R::kKeys + i * 1024);
+          stream16_to_lds(kb + from[x], to + x * 1024);
+          stream16_to_lds(vb + from[x], to + R::kKeys + x * 1024);
         }
       }
     };
     if (a.dim == DP) rows(std::true_type{});
     else rows(std::false_type{});
-    if constexpr (E4M3) {
-      const unsigned j = key_of(keys, lane & 31), pg = page_of(j, a.cache), in = j - pg * a.cache.size;
-      const size_t o = (size_t)min(id_scale, top_page) * a.cache.spage + (size_t)in * a.cache.sts + kvh * a.cache.shs;
-      copy4_to_lds((lane < 32 ? a.cache.k_scales : a.cache.v_scales) + o, to + 2 * R::kKeys);
-    }
+    if constexpr (E4M3)
+      copy4_to_lds((lane < 32 ? a.cache.k_scales : a.cache.v_scales) + from_scale, to + 2 * R::kKeys);
     fetch_ids(p, min(i + 2, p.count - 1), (slot + 2) & 3);
   };
   // Starts a part's first two tiles: slots 0 and 1, stages 0 and 1.
@@ -226,19 +241,31 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
     fetch_ids(p, 0, 0);
     fetch_ids(p, min(1u, p.count - 1), 1);
     wait_copies();
-    read_ids(0);
+    locate(p, 0, 0);
     fetch(p, 0, 0, 0);
     if (p.count > 1) {
-      read_ids(1);
+      locate(p, 1, 1);
       fetch(p, 1, 1, 1);
     }
   };
 
-  start(now);
   Frag8 q[KS];
   f32x4 o[DT];
   float m = AR_NEG_INF, l = 0.f;
   const float c = a.scale * kLog2e;
+  // (columns past the last head are those of the last; their results are not kept)
+  auto load_queries = [&](const Part& p) {
+    const unsigned kvh = (unsigned)p.hx / head_tiles, ht = (unsigned)p.hx % head_tiles;
+    const unsigned here = min(group - ht * kHeads, kHeads), h = kvh * group + ht * kHeads + min((unsigned)hd, here - 1);
+    const uint16_t* qp = a.q.p + (size_t)p.seq * a.q.ts + h * a.q.hs;
+#pragma unroll
+    for (int x = 0; x < KS; ++x) {
+      const unsigned d = E4M3 ? 64 * (x / 2) + 16 * g + 8 * (x & 1) : 32 * x + 8 * g;
+      q[x].u = d < a.dim ? *reinterpret_cast<const u32x4*>(qp + d) : u32x4{0, 0, 0, 0};
+    }
+  };
+  load_queries(now);
+  start(now);
   for (;;) {
     const unsigned kvh = (unsigned)now.hx / head_tiles, ht = (unsigned)now.hx % head_tiles;
     const unsigned here = min(group - ht * kHeads, kHeads), head0 = kvh * group + ht * kHeads;
@@ -246,23 +273,13 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
     l = 0.f;
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
-    {
-      // columns past the last head are those of the last; their results are not kept
-      const uint16_t* qp = a.q.p + (size_t)now.seq * a.q.ts + (head0 + min((unsigned)hd, here - 1)) * a.q.hs;
-#pragma unroll
-      for (int x = 0; x < KS; ++x) {
-        const unsigned d = E4M3 ? 64 * (x / 2) + 16 * g + 8 * (x & 1) : 32 * x + 8 * g;
-        q[x].u = d < a.dim ? *reinterpret_cast<const u32x4*>(qp + d) : u32x4{0, 0, 0, 0};
-      }
-    }
-    wait_copies();                             // the queries are here (and the copies before them)
 #pragma unroll 1
     for (unsigned i = 0; i < now.count; ++i) {
     const int stage = i & 1, slot = i & 3;
     // the tile's copies are done when only the next one's are left
     if (i + 1 < now.count) asm volatile("s_waitcnt vmcnt(%0)" :: "n"(R::kCopies) : "memory");
     else wait_copies();
-    if (i + 2 < now.count) read_ids((slot + 2) & 3);
+    if (i + 2 < now.count) locate(now, i + 2, (slot + 2) & 3);
     const Keys tile = keys_of(now, i);
     const int keys = min(tile.end - tile.j0 - wave * STEP, STEP);   // of this wave's step
     if (keys > 0) {
@@ -283,6 +300,14 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
           const int r = 4 * g + (lane & 15) / 4, ch = 2 * d + (lane & 3) / 2;
 #pragma unroll
           for (int b = 0; b < NB; ++b) v[d].s[b] = read_tr16(lv + chunk_at<RB>(r + 16 * b, ch) + (lane & 1) * 8);
+        }
+      }
+      f32x4 scale_k[NB], scale_v[NB];
+      if constexpr (E4M3) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          scale_k[b] = *reinterpret_cast<const f32x4*>(lk + 2 * R::kKeys + (16 * b + 4 * g) * 4);
+          scale_v[b] = *reinterpret_cast<const f32x4*>(lk + 2 * R::kKeys + (STEP + 16 * b + 4 * g) * 4);
         }
       }
       f32x4 s[NB];
@@ -307,9 +332,8 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
               s[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k.b, q[2 * x + y].b, s[b], 0, 0, 0);
             }
           }
-          const f32x4 f = *reinterpret_cast<const f32x4*>(lk + 2 * R::kKeys + (16 * b + 4 * g) * 4);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) s[b][r] *= f[r];
+          for (int r = 0; r < 4; ++r) s[b][r] *= scale_k[b][r];
         } else {
 #pragma unroll
           for (int x = 0; x < KS; ++x) {
@@ -350,9 +374,12 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
       if constexpr (E4M3) {
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          const f32x4 f = *reinterpret_cast<const f32x4*>(lk + 2 * R::kKeys + (STEP + 16 * b + 4 * g) * 4);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) s[b][r] = 16 * b + 4 * g + r < keys ? s[b][r] * f[r] : 0.f;
+          for (int r = 0; r < 4; ++r) s[b][r] *= scale_v[b][r];
+          if (keys < STEP) {                   // (a masked place's scale may be no number)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s[b][r] = 16 * b + 4 * g + r < keys ? s[b][r] : 0.f;
+          }
         }
       }
       Frag8 p;
@@ -398,7 +425,10 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
     // the run's next sequence is on its way while this one's results are joined
     const Part s0 = now;
     const bool more = follow(now);
-    if (more) start(now);
+    if (more) {
+      load_queries(now);
+      start(now);
+    }
     {
       // the waves' results are one
       l = sum_of(swap32(sum_of(swap16(l))));
@@ -459,25 +489,32 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
           auto part_of = [&](unsigned i) { return parts + (size_t)((begin + i) * 2 + (i == 0 ? 1 : 0)) * kPart; };
           const unsigned h = oh, lane32 = t % 32, d = lane32 * 4;
           if (h < here) {
-            float M2 = AR_NEG_INF, L2 = 0.f;
-            for (unsigned i = lane32; i < count; i += 32) M2 = fmaxf(M2, part_of(i)[h]);
+            const unsigned col = h * DP + min(d, (unsigned)DP - 4);
+            f32x4 v[8];
+            // eight parts at a time are on their way at once
+            auto load_parts = [&](unsigned i0) {
+#pragma unroll
+              for (unsigned i = 0; i < 8; ++i)
+                v[i] = *reinterpret_cast<const f32x4*>(part_of(min(i0 + i, count - 1)) + 2 * kHeads + col);
+            };
+            // lane i's part: its maximum, its sum
+            float pm = AR_NEG_INF, pl = 0.f;
+            auto load_sums = [&](unsigned i) {
+              pm = i < count ? part_of(i)[h] : AR_NEG_INF;
+              pl = i < count ? part_of(i)[kHeads + h] : 0.f;
+            };
+            load_sums(lane32);
+            load_parts(0);
+            float M2 = pm, L2 = 0.f;
+            for (unsigned i = 32 + lane32; i < count; i += 32) M2 = fmaxf(M2, part_of(i)[h]);
 #pragma unroll
             for (int x = 1; x < 32; x *= 2) M2 = fmaxf(M2, __shfl_xor(M2, x));
             f32x4 acc = {0.f, 0.f, 0.f, 0.f};
             for (unsigned i0 = 0; i0 < count; i0 += 32) {
-              // lane i's part: what it weighs, and its sum
-              float w = 0.f, s = 0.f;
-              if (i0 + lane32 < count) {
-                const float pm = part_of(i0 + lane32)[h], pl = part_of(i0 + lane32)[kHeads + h];
-                w = pm == AR_NEG_INF ? 0.f : exp2_fast(pm - M2);
-                s = pm == AR_NEG_INF ? pl : pl * w;
-              }
-              // eight parts at a time are on their way at once
+              if (i0) load_sums(i0 + lane32);
+              const float w = pm == AR_NEG_INF ? 0.f : exp2_fast(pm - M2), s = pm == AR_NEG_INF ? pl : pl * w;
               for (unsigned i1 = 0; i1 < min(32u, count - i0); i1 += 8) {
-                f32x4 v[8];
-#pragma unroll
-                for (unsigned i = 0; i < 8; ++i)
-                  v[i] = *reinterpret_cast<const f32x4*>(part_of(min(i0 + i1 + i, count - 1)) + 2 * kHeads + h * DP + min(d, (unsigned)DP - 4));
+                if (i0 + i1) load_parts(i0 + i1);
 #pragma unroll
                 for (unsigned i = 0; i < 8; ++i) {
                   const int from = (int)((lane & 32) + i1 + i);
