@@ -220,18 +220,14 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
   auto fetch = [&](const Part& p, unsigned i, int stage, int slot) {
     const uint32_t to = lmine + stage * R::kStage;
     const char *kb = static_cast<const char*>(a.cache.k), *vb = static_cast<const char*>(a.cache.v);
-    auto rows = [&](auto whole) {
 #pragma unroll
-      for (int x = 0; x < COPIES; ++x) {
-        const uint32_t ch = chunk ^ (uint32_t)((swizzle_bytes<RB>(x * RPC + crow) ^ swizzle_bytes<RB>(crow)) * 16);
-        if (decltype(whole)::value || ch < a.dim * ES) {
-          stream16_to_lds(kb + from[x], to + x * 1024);
-          stream16_to_lds(vb + from[x], to + R::kKeys + x * 1024);
-        }
+    for (int x = 0; x < COPIES; ++x) {
+      const uint32_t ch = chunk ^ (uint32_t)((swizzle_bytes<RB>(x * RPC + crow) ^ swizzle_bytes<RB>(crow)) * 16);
+      if (ch < a.dim * ES) {
+        stream16_to_lds(kb + from[x], to + x * 1024);
+        stream16_to_lds(vb + from[x], to + R::kKeys + x * 1024);
       }
-    };
-    if (a.dim == DP) rows(std::true_type{});
-    else rows(std::false_type{});
+    }
     if constexpr (E4M3)
       copy4_to_lds((lane < 32 ? a.cache.k_scales : a.cache.v_scales) + from_scale, to + 2 * R::kKeys);
     fetch_ids(p, min(i + 2, p.count - 1), (slot + 2) & 3);
@@ -241,11 +237,10 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
     fetch_ids(p, 0, 0);
     fetch_ids(p, min(1u, p.count - 1), 1);
     wait_copies();
-    locate(p, 0, 0);
-    fetch(p, 0, 0, 0);
-    if (p.count > 1) {
-      locate(p, 1, 1);
-      fetch(p, 1, 1, 1);
+#pragma unroll 1
+    for (unsigned x = 0; x < min(2u, p.count); ++x) {
+      locate(p, x, (int)x);
+      fetch(p, x, (int)x, (int)x);
     }
   };
 
@@ -264,172 +259,17 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
       q[x].u = d < a.dim ? *reinterpret_cast<const u32x4*>(qp + d) : u32x4{0, 0, 0, 0};
     }
   };
-  load_queries(now);
-  start(now);
+  // A part's copies are under way while the one before it is joined.
+  Part s0 = now;                               // the part that is computed, or joined
+  bool more = true, done = false;
   for (;;) {
-    const unsigned kvh = (unsigned)now.hx / head_tiles, ht = (unsigned)now.hx % head_tiles;
-    const unsigned here = min(group - ht * kHeads, kHeads), head0 = kvh * group + ht * kHeads;
-    m = AR_NEG_INF;
-    l = 0.f;
-#pragma unroll
-    for (int d = 0; d < DT; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-    for (unsigned i = 0; i < now.count; ++i) {
-    const int stage = i & 1, slot = i & 3;
-    // the tile's copies are done when only the next one's are left
-    if (i + 1 < now.count) asm volatile("s_waitcnt vmcnt(%0)" :: "n"(R::kCopies) : "memory");
-    else wait_copies();
-    if (i + 2 < now.count) locate(now, i + 2, (slot + 2) & 3);
-    const Keys tile = keys_of(now, i);
-    const int keys = min(tile.end - tile.j0 - wave * STEP, STEP);   // of this wave's step
-    if (keys > 0) {
-      if (__any((lane & (STEP - 1)) < keys && ids[slot * kWave + (lane & (STEP - 1))] >= a.cache.pages))
-        l = __uint_as_float(0x7FC00000u);
-      const char* lk = mine + stage * R::kStage;
-      const uint32_t lv = lmine + stage * R::kStage + R::kKeys;
-      // values are read first: they arrive while the scores are formed
-      Frag8 v[DT];
-#pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        if constexpr (E4M3) {
-          const int e = (lane & 15) / 2, r = 4 * g + (e & 3) + (e >= 4 ? 16 : 0);
-          const i32x2 w = read_tr8(lv + chunk_at<RB>(r, d) + (lane & 1) * 8);
-          v[d].w[0] = (uint32_t)w[0];
-          v[d].w[1] = (uint32_t)w[1];
-        } else {
-          const int r = 4 * g + (lane & 15) / 4, ch = 2 * d + (lane & 3) / 2;
-#pragma unroll
-          for (int b = 0; b < NB; ++b) v[d].s[b] = read_tr16(lv + chunk_at<RB>(r + 16 * b, ch) + (lane & 1) * 8);
-        }
-      }
-      f32x4 scale_k[NB], scale_v[NB];
-      if constexpr (E4M3) {
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          scale_k[b] = *reinterpret_cast<const f32x4*>(lk + 2 * R::kKeys + (16 * b + 4 * g) * 4);
-          scale_v[b] = *reinterpret_cast<const f32x4*>(lk + 2 * R::kKeys + (STEP + 16 * b + 4 * g) * 4);
-        }
-      }
-      f32x4 s[NB];
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        s[b] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if constexpr (E4M3) {
-#pragma unroll
-          for (int x = 0; x < KS / 2; ++x) {
-            const u32x4 w = *reinterpret_cast<const u32x4*>(lk + chunk_at<RB>(16 * b + hd, 4 * x + g));
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              Frag8 k;
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                union { b16x2 b; uint32_t u; } lo, hi;
-                lo.b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[2 * y + e], 1.0f, false);
-                hi.b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[2 * y + e], 1.0f, true);
-                k.w[2 * e] = lo.u;
-                k.w[2 * e + 1] = hi.u;
-              }
-              s[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k.b, q[2 * x + y].b, s[b], 0, 0, 0);
-            }
-          }
-#pragma unroll
-          for (int r = 0; r < 4; ++r) s[b][r] *= scale_k[b][r];
-        } else {
-#pragma unroll
-          for (int x = 0; x < KS; ++x) {
-            Frag8 k;
-            k.u = *reinterpret_cast<const u32x4*>(lk + chunk_at<RB>(16 * b + hd, 4 * x + g));
-            s[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k.b, q[x].b, s[b], 0, 0, 0);
-          }
-        }
-      }
-      // register r of block b is key 16 b + 4 g + r of the step
-      if (keys < STEP) {
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) s[b][r] = 16 * b + 4 * g + r < keys ? s[b][r] : AR_NEG_INF;
-      }
-      float top = AR_NEG_INF;
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) top = fmaxf(top, s[b][r]);
-      top = max_of(swap32(max_of(swap16(top)))) * c;
-      if (__any(top > m + 8.0f)) {
-        const float up = fmaxf(m, top), f = m == AR_NEG_INF ? 1.0f : exp2_fast(m - up);
-        m = up;
-        l *= f;
-#pragma unroll
-        for (int d = 0; d < DT; ++d) o[d] *= f;
-      }
-      const float base = m == AR_NEG_INF ? 0.f : m;
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          s[b][r] = exp2_fast(__builtin_fmaf(s[b][r], c, -base));
-          l += s[b][r];
-        }
-      if constexpr (E4M3) {
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) s[b][r] *= scale_v[b][r];
-          if (keys < STEP) {                   // (a masked place's scale may be no number)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) s[b][r] = 16 * b + 4 * g + r < keys ? s[b][r] : 0.f;
-          }
-        }
-      }
-      Frag8 p;
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        p.w[2 * b] = cvt_bf16x2(s[b][0], s[b][1]);
-        p.w[2 * b + 1] = cvt_bf16x2(s[b][2], s[b][3]);
-      }
-      // whether element e of the lane's values is of a key of the step: 0
-      // times what a masked place holds must be 0
-      const int beyond = keys - 4 * g;         // of keys 4 g + ...; 16 less for the second four
-      if constexpr (E4M3) {
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          const i32x2 w = {(int)v[d].w[0], (int)v[d].w[1]};
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            union { b16x2 b; uint32_t u; } lo, hi;
-            lo.b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[x], 1.0f, false);
-            hi.b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[x], 1.0f, true);
-            v[d].w[2 * x] = lo.u;
-            v[d].w[2 * x + 1] = hi.u;
-          }
-        }
-      }
-      if (keys < STEP) {
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-          for (int e = 0; e < 4 * NB; ++e)
-            if ((e & 3) + (e >= 4 ? 16 : 0) >= beyond) v[d].w[e / 2] &= e & 1 ? 0xFFFFu : 0xFFFF0000u;
-      }
-#pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        if constexpr (NB == 2) o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[d].b, p.b, o[d], 0, 0, 0);
-        else o[d] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(v[d].s[0], p.s[0], o[d], 0, 0, 0);
-      }
-    }
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the stage has been read
-    if (i + 2 < now.count) fetch(now, i + 2, stage, (slot + 2) & 3);
-    }
-
-    // the run's next sequence is on its way while this one's results are joined
-    const Part s0 = now;
-    const bool more = follow(now);
     if (more) {
       load_queries(now);
       start(now);
     }
-    {
+    if (done) {
+      const unsigned kvh = (unsigned)s0.hx / head_tiles, ht = (unsigned)s0.hx % head_tiles;
+      const unsigned here = min(group - ht * kHeads, kHeads), head0 = kvh * group + ht * kHeads;
       // the waves' results are one
       l = sum_of(swap32(sum_of(swap16(l))));
       if (lane < 16) {
@@ -543,6 +383,162 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
       }
     }
     if (!more) break;
+    m = AR_NEG_INF;
+    l = 0.f;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (unsigned i = 0; i < now.count; ++i) {
+      const int stage = i & 1, slot = i & 3;
+      // the tile's copies are done when only the next one's are left
+      if (i + 1 < now.count) asm volatile("s_waitcnt vmcnt(%0)" :: "n"(R::kCopies) : "memory");
+      else wait_copies();
+      if (i + 2 < now.count) locate(now, i + 2, (slot + 2) & 3);
+      const Keys tile = keys_of(now, i);
+      const int keys = min(tile.end - tile.j0 - wave * STEP, STEP);   // of this wave's step
+      if (keys > 0) {
+        if (__any((lane & (STEP - 1)) < keys && ids[slot * kWave + (lane & (STEP - 1))] >= a.cache.pages))
+          l = __uint_as_float(0x7FC00000u);
+        const char* lk = mine + stage * R::kStage;
+        const uint32_t lv = lmine + stage * R::kStage + R::kKeys;
+        // values are read first: they arrive while the scores are formed
+        Frag8 v[DT];
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          if constexpr (E4M3) {
+            const int e = (lane & 15) / 2, r = 4 * g + (e & 3) + (e >= 4 ? 16 : 0);
+            const i32x2 w = read_tr8(lv + chunk_at<RB>(r, d) + (lane & 1) * 8);
+            v[d].w[0] = (uint32_t)w[0];
+            v[d].w[1] = (uint32_t)w[1];
+          } else {
+            const int r = 4 * g + (lane & 15) / 4, ch = 2 * d + (lane & 3) / 2;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) v[d].s[b] = read_tr16(lv + chunk_at<RB>(r + 16 * b, ch) + (lane & 1) * 8);
+          }
+        }
+        f32x4 scale_k[NB], scale_v[NB];
+        if constexpr (E4M3) {
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            scale_k[b] = *reinterpret_cast<const f32x4*>(lk + 2 * R::kKeys + (16 * b + 4 * g) * 4);
+            scale_v[b] = *reinterpret_cast<const f32x4*>(lk + 2 * R::kKeys + (STEP + 16 * b + 4 * g) * 4);
+          }
+        }
+        f32x4 s[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          s[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+          if constexpr (E4M3) {
+#pragma unroll
+            for (int x = 0; x < KS / 2; ++x) {
+              const u32x4 w = *reinterpret_cast<const u32x4*>(lk + chunk_at<RB>(16 * b + hd, 4 * x + g));
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                Frag8 k;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  union { b16x2 b; uint32_t u; } lo, hi;
+                  lo.b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[2 * y + e], 1.0f, false);
+                  hi.b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[2 * y + e], 1.0f, true);
+                  k.w[2 * e] = lo.u;
+                  k.w[2 * e + 1] = hi.u;
+                }
+                s[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k.b, q[2 * x + y].b, s[b], 0, 0, 0);
+              }
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s[b][r] *= scale_k[b][r];
+          } else {
+#pragma unroll
+            for (int x = 0; x < KS; ++x) {
+              Frag8 k;
+              k.u = *reinterpret_cast<const u32x4*>(lk + chunk_at<RB>(16 * b + hd, 4 * x + g));
+              s[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k.b, q[x].b, s[b], 0, 0, 0);
+            }
+          }
+        }
+        // register r of block b is key 16 b + 4 g + r of the step
+        if (keys < STEP) {
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s[b][r] = 16 * b + 4 * g + r < keys ? s[b][r] : AR_NEG_INF;
+        }
+        float top = AR_NEG_INF;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) top = fmaxf(top, s[b][r]);
+        top = max_of(swap32(max_of(swap16(top)))) * c;
+        if (__any(top > m + 8.0f)) {
+          const float up = fmaxf(m, top), f = m == AR_NEG_INF ? 1.0f : exp2_fast(m - up);
+          m = up;
+          l *= f;
+#pragma unroll
+          for (int d = 0; d < DT; ++d) o[d] *= f;
+        }
+        const float base = m == AR_NEG_INF ? 0.f : m;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            s[b][r] = exp2_fast(__builtin_fmaf(s[b][r], c, -base));
+            l += s[b][r];
+          }
+        if constexpr (E4M3) {
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s[b][r] *= scale_v[b][r];
+            if (keys < STEP) {                   // (a masked place's scale may be no number)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) s[b][r] = 16 * b + 4 * g + r < keys ? s[b][r] : 0.f;
+            }
+          }
+        }
+        Frag8 p;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          p.w[2 * b] = cvt_bf16x2(s[b][0], s[b][1]);
+          p.w[2 * b + 1] = cvt_bf16x2(s[b][2], s[b][3]);
+        }
+        // whether element e of the lane's values is of a key of the step: 0
+        // times what a masked place holds must be 0
+        const int beyond = keys - 4 * g;         // of keys 4 g + ...; 16 less for the second four
+        if constexpr (E4M3) {
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            const i32x2 w = {(int)v[d].w[0], (int)v[d].w[1]};
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              union { b16x2 b; uint32_t u; } lo, hi;
+              lo.b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[x], 1.0f, false);
+              hi.b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[x], 1.0f, true);
+              v[d].w[2 * x] = lo.u;
+              v[d].w[2 * x + 1] = hi.u;
+            }
+          }
+        }
+        if (keys < STEP) {
+#pragma unroll
+          for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int e = 0; e < 4 * NB; ++e)
+              if ((e & 3) + (e >= 4 ? 16 : 0) >= beyond) v[d].w[e / 2] &= e & 1 ? 0xFFFFu : 0xFFFF0000u;
+        }
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          if constexpr (NB == 2) o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[d].b, p.b, o[d], 0, 0, 0);
+          else o[d] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(v[d].s[0], p.s[0], o[d], 0, 0, 0);
+        }
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the stage has been read
+      if (i + 2 < now.count) fetch(now, i + 2, stage, (slot + 2) & 3);
+    }
+
+    s0 = now;
+    done = true;
+    more = follow(now);
   }
 }
 
