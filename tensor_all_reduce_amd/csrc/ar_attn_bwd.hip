@@ -22,26 +22,6 @@ constexpr int kWavesK = 8, kKeysB = kWavesK / 2 * 32;  // keys of a workgroup, e
 constexpr int kBT = 64;                            // rows of the other side at a time
 constexpr unsigned kFar = 2048;                    // queries of a run
 
-// delta of every query and head, 16 lanes each: [hq][rows_q]
-__global__ __launch_bounds__(256) void k_attn_delta(HeadRows out, HeadRows d_out, float* delta, unsigned rows, unsigned hq,
-                                                    unsigned dim) {
-  const size_t at = (size_t)blockIdx.x * 16 + threadIdx.x / 16;
-  const unsigned row = (unsigned)(at / hq), head = (unsigned)(at % hq), i = threadIdx.x % 16;
-  float sum = 0.f;
-  if (row < rows && i * 8 < dim) {
-    const u32x4 x = *reinterpret_cast<const u32x4*>(out.p + (size_t)row * out.ts + head * out.hs + i * 8);
-    const u32x4 y = *reinterpret_cast<const u32x4*>(d_out.p + (size_t)row * d_out.ts + head * d_out.hs + i * 8);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      sum = __builtin_fmaf(lo_f32(x[e]), lo_f32(y[e]), sum);
-      sum = __builtin_fmaf(hi_f32(x[e]), hi_f32(y[e]), sum);
-    }
-  }
-#pragma unroll
-  for (int d = 1; d < 16; d *= 2) sum += __shfl_xor(sum, d);
-  if (row < rows && i == 0) delta[(size_t)head * rows + row] = sum;
-}
-
 __device__ __forceinline__ void zero_lds(char* lds, int bytes) {
   for (int o = threadIdx.x * 16; o < bytes; o += blockDim.x * 16) *reinterpret_cast<u32x4*>(lds + o) = u32x4{0, 0, 0, 0};
   __syncthreads();
@@ -93,9 +73,17 @@ __device__ __forceinline__ void store_row(float* p, const f32x16 (&o)[DT], int h
 // lse, of a query without keys 0.
 __device__ __forceinline__ float finite_lse(float lse) { return lse == AR_NEG_INF ? 0.f : lse; }
 
-// dQ: 256 queries of one head, 64 keys at a time.
-template <int DP>
-__device__ __forceinline__ void queries_pass(const AttnBwdArgs& b, const float* delta, unsigned block, char* lds) {
+// dQ: 256 queries of one head, 64 keys at a time.  DELTA: delta instead.
+//
+// delta is rowsum(d_out * out) from the out that was rounded to bf16, and its
+// error reaches all of a row's dS alike.  Among many keys that is little beside
+// dS' own rounding, among few it is most of the error (8 keys: dQ and dK 0.0034
+// off, where their rounding alone leaves 0.0017).  So for queries that see up
+// to kFew keys delta is formed from its definition, the sum of P dP, which
+// costs the first two products once more.
+constexpr int kFew = 256;
+template <int DP, bool DELTA>
+__device__ __forceinline__ void queries_pass(const AttnBwdArgs& b, float* delta, unsigned block, char* lds) {
   constexpr int KS = DP / 16, DT = DP / 32;
   constexpr uint32_t kTile = kBT * DP * 2;
   const AttnArgs& a = b.f;
@@ -109,6 +97,36 @@ __device__ __forceinline__ void queries_pass(const AttnBwdArgs& b, const float* 
   const int shift = (int)rk.count - (int)rq.count, last = (int)rq.count - 1;
   const int p0 = shift + (int)tile.row, p1 = shift + min((int)tile.row + kQueries - 1, last);
   const KeyRange keys = key_range(p0, p1, a.window, a.sinks, kBT);
+  if constexpr (DELTA) {
+    if ((long long)p1 + 1 > kFew && (long long)a.window + a.sinks > kFew) {
+      // 16 lanes a row, eight rows of a lane on their way at once
+      const unsigned i = t % 16, end = min(tile.row + kQueries, rq.count);
+      constexpr int N = kQueries / (kWavesQ * 4);
+      u32x4 x[N], y[N];
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const size_t at = rq.first + min(tile.row + t / 16 + n * kWavesQ * 4, end - 1);
+        const unsigned d = min(i * 8, a.dim - 8);
+        x[n] = *reinterpret_cast<const u32x4*>(b.out.p + at * b.out.ts + head * b.out.hs + d);
+        y[n] = *reinterpret_cast<const u32x4*>(b.d_out.p + at * b.d_out.ts + head * b.d_out.hs + d);
+      }
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const unsigned r = tile.row + t / 16 + n * kWavesQ * 4;
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sum = __builtin_fmaf(lo_f32(x[n][e]), lo_f32(y[n][e]), sum);
+          sum = __builtin_fmaf(hi_f32(x[n][e]), hi_f32(y[n][e]), sum);
+        }
+        sum = i * 8 < a.dim ? sum : 0.f;
+#pragma unroll
+        for (int d = 1; d < 16; d *= 2) sum += __shfl_xor(sum, d);
+        if (i == 0 && r < end) delta[(size_t)head * a.rows_q + rq.first + r] = sum;
+      }
+      return;
+    }
+  }
   const int row = (int)tile.row + wave * 32 + col, p = shift + min(row, last), start = window_start(p, a.window);
   const int wp0 = shift + min((int)tile.row + wave * 32, last), wp1 = shift + min((int)tile.row + wave * 32 + 31, last);
   const int wstart0 = window_start(wp0, a.window), wstart1 = window_start(wp1, a.window);
@@ -118,7 +136,7 @@ __device__ __forceinline__ void queries_pass(const AttnBwdArgs& b, const float* 
   Frag8 q[KS], g[KS];
   load_row(q, a.q.p + at * a.q.ts + head * a.q.hs, hh, a.dim);
   load_row(g, b.d_out.p + at * b.d_out.ts + head * b.d_out.hs, hh, a.dim);
-  const float lse2 = finite_lse(a.lse[at * a.lse_ts + head * a.lse_hs]) * kLog2e, dl = delta[(size_t)head * a.rows_q + at];
+  const float lse2 = finite_lse(a.lse[at * a.lse_ts + head * a.lse_hs]) * kLog2e, dl = DELTA ? 0.f : delta[(size_t)head * a.rows_q + at];
   const float c = a.scale * kLog2e;
   const uint16_t* kb = a.k.p + (size_t)rk.first * a.k.ts + kvh * a.k.hs;
   const uint16_t* vb = a.v.p + (size_t)rk.first * a.v.ts + kvh * a.v.hs;
@@ -130,6 +148,7 @@ __device__ __forceinline__ void queries_pass(const AttnBwdArgs& b, const float* 
   };
   f32x16 o[DT];
   clear(o);
+  float sum = 0.f;                             // DELTA: of P dP
   if (keys.steps > 0) copy(0, 0);
   for (int n = 0; n < keys.steps; ++n) {
     const int buf = n & 1;
@@ -148,7 +167,7 @@ __device__ __forceinline__ void queries_pass(const AttnBwdArgs& b, const float* 
       for (int r0 = 0; r0 < kBT; r0 += 32) {
         const LaneAddr<DP> from = {at_k, (uint32_t)(r0 * DP * 2)};
         // products 0 .. KS - 1: scores; then dP; then dQ
-        constexpr int ALL = 2 * KS + 2 * DT, AHEAD = 4;
+        constexpr int ALL = 2 * KS + (DELTA ? 0 : 2 * DT), AHEAD = 4;
         Frag8 f[AHEAD], pd[2];
         f32x16 s, d;
 #pragma unroll
@@ -185,7 +204,8 @@ __device__ __forceinline__ void queries_pass(const AttnBwdArgs& b, const float* 
                 y[e] = s[r + e] * d[r + e];
                 if (MASK) y[e] = view.has(r0 + 8 * (r / 4) + r % 4 + e) ? y[e] : 0.f;
               }
-              pd[r / 8].w[r % 8 / 2] = cvt_bf16x2(y[0], y[1]);
+              if constexpr (DELTA) sum += y[0] + y[1];
+              else pd[r / 8].w[r % 8 / 2] = cvt_bf16x2(y[0], y[1]);
             }
           }
           keep_order();
@@ -195,7 +215,18 @@ __device__ __forceinline__ void queries_pass(const AttnBwdArgs& b, const float* 
     if (whole) tile_step(std::false_type{});
     else tile_step(std::true_type{});
   }
-  if (row <= last) store_row(b.dq.p + at * b.dq.ts + head * b.dq.hs, o, a.scale, hh, a.dim);
+  if constexpr (DELTA) {
+    sum += __shfl_xor(sum, 32);
+    if (row <= last && hh == 0) delta[(size_t)head * a.rows_q + at] = sum;
+  } else if (row <= last) {
+    store_row(b.dq.p + at * b.dq.ts + head * b.dq.hs, o, a.scale, hh, a.dim);
+  }
+}
+
+template <int DP>
+__global__ __launch_bounds__(kWavesQ * 64, 2) void k_attn_delta(AttnBwdArgs b, float* delta) {
+  __shared__ __align__(1024) char lds[4 * kBT * DP * 2];
+  queries_pass<DP, true>(b, delta, blockIdx.x, lds);
 }
 
 // The queries that a tile of keys meets in its own pass, and of a tile with
@@ -445,12 +476,12 @@ __device__ __forceinline__ void keys_pass(const AttnBwdArgs& b, const float* del
 // Both passes in one launch, the keys' first, whose workgroups have more to do:
 // short batches wait for one of them only, and long ones end together.
 template <int DP>
-__global__ __launch_bounds__(kWavesQ * 64, 2) void k_attn_bwd(AttnBwdArgs b, const float* delta, KeySums sums, unsigned key_blocks) {
+__global__ __launch_bounds__(kWavesQ * 64, 2) void k_attn_bwd(AttnBwdArgs b, float* delta, KeySums sums, unsigned key_blocks) {
   static_assert(kWavesQ == kWavesK, "both passes have one workgroup size");
   __shared__ __align__(1024) char lds[8 * kBT * DP * 2];
   __shared__ __align__(16) float lrow[2][2][kBT];
   if (blockIdx.x < key_blocks) keys_pass<DP>(b, delta, sums, blockIdx.x, lds, lrow);
-  else queries_pass<DP>(b, delta, blockIdx.x - key_blocks, lds);
+  else queries_pass<DP, false>(b, delta, blockIdx.x - key_blocks, lds);
 }
 
 // Joins the sums of a key's query heads and runs: a workgroup takes 8 rows of
@@ -530,8 +561,7 @@ hipError_t launch(const Launch& L, const AttnBwdArgs& b) {
   float* delta = static_cast<float*>(b.workspace);
   hipError_t e;
   if (a.rows_q) {
-    e = launch_k(k_attn_delta, dim3((unsigned)cdiv((size_t)a.rows_q * a.hq, 16)), dim3(256), 0, L.stream, b.out, b.d_out, delta,
-                 a.rows_q, a.hq, a.dim);
+    e = launch_k(k_attn_delta<DP>, dim3((a.rows_q / kQueries + a.seqs) * a.hq), dim3(kWavesQ * 64), 0, L.stream, b, delta);
     if (e != hipSuccess) return e;
   }
   const KeySums sums{room.near ? delta + room.delta : nullptr, room.far ? delta + room.delta + room.near : nullptr,
@@ -558,7 +588,7 @@ bool attn_bwd_fits(size_t rows_q, size_t rows_k, size_t seqs, size_t hq, size_t 
   const Room r = room_of(rows_q, rows_k, hq, hkv, dim, window, sinks);
   const size_t blocks = ((size_t)r.runs * r.sink_tiles + rows_k / kKeysB + seqs) * r.sets + (rows_q / kQueries + seqs) * hq;
   const size_t join = (rows_k / kJoinRows + seqs) * hkv * 2;
-  return (rows_q * hq) / 16 < 0x7FFFFFFF && blocks <= 0x7FFFFFFF && join <= 0x7FFFFFFF;
+  return blocks <= 0x7FFFFFFF && join <= 0x7FFFFFFF;
 }
 
 hipError_t launch_attn_bwd(const Launch& L, const AttnBwdArgs& b) {

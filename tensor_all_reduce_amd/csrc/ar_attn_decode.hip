@@ -496,12 +496,16 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
             }
           }
         }
-        Frag8 p;
+        // as two bf16 numbers each, 2^-17 off: the matrix cores have the time
+        Frag8 p, rest;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          p.w[2 * b] = cvt_bf16x2(s[b][0], s[b][1]);
-          p.w[2 * b + 1] = cvt_bf16x2(s[b][2], s[b][3]);
-        }
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int r = 0; r < 4; r += 2) {
+            const uint32_t w = cvt_bf16x2(s[b][r], s[b][r + 1]);
+            p.w[2 * b + r / 2] = w;
+            rest.w[2 * b + r / 2] = cvt_bf16x2(s[b][r] - lo_f32(w), s[b][r + 1] - hi_f32(w));
+          }
         // whether element e of the lane's values is of a key of the step: 0
         // times what a masked place holds must be 0
         const int beyond = keys - 4 * g;         // of keys 4 g + ...; 16 less for the second four
@@ -528,8 +532,18 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
         }
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-          if constexpr (NB == 2) o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[d].b, p.b, o[d], 0, 0, 0);
-          else o[d] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(v[d].s[0], p.s[0], o[d], 0, 0, 0);
+          if constexpr (NB == 2) {
+            o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[d].b, p.b, o[d], 0, 0, 0);
+            o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[d].b, rest.b, o[d], 0, 0, 0);
+          } else {
+            // both in one: the second four of a lane's keys are the first again
+            Frag8 twice;
+            twice.s[0] = twice.s[1] = v[d].s[0];
+            Frag8 both;
+            both.s[0] = p.s[0];
+            both.s[1] = rest.s[0];
+            o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(twice.b, both.b, o[d], 0, 0, 0);
+          }
         }
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the stage has been read
