@@ -9,6 +9,15 @@
 // maxima, sums and results are binary32; the softmax's numerators become bf16
 // for their product with the values, 2^-9 of each, which is what the rounding
 // of the values' own sum to bf16 costs once more.
+//
+// Bound by the matrix cores and, beside them, the softmax's arithmetic: of a
+// tile of 64 keys a wave has 32 products of 32 cycles and about 240 vector
+// instructions of 4, of which two waves a SIMD overlap a part.  Operands are
+// read from LDS four products ahead, in a fixed order, so that nothing is
+// spilled: a reload would wait for the copies under way, which share its
+// counter.  16384 tokens, 64 heads of 128 on 8, causal: 4220 us, 1.04 PFLOP/s
+// (order left to the compiler 4932, one spilled register in the loop 4700; a
+// third tile of LDS, wave priorities and 128 queries a workgroup within 4%).
 #include "ar_attn.hpp"
 
 namespace ar {

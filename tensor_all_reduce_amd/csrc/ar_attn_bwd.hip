@@ -8,10 +8,15 @@
 // dP, dV, dK).  A single pass would need five products, but sums of dQ that
 // many workgroups add to, in no order.
 //
-// For keys, each query head is a workgroup's work, and its sums are joined
-// over the heads of a key head afterwards.  The first keys of a sequence that
-// all queries see (sinks) have their far queries cut into runs, joined there
-// too.
+// For keys, a workgroup takes some of a key head's query heads, and where that
+// is not all of them their sums are joined afterwards.  The first keys of a
+// sequence that all queries see (sinks) have their far queries cut into runs,
+// joined there too.
+//
+// Bound by the matrix cores.  2 x 4096 tokens, 64 heads of 128 on 8, causal:
+// 2010 us for both passes, 0.96 PFLOP/s of their seven products (the
+// queries' alone 800, the keys' 1190); delta 74, of which the read of out and
+// d_out is 42.
 #include "ar_attn.hpp"
 
 namespace ar {

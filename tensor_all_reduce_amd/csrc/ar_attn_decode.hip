@@ -16,6 +16,12 @@
 // ahead: 64 to 128 KiB a CU are on their way, which is what its share of the
 // memory's rate takes over the memory's latency.  The page numbers of a step
 // come the same way, two steps before its keys.
+//
+// 48 sequences of 111 to 16384 keys, 8 key heads of 128 in bf16: 122 us, 5.3
+// TB/s; 8 of 120k to 131k in E4M3 386 us, 5.5.  Kept for what they gave there:
+// eight waves instead of four (171 -> 156 and 750 -> 497 us), one loop a
+// sequence (142 -> 134, 475 -> 458), copies past the caches (134 -> 122, 458
+// -> 402), ends of sequences counted in the spread (156 -> 142).
 #include "ar_attn.hpp"
 
 namespace ar {

@@ -59,6 +59,86 @@ def test_more_or_fewer_queries_than_keys(window, sinks):
     assert bool((got["lse"][5:9] == -math.inf).all())
 
 
+@pytest.mark.parametrize("hq,hkv,dim", [(2, 2, 16), (4, 1, 32), (3, 3, 48), (2, 1, 96), (8, 2, 112), (33, 1, 64)])
+def test_head_sizes(hq, hkv, dim):
+    note(f"heads {hq}/{hkv}x{dim}")
+    g, lengths = gen(dim), [65, 7, 130]
+    n = sum(lengths)
+    q, k, v, go = (heads(g, n, h, dim) for h in (hq, hkv, hkv, hq))
+    offs = cu(lengths)
+    check(step(q, k, v, offs, offs, go, 50, 3), q, k, v, offs, offs, go, 50, 3)
+
+
+@pytest.mark.parametrize("std", [1e-3, 8.0])
+def test_flat_and_steep_softmaxes(std):
+    """Scores that hardly differ, and such that one key takes nearly all."""
+    g, lengths = gen(24), [300, 5]
+    q, k = heads(g, 305, 4, 64, std), heads(g, 305, 2, 64, std)
+    v, go = heads(g, 305, 2, 64), heads(g, 305, 4, 64)
+    offs = cu(lengths)
+    check(step(q, k, v, offs, offs, go), q, k, v, offs, offs, go)
+
+
+@pytest.mark.parametrize("source", ["rows", "pages", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128, 80])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (300, 70)])
+def test_enough_for_wide_workgroups(dim, source, window, sinks):
+    """So many queries and heads that a workgroup takes 256 of them."""
+    note(f"wide {source} {dim} window {window}")
+    g, new, hq, hkv, past = gen(dim), [2043, 1, 300], 64, 4, 37
+    n, offs = sum(new), cu(new)
+    assert n * hq >= 2 * 256 * 256                  # of 256 compute units
+    q = heads(g, n, hq, dim)
+    out, lse = torch.empty_like(q), torch.empty(n, hq, device=DEV)
+    if source == "rows":
+        total = new
+        k, v = heads(g, n, hkv, dim), heads(g, n, hkv, dim)
+        tar.ar_attn(q, k, v, offs, offs, out, window=window, sinks=sinks, lse=lse)
+    else:
+        total = [m + past for m in new]
+        table, pages = tables(g, total, 48)
+        cache = filled(g, pages, 48, hkv, dim, source == "e4m3")
+        lens = torch.tensor(total, device=DEV, dtype=torch.int32)
+        tar.ar_attn_paged(q, cache, table, lens, offs, out, window=window, sinks=sinks, lse=lse)
+    torch.cuda.synchronize()
+    for i in range(3):
+        a = slice(int(offs[i]), int(offs[i + 1]))
+        kk, vv = (k[a], v[a]) if source == "rows" else ref.paged(cache, table[i], total[i])
+        for h in (0, 17, 63):
+            want = ref.attend(q[a, h], kk[:, h // 16], vv[:, h // 16], dim ** -0.5, window, sinks)
+            ref.close(out[a, h], want["out"], want["out_t"], f"out of sequence {i}, head {h}")
+            ref.close(lse[a, h], want["lse"], want["lse_t"], f"lse of sequence {i}, head {h}")
+
+
+def test_several_heads_of_one_workgroup():
+    """So many keys that a workgroup of the keys' pass takes several heads."""
+    note("several heads")
+    g, lengths, hq, hkv = gen(31), [16500, 200], 8, 4
+    n, offs = sum(lengths), cu(lengths)
+    q, k, v, go = (heads(g, n, h, 64) for h in (hq, hkv, hkv, hq))
+    got = step(q, k, v, offs, offs, go, 500, 2)
+    # the short sequence whole, of the long one the last keys (its window's reach) and rows
+    a = slice(16500, 16700)
+    want = ref.ragged(q[a], k[a], v[a], [0, 200], [0, 200], 0.125, 500, 2, go[a])
+    for x, y in got.items():
+        ref.close(y[a], want[x], want[x + "_t"], x)
+    for h in (0, 7):
+        one = ref.attend(q[:16500, h], k[:16500, h // 2], v[:16500, h // 2], 0.125, 500, 2)
+        ref.close(got["out"][:16500, h], one["out"], one["out_t"], "out")
+    # all gradients of one key head
+    dk, dv, tk, tv = (torch.zeros(16500, 64, device=DEV, dtype=torch.float64) for _ in range(4))
+    for h in (2, 3):
+        w = ref.attend(q[:16500, h], k[:16500, 1], v[:16500, 1], 0.125, 500, 2, go[:16500, h])
+        ref.close(got["dq"][:16500, h], w["dq"], w["dq_t"], "dq")
+        dk += w["dk"]
+        dv += w["dv"]
+        tk += w["dk_t"]
+        tv += w["dv_t"]
+        del w
+    ref.close(got["dk"][:16500, 1], dk, tk + (ref.U + 2 * ref.E) * dk.abs(), "dk")
+    ref.close(got["dv"][:16500, 1], dv, tv + (ref.U + 2 * ref.E) * dv.abs(), "dv")
+
+
 def test_no_rows_at_all():
     q, k = heads(gen(1), 0, 2, 64), heads(gen(1), 3, 1, 64)
     got = step(q, k, k.clone(), cu([0]), cu([3]), q)
