@@ -25,15 +25,20 @@ namespace {
 
 constexpr int kBN = 64;  // keys of a tile
 
-template <int DP, int NW, KeySource SRC>
+// NW waves; KG 2: two halves of them have the same queries and every other tile
+// of keys each, in LDS of their own, and are joined at the end.
+template <int DP, int NW, int KG, KeySource SRC>
 __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
-  constexpr int BM = NW * 32, KS = DP / 16, DT = DP / 32;
+  constexpr int NQ = NW / KG, BM = NQ * 32, KS = DP / 16, DT = DP / 32;
   constexpr uint32_t kTile = kBN * DP * 2;     // bytes of a tile of keys, or of values
-  __shared__ __align__(1024) char lds[4 * kTile];            // keys, values; keys, values
-  __shared__ __align__(16) float lscale[SRC == kKeyPagesE4M3 ? 4 * kBN : 4];  // their scales
+  __shared__ __align__(1024) char all_lds[KG * 4 * kTile];   // keys, values; keys, values
+  __shared__ __align__(16) float all_scales[SRC == kKeyPagesE4M3 ? KG * 4 * kBN : 4];  // their scales
   __shared__ int lflag[2];
-  const int t = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(t / kWave);
+  const int lane = lane_id(), part = KG == 1 ? 0 : uniform(threadIdx.x / (NQ * kWave));   // the wave's half
+  const int t = threadIdx.x - part * NQ * kWave, wave = uniform(t / kWave);               // in its half
   const int col = lane & 31, hh = lane >> 5;
+  char* const lds = all_lds + part * 4 * kTile;
+  float* const lscale = all_scales + (SRC == kKeyPagesE4M3 ? part * 4 * kBN : 0);
 
   // queries of one tile and, if there are eight heads of keys, those that
   // share keys on one XCD
@@ -72,20 +77,20 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
   const uint32_t lbase = lds_addr(lds);
 
   if (a.dim < DP) {   // places that no copy fills
-    for (uint32_t o = t * 16; o < 4 * kTile; o += NW * 64 * 16) *reinterpret_cast<u32x4*>(lds + o) = u32x4{0, 0, 0, 0};
+    for (uint32_t o = t * 16; o < 4 * kTile; o += NQ * 64 * 16) *reinterpret_cast<u32x4*>(lds + o) = u32x4{0, 0, 0, 0};
     __syncthreads();
   }
 
   unsigned bad = 0;                            // a page number out of range was met
-  const TileCopy<DP, NW> copy_rows(a.k.ts, a.v.ts, a.dim, wave, lane);
+  const TileCopy<DP, NQ> copy_rows(a.k.ts, a.v.ts, a.dim, wave, lane);
   const uint16_t *kb = a.k.p + (size_t)k_first * a.k.ts + kvh * a.k.hs, *vb = a.v.p + (size_t)k_first * a.v.ts + kvh * a.v.hs;
   // Pages: the numbers of a tile's pages are read one tile before its keys.
-  constexpr int ALL = kBN * DP / 16, CHUNKS = SRC == kKeyPagesE4M3 ? (ALL + NW * 64 - 1) / (NW * 64) : 1;  // of 16 codes
+  constexpr int ALL = kBN * DP / 16, CHUNKS = SRC == kKeyPagesE4M3 ? (ALL + NQ * 64 - 1) / (NQ * 64) : 1;  // of 16 codes
   constexpr int IDS = SRC == kKeyPagesE4M3 ? CHUNKS + 1 : copy_rows.COPIES;
   unsigned ids[IDS];
   auto id_row = [&](int i) {                   // the tile's row that number i is for
-    if constexpr (SRC == kKeyPagesE4M3) return i < CHUNKS ? (i * NW * 64 + t) / (DP / 16) : t % kBN;
-    else return i * NW * copy_rows.RPC + copy_rows.row;
+    if constexpr (SRC == kKeyPagesE4M3) return i < CHUNKS ? (i * NQ * 64 + t) / (DP / 16) : t % kBN;
+    else return i * NQ * copy_rows.RPC + copy_rows.row;
   };
   auto look_up = [&](int n) {
     if constexpr (SRC != kKeyRows) {
@@ -112,9 +117,10 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
     } else {
 #pragma unroll
       for (int i = 0; i < copy_rows.COPIES; ++i) {
-        const size_t at = token(k, i * NW * copy_rows.RPC + copy_rows.row, ids[SRC == kKeyPages ? i : 0], a.cache.page, a.cache.ts) + kvh * a.cache.hs;
+        const int r = i * NQ * copy_rows.RPC + copy_rows.row;
+        const size_t at = token(k, r, ids[SRC == kKeyPages ? i : 0], a.cache.page, a.cache.ts) + kvh * a.cache.hs;
         if (copy_rows.on) {
-          const uint32_t here = to + (i * NW + wave) * 1024;
+          const uint32_t here = to + (i * NQ + wave) * 1024;
           copy16_to_lds(reinterpret_cast<const char*>(static_cast<const uint16_t*>(a.cache.k) + at) + copy_rows.chunk, here);
           copy16_to_lds(reinterpret_cast<const char*>(static_cast<const uint16_t*>(a.cache.v) + at) + copy_rows.chunk, here + kTile);
         }
@@ -128,7 +134,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
     const KeyStep k = key_step(keys, n, kBN);
 #pragma unroll
     for (int i = 0; i < CHUNKS; ++i) {
-      const int at = i * NW * 64 + t, r = at / (DP / 16), ch = at % (DP / 16);
+      const int at = i * NQ * 64 + t, r = at / (DP / 16), ch = at % (DP / 16);
       const size_t o = token(k, r, ids[SRC == kKeyPagesE4M3 ? i : 0], a.cache.page, a.cache.ts) + kvh * a.cache.hs + ch * 16;
       ck[i] = cv[i] = u32x4{0, 0, 0, 0};
       if (at < ALL && ch * 16 < (int)a.dim) {
@@ -142,7 +148,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
   auto put = [&](int buf) {
 #pragma unroll
     for (int i = 0; i < CHUNKS; ++i) {
-      const int at = i * NW * 64 + t, r = at / (DP / 16), ch = at % (DP / 16);
+      const int at = i * NQ * 64 + t, r = at / (DP / 16), ch = at % (DP / 16);
       if (at >= ALL) continue;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -178,21 +184,25 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
     for (int d = 0; d < DT; ++d)
 #pragma unroll
       for (int r = 0; r < 16; ++r) o[d][r] = 0.f;
-    if (keys.steps > 0) {
-      look_up(0);
-      if constexpr (SRC == kKeyPagesE4M3) fetch(0);
-      else copy(0, 0);
-      if (keys.steps > 1) look_up(1);
+    if (part < keys.steps) {
+      look_up(part);
+      if constexpr (SRC == kKeyPagesE4M3) fetch(part);
+      else copy(part, 0);
+      if (part + KG < keys.steps) look_up(part + KG);
     }
-    for (int n = 0; n < keys.steps; ++n) {
-      const int buf = n & 1;
-      if constexpr (SRC == kKeyPagesE4M3) put(buf);
-      else wait_copies();
+    for (int i = 0; i * KG < keys.steps; ++i) {
+      const int buf = i & 1, n = i * KG + part;
+      const bool mine = KG == 1 || n < keys.steps;   // the second half may have one tile less
+      if constexpr (SRC == kKeyPagesE4M3) {
+        if (mine) put(buf);
+      } else {
+        wait_copies();
+      }
       __syncthreads();
-      if (n + 1 < keys.steps) {
-        if constexpr (SRC == kKeyPagesE4M3) fetch(n + 1);
-        else copy(n + 1, buf ^ 1);
-        if (n + 2 < keys.steps) look_up(n + 2);
+      if (n + KG < keys.steps) {
+        if constexpr (SRC == kKeyPagesE4M3) fetch(n + KG);
+        else copy(n + KG, buf ^ 1);
+        if (n + 2 * KG < keys.steps) look_up(n + 2 * KG);
       }
       const KeyStep k = key_step(keys, n, kBN);
       const int j0 = k.j0;
@@ -201,7 +211,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
       if (care) {
         char* tv = lds + (buf * 2 + 1) * kTile;
 #pragma unroll 1
-        for (int r = 0; r < kBN; ++r) {
+        for (int r = 0; r < (mine ? kBN : 0); ++r) {
           const bool sees = view.has(r - 4 * hh);
 #pragma unroll
           for (int x = 0; x < DT * 4; ++x) {
@@ -214,14 +224,14 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
           }
         }
         __syncthreads();
-        for (uint32_t at = t * 4; at < kTile; at += NW * 64 * 4) {
+        for (uint32_t at = t * 4; at < (mine ? kTile : 0); at += NQ * 64 * 4) {
           uint32_t& w = *reinterpret_cast<uint32_t*>(tv + at);
           w &= ((w & 0x7F80u) == 0x7F80u ? 0xFFFF0000u : ~0u) & ((w & 0x7F800000u) == 0x7F800000u ? 0xFFFFu : ~0u);
         }
         __syncthreads();
       }
       // no key of the tile is visible to the wave's queries
-      if ((int)tile.row + wave * 32 > last || j0 > wp1 || (!k.sinks && j0 + kBN <= wstart0)) continue;
+      if (!mine || (int)tile.row + wave * 32 > last || j0 > wp1 || (!k.sinks && j0 + kBN <= wstart0)) continue;
       const bool whole = j0 + kBN - 1 <= min(wp0, k.end - 1) && (k.sinks || j0 >= wstart1);
       const LaneAddr<DP> from(lbase + buf * 2 * kTile, lane);
       // register r of block b: key 32 b + 8 (r / 4) + 4 hh + r % 4
@@ -323,7 +333,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
     for (int d = 0; d < DT; ++d)
 #pragma unroll
       for (int r = 0; r < 16; ++r) odd = __builtin_fmaf(o[d][r], 0.f, odd);
-    if (t == 0) lflag[0] = lflag[1] = 0;
+    if (threadIdx.x == 0) lflag[0] = lflag[1] = 0;
     __syncthreads();
     if (odd != 0.f) lflag[0] = 1;              // true of NaN
     if (bad) lflag[1] = 1;
@@ -333,6 +343,28 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
   }
 
   l += __shfl_xor(l, 32);
+  if constexpr (KG == 2) {
+    // (the tiles are no longer read) the second half's results, a wave's lane by lane
+    float* give = reinterpret_cast<float*>(all_lds) + wave * (DT * 16 + 2) * kWave + lane;
+    if (part == 1) {
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) give[(d * 16 + r) * kWave] = o[d][r];
+      give[DT * 16 * kWave] = m;
+      give[(DT * 16 + 1) * kWave] = l;
+    }
+    __syncthreads();
+    if (part == 1) return;
+    const float m2 = give[DT * 16 * kWave], l2 = give[(DT * 16 + 1) * kWave], top = fmaxf(m, m2);
+    const float f1 = m == AR_NEG_INF ? 1.0f : exp2_fast(m - top), f2 = m2 == AR_NEG_INF ? 1.0f : exp2_fast(m2 - top);
+    m = top;                                   // (all is 0 of a half without scores)
+    l = l * f1 + l2 * f2;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) o[d][r] = o[d][r] * f1 + give[(d * 16 + r) * kWave] * f2;
+  }
   if (row > last) return;
   float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;   // no visible key: zeros; NaN stays
   if (SRC != kKeyRows && lflag[1]) inv = __uint_as_float(0x7FC00000u);
@@ -353,20 +385,35 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
 
 constexpr unsigned tiles_at_most(size_t rows, size_t seqs, unsigned bm) { return (unsigned)(rows / bm + seqs); }
 
-template <int DP, int NW, KeySource SRC>
+template <int DP, int NW, int KG, KeySource SRC>
 hipError_t launch(const Launch& L, const AttnArgs& a) {
-  const unsigned tiles = tiles_at_most(a.rows_q, a.seqs, NW * 32);
-  return launch_k(k_attn<DP, NW, SRC>, dim3(tiles * a.hq), dim3(NW * 64), 0, L.stream, a);
+  const unsigned tiles = tiles_at_most(a.rows_q, a.seqs, NW / KG * 32);
+  return launch_k(k_attn<DP, NW, KG, SRC>, dim3(tiles * a.hq), dim3(NW * 64), 0, L.stream, a);
 }
 
 // 256 queries a workgroup where that gives every CU two, else 128, of which
-// two share a CU.  (16384 tokens, 64 heads of 128: 4187 us and 4391; 647 tokens,
-// 6 heads of 64: 15.4 and 11.9.)
+// two share a CU (16384 tokens, 64 heads of 128: 4187 us and 4391; 647 tokens,
+// 6 heads of 64: 15.4 and 11.9).  Where most CUs have no second workgroup, one
+// of 128 queries has eight waves, half of them on every other tile of keys
+// (4096 tokens, 8 heads of 128: 71 us, with four waves 95; 2048 of them behind
+// 8192: 172 and 243; 7 sequences of 1 to 700 of them, 16 heads of 64, E4M3: 19
+// and 24; but 16 prompts of 256 to 768 of them, 8 heads: 33 and 29; 32 of 128:
+// 13.4 and 11.8).  So too where two would share a CU, if prompts are long and
+// have no window, since the launch then waits for the last queries' keys (8192
+// tokens, 8 heads of 128: 155 and 194; two prompts of 4096: 92 and 130; 10240
+// tokens: 253 and 260; but 8 prompts of 1024: 45 and 40; 8192 tokens with a
+// window of 4096: 144 and 135).
+template <int DP, KeySource SRC>
+hipError_t launch_dim(const Launch& L, const AttnArgs& a) {
+  const size_t rows = a.rows_q, cus = L.cus;
+  const size_t groups = (rows / 128 + a.seqs / 2) * a.hq;   // about: a sequence's last one is half full
+  if (rows * a.hq >= 2 * cus * 256) return launch<DP, 8, 1, SRC>(L, a);
+  const bool deep = rows >= (size_t)a.seqs * 2048 && (size_t)a.window * a.seqs >= rows;
+  return groups * 20 <= cus * (deep ? 45 : 28) ? launch<DP, 8, 2, SRC>(L, a) : launch<DP, 4, 1, SRC>(L, a);
+}
 template <KeySource SRC>
 hipError_t launch_src(const Launch& L, const AttnArgs& a) {
-  const bool wide = (size_t)a.rows_q * a.hq >= (size_t)2 * L.cus * 256;
-  if (a.dim > 64) return wide ? launch<128, 8, SRC>(L, a) : launch<128, 4, SRC>(L, a);
-  return wide ? launch<64, 8, SRC>(L, a) : launch<64, 4, SRC>(L, a);
+  return a.dim > 64 ? launch_dim<128, SRC>(L, a) : launch_dim<64, SRC>(L, a);
 }
 
 }  // namespace

@@ -562,3 +562,73 @@ def test_two_streams_at_once():
         torch.cuda.synchronize()
         for x in o:
             assert torch.equal(x, want)
+
+
+@pytest.mark.parametrize("source", ["rows", "pages", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("new", [[640, 1, 300, 0, 129, 700, 513], [2050]])
+def test_workgroups_by_their_number(dim, source, new):
+    """Workgroups of 128 queries: so many that two share a compute unit, and
+    long prompts of which half a workgroup takes every other tile of keys; with
+    a mask that leaves such a half no key, or one of its sides a single one."""
+    note(f"number {source} {dim} {new}")
+    hq, hkv, g, n, offs = 24, 4, gen(dim + len(new)), sum(new), cu(new)
+    q = heads(g, n, hq, dim)
+    for window, sinks, past in ((0, 0, 0), (64, 0, 63), (1, 1, 64), (97, 65, 5)):
+        out, lse = torch.empty_like(q), torch.empty(n, hq, device=DEV)
+        total = [m + past if m else 0 for m in new]
+        if source == "rows":
+            ko = cu(total)
+            k, v = heads(g, sum(total), hkv, dim), heads(g, sum(total), hkv, dim)
+            tar.ar_attn(q, k, v, offs, ko, out, window=window, sinks=sinks, lse=lse)
+        else:
+            table, pages = tables(g, total, 16)
+            cache = filled(g, pages, 16, hkv, dim, source == "e4m3")
+            lens = torch.tensor(total, device=DEV, dtype=torch.int32)
+            tar.ar_attn_paged(q, cache, table, lens, offs, out, window=window, sinks=sinks, lse=lse)
+        torch.cuda.synchronize()
+        for i in range(len(new)):
+            if not new[i]:
+                continue
+            a = slice(int(offs[i]), int(offs[i + 1]))
+            kk, vv = (k[int(ko[i]):int(ko[i + 1])], v[int(ko[i]):int(ko[i + 1])]) if source == "rows" else ref.paged(cache, table[i], total[i])
+            for h in (0, hq - 1):
+                want = ref.attend(q[a, h], kk[:, h // (hq // hkv)], vv[:, h // (hq // hkv)], dim ** -0.5, window, sinks)
+                ref.close(out[a, h], want["out"], want["out_t"], f"out of sequence {i}, head {h}, window {window}")
+                ref.close(lse[a, h], want["lse"], want["lse_t"], f"lse of sequence {i}, head {h}, window {window}")
+
+
+@pytest.mark.parametrize("source", ["rows", "pages"])
+def test_halves_with_values_that_are_no_numbers(source):
+    """Values that are no numbers in either half's tiles of keys: where they
+    are masked they change nothing, where they are visible they are seen."""
+    note(f"halves, no numbers, {source}")
+    g, n, hq, hkv, dim = gen(5), 330, 4, 2, 128
+    q, k, v = heads(g, n, hq, dim), heads(g, n, hkv, dim), heads(g, n, hkv, dim)
+    offs = cu([n])
+    for at in (70, 140, 300):                       # tiles 1, 2 and 4
+        clean, lse0 = torch.empty_like(q), torch.empty(n, hq, device=DEV)
+        out, lse = torch.empty_like(q), torch.empty(n, hq, device=DEV)
+        odd = v.clone()
+        odd[at, 0] = float("nan")
+        odd[at, 1, :3] = float("inf")
+        if source == "rows":
+            run = lambda vv, o, s: tar.ar_attn(q, k, vv, offs, offs, o, lse=s)
+        else:
+            table = torch.arange((n + 15) // 16, device=DEV, dtype=torch.int32).view(1, -1)
+            lens = torch.tensor([n], device=DEV, dtype=torch.int32)
+
+            def run(vv, o, s):
+                cache = tar.kv_cache_empty(table.numel(), 16, hkv, dim, device=DEV)
+                pad = table.numel() * 16 - n
+                for x, y in zip(cache, (k, vv)):
+                    x.copy_(torch.nn.functional.pad(y, (0, 0, 0, 0, 0, pad)).view(x.shape))
+                tar.ar_attn_paged(q, cache, table, lens, offs, o, lse=s)
+        run(v, clean, lse0)
+        run(odd, out, lse)
+        torch.cuda.synchronize()
+        assert torch.isfinite(clean).all() and torch.equal(lse, lse0)
+        assert torch.equal(out[:at], clean[:at])
+        assert out[at:, :2].isnan().all()           # heads 0, 1 read key head 0
+        assert (~torch.isfinite(out[at:, 2:, :3])).all()
+        assert torch.equal(out[at:, 2:, 3:], clean[at:, 2:, 3:])
