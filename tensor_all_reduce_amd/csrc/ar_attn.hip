@@ -219,14 +219,14 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float v = e & 1 ? hi_f32(w[e / 2]) : lo_f32(w[e / 2]);
-              if (sees && !(__builtin_fabsf(v) < __builtin_huge_valf())) o[x / 4][x % 4 * 4 + e] += v;
+              if (sees && !is_number(v)) o[x / 4][x % 4 * 4 + e] += v;
             }
           }
         }
         __syncthreads();
         for (uint32_t at = t * 4; at < (mine ? kTile : 0); at += NQ * 64 * 4) {
           uint32_t& w = *reinterpret_cast<uint32_t*>(tv + at);
-          w &= ((w & 0x7F80u) == 0x7F80u ? 0xFFFF0000u : ~0u) & ((w & 0x7F800000u) == 0x7F800000u ? 0xFFFFu : ~0u);
+          w = numbers_only(w);
         }
         __syncthreads();
       }

@@ -34,6 +34,7 @@ union Frag8 {
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.693147180559945309f;
 #define AR_NEG_INF (-__builtin_huge_valf())
+#define AR_RARE(x) (__builtin_expect((x), 0))
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -47,6 +48,12 @@ __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
 __device__ __forceinline__ uint32_t result_bf16x2(float lo, float hi) {
   const float nan = __uint_as_float(0x7FC00000u);
   return cvt_bf16x2(__builtin_isnan(lo) ? nan : lo, __builtin_isnan(hi) ? nan : hi);
+}
+
+// Neither infinite nor NaN; two bf16 values with 0 in the place of such.
+__device__ __forceinline__ bool is_number(float x) { return __builtin_fabsf(x) < __builtin_huge_valf(); }
+__device__ __forceinline__ uint32_t numbers_only(uint32_t w) {
+  return w & ((w & 0x7F80u) == 0x7F80u ? 0xFFFF0000u : ~0u) & ((w & 0x7F800000u) == 0x7F800000u ? 0xFFFFu : ~0u);
 }
 
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {

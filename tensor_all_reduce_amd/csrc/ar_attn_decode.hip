@@ -98,9 +98,10 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
   using R = Ring<DP, E4M3>;
   constexpr int RB = R::kRow, KS = DP / 32, DT = DP / 16, STEP = R::kStep, TILE = R::kTileKeys, NB = STEP / 16;
   __shared__ __align__(1024) char ring[kWaves * R::kBytes];
-  __shared__ __align__(16) float lo_[kWaves][kHeads][36];      // 32 columns of each wave's result
+  __shared__ __align__(16) float lo_[kWaves][kHeads][36];      // 32 columns of each wave's result; its odd values' sums
   __shared__ float lm[kWaves][kHeads], ll[kWaves][kHeads];
-  __shared__ unsigned lcount;
+  __shared__ unsigned lcount, lodds[kWaves / 4];               // (a byte of lodds a wave)
+  uint8_t* const lodd = reinterpret_cast<uint8_t*>(lodds);
   const int t = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(t / kWave);
   const int hd = lane & 15, g = lane >> 4;
   const unsigned group = a.hq / a.hkv;
@@ -268,6 +269,13 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
   // A part's copies are under way while the one before it is joined.
   Part s0 = now;                               // the part that is computed, or joined
   bool more = true, done = false;
+  // Infinite values: 0 times one is NaN, and half of the numerators' rests
+  // have the other sign.  So where a result is no number, the wave computes
+  // its part again with care: values that are no numbers are 0 in the product
+  // and summed apart, a column a lane, for all heads.  (The wave alone: no
+  // barrier lies between a part's start and its join.)
+  bool care = false;
+  float odd[DP / 64];                          // columns lane, lane + 64
   for (;;) {
     if (more) {
       load_queries(now);
@@ -282,7 +290,10 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
         lm[wave][hd] = m;
         ll[wave][hd] = l;
       }
+      if (lane == 0) lodd[wave] = care;
+      care = false;
       __syncthreads();
+      const bool some = uniform((int)(lodds[0] | lodds[1])) != 0;   // values that are no numbers
       float M = AR_NEG_INF, sum = 0.f;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) M = fmaxf(M, lm[w][hd]);
@@ -307,10 +318,15 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
           for (int r = 0; r < 4; ++r) v[r] *= f;
           *reinterpret_cast<f32x4*>(&lo_[wave][hd][16 * x + 4 * g]) = v;
         }
+        if (AR_RARE(some) && lane / 32 == d2 % 2) lo_[wave][od / 4][32 + od % 4] = odd[d2 / 2];
         __syncthreads();
         float sum2 = 0.f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) sum2 += lo_[w][oh][od];
+        if (AR_RARE(some)) {
+#pragma unroll 1
+          for (int w = 0; w < kWaves; ++w) sum2 += lo_[w][od / 4][32 + od % 4];
+        }
         const unsigned at = 32 * d2 + od;
         if (oh < here && at < a.dim) {
           if (part) __hip_atomic_store(part + 2 * kHeads + oh * DP + at, sum2, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -373,6 +389,18 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
                 }
               }
             }
+            if (AR_RARE(!(is_number(acc[0]) && is_number(acc[1]) && is_number(acc[2]) && is_number(acc[3])))) {
+              // (a part's infinity has met a weight of 0)
+              acc = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+              for (unsigned i = 0; i < count; ++i) {
+                const float* from = part_of(i);
+                const f32x4 x = *reinterpret_cast<const f32x4*>(from + 2 * kHeads + col);
+                const float w = from[h] == AR_NEG_INF ? 0.f : exp2_fast(from[h] - M2);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[r] += is_number(x[r]) ? x[r] * w : x[r];
+              }
+            }
             const float i2 = L2 > 0.f ? 1.0f / L2 : L2;
             if (d < a.dim)
               *reinterpret_cast<u32x2*>(a.out.p + (size_t)s0.seq * a.out.ts + (head0 + h) * a.out.hs + d) =
@@ -392,6 +420,8 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
     m = AR_NEG_INF;
     l = 0.f;
 #pragma unroll
+    for (int x = 0; x < DP / 64; ++x) odd[x] = 0.f;
+#pragma unroll
     for (int d = 0; d < DT; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
     for (unsigned i = 0; i < now.count; ++i) {
@@ -407,6 +437,25 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
           l = __uint_as_float(0x7FC00000u);
         const char* lk = mine + stage * R::kStage;
         const uint32_t lv = lmine + stage * R::kStage + R::kKeys;
+        if (AR_RARE(care)) {
+          char* tv = mine + stage * R::kStage + R::kKeys;
+#pragma unroll 1
+          for (int r = 0; r < keys; ++r) {
+#pragma unroll
+            for (int x = 0; x < DP / 64; ++x) {
+              const char* p = tv + chunk_at<RB>(r, lane * ES / 16 + x * 4 * ES) + lane * ES % 16;
+              const float v = E4M3 ? ((*p & 0x7F) == 0x7F ? __uint_as_float(0x7FC00000u) : 0.f)
+                                   : bf16_f32(*reinterpret_cast<const uint16_t*>(p));
+              if (!is_number(v)) odd[x] += v;
+            }
+          }
+#pragma unroll 1
+          for (int at = lane * 4; at < R::kKeys; at += kWave * 4) {
+            uint32_t& w = *reinterpret_cast<uint32_t*>(tv + at);
+            if constexpr (E4M3) w &= ~((((w & 0x7F7F7F7Fu) + 0x01010101u) >> 7 & 0x01010101u) * 0xFFu);
+            else w = numbers_only(w);
+          }
+        }
         // values are read first: they arrive while the scores are formed
         Frag8 v[DT];
 #pragma unroll
@@ -536,6 +585,10 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
             for (int e = 0; e < 4 * NB; ++e)
               if ((e & 3) + (e >= 4 ? 16 : 0) >= beyond) v[d].w[e / 2] &= e & 1 ? 0xFFFFu : 0xFFFF0000u;
         }
+        if (E4M3 && AR_RARE(care)) {             // (an infinite scale's numerator has no rest)
+#pragma unroll
+          for (int w = 0; w < 2 * NB; ++w) rest.w[w] = numbers_only(rest.w[w]);
+        }
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
           if constexpr (NB == 2) {
@@ -556,6 +609,16 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
       if (i + 2 < now.count) fetch(now, i + 2, stage, (slot + 2) & 3);
     }
 
+    if (!care) {
+      f32x4 all = o[0];
+#pragma unroll
+      for (int d = 1; d < DT; ++d) all += o[d];
+      if (AR_RARE(__any(!is_number((all[0] + all[1]) + (all[2] + all[3]))))) {
+        care = true;
+        done = false;
+        continue;
+      }
+    }
     s0 = now;
     done = true;
     more = follow(now);

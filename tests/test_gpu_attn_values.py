@@ -1,0 +1,146 @@
+"""Attention over values that are infinite, no numbers or very large: what is
+visible shows in the result as the formula has it, over pages as over rows,
+for single tokens as for prompts."""
+import math
+
+import pytest
+import torch
+
+import attn_ref as ref
+import tensor_all_reduce_amd as tar
+from gpu_util import note
+from test_gpu_attn import cu, gen, heads
+from test_gpu_attn_cache import filled, normal, tables
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def place(table, i, j, page):
+    return int(table[i, j // page]), j % page
+
+
+def same(got, want, what):
+    """Infinities and NaN in the same places."""
+    inf = torch.isinf(want)
+    nans, infs = (got.isnan() != want.isnan()).sum(), ((got != want) & (inf | got.isinf())).sum()
+    assert int(nans) == 0 and int(infs) == 0, what
+
+
+class Served:
+    """Sequences in pages and one new token of each."""
+
+    def __init__(self, g, lengths, hq, hkv, dim, page, e4m3):
+        self.lengths, self.page, self.dim = lengths, page, dim
+        self.table, pages = tables(g, lengths, page)
+        self.cache = filled(g, pages, page, hkv, dim, e4m3)
+        self.q = normal(g, len(lengths), hq, dim).to(torch.bfloat16)
+        self.lens = torch.tensor(lengths, device=DEV, dtype=torch.int32)
+        self.ws = torch.zeros(tar.attn_decode_workspace(len(lengths), hq, hkv, dim), device=DEV, dtype=torch.uint8)
+
+    def decode(self, cut, **mask):
+        out = torch.full_like(self.q, 7.0)
+        tar.ar_attn_decode(self.q, self.cache, self.table, self.lens, out, workspace=self.ws if cut else None, **mask)
+        torch.cuda.synchronize()
+        return out
+
+    def prompt(self, **mask):
+        out = torch.full_like(self.q, 7.0)
+        tar.ar_attn_paged(self.q, self.cache, self.table, self.lens, cu([1] * len(self.lengths)), out, **mask)
+        torch.cuda.synchronize()
+        return out
+
+
+# ------------------------------------------------- single tokens, visible values
+
+@pytest.mark.parametrize("cut", [False, True])
+@pytest.mark.parametrize("hq,hkv,dim,page,e4m3", [(8, 2, 128, 16, False), (6, 3, 64, 48, False), (40, 2, 80, 7, False),
+                                                  (16, 2, 128, 16, True), (4, 4, 64, 32, True)])
+def test_single_tokens_see_what_is_no_number(hq, hkv, dim, page, e4m3, cut):
+    note(f"visible {hq}/{hkv}x{dim} page {page} e4m3 {e4m3} cut {cut}")
+    lengths, at = [1, 20, 129, 700, 3000], [0, 19, 64, 333, 2900]
+    s = Served(gen(dim + hq), lengths, hq, hkv, dim, page, e4m3)
+    clean = s.decode(cut)
+    kept = [ref.paged(s.cache, s.table[i], n) for i, n in enumerate(lengths)]
+    h = hkv - 1                                       # only this key head has such values
+    for i, j in enumerate(at):
+        p = place(s.table, i, j, page)
+        v = s.cache[1][p][h]
+        if e4m3:
+            v.view(torch.uint8)[5] = 0x7F
+        else:
+            v[3], v[4], v[5], v[6] = math.inf, -math.inf, math.nan, math.inf
+            s.cache[1][place(s.table, i, j // 2, page)][h][6] = -math.inf if j else math.inf
+    out, prompt = s.decode(cut), s.prompt()
+    group, first = hq // hkv, h * (hq // hkv)
+    assert torch.equal(out[:, :first], clean[:, :first])
+    same(out, prompt, "single token and prompt")
+    for i, n in enumerate(lengths):
+        bad = out[i, first:]
+        assert bool(torch.isnan(bad[:, 5]).all())
+        cols = {5}
+        if not e4m3:
+            assert bool((bad[:, 3] == math.inf).all()) and bool((bad[:, 4] == -math.inf).all())
+            assert bool((bad[:, 6] == math.inf).all()) if i == 0 else bool(torch.isnan(bad[:, 6]).all())
+            cols |= {3, 4, 6}
+        rest = [c for c in range(dim) if c not in cols]
+        for x in range(group):
+            want = ref.attend(s.q[i:i + 1, first + x], kept[i][0][:, h], kept[i][1][:, h], dim ** -0.5)
+            ref.close(bad[x:x + 1, rest], want["out"][:, rest], want["out_t"][:, rest], f"out of {n} keys, head {x}")
+
+
+@pytest.mark.parametrize("cut", [False, True])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_single_tokens_and_infinite_scales(dim, cut):
+    """A value is its code times its scale: infinities with the codes' signs."""
+    note(f"infinite scales {dim} cut {cut}")
+    s = Served(gen(dim), [40, 2000], 8, 1, dim, 16, True)
+    for i, j in enumerate((7, 1234)):
+        p = place(s.table, i, j, 16)
+        codes = torch.ones(dim, device=DEV)
+        codes[1::2] = -2.0
+        codes[6] = 0.0
+        s.cache[1][p][0].copy_(codes)
+        s.cache[3][p][0] = math.inf
+    out = s.decode(cut)
+    want = torch.full((dim,), math.inf, device=DEV)
+    want[1::2] = -math.inf
+    want[6] = math.nan
+    for x in out.flatten(0, 1):
+        same(x, want.to(x.dtype), "out")
+
+
+def far_scores(cache, q, table, page, lengths, low):
+    """Scores of 256, and of 0 for the keys `low`: weights of e^-256 of the others'."""
+    for c in cache[:1]:
+        c.zero_()
+        c[..., 0] = 16.0
+    q.zero_()
+    q[..., 0] = 16.0
+    for i, n in enumerate(lengths):
+        for j in low[i]:
+            cache[0][place(table, i, j, page)][:, 0] = 0.0
+
+
+FAR = [[0], [39], [128], range(2816, 2944), range(0, 700)]   # the first and the last key; a wave's step, a part, an earlier part
+
+
+@pytest.mark.parametrize("cut", [False, True])
+@pytest.mark.parametrize("hq,hkv,dim,page", [(8, 1, 128, 16), (4, 2, 64, 48)])
+def test_single_tokens_and_infinities_of_little_weight(hq, hkv, dim, page, cut):
+    note(f"little weight {hq}/{hkv}x{dim} cut {cut}")
+    lengths = [40, 40, 129, 3000, 3000]
+    s = Served(gen(dim), lengths, hq, hkv, dim, page, False)
+    far_scores(s.cache, s.q, s.table, page, lengths, FAR)
+    kept = [ref.paged(s.cache, s.table[i], n) for i, n in enumerate(lengths)]
+    for i, low in enumerate(FAR):
+        s.cache[1][place(s.table, i, low[len(low) // 2], page)][:, 3] = math.inf
+        s.cache[1][place(s.table, i, low[0], page)][:, 4] = -math.inf
+    out = s.decode(cut, scale=1.0)
+    assert bool((out[..., 3] == math.inf).all()) and bool((out[..., 4] == -math.inf).all())
+    rest = [c for c in range(dim) if c not in (3, 4)]
+    for i in range(len(lengths)):
+        for h in range(hq):
+            kh = h // (hq // hkv)
+            want = ref.attend(s.q[i:i + 1, h], kept[i][0][:, kh], kept[i][1][:, kh], 1.0)
+            ref.close(out[i:i + 1, h][:, rest], want["out"][:, rest], want["out_t"][:, rest], f"sequence {i}, head {h}")
