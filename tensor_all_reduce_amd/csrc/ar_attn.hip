@@ -33,7 +33,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
   constexpr uint32_t kTile = kBN * DP * 2;     // bytes of a tile of keys, or of values
   __shared__ __align__(1024) char all_lds[KG * 4 * kTile];   // keys, values; keys, values
   __shared__ __align__(16) float all_scales[SRC == kKeyPagesE4M3 ? KG * 4 * kBN : 4];  // their scales
-  __shared__ int lflag[2];
+  __shared__ int lflag;
   const int lane = lane_id(), part = KG == 1 ? 0 : uniform(threadIdx.x / (NQ * kWave));   // the wave's half
   const int t = threadIdx.x - part * NQ * kWave, wave = uniform(t / kWave);               // in its half
   const int col = lane & 31, hh = lane >> 5;
@@ -175,7 +175,8 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
   // Values that are no numbers under masked scores: such a score counts 0,
   // but 0 times them is NaN.  So where a result is no number the pass is made
   // again with care: such values are added where they are visible, and are 0
-  // in the product.
+  // in the product.  So too where a page number out of range was met: the
+  // queries that see a key of that page have a sum that is no number.
   bool care = false;
   for (;;) {
     m = AR_NEG_INF;
@@ -210,6 +211,14 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
       const Interval view((k.sinks ? 0 : start) - j0 - 4 * hh, min(p, k.end - 1) - j0 - 4 * hh);
       if (care) {
         char* tv = lds + (buf * 2 + 1) * kTile;
+        if constexpr (SRC != kKeyRows) {
+          if (mine) {
+            const unsigned j = (unsigned)min(j0 + lane, k.end - 1);   // a lane's key
+            const uint64_t lost = __ballot((unsigned)a.table[tile.seq * a.table_ld + page_of(j, a.cache)] >= a.cache.pages);
+            const int from = max((k.sinks ? 0 : start) - j0, 0), to = min(min(p, k.end - 1) - j0, kBN - 1);
+            if (to >= from && (lost >> from) << from << (kBN - 1 - to)) l = __uint_as_float(0x7FC00000u);
+          }
+        }
 #pragma unroll 1
         for (int r = 0; r < (mine ? kBN : 0); ++r) {
           const bool sees = view.has(r - 4 * hh);
@@ -333,12 +342,11 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
     for (int d = 0; d < DT; ++d)
 #pragma unroll
       for (int r = 0; r < 16; ++r) odd = __builtin_fmaf(o[d][r], 0.f, odd);
-    if (threadIdx.x == 0) lflag[0] = lflag[1] = 0;
+    if (threadIdx.x == 0) lflag = 0;
     __syncthreads();
-    if (odd != 0.f) lflag[0] = 1;              // true of NaN
-    if (bad) lflag[1] = 1;
+    if (odd != 0.f || bad) lflag = 1;          // true of NaN
     __syncthreads();
-    if (care || uniform(lflag[0]) == 0) break;
+    if (care || uniform(lflag) == 0) break;
     care = true;
   }
 
@@ -366,8 +374,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
       for (int r = 0; r < 16; ++r) o[d][r] = o[d][r] * f1 + give[(d * 16 + r) * kWave] * f2;
   }
   if (row > last) return;
-  float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;   // no visible key: zeros; NaN stays
-  if (SRC != kKeyRows && lflag[1]) inv = __uint_as_float(0x7FC00000u);
+  const float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;   // no visible key: zeros; NaN stays
   uint16_t* op = a.out.p + (size_t)(rq.first + row) * a.out.ts + head * a.out.hs;
 #pragma unroll
   for (int d = 0; d < DT; ++d)
