@@ -174,17 +174,20 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
   float m, l;
   // Values that are no numbers under masked scores: such a score counts 0,
   // but 0 times them is NaN.  So where a result is no number the pass is made
-  // again with care: such values are added where they are visible, and are 0
-  // in the product.  So too where a page number out of range was met: the
-  // queries that see a key of that page have a sum that is no number.
-  bool care = false;
-  for (;;) {
-    m = AR_NEG_INF;
-    l = 0.f;
+  // again with such values as 0 (care 1), and then once more, without products,
+  // to add them where they are visible (care 2): no weight makes them 0 any
+  // more.  So too where a page number out of range was met: the queries that
+  // see a key of that page have a sum that is no number.
+  auto pass = [&](auto mode) {
+    constexpr int CARE = decltype(mode)::value;
+    if constexpr (CARE < 2) {
+      m = AR_NEG_INF;
+      l = 0.f;
 #pragma unroll
-    for (int d = 0; d < DT; ++d)
+      for (int d = 0; d < DT; ++d)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) o[d][r] = 0.f;
+        for (int r = 0; r < 16; ++r) o[d][r] = 0.f;
+    }
     if (part < keys.steps) {
       look_up(part);
       if constexpr (SRC == kKeyPagesE4M3) fetch(part);
@@ -209,8 +212,24 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
       const int j0 = k.j0;
       // of the tile's keys, less 4 hh, those that the lane's query sees
       const Interval view((k.sinks ? 0 : start) - j0 - 4 * hh, min(p, k.end - 1) - j0 - 4 * hh);
-      if (care) {
+      if constexpr (CARE > 0) {
         char* tv = lds + (buf * 2 + 1) * kTile;
+        if constexpr (CARE == 2) {
+#pragma unroll 1
+          for (int r = 0; r < (mine ? kBN : 0); ++r) {
+            const bool sees = view.has(r - 4 * hh);
+#pragma unroll
+            for (int x = 0; x < DT * 4; ++x) {
+              const u32x2 w = *reinterpret_cast<const u32x2*>(tv + chunk_addr<DP>(r, x) + 8 * hh);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float v = e & 1 ? hi_f32(w[e / 2]) : lo_f32(w[e / 2]);
+                if (sees && !is_number(v)) o[x / 4][x % 4 * 4 + e] += v;
+              }
+            }
+          }
+          continue;
+        }
         if constexpr (SRC != kKeyRows) {
           if (mine) {
             const unsigned j = (unsigned)min(j0 + lane, k.end - 1);   // a lane's key
@@ -219,20 +238,6 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
             if (to >= from && (lost >> from) << from << (kBN - 1 - to)) l = __uint_as_float(0x7FC00000u);
           }
         }
-#pragma unroll 1
-        for (int r = 0; r < (mine ? kBN : 0); ++r) {
-          const bool sees = view.has(r - 4 * hh);
-#pragma unroll
-          for (int x = 0; x < DT * 4; ++x) {
-            const u32x2 w = *reinterpret_cast<const u32x2*>(tv + chunk_addr<DP>(r, x) + 8 * hh);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float v = e & 1 ? hi_f32(w[e / 2]) : lo_f32(w[e / 2]);
-              if (sees && !is_number(v)) o[x / 4][x % 4 * 4 + e] += v;
-            }
-          }
-        }
-        __syncthreads();
         for (uint32_t at = t * 4; at < (mine ? kTile : 0); at += NQ * 64 * 4) {
           uint32_t& w = *reinterpret_cast<uint32_t*>(tv + at);
           w = numbers_only(w);
@@ -334,20 +339,26 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
         });
         l += more;
       };
-      if (whole) tile_step(std::false_type{});
+      if (CARE == 0 && whole) tile_step(std::false_type{});
       else tile_step(std::true_type{});
     }
-    float odd = 0.f;   // NaN if any result is no number
+  };
+  pass(SPc<0>{});
+  float odd = 0.f;                             // NaN if any result is no number
 #pragma unroll
-    for (int d = 0; d < DT; ++d)
+  for (int d = 0; d < DT; ++d)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) odd = __builtin_fmaf(o[d][r], 0.f, odd);
-    if (threadIdx.x == 0) lflag = 0;
+    for (int r = 0; r < 16; ++r) odd = __builtin_fmaf(o[d][r], 0.f, odd);
+  if (threadIdx.x == 0) lflag = 0;
+  __syncthreads();
+  if (odd != 0.f || bad) lflag = 1;            // true of NaN
+  __syncthreads();
+  const bool care = uniform(lflag) != 0;
+  if (AR_RARE(care)) {
+    pass(SPc<1>{});
+    __syncthreads();                           // (no wave reads a tile any more)
+    pass(SPc<2>{});
     __syncthreads();
-    if (odd != 0.f || bad) lflag = 1;          // true of NaN
-    __syncthreads();
-    if (care || uniform(lflag) == 0) break;
-    care = true;
   }
 
   l += __shfl_xor(l, 32);
@@ -368,10 +379,20 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
     const float f1 = m == AR_NEG_INF ? 1.0f : exp2_fast(m - top), f2 = m2 == AR_NEG_INF ? 1.0f : exp2_fast(m2 - top);
     m = top;                                   // (all is 0 of a half without scores)
     l = l * f1 + l2 * f2;
+    if (AR_RARE(care)) {
 #pragma unroll
-    for (int d = 0; d < DT; ++d)
+      for (int d = 0; d < DT; ++d)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) o[d][r] = o[d][r] * f1 + give[(d * 16 + r) * kWave] * f2;
+        for (int r = 0; r < 16; ++r) {
+          const float x = give[(d * 16 + r) * kWave];
+          o[d][r] = (is_number(o[d][r]) ? o[d][r] * f1 : o[d][r]) + (is_number(x) ? x * f2 : x);
+        }
+    } else {
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[d][r] = o[d][r] * f1 + give[(d * 16 + r) * kWave] * f2;
+    }
   }
   if (row > last) return;
   const float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;   // no visible key: zeros; NaN stays

@@ -144,3 +144,34 @@ def test_single_tokens_and_infinities_of_little_weight(hq, hkv, dim, page, cut):
             kh = h // (hq // hkv)
             want = ref.attend(s.q[i:i + 1, h], kept[i][0][:, kh], kept[i][1][:, kh], 1.0)
             ref.close(out[i:i + 1, h][:, rest], want["out"][:, rest], want["out_t"][:, rest], f"sequence {i}, head {h}")
+
+
+# --------------------------------------------------------------------- prompts
+
+@pytest.mark.parametrize("n,hq,hkv,dim", [(330, 4, 2, 128), (2048, 24, 4, 64), (2100, 64, 8, 128)])
+def test_prompts_and_infinities_of_little_weight(n, hq, hkv, dim):
+    """Weights of e^-256 of the others', met before, among and behind those."""
+    note(f"little weight, prompt {n} {hq}/{hkv}x{dim}")
+    g, offs = gen(n), cu([n])
+    q, k, v = heads(g, n, hq, dim), heads(g, n, hkv, dim), heads(g, n, hkv, dim)
+    q.zero_()
+    k.zero_()
+    q[..., 0], k[..., 0] = 16.0, 16.0
+    low = (0, 64, 65, 200, 321)
+    for j in low:
+        k[j] = 0.0
+    kept = v.clone()
+    for i, j in enumerate(low):
+        v[j, :, 2 * i], v[j, :, 2 * i + 1] = math.inf, -math.inf
+    out = torch.empty_like(q)
+    tar.ar_attn(q, k, v, offs, offs, out, scale=1.0)
+    torch.cuda.synchronize()
+    for i, j in enumerate(low):
+        assert bool((out[j:, :, 2 * i] == math.inf).all()) and bool((out[j:, :, 2 * i + 1] == -math.inf).all()), j
+        assert bool(torch.isfinite(out[:j, :, 2 * i:2 * i + 2]).all()), j
+    for h in (0, hq - 1):
+        want = ref.attend(q[:, h], k[:, h // (hq // hkv)], kept[:, h // (hq // hkv)], 1.0)
+        tol = want["out_t"].clone()
+        for i, j in enumerate(low):
+            tol[j:, 2 * i:2 * i + 2] = -1.0
+        ref.close(out[:, h], want["out"], tol, f"head {h}")
