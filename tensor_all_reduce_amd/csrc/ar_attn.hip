@@ -174,10 +174,15 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
   float m, l;
   // Values that are no numbers under masked scores: such a score counts 0,
   // but 0 times them is NaN.  So where a result is no number the pass is made
-  // again with such values as 0 (care 1), and then once more, without products,
-  // to add them where they are visible (care 2): no weight makes them 0 any
+  // again with such values as 0 (CARE 1), and then once more, without products,
+  // to add them where they are visible (CARE 2): no weight makes them 0 any
   // more.  So too where a page number out of range was met: the queries that
-  // see a key of that page have a sum that is no number.
+  // see a key of that page have a sum that is no number.  And where a sum is
+  // beyond binary32: numerators are up to 2^8, and as many as there are keys,
+  // so that large values' sums can be though their mean is not.  With care
+  // numerators are so much smaller that nothing is.
+  const int headroom = 10 + 31 - __builtin_clz(nk | 1);   // 2^headroom > 2^8 times the keys, and twice that
+  const float down = __uint_as_float((127u - headroom) << 23), up = __uint_as_float((127u + headroom) << 23);
   auto pass = [&](auto mode) {
     constexpr int CARE = decltype(mode)::value;
     if constexpr (CARE < 2) {
@@ -323,6 +328,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
               w[e] = exp2_fast(__builtin_fmaf(s[b][x + e], c, -base));
               if (e) more += w[e];
               else l += w[e];
+              if constexpr (CARE > 0) w[e] *= down;
               if constexpr (SRC == kKeyPagesE4M3) w[e] = !MASK || seen(b, x + e) ? w[e] * f[x + e] : 0.f;
             }
             pf[2 * b + x / 8].w[x % 8 / 2] = cvt_bf16x2(w[0], w[1]);
@@ -344,58 +350,70 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
     }
   };
   pass(SPc<0>{});
-  float odd = 0.f;                             // NaN if any result is no number
+  float odd = 0.f;                             // a number only if every result is, and below 2^126: halves are added
 #pragma unroll
   for (int d = 0; d < DT; ++d)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) odd = __builtin_fmaf(o[d][r], 0.f, odd);
+    for (int r = 0; r < 16; ++r) odd = __builtin_fmaf(o[d][r], 8.0f, odd);
   if (threadIdx.x == 0) lflag = 0;
   __syncthreads();
-  if (odd != 0.f || bad) lflag = 1;            // true of NaN
+  if (!is_number(odd) || bad) lflag = 1;
   __syncthreads();
   const bool care = uniform(lflag) != 0;
   if (AR_RARE(care)) {
     pass(SPc<1>{});
     __syncthreads();                           // (no wave reads a tile any more)
-    pass(SPc<2>{});
-    __syncthreads();
   }
 
   l += __shfl_xor(l, 32);
+  // (the tiles are no longer read) the second half's results, a wave's lane by lane
+  float* give = reinterpret_cast<float*>(all_lds) + wave * (DT * 16 + 2) * kWave + lane;
+  auto hand_over = [&] {
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) give[(d * 16 + r) * kWave] = o[d][r];
+  };
   if constexpr (KG == 2) {
-    // (the tiles are no longer read) the second half's results, a wave's lane by lane
-    float* give = reinterpret_cast<float*>(all_lds) + wave * (DT * 16 + 2) * kWave + lane;
     if (part == 1) {
-#pragma unroll
-      for (int d = 0; d < DT; ++d)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) give[(d * 16 + r) * kWave] = o[d][r];
+      hand_over();
       give[DT * 16 * kWave] = m;
       give[(DT * 16 + 1) * kWave] = l;
     }
     __syncthreads();
-    if (part == 1) return;
+    if (part == 1 && !care) return;
     const float m2 = give[DT * 16 * kWave], l2 = give[(DT * 16 + 1) * kWave], top = fmaxf(m, m2);
     const float f1 = m == AR_NEG_INF ? 1.0f : exp2_fast(m - top), f2 = m2 == AR_NEG_INF ? 1.0f : exp2_fast(m2 - top);
     m = top;                                   // (all is 0 of a half without scores)
     l = l * f1 + l2 * f2;
-    if (AR_RARE(care)) {
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) o[d][r] = o[d][r] * f1 + give[(d * 16 + r) * kWave] * f2;
+  }
+  if (AR_RARE(care)) {
+    if constexpr (KG == 2) {
+      __syncthreads();
+      if (part == 1) {
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[d] = f32x16{};
+      }
+    }
+    pass(SPc<2>{});
+    if constexpr (KG == 2) {
+      __syncthreads();
+      if (part == 1) hand_over();
+      __syncthreads();
+      if (part == 1) return;
 #pragma unroll
       for (int d = 0; d < DT; ++d)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const float x = give[(d * 16 + r) * kWave];
-          o[d][r] = (is_number(o[d][r]) ? o[d][r] * f1 : o[d][r]) + (is_number(x) ? x * f2 : x);
-        }
-    } else {
-#pragma unroll
-      for (int d = 0; d < DT; ++d)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) o[d][r] = o[d][r] * f1 + give[(d * 16 + r) * kWave] * f2;
+        for (int r = 0; r < 16; ++r) o[d][r] += give[(d * 16 + r) * kWave];
     }
   }
   if (row > last) return;
   const float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;   // no visible key: zeros; NaN stays
+  const float f = AR_RARE(care) ? inv * up : inv;
   uint16_t* op = a.out.p + (size_t)(rq.first + row) * a.out.ts + head * a.out.hs;
 #pragma unroll
   for (int d = 0; d < DT; ++d)
@@ -404,7 +422,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
       const unsigned at = 32 * d + 8 * g + 4 * hh;
       if (at < a.dim)
         *reinterpret_cast<u32x2*>(op + at) =
-            u32x2{result_bf16x2(o[d][4 * g] * inv, o[d][4 * g + 1] * inv), result_bf16x2(o[d][4 * g + 2] * inv, o[d][4 * g + 3] * inv)};
+            u32x2{result_bf16x2(o[d][4 * g] * f, o[d][4 * g + 1] * f), result_bf16x2(o[d][4 * g + 2] * f, o[d][4 * g + 3] * f)};
     }
   if (a.lse && hh == 0)
     a.lse[(size_t)(rq.first + row) * a.lse_ts + head * a.lse_hs] =

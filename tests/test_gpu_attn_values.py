@@ -175,3 +175,38 @@ def test_prompts_and_infinities_of_little_weight(n, hq, hkv, dim):
         for i, j in enumerate(low):
             tol[j:, 2 * i:2 * i + 2] = -1.0
         ref.close(out[:, h], want["out"], tol, f"head {h}")
+
+
+@pytest.mark.parametrize("source", ["rows", "pages", "e4m3"])
+@pytest.mark.parametrize("n,hq,hkv,dim", [(330, 4, 2, 128), (128, 2, 2, 64), (2048, 24, 4, 64), (2100, 64, 8, 128)])
+def test_prompts_and_large_values(n, hq, hkv, dim, source):
+    """Means of many keys below the largest value, which their numerators' sum
+    is not; a key head each magnitude."""
+    note(f"large values, prompt {n} {hq}/{hkv}x{dim} {source}")
+    g, offs = gen(n), cu([n])
+    q, k = heads(g, n, hq, dim, 0.25), heads(g, n, hkv, dim)
+    v = 1.0 + 0.75 * torch.rand(n, hkv, dim, generator=g, device=DEV)
+    for powers in ((126, 110), (124, 122), (121, 120), (118, 119)):
+        size = torch.tensor([2.0 ** powers[h % 2] for h in range(hkv)], device=DEV)[None, :, None]
+        out, lse = torch.empty_like(q), torch.empty(n, hq, device=DEV)
+        if source == "rows":
+            kk, vv = k, (v * size).to(torch.bfloat16)
+            tar.ar_attn(q, kk, vv, offs, offs, out, lse=lse)
+        else:
+            table, pages = tables(g, [n], 16)
+            cache = filled(g, pages, 16, hkv, dim, source == "e4m3")
+            slots = torch.arange(n, device=DEV)
+            at = (table[0].long()[slots // 16], slots % 16)
+            if source == "e4m3":
+                cache[1][at] = (v * 128).to(torch.float8_e4m3fn)
+                cache[3][at] = (size / 128).expand(n, hkv, 1)[..., 0]
+            else:
+                cache[1][at] = (v * size).to(torch.bfloat16)
+            tar.ar_attn_paged(q, cache, table, torch.tensor([n], device=DEV, dtype=torch.int32), offs, out, lse=lse)
+            kk, vv = ref.paged(cache, table[0], n)
+        torch.cuda.synchronize()
+        for h in (0, hq - 1):
+            kh = h // (hq // hkv)
+            want = ref.attend(q[:, h], kk[:, kh], vv[:, kh], dim ** -0.5)
+            ref.close(out[:, h], want["out"], want["out_t"], f"2^{powers}, head {h}")
+            ref.close(lse[:, h], want["lse"], want["lse_t"], f"lse, 2^{powers}, head {h}")
