@@ -583,7 +583,9 @@ int ar_gemm_fp8(const ar_fp8_matrix* a, const ar_fp8_matrix* b, void* const* c, 
  *   lse[i] = log(sum_j exp(scale * q_i . k_j))      binary32
  * Scores, maxima and sums are binary32; the softmax's numerators, and what
  * multiplies a matrix in the gradients, are rounded to bf16 for their
- * products.
+ * products.  A result of visible values up to 2^127 is finite, however many
+ * there are; a visible infinity or NaN shows in it whatever its weight (ar_attn,
+ * ar_attn_paged, ar_attn_decode).
  *
  * Numbers on the device (lengths, offsets, positions, page numbers, slots) are
  * not known to the caller's thread and not refused: lengths and offsets are

@@ -98,10 +98,9 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
   using R = Ring<DP, E4M3>;
   constexpr int RB = R::kRow, KS = DP / 32, DT = DP / 16, STEP = R::kStep, TILE = R::kTileKeys, NB = STEP / 16;
   __shared__ __align__(1024) char ring[kWaves * R::kBytes];
-  __shared__ __align__(16) float lo_[kWaves][kHeads][36];      // 32 columns of each wave's result; its odd values' sums
+  __shared__ __align__(16) float lo_[kWaves][kHeads][36];      // 32 columns of each wave's result
   __shared__ float lm[kWaves][kHeads], ll[kWaves][kHeads];
-  __shared__ unsigned lcount, lodds[kWaves / 4];               // (a byte of lodds a wave)
-  uint8_t* const lodd = reinterpret_cast<uint8_t*>(lodds);
+  __shared__ unsigned lcount;
   const int t = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(t / kWave);
   const int hd = lane & 15, g = lane >> 4;
   const unsigned group = a.hq / a.hkv;
@@ -273,7 +272,10 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
   // have the other sign.  So where a result is no number, the wave computes
   // its part again with care: values that are no numbers are 0 in the product
   // and summed apart, a column a lane, for all heads.  (The wave alone: no
-  // barrier lies between a part's start and its join.)
+  // barrier lies between a part's start and its join.)  So too where a sum is
+  // 2^115 or more, of which the 2^11 that are joined could pass binary32's
+  // end though their mean does not: with care the maximum is followed 2^lift
+  // above, and numerators are at most 2^-2 of one over the keys.
   bool care = false;
   float odd[DP / 64];                          // columns lane, lane + 64
   for (;;) {
@@ -290,17 +292,22 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
         lm[wave][hd] = m;
         ll[wave][hd] = l;
       }
-      if (lane == 0) lodd[wave] = care;
-      care = false;
       __syncthreads();
-      const bool some = uniform((int)(lodds[0] | lodds[1])) != 0;   // values that are no numbers
       float M = AR_NEG_INF, sum = 0.f;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) M = fmaxf(M, lm[w][hd]);
 #pragma unroll
       for (int w = 0; w < kWaves; ++w)
         sum += lm[w][hd] == AR_NEG_INF ? ll[w][hd] : ll[w][hd] * exp2_fast(lm[w][hd] - M);
-      const float f = m == AR_NEG_INF ? 0.f : exp2_fast(m - M);
+      float f = m == AR_NEG_INF ? 0.f : exp2_fast(m - M);
+      if (AR_RARE(care)) {                       // (no weight makes such values 0 any more)
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) o[d][r] = o[d][r] * f + __shfl(odd[d / 4], (16 * d + 4 * g + r) & 63);
+        f = 1.0f;
+        care = false;
+      }
       const unsigned begin = split ? s0.seq_u / per : 0, finish = split ? (s0.seq_u + (unsigned)s0.cut.n - 1) / per : 0;
       const unsigned count = finish - begin + 1;   // runs that hold parts of the sequence
       const float inv = sum > 0.f ? 1.0f / sum : sum;   // no key: zeros; NaN stays
@@ -318,15 +325,10 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
           for (int r = 0; r < 4; ++r) v[r] *= f;
           *reinterpret_cast<f32x4*>(&lo_[wave][hd][16 * x + 4 * g]) = v;
         }
-        if (AR_RARE(some) && lane / 32 == d2 % 2) lo_[wave][od / 4][32 + od % 4] = odd[d2 / 2];
         __syncthreads();
         float sum2 = 0.f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) sum2 += lo_[w][oh][od];
-        if (AR_RARE(some)) {
-#pragma unroll 1
-          for (int w = 0; w < kWaves; ++w) sum2 += lo_[w][od / 4][32 + od % 4];
-        }
         const unsigned at = 32 * d2 + od;
         if (oh < here && at < a.dim) {
           if (part) __hip_atomic_store(part + 2 * kHeads + oh * DP + at, sum2, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -389,7 +391,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
                 }
               }
             }
-            if (AR_RARE(!(is_number(acc[0]) && is_number(acc[1]) && is_number(acc[2]) && is_number(acc[3])))) {
+            if (AR_RARE(!is_number((acc[0] + acc[1]) + (acc[2] + acc[3])))) {
               // (a part's infinity has met a weight of 0)
               acc = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
@@ -419,6 +421,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
     if (!more) break;
     m = AR_NEG_INF;
     l = 0.f;
+    const float lift = care ? (float)(10 + 31 - __builtin_clz(now.cut.len | 1)) : 0.f;   // 2^lift > 2^10 times the keys / 2
 #pragma unroll
     for (int x = 0; x < DP / 64; ++x) odd[x] = 0.f;
 #pragma unroll
@@ -524,7 +527,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
         for (int b = 0; b < NB; ++b)
 #pragma unroll
           for (int r = 0; r < 4; ++r) top = fmaxf(top, s[b][r]);
-        top = max_of(swap32(max_of(swap16(top)))) * c;
+        top = max_of(swap32(max_of(swap16(top)))) * c + lift;
         if (__any(top > m + 8.0f)) {
           const float up = fmaxf(m, top), f = m == AR_NEG_INF ? 1.0f : exp2_fast(m - up);
           m = up;
@@ -610,9 +613,11 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
     }
 
     if (!care) {
-      f32x4 all = o[0];
+      f32x4 all = {0.f, 0.f, 0.f, 0.f};        // numbers only if every result is, and below 2^115
 #pragma unroll
-      for (int d = 1; d < DT; ++d) all += o[d];
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) all[r] = __builtin_fmaf(o[d][r], 0x1p13f, all[r]);
       if (AR_RARE(__any(!is_number((all[0] + all[1]) + (all[2] + all[3]))))) {
         care = true;
         done = false;

@@ -210,3 +210,49 @@ def test_prompts_and_large_values(n, hq, hkv, dim, source):
             want = ref.attend(q[:, h], kk[:, kh], vv[:, kh], dim ** -0.5)
             ref.close(out[:, h], want["out"], want["out_t"], f"2^{powers}, head {h}")
             ref.close(lse[:, h], want["lse"], want["lse_t"], f"lse, 2^{powers}, head {h}")
+
+
+# ---------------------------------------------------------------- large values
+
+EXPONENTS = [100, 112, 114, 116, 118, 120, 122, 124, 126]
+
+
+@pytest.mark.parametrize("cut", [False, True])
+@pytest.mark.parametrize("keys", [1, 129, 20000])
+@pytest.mark.parametrize("dim,e4m3", [(128, False), (64, False), (128, True)])
+def test_single_tokens_and_large_values(dim, e4m3, keys, cut):
+    """The mean of many equal weights: below the largest value, which the
+    numerators' own sum is not."""
+    note(f"large values, {keys} keys of {dim}, e4m3 {e4m3}, cut {cut}")
+    g = gen(keys)
+    s = Served(g, [keys] * len(EXPONENTS), 8, 1, dim, 16, e4m3)
+    s.q.mul_(0.25)
+    top = 1.0 + 0.5 * torch.rand(dim, generator=g, device=DEV)
+    for i, e in enumerate(EXPONENTS):
+        rows = s.table[i, :-(-keys // 16)].long()
+        noise = 1.0 + 0.25 * torch.rand(len(rows), 16, 1, 1, generator=g, device=DEV)
+        if e4m3:                                     # codes up to 1.875 * 2^7
+            s.cache[1][rows] = (128.0 * top * noise).to(torch.float8_e4m3fn)
+            s.cache[3][rows] = 2.0 ** (e - 7)
+        else:
+            s.cache[1][rows] = (2.0 ** e * top * noise).to(torch.bfloat16)
+    out = s.decode(cut)
+    for i, e in enumerate(EXPONENTS):
+        k, v = ref.paged(s.cache, s.table[i], keys)
+        for h in (0, 7):
+            want = ref.attend(s.q[i:i + 1, h], k[:, 0], v[:, 0], dim ** -0.5)
+            ref.close(out[i:i + 1, h], want["out"], want["out_t"], f"values of 2^{e}, head {h}")
+
+
+def test_single_tokens_and_values_that_cancel():
+    """Large values of both signs, of which little is left, in one column of
+    many and beside ordinary ones."""
+    g, n = gen(3), 3000
+    s = Served(g, [n], 8, 1, 128, 16, False)
+    s.cache[1][:, :, 0, 7] = 2.0 ** 126 * (1 - 2 * torch.randint(0, 2, s.cache[1].shape[:2], generator=g, device=DEV))
+    k, v = ref.paged(s.cache, s.table[0], n)
+    for cut in (False, True):
+        out = s.decode(cut)
+        for h in (0, 5):
+            want = ref.attend(s.q[:, h], k[:, 0], v[:, 0], 128 ** -0.5)
+            ref.close(out[:, h], want["out"], want["out_t"], f"head {h}, cut {cut}")
