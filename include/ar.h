@@ -587,6 +587,13 @@ int ar_gemm_fp8(const ar_fp8_matrix* a, const ar_fp8_matrix* b, void* const* c, 
  * there are; a visible infinity or NaN shows in it whatever its weight (ar_attn,
  * ar_attn_paged, ar_attn_decode).
  *
+ * AR_ERR_UNSUPPORTED is also a call of 2^32 work items or more, the most that
+ * a launch takes: of ar_rope_kv one for every 16 elements of a head of every
+ * token (their number rounded up to 2^n), of the others 512 for a query head
+ * of 256 queries (or a part of a sequence's), and of ar_attn_decode without a
+ * workspace 512 for every key head (or part of it with 16 query heads) of a
+ * sequence.
+ *
  * Numbers on the device (lengths, offsets, positions, page numbers, slots) are
  * not known to the caller's thread and not refused: lengths and offsets are
  * held within the buffers (a length below 0 is 0), and a page number outside

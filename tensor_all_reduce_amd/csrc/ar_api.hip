@@ -1085,7 +1085,7 @@ int ar_rope_kv(const ar_heads* q, const ar_heads* k, const ar_heads* v, size_t t
   if (tokens == 0 || hq + hkv == 0) return AR_OK;
   if (rot && (!cos_sin || table_rows == 0 || !positions)) return AR_ERR_INVALID;
   if (cache && !slots) return AR_ERR_INVALID;
-  if (table_rows >> 31 || tokens * (hq + 2 * hkv) > 0x7FFFFFFF) return AR_ERR_UNSUPPORTED;
+  if (table_rows >> 31 || !ar::rope_fits(tokens, hq + (cache ? 2 : 1) * hkv, dim)) return AR_ERR_UNSUPPORTED;
   if ((rot && !aligned16(cos_sin)) || (reinterpret_cast<uintptr_t>(positions) & 3u) ||
       (cache && (reinterpret_cast<uintptr_t>(slots) & 7u)))
     return AR_ERR_ALIGN;
@@ -1177,6 +1177,7 @@ int ar_attn_decode(const ar_heads* q, const ar_kv_cache* cache, const int32_t* t
   // the row of all tiles is counted in 32 bits (of tiles of 128 keys at least, each sequence with a few more)
   const size_t tiles = a.capacity / 128 + 6, heads = cache->heads * (((hq / cache->heads) + 15) / 16);
   if (mul3_overflows(tiles, heads, seqs) || tiles * heads * seqs >> 31) return AR_ERR_UNSUPPORTED;
+  if (!need && !ar::attn_decode_fits(seqs, hq, cache->heads)) return AR_ERR_UNSUPPORTED;
   a.q = rows_arg(q);
   a.out = out_arg(out);
   a.lens = lens;

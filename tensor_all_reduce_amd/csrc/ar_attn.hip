@@ -464,7 +464,9 @@ hipError_t launch_src(const Launch& L, const AttnArgs& a) {
 
 }  // namespace
 
-bool attn_fits(size_t rows_q, size_t seqs, size_t hq) { return (rows_q / 128 + seqs) <= 0x7FFFFFFFu / hq; }
+// (512 work items for up to 256 queries, or 256 for up to 128; with 512 for 128
+// only where there are few)
+bool attn_fits(size_t rows_q, size_t seqs, size_t hq) { return fits_launch(rows_q / 256 + seqs, hq, 512); }
 
 hipError_t launch_attn(const Launch& L, const AttnArgs& a, KeySource src) {
   switch (src) {

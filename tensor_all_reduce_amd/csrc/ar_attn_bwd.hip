@@ -593,7 +593,7 @@ bool attn_bwd_fits(size_t rows_q, size_t rows_k, size_t seqs, size_t hq, size_t 
   const Room r = room_of(rows_q, rows_k, hq, hkv, dim, window, sinks);
   const size_t blocks = ((size_t)r.runs * r.sink_tiles + rows_k / kKeysB + seqs) * r.sets + (rows_q / kQueries + seqs) * hq;
   const size_t join = (rows_k / kJoinRows + seqs) * hkv * 2;
-  return blocks <= 0x7FFFFFFF && join <= 0x7FFFFFFF;
+  return fits_launch(blocks, 1, kWavesQ * 64) && fits_launch(join, 1, 256);
 }
 
 hipError_t launch_attn_bwd(const Launch& L, const AttnBwdArgs& b) {

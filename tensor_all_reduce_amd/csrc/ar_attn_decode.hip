@@ -649,6 +649,8 @@ hipError_t launch(const Launch& L, const AttnArgs& a, void* ws) {
 
 size_t attn_decode_workspace(size_t seqs, size_t hq, size_t hkv) { return kPartsBytes + counters_bytes(seqs, hq, hkv); }
 
+bool attn_decode_fits(size_t seqs, size_t hq, size_t hkv) { return fits_launch(seqs, hkv * head_tiles_of(hq, hkv), kWaves * 64); }
+
 hipError_t launch_attn_decode(const Launch& L, const AttnArgs& a, bool e4m3, void* ws) {
   if (a.dim > 64) return e4m3 ? launch<128, true>(L, a, ws) : launch<128, false>(L, a, ws);
   return e4m3 ? launch<64, true>(L, a, ws) : launch<64, false>(L, a, ws);

@@ -217,6 +217,11 @@ struct RopeArgs {
   int pairs, inverse, e4m3;
 };
 hipError_t launch_rope_kv(const Launch& L, const RopeArgs& a);
+bool rope_fits(size_t tokens, size_t heads, size_t dim);  // whether its grid fits a launch
+
+// Whether a launch of a x b workgroups has less than 2^32 work items, the most
+// that HIP takes in a dimension.
+inline bool fits_launch(size_t a, size_t b, size_t threads) { return a == 0 || b <= 0xFFFFFFFFu / threads / a; }
 
 struct AttnArgs {
   HeadRows q, k, v;            // k, v: unless the keys are in pages
@@ -237,6 +242,7 @@ hipError_t launch_attn(const Launch& L, const AttnArgs& a, KeySource src);
 bool attn_fits(size_t rows_q, size_t seqs, size_t hq);  // whether its grid fits a launch
 
 size_t attn_decode_workspace(size_t seqs, size_t hq, size_t hkv);
+bool attn_decode_fits(size_t seqs, size_t hq, size_t hkv);  // whether its grid without a workspace fits a launch
 hipError_t launch_attn_decode(const Launch& L, const AttnArgs& a, bool e4m3, void* workspace);
 
 struct AttnBwdArgs {

@@ -109,13 +109,23 @@ __global__ __launch_bounds__(256) void k_rope_kv(RopeArgs a, int lg, unsigned he
   }
 }
 
+// 2^lg lanes of 16 values each a head
+int lanes_log(unsigned dim) {
+  int lg = 0;
+  while ((16u << lg) < dim) ++lg;
+  return lg;
+}
+
 }  // namespace
+
+bool rope_fits(size_t tokens, size_t heads, size_t dim) {
+  return tokens * heads <= 0x7FFFFFFF && fits_launch(cdiv(tokens * heads, 256u >> lanes_log(dim)), 1, 256);
+}
 
 hipError_t launch_rope_kv(const Launch& L, const RopeArgs& a) {
   // heads of a token that have work: values only with a cache
   const unsigned heads = a.hq + a.hkv + (a.cache.k ? a.hkv : 0);
-  int lg = 0;
-  while ((16u << lg) < a.dim) ++lg;
+  const int lg = lanes_log(a.dim);
   const size_t work = a.tokens * heads, per = 256u >> lg;
   // (16384 tokens of 80 heads of 128: 126 us through the caches, 111 past them)
   const bool nt = a.tokens * (2 * a.hq + 2 * a.hkv) * a.dim * 2 > (size_t)256 << 20;
