@@ -944,8 +944,10 @@ def ar_attn_bwd(q, k, v, out, lse, d_out, cu_q, cu_k, dq=None, dk=None, dv=None,
     attn_bwd_workspace(...) bytes."""
     qp, kp = _heads(q, "q"), _heads(k, "k")
     (rows, hq, dim), (rows_k, hkv) = q.shape, k.shape[:2]
+    if k.shape[2] != dim:
+        raise ValueError(f"k must have heads of {dim}, not {k.shape[2]}")
     shape_q, shape_k = (rows, hq, dim), (rows_k, hkv, dim)
-    kp, vp = _heads(k, "k", shape_k), _heads(v, "v", shape_k)
+    vp = _heads(v, "v", shape_k)
     op, gp = _heads(out, "out", shape_q), _heads(d_out, "d_out", shape_q)
     if lse is None:
         raise ValueError("lse is needed")

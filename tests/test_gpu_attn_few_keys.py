@@ -8,6 +8,7 @@ import attn_ref as ref
 import attn_tight as tight
 import tensor_all_reduce_amd as tar
 from gpu_util import note
+from test_attn_tight import cancelling
 from test_gpu_attn import cu, gen, heads
 from test_gpu_attn_cache import tables
 
@@ -37,3 +38,26 @@ def test_gradients_of_queries_with_few_keys(dim, nq, nk, window, sinks):
         ref.close(dq[:, x][few], want["dq"][few], want["dq_t"][few], f"dq, head {x}")
         if bool(few.all()):
             ref.close(dk[:, x], want["dk"], want["dk_t"], f"dk, head {x}")
+
+
+@pytest.mark.parametrize("cut", [False, True])
+@pytest.mark.parametrize("keys", [24, 130, 700])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_single_tokens_numerators(dim, keys, cut):
+    """Values of which the softmax leaves hardly anything."""
+    note(f"numerators {keys} of {dim}, cut {cut}")
+    g, h, page = gen(keys), 4, 16
+    table, pages = tables(g, [keys], page)
+    cache = tar.kv_cache_empty(pages, page, h, dim, DEV)
+    q, k = heads(g, 1, h, dim, 0.25), heads(g, keys, h, dim)
+    v = torch.stack([cancelling(g, keys, dim, q[:, x], k[:, x], dim ** -0.5) for x in range(h)], 1)
+    j = torch.arange(keys, device=DEV)
+    for c, x in zip(cache, (k, v)):
+        c[table[0].long()[j // page], j % page] = x
+    ws = torch.zeros(tar.attn_decode_workspace(1, h, h, dim), device=DEV, dtype=torch.uint8)
+    out = torch.empty_like(q)
+    tar.ar_attn_decode(q, cache, table, torch.tensor([keys], device=DEV, dtype=torch.int32), out, workspace=ws if cut else None)
+    torch.cuda.synchronize()
+    for x in range(h):
+        want = ref.attend(q[:, x], k[:, x], v[:, x], dim ** -0.5)
+        ref.close(out[:, x], want["out"], tight.out_bound(q[:, x], k[:, x], v[:, x], dim ** -0.5), f"head {x}")
