@@ -183,7 +183,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
   // numerators are so much smaller that nothing is.
   const int headroom = 10 + 31 - __builtin_clz(nk | 1);   // 2^headroom > 2^8 times the keys, and twice that
   const float down = __uint_as_float((127u - headroom) << 23), up = __uint_as_float((127u + headroom) << 23);
-  auto pass = [&](auto mode) {
+  auto pass = [&](auto mode) __attribute__((always_inline)) {
     constexpr int CARE = decltype(mode)::value;
     if constexpr (CARE < 2) {
       m = AR_NEG_INF;
@@ -368,7 +368,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
   l += __shfl_xor(l, 32);
   // (the tiles are no longer read) the second half's results, a wave's lane by lane
   float* give = reinterpret_cast<float*>(all_lds) + wave * (DT * 16 + 2) * kWave + lane;
-  auto hand_over = [&] {
+  auto hand_over = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
