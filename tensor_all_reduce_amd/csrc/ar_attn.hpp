@@ -56,6 +56,13 @@ __device__ __forceinline__ uint32_t numbers_only(uint32_t w) {
   return w & ((w & 0x7F80u) == 0x7F80u ? 0xFFFF0000u : ~0u) & ((w & 0x7F800000u) == 0x7F800000u ? 0xFFFFu : ~0u);
 }
 
+// x, of which the compiler knows nothing: what rare code makes of it is not
+// formed ahead of the branch to that code.
+__device__ __forceinline__ int late(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }

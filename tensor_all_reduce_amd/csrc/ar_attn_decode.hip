@@ -301,6 +301,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
         sum += lm[w][hd] == AR_NEG_INF ? ll[w][hd] : ll[w][hd] * exp2_fast(lm[w][hd] - M);
       float f = m == AR_NEG_INF ? 0.f : exp2_fast(m - M);
       if (AR_RARE(care)) {                       // (no weight makes such values 0 any more)
+        const int g = late(lane) >> 4;
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -419,210 +420,214 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
       }
     }
     if (!more) break;
-    m = AR_NEG_INF;
-    l = 0.f;
-    const float lift = care ? (float)(10 + 31 - __builtin_clz(now.cut.len | 1)) : 0.f;   // 2^lift > 2^10 times the keys / 2
+    auto compute = [&](auto careful) __attribute__((always_inline)) {
+      constexpr bool CARE = decltype(careful)::value;
+      m = AR_NEG_INF;
+      l = 0.f;
+      const float lift = CARE ? (float)(10 + 31 - __builtin_clz(now.cut.len | 1)) : 0.f;   // 2^lift > 2^10 times the keys / 2
 #pragma unroll
-    for (int x = 0; x < DP / 64; ++x) odd[x] = 0.f;
+      for (int x = 0; x < DP / 64; ++x) odd[x] = 0.f;
 #pragma unroll
-    for (int d = 0; d < DT; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int d = 0; d < DT; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-    for (unsigned i = 0; i < now.count; ++i) {
-      const int stage = i & 1, slot = i & 3;
-      // the tile's copies are done when only the next one's are left
-      if (i + 1 < now.count) asm volatile("s_waitcnt vmcnt(%0)" :: "n"(R::kCopies) : "memory");
-      else wait_copies();
-      if (i + 2 < now.count) locate(now, i + 2, (slot + 2) & 3);
-      const Keys tile = keys_of(now, i);
-      const int keys = min(tile.end - tile.j0 - wave * STEP, STEP);   // of this wave's step
-      if (keys > 0) {
-        if (__any((lane & (STEP - 1)) < keys && ids[slot * kWave + (lane & (STEP - 1))] >= a.cache.pages))
-          l = __uint_as_float(0x7FC00000u);
-        const char* lk = mine + stage * R::kStage;
-        const uint32_t lv = lmine + stage * R::kStage + R::kKeys;
-        if (AR_RARE(care)) {
-          char* tv = mine + stage * R::kStage + R::kKeys;
+      for (unsigned i = 0; i < now.count; ++i) {
+        const int stage = i & 1, slot = i & 3;
+        // the tile's copies are done when only the next one's are left
+        if (i + 1 < now.count) asm volatile("s_waitcnt vmcnt(%0)" :: "n"(R::kCopies) : "memory");
+        else wait_copies();
+        if (i + 2 < now.count) locate(now, i + 2, (slot + 2) & 3);
+        const Keys tile = keys_of(now, i);
+        const int keys = min(tile.end - tile.j0 - wave * STEP, STEP);   // of this wave's step
+        if (keys > 0) {
+          if (__any((lane & (STEP - 1)) < keys && ids[slot * kWave + (lane & (STEP - 1))] >= a.cache.pages))
+            l = __uint_as_float(0x7FC00000u);
+          const char* lk = mine + stage * R::kStage;
+          const uint32_t lv = lmine + stage * R::kStage + R::kKeys;
+          if constexpr (CARE) {
+            const int lane = late(lane_id());
+            char* tv = mine + stage * R::kStage + R::kKeys;
 #pragma unroll 1
-          for (int r = 0; r < keys; ++r) {
+            for (int r = 0; r < keys; ++r) {
 #pragma unroll
-            for (int x = 0; x < DP / 64; ++x) {
-              const char* p = tv + chunk_at<RB>(r, lane * ES / 16 + x * 4 * ES) + lane * ES % 16;
-              const float v = E4M3 ? ((*p & 0x7F) == 0x7F ? __uint_as_float(0x7FC00000u) : 0.f)
-                                   : bf16_f32(*reinterpret_cast<const uint16_t*>(p));
-              if (!is_number(v)) odd[x] += v;
-            }
-          }
-#pragma unroll 1
-          for (int at = lane * 4; at < R::kKeys; at += kWave * 4) {
-            uint32_t& w = *reinterpret_cast<uint32_t*>(tv + at);
-            if constexpr (E4M3) w &= ~((((w & 0x7F7F7F7Fu) + 0x01010101u) >> 7 & 0x01010101u) * 0xFFu);
-            else w = numbers_only(w);
-          }
-        }
-        // values are read first: they arrive while the scores are formed
-        Frag8 v[DT];
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          if constexpr (E4M3) {
-            const int e = (lane & 15) / 2, r = 4 * g + (e & 3) + (e >= 4 ? 16 : 0);
-            const i32x2 w = read_tr8(lv + chunk_at<RB>(r, d) + (lane & 1) * 8);
-            v[d].w[0] = (uint32_t)w[0];
-            v[d].w[1] = (uint32_t)w[1];
-          } else {
-            const int r = 4 * g + (lane & 15) / 4, ch = 2 * d + (lane & 3) / 2;
-#pragma unroll
-            for (int b = 0; b < NB; ++b) v[d].s[b] = read_tr16(lv + chunk_at<RB>(r + 16 * b, ch) + (lane & 1) * 8);
-          }
-        }
-        f32x4 scale_k[NB], scale_v[NB];
-        if constexpr (E4M3) {
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            scale_k[b] = *reinterpret_cast<const f32x4*>(lk + 2 * R::kKeys + (16 * b + 4 * g) * 4);
-            scale_v[b] = *reinterpret_cast<const f32x4*>(lk + 2 * R::kKeys + (STEP + 16 * b + 4 * g) * 4);
-          }
-        }
-        f32x4 s[NB];
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          s[b] = f32x4{0.f, 0.f, 0.f, 0.f};
-          if constexpr (E4M3) {
-#pragma unroll
-            for (int x = 0; x < KS / 2; ++x) {
-              const u32x4 w = *reinterpret_cast<const u32x4*>(lk + chunk_at<RB>(16 * b + hd, 4 * x + g));
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                Frag8 k;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  union { b16x2 b; uint32_t u; } lo, hi;
-                  lo.b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[2 * y + e], 1.0f, false);
-                  hi.b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[2 * y + e], 1.0f, true);
-                  k.w[2 * e] = lo.u;
-                  k.w[2 * e + 1] = hi.u;
-                }
-                s[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k.b, q[2 * x + y].b, s[b], 0, 0, 0);
+              for (int x = 0; x < DP / 64; ++x) {
+                const char* p = tv + chunk_at<RB>(r, lane * ES / 16 + x * 4 * ES) + lane * ES % 16;
+                const float v = E4M3 ? ((*p & 0x7F) == 0x7F ? __uint_as_float(0x7FC00000u) : 0.f)
+                                     : bf16_f32(*reinterpret_cast<const uint16_t*>(p));
+                if (!is_number(v)) odd[x] += v;
               }
             }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) s[b][r] *= scale_k[b][r];
-          } else {
-#pragma unroll
-            for (int x = 0; x < KS; ++x) {
-              Frag8 k;
-              k.u = *reinterpret_cast<const u32x4*>(lk + chunk_at<RB>(16 * b + hd, 4 * x + g));
-              s[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k.b, q[x].b, s[b], 0, 0, 0);
+#pragma unroll 1
+            for (int at = lane * 4; at < R::kKeys; at += kWave * 4) {
+              uint32_t& w = *reinterpret_cast<uint32_t*>(tv + at);
+              if constexpr (E4M3) w &= ~((((w & 0x7F7F7F7Fu) + 0x01010101u) >> 7 & 0x01010101u) * 0xFFu);
+              else w = numbers_only(w);
             }
           }
-        }
-        // register r of block b is key 16 b + 4 g + r of the step
-        if (keys < STEP) {
+          // values are read first: they arrive while the scores are formed
+          Frag8 v[DT];
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            if constexpr (E4M3) {
+              const int e = (lane & 15) / 2, r = 4 * g + (e & 3) + (e >= 4 ? 16 : 0);
+              const i32x2 w = read_tr8(lv + chunk_at<RB>(r, d) + (lane & 1) * 8);
+              v[d].w[0] = (uint32_t)w[0];
+              v[d].w[1] = (uint32_t)w[1];
+            } else {
+              const int r = 4 * g + (lane & 15) / 4, ch = 2 * d + (lane & 3) / 2;
+#pragma unroll
+              for (int b = 0; b < NB; ++b) v[d].s[b] = read_tr16(lv + chunk_at<RB>(r + 16 * b, ch) + (lane & 1) * 8);
+            }
+          }
+          f32x4 scale_k[NB], scale_v[NB];
+          if constexpr (E4M3) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              scale_k[b] = *reinterpret_cast<const f32x4*>(lk + 2 * R::kKeys + (16 * b + 4 * g) * 4);
+              scale_v[b] = *reinterpret_cast<const f32x4*>(lk + 2 * R::kKeys + (STEP + 16 * b + 4 * g) * 4);
+            }
+          }
+          f32x4 s[NB];
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            s[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if constexpr (E4M3) {
+#pragma unroll
+              for (int x = 0; x < KS / 2; ++x) {
+                const u32x4 w = *reinterpret_cast<const u32x4*>(lk + chunk_at<RB>(16 * b + hd, 4 * x + g));
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  Frag8 k;
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    union { b16x2 b; uint32_t u; } lo, hi;
+                    lo.b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[2 * y + e], 1.0f, false);
+                    hi.b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[2 * y + e], 1.0f, true);
+                    k.w[2 * e] = lo.u;
+                    k.w[2 * e + 1] = hi.u;
+                  }
+                  s[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k.b, q[2 * x + y].b, s[b], 0, 0, 0);
+                }
+              }
+#pragma unroll
+              for (int r = 0; r < 4; ++r) s[b][r] *= scale_k[b][r];
+            } else {
+#pragma unroll
+              for (int x = 0; x < KS; ++x) {
+                Frag8 k;
+                k.u = *reinterpret_cast<const u32x4*>(lk + chunk_at<RB>(16 * b + hd, 4 * x + g));
+                s[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k.b, q[x].b, s[b], 0, 0, 0);
+              }
+            }
+          }
+          // register r of block b is key 16 b + 4 g + r of the step
+          if (keys < STEP) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) s[b][r] = 16 * b + 4 * g + r < keys ? s[b][r] : AR_NEG_INF;
+          }
+          float top = AR_NEG_INF;
 #pragma unroll
           for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) s[b][r] = 16 * b + 4 * g + r < keys ? s[b][r] : AR_NEG_INF;
-        }
-        float top = AR_NEG_INF;
+            for (int r = 0; r < 4; ++r) top = fmaxf(top, s[b][r]);
+          top = max_of(swap32(max_of(swap16(top)))) * c;
+          if constexpr (CARE) top += lift;
+          if (__any(top > m + 8.0f)) {
+            const float up = fmaxf(m, top), f = m == AR_NEG_INF ? 1.0f : exp2_fast(m - up);
+            m = up;
+            l *= f;
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) top = fmaxf(top, s[b][r]);
-        top = max_of(swap32(max_of(swap16(top)))) * c + lift;
-        if (__any(top > m + 8.0f)) {
-          const float up = fmaxf(m, top), f = m == AR_NEG_INF ? 1.0f : exp2_fast(m - up);
-          m = up;
-          l *= f;
-#pragma unroll
-          for (int d = 0; d < DT; ++d) o[d] *= f;
-        }
-        const float base = m == AR_NEG_INF ? 0.f : m;
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            s[b][r] = exp2_fast(__builtin_fmaf(s[b][r], c, -base));
-            l += s[b][r];
+            for (int d = 0; d < DT; ++d) o[d] *= f;
           }
-        if constexpr (E4M3) {
+          const float base = m == AR_NEG_INF ? 0.f : m;
 #pragma unroll
-          for (int b = 0; b < NB; ++b) {
+          for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) s[b][r] *= scale_v[b][r];
-            if (keys < STEP) {                   // (a masked place's scale may be no number)
+            for (int r = 0; r < 4; ++r) {
+              s[b][r] = exp2_fast(__builtin_fmaf(s[b][r], c, -base));
+              l += s[b][r];
+            }
+          if constexpr (E4M3) {
 #pragma unroll
-              for (int r = 0; r < 4; ++r) s[b][r] = 16 * b + 4 * g + r < keys ? s[b][r] : 0.f;
+            for (int b = 0; b < NB; ++b) {
+#pragma unroll
+              for (int r = 0; r < 4; ++r) s[b][r] *= scale_v[b][r];
+              if (keys < STEP) {                   // (a masked place's scale may be no number)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) s[b][r] = 16 * b + 4 * g + r < keys ? s[b][r] : 0.f;
+              }
             }
           }
-        }
-        // as two bf16 numbers each, 2^-17 off: the matrix cores have the time
-        Frag8 p, rest;
+          // as two bf16 numbers each, 2^-17 off: the matrix cores have the time
+          Frag8 p, rest;
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+          for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int r = 0; r < 4; r += 2) {
-            const uint32_t w = cvt_bf16x2(s[b][r], s[b][r + 1]);
-            p.w[2 * b + r / 2] = w;
-            rest.w[2 * b + r / 2] = cvt_bf16x2(s[b][r] - lo_f32(w), s[b][r + 1] - hi_f32(w));
+            for (int r = 0; r < 4; r += 2) {
+              const uint32_t w = cvt_bf16x2(s[b][r], s[b][r + 1]);
+              p.w[2 * b + r / 2] = w;
+              rest.w[2 * b + r / 2] = cvt_bf16x2(s[b][r] - lo_f32(w), s[b][r + 1] - hi_f32(w));
+            }
+          // whether element e of the lane's values is of a key of the step: 0
+          // times what a masked place holds must be 0
+          const int beyond = keys - 4 * g;         // of keys 4 g + ...; 16 less for the second four
+          if constexpr (E4M3) {
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+              const i32x2 w = {(int)v[d].w[0], (int)v[d].w[1]};
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                union { b16x2 b; uint32_t u; } lo, hi;
+                lo.b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[x], 1.0f, false);
+                hi.b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[x], 1.0f, true);
+                v[d].w[2 * x] = lo.u;
+                v[d].w[2 * x + 1] = hi.u;
+              }
+            }
           }
-        // whether element e of the lane's values is of a key of the step: 0
-        // times what a masked place holds must be 0
-        const int beyond = keys - 4 * g;         // of keys 4 g + ...; 16 less for the second four
-        if constexpr (E4M3) {
+          if (keys < STEP) {
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+              for (int e = 0; e < 4 * NB; ++e)
+                if ((e & 3) + (e >= 4 ? 16 : 0) >= beyond) v[d].w[e / 2] &= e & 1 ? 0xFFFFu : 0xFFFF0000u;
+          }
+          if constexpr (E4M3 && CARE) {            // (an infinite scale's numerator has no rest)
+#pragma unroll
+            for (int w = 0; w < 2 * NB; ++w) rest.w[w] = numbers_only(rest.w[w]);
+          }
 #pragma unroll
           for (int d = 0; d < DT; ++d) {
-            const i32x2 w = {(int)v[d].w[0], (int)v[d].w[1]};
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              union { b16x2 b; uint32_t u; } lo, hi;
-              lo.b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[x], 1.0f, false);
-              hi.b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[x], 1.0f, true);
-              v[d].w[2 * x] = lo.u;
-              v[d].w[2 * x + 1] = hi.u;
+            if constexpr (NB == 2) {
+              o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[d].b, p.b, o[d], 0, 0, 0);
+              o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[d].b, rest.b, o[d], 0, 0, 0);
+            } else {
+              // both in one: the second four of a lane's keys are the first again
+              Frag8 twice;
+              twice.s[0] = twice.s[1] = v[d].s[0];
+              Frag8 both;
+              both.s[0] = p.s[0];
+              both.s[1] = rest.s[0];
+              o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(twice.b, both.b, o[d], 0, 0, 0);
             }
           }
         }
-        if (keys < STEP) {
-#pragma unroll
-          for (int d = 0; d < DT; ++d)
-#pragma unroll
-            for (int e = 0; e < 4 * NB; ++e)
-              if ((e & 3) + (e >= 4 ? 16 : 0) >= beyond) v[d].w[e / 2] &= e & 1 ? 0xFFFFu : 0xFFFF0000u;
-        }
-        if (E4M3 && AR_RARE(care)) {             // (an infinite scale's numerator has no rest)
-#pragma unroll
-          for (int w = 0; w < 2 * NB; ++w) rest.w[w] = numbers_only(rest.w[w]);
-        }
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          if constexpr (NB == 2) {
-            o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[d].b, p.b, o[d], 0, 0, 0);
-            o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[d].b, rest.b, o[d], 0, 0, 0);
-          } else {
-            // both in one: the second four of a lane's keys are the first again
-            Frag8 twice;
-            twice.s[0] = twice.s[1] = v[d].s[0];
-            Frag8 both;
-            both.s[0] = p.s[0];
-            both.s[1] = rest.s[0];
-            o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(twice.b, both.b, o[d], 0, 0, 0);
-          }
-        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the stage has been read
+        if (i + 2 < now.count) fetch(now, i + 2, stage, (slot + 2) & 3);
       }
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the stage has been read
-      if (i + 2 < now.count) fetch(now, i + 2, stage, (slot + 2) & 3);
-    }
 
-    if (!care) {
-      f32x4 all = {0.f, 0.f, 0.f, 0.f};        // numbers only if every result is, and below 2^115
+    };
+    compute(std::false_type{});
+    f32x4 all = {0.f, 0.f, 0.f, 0.f};          // numbers only if every result is, and below 2^115
 #pragma unroll
-      for (int d = 0; d < DT; ++d)
+    for (int d = 0; d < DT; ++d)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) all[r] = __builtin_fmaf(o[d][r], 0x1p13f, all[r]);
-      if (AR_RARE(__any(!is_number((all[0] + all[1]) + (all[2] + all[3]))))) {
-        care = true;
-        done = false;
-        continue;
-      }
+      for (int r = 0; r < 4; ++r) all[r] = __builtin_fmaf(o[d][r], 0x1p13f, all[r]);
+    if (AR_RARE(__any(!is_number((all[0] + all[1]) + (all[2] + all[3]))))) {
+      care = true;
+      start(now);
+      compute(std::true_type{});
     }
     s0 = now;
     done = true;
