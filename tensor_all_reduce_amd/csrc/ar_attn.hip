@@ -199,6 +199,9 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
       else copy(part, 0);
       if (part + KG < keys.steps) look_up(part + KG);
     }
+    // (the queries have come: a wait for them in the loop would be one for the
+    // tile under way, too)
+    if constexpr (SRC == kKeyPagesE4M3) wait_copies();
     for (int i = 0; i * KG < keys.steps; ++i) {
       const int buf = i & 1, n = i * KG + part;
       const bool mine = KG == 1 || n < keys.steps;   // the second half may have one tile less
