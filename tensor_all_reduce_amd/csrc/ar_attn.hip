@@ -7,17 +7,18 @@
 // two 32 x 32 products; the workgroup's waves share the keys' and values'
 // tiles in LDS, copied there past the registers one tile ahead.  Scores,
 // maxima, sums and results are binary32; the softmax's numerators become bf16
-// for their product with the values, 2^-9 of each, which is what the rounding
-// of the values' own sum to bf16 costs once more.
+// for their product with the values, up to 2^-8 of each, which is what the
+// rounding of the values' own sum to bf16 costs once more.
 //
 // Bound by the matrix cores and, beside them, the softmax's arithmetic: of a
 // tile of 64 keys a wave has 32 products of 32 cycles and about 240 vector
 // instructions of 4, of which two waves a SIMD overlap a part.  Operands are
 // read from LDS four products ahead, in a fixed order, so that nothing is
 // spilled: a reload would wait for the copies under way, which share its
-// counter.  16384 tokens, 64 heads of 128 on 8, causal: 4220 us, 1.04 PFLOP/s
-// (order left to the compiler 4932, one spilled register in the loop 4700; a
-// third tile of LDS, wave priorities and 128 queries a workgroup within 4%).
+// counter.  16384 tokens, 64 heads of 128 on 8, causal: 4130 to 4250 us, 1.04 to
+// 1.06 PFLOP/s (order left to the compiler 4932, one spilled register in the loop
+// 4700; a third tile of LDS, wave priorities and 128 queries a workgroup within
+// 4%); over E4M3 pages 5040, 0.87 PFLOP/s.
 #include "ar_attn.hpp"
 
 namespace ar {
@@ -180,7 +181,9 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn(AttnArgs a) {
   // see a key of that page have a sum that is no number.  And where a sum is
   // beyond binary32: numerators are up to 2^8, and as many as there are keys,
   // so that large values' sums can be though their mean is not.  With care
-  // numerators are so much smaller that nothing is.
+  // numerators are so much smaller that nothing is.  (These passes are code of
+  // their own: as branches of one loop they cost the ordinary pass 10 to 20
+  // registers and 1 to 3%.)
   const int headroom = 10 + 31 - __builtin_clz(nk | 1);   // 2^headroom > 2^8 times the keys, and twice that
   const float down = __uint_as_float((127u - headroom) << 23), up = __uint_as_float((127u + headroom) << 23);
   auto pass = [&](auto mode) __attribute__((always_inline)) {

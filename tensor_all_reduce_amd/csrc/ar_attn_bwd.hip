@@ -545,7 +545,7 @@ Room room_of(size_t rows_q, size_t rows_k, size_t hq, size_t hkv, size_t dim, si
   r.delta = cdiv(rows_q * hq, 64) * 64;
   // Query heads of a key head that one workgroup takes one after the other, each
   // of which spares a write and a read of its sums and a start: as many as
-  // leave two workgroups a CU.
+  // leave 512 workgroups, two rounds of one a CU (whose LDS one fills).
   const size_t group = hq / hkv, tiles = cdiv(rows_k ? rows_k : 1, kKeysB) * hkv;
   size_t per = group;
   while (per > 1 && (group % per || tiles * (group / per) < 512)) --per;

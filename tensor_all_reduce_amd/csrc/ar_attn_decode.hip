@@ -13,22 +13,30 @@
 // depend on which one was last.
 //
 // Keys and values are copied to LDS past the registers, two steps of a wave
-// ahead: 64 to 128 KiB a CU are on their way, which is what its share of the
-// memory's rate takes over the memory's latency.  The page numbers of a step
-// come the same way, two steps before its keys.
+// ahead: for heads of 128, 128 KiB a CU are on their way, which is what its share
+// of the memory's rate takes over the memory's latency.  The page numbers of a
+// step come the same way, two steps before its keys.
 //
 // 48 sequences of 111 to 16384 keys, 8 key heads of 128 in bf16: 122 us, 5.3
-// TB/s; 8 of 120k to 131k in E4M3 386 us, 5.5.  Kept for what they gave there:
+// TB/s; 8 of 120k to 131k in E4M3 382 us, 5.5.  Kept for what they gave there:
 // eight waves instead of four (171 -> 156 and 750 -> 497 us), one loop a
 // sequence (142 -> 134, 475 -> 458), copies past the caches (134 -> 122, 458
 // -> 402), ends of sequences counted in the spread (156 -> 142).
+//
+// Narrower heads: a step holds rows of 64 or 128 whatever the head, so that of 80,
+// 96 and 112 only 63 to 88% of those bytes are on their way (64 KiB in E4M3 of
+// 64).  The same 48 sequences: of 64 in bf16 78 us, 4.2 TB/s (8 of 120k to 131k
+// keys: 5.3), 80 95 us, 4.3, 96 105 us, 4.7, 112 134 us, 4.25; in E4M3 72, 94, 95,
+// 98 us, 2.3 to 3.0 TB/s, and of 128 85 us, 4.0.  With a window of 4096 and 4
+// sinks, which are a tile of their own, 79 us of 128 in bf16, 4.8 TB/s, 61 in
+// E4M3, 3.2; with a window of 512 30, 2.9.
 #include "ar_attn.hpp"
 
 namespace ar {
 namespace {
 
 constexpr int kWaves = 8;
-constexpr unsigned kWorkers = 256;             // one a CU: the LDS of a workgroup fills it
+constexpr unsigned kWorkers = 256;             // one a CU of a whole device: the LDS of a workgroup fills it
 constexpr unsigned kHeads = 16;                // query heads of a tile
 
 // What a wave has in LDS: two steps' keys and values, four steps' page numbers.
@@ -275,7 +283,8 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_decode(AttnArgs a, unsi
   // barrier lies between a part's start and its join.)  So too where a sum is
   // 2^115 or more, of which the 2^11 that are joined could pass binary32's
   // end though their mean does not: with care the maximum is followed 2^lift
-  // above, and numerators are at most 2^-2 of one over the keys.
+  // above, and numerators are at most 2^-2 of one over the keys.  (Code of its
+  // own: as branches of one loop it cost heads of 64 in bf16 a tenth.)
   bool care = false;
   float odd[DP / 64];                          // columns lane, lane + 64
   for (;;) {

@@ -12,7 +12,8 @@ fills the rank's `attn` buffer:
   prompt  the next chunks of ragged prompts, ar_attn_paged over the pages
   train   ragged sequences without pages, ar_attn; backward() takes the
           gradient of `attn` through ar_attn_bwd and the rotation back to the
-          projection's result
+          projection's result.  The caller fills that gradient: TPBlock's
+          backward pass ends before the row-parallel projection
 
 Every buffer is allocated once and every call prepared once; a step is a
 handful of launches on one stream and can be captured in a HIP graph.  Run as
