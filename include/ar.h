@@ -590,9 +590,9 @@ int ar_gemm_fp8(const ar_fp8_matrix* a, const ar_fp8_matrix* b, void* const* c, 
  * AR_ERR_UNSUPPORTED is also a call of 2^32 work items or more, the most that
  * a launch takes: of ar_rope_kv one for every 16 elements of a head of every
  * token (their number rounded up to 2^n), of the others 512 for a query head
- * of 256 queries (or a part of a sequence's), and of ar_attn_decode without a
- * workspace 512 for every key head (or part of it with 16 query heads) of a
- * sequence.
+ * of 256 queries (or a part of a sequence's), of ar_attn_bwd also for one of 128
+ * keys and for a key head of 8 keys, and of ar_attn_decode without a workspace
+ * for every key head (or part of it with 16 query heads) of a sequence.
  *
  * Numbers on the device (lengths, offsets, positions, page numbers, slots) are
  * not known to the caller's thread and not refused: lengths and offsets are
