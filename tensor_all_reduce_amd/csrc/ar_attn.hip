@@ -15,8 +15,8 @@
 // instructions of 4, of which two waves a SIMD overlap a part.  Operands are
 // read from LDS four products ahead, in a fixed order, so that nothing is
 // spilled: a reload would wait for the copies under way, which share its
-// counter.  16384 tokens, 64 heads of 128 on 8, causal: 4130 to 4250 us, 1.04 to
-// 1.06 PFLOP/s (order left to the compiler 4932, one spilled register in the loop
+// counter.  16384 tokens, 64 heads of 128 on 8, causal: 4060 to 4350 us, 1.01 to
+// 1.08 PFLOP/s (order left to the compiler 4932, one spilled register in the loop
 // 4700; a third tile of LDS, wave priorities and 128 queries a workgroup within
 // 4%); over E4M3 pages 5040, 0.87 PFLOP/s.
 #include "ar_attn.hpp"
