@@ -134,3 +134,33 @@ def test_workspaces_of_any_contents():
         res.append(o)
     torch.cuda.synchronize()
     assert torch.equal(*res) and bool(torch.isfinite(res[0]).all())
+
+
+@pytest.mark.parametrize("power", [-64, -40, 40, 64])
+def test_scales_far_from_one(power):
+    """Queries and keys as large or small as the scale makes up for."""
+    note(f"scale 2^{power}")
+    g, lengths, hq, hkv, dim = gen(8), [200, 33], 4, 2, 64
+    n, offs, by = sum(lengths), cu(lengths), 2.0 ** (-power // 2 - 1)
+    q, k, v, go = (heads(g, n, h, dim) for h in (hq, hkv, hkv, hq))
+    q, k, scale = q * by, k * by, 2.0 ** power            # exact; scores of 2^-2 q . k
+    out, lse = torch.empty_like(q), torch.empty(n, hq, device=DEV)
+    tar.ar_attn(q, k, v, offs, offs, out, scale=scale, lse=lse)
+    ws = torch.empty(tar.attn_bwd_workspace(n, n, 2, hq, hkv, dim), device=DEV, dtype=torch.uint8)
+    d = [torch.empty_like(x) for x in (q, k, v)]
+    tar.ar_attn_bwd(q, k, v, out, lse, go, offs, offs, dq=d[0], dk=d[1], dv=d[2], workspace=ws, scale=scale)
+    torch.cuda.synchronize()
+    want = ref.ragged(q, k, v, offs.tolist(), offs.tolist(), scale, 0, 0, go)
+    for x, y in zip(("out", "lse", "dq", "dk", "dv"), (out, lse, *d)):
+        ref.close(y, want[x], want[x + "_t"], x)
+    table, pages = tables(g, lengths, 16)
+    cache = filled(g, pages, 16, hkv, dim, False)
+    cache[0].mul_(by)
+    one = torch.empty_like(q[:2])
+    tar.ar_attn_decode(q[:2], cache, table, torch.tensor(lengths, device=DEV, dtype=torch.int32), one, scale=scale)
+    torch.cuda.synchronize()
+    for i, m in enumerate(lengths):
+        kk, vv = ref.paged(cache, table[i], m)
+        for h in range(hq):
+            w = ref.attend(q[i:i + 1, h], kk[:, h // 2], vv[:, h // 2], scale)
+            ref.close(one[i:i + 1, h], w["out"], w["out_t"], "single token")
